@@ -72,6 +72,13 @@ typedef enum {
 
 typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 
+/* What spec_history_append adds to a slot: emitted tokens (counted) or prompt tokens. */
+typedef enum { SV_HISTORY_OUTPUT = 0, SV_HISTORY_PROMPT = 1 } sv_history_kind;
+
+/* Blocks of 4-bit values (spec_quantize_fp4): blocks of 32 under a power-of-two scale, or blocks of
+ * 16 under an e4m3 scale times a power of two for the row. */
+typedef enum { SV_FP4_E8M0_32 = 0, SV_FP4_E4M3_16 = 1 } sv_fp4_format;
+
 /* Largest drafted length per request accepted by the verify calls and the Markov head. */
 #define SV_MAX_DRAFT_LEN 64
 
@@ -285,6 +292,116 @@ sv_status spec_verify_lmhead(const void* target_hidden, const void* draft_hidden
                              int32_t* out_tokens, int64_t out_ld, int32_t* correction_token,
                              float* accept_ratio, int32_t* recomputed, int32_t* status,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Logits before verification: penalties for repeated tokens, biases and grammar masks, and the
+ * history they are computed from.  No page covers them: an engine applies them to the target's
+ * and to the draft's rows alike, so that p and q are the distributions the tokens really come from.
+ *
+ * History of a slot (a place a request holds while it is served), all DEVICE, owned by the caller:
+ *   counts       int32 [n_slots][ld_counts]: how often each token was emitted (ld_counts >= V)
+ *   prompt_bits  uint32 [n_slots][ld_bits]: the tokens of the prompt, token v in bit v % 32 of
+ *                word v / 32 (ld_bits >= ceil(V / 32))
+ *   output_bits  the same for the emitted tokens: set exactly where the count is positive
+ * ------------------------------------------------------------------------------------------- */
+
+/* Adds the tokens of B rows to the history: row r is tokens[r * ld_tokens + 0 .. n - 1] (DEVICE
+ * int32), or its first lens[r] (nullable, [B]) columns; negative tokens are padding and skipped, so
+ * spec_verify_token's and spec_verify_block's out_tokens go in as they are.  slots (nullable, [B];
+ * NULL: r) names each row's slot.  kind: SV_HISTORY_OUTPUT counts the tokens, SV_HISTORY_PROMPT
+ * marks them as seen in the prompt.  reset = 1 first clears the whole history of the listed slots
+ * (a request admitted to a slot); a slot may then be listed once only.  With reset = 0 a slot may
+ * be listed several times.  Counts are added modulo 2^32.
+ * A slot outside [0, n_slots), a length outside [0, n], a token >= V, or a slot listed twice with
+ * reset writes SV_ERR_BAD_INPUT to status; that row or token is left out.  Slots that are not
+ * listed keep their history.  The result does not depend on the order of the rows. */
+sv_status spec_history_append(const int32_t* tokens, int64_t ld_tokens, const int32_t* lens,
+                              int32_t n, const int32_t* slots, int32_t B, int32_t kind,
+                              int32_t reset, int64_t V, int32_t n_slots, int32_t* counts,
+                              int64_t ld_counts, uint32_t* prompt_bits, uint32_t* output_bits,
+                              int64_t ld_bits, int32_t* status, void* stream);
+
+/* Penalties, biases and masks on the logit rows of a speculative round.  Request r's rows are
+ * row0[r] + i for i = first_row .. draft_len[r] + bonus_row - 1, `dtype` elements, ld apart, read
+ * from `logits` and written to `out` (ld_out apart); `out` equal to `logits` works in place (then
+ * ld_out = ld), any other overlap is not allowed.  bonus_row = 1 for target rows (one more than
+ * drafts), 0 for draft rows; first_row > 0 leaves the rows before it alone: a draft model calls
+ * with draft_len = first_row = i, bonus_row = 1 for the row it has just made, and a request that
+ * decodes without drafts has draft_len 0.  Rows outside, and columns from V on, are not written.
+ * Row i follows the first i drafted tokens draft_tokens[draft_row0[r] + 0 .. i - 1].  With
+ * n(v) = counts[slot][v] (where output_bits is set) + occurrences of v among those i tokens:
+ *   l = seen ? (l > 0 ? l / repetition[r] : l * repetition[r]) : l   (seen: prompt bit or n > 0)
+ *   l = l - frequency[r] * n - (n > 0 ? presence[r] : 0)
+ *   l = l + bias(v)                        if v is in the request's bias list
+ *   l = allowed(v) ? l : -inf              whatever l is, NaN and infinities included
+ * in binary32, rounded once to dtype; an element none of this touches keeps its bits.
+ *   slots (nullable, [B], NULL: r), n_slots and the history: needed with any of the penalties.
+ *   repetition (finite, > 0), presence, frequency (finite): DEVICE fp32 [B], each nullable (1, 0, 0);
+ *     a request with repetition 1 and the others 0 does not read its history.
+ *   bias_start: DEVICE int32 [B + 1] (nullable: no biases); request r's list is entries
+ *     bias_start[r] .. bias_start[r + 1] - 1 of bias_tokens (strictly ascending) and bias_values
+ *     (fp32), n_bias entries in all.
+ *   mask_row: DEVICE int32, indexed like the logit rows (nullable: no masks): the row of
+ *     mask uint32 [n_mask][ld_mask] that applies, or -1 for none; bit 1 allows a token.  A mask
+ *     that allows nothing leaves a row of -inf, which verification reports.
+ * Values out of the ranges above, draft lengths outside [0, max_draft_len], drafted tokens outside
+ * [0, V) (where penalties read them) and lists that do not ascend write SV_ERR_BAD_INPUT to status.
+ * Rows are 16-byte aligned as for verification.  V at most 2^31 - 4097. */
+sv_status spec_process_logits(const void* logits, int64_t ld, void* out, int64_t ld_out,
+                              sv_dtype dtype, int64_t V, const int64_t* row0,
+                              const int64_t* draft_row0, const int32_t* draft_len,
+                              int32_t max_draft_len, int32_t first_row, int32_t bonus_row,
+                              const int32_t* draft_tokens, int32_t B, const int32_t* slots,
+                              int32_t n_slots, const int32_t* counts, int64_t ld_counts,
+                              const uint32_t* prompt_bits, const uint32_t* output_bits,
+                              int64_t ld_bits, const float* repetition, const float* presence,
+                              const float* frequency, const int32_t* bias_start,
+                              const int32_t* bias_tokens, const float* bias_values,
+                              int64_t n_bias, const uint32_t* mask, int64_t ld_mask,
+                              int32_t n_mask, const int32_t* mask_row, int32_t* status,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The output projection in 4 bits.  A block of values shares a scale S; each is c * S with c in
+ * {0, 0.5, 1, 1.5, 2, 3, 4, 6} and their negatives (a 4-bit code: sign, two exponent bits, one
+ * mantissa bit).
+ *   SV_FP4_E8M0_32  blocks of 32; S = 2^e, e = floor(log2 max|x|) - 2 within [-127, 127], stored
+ *                   as e + 127 in 8 bits.
+ *   SV_FP4_E4M3_16  blocks of 16; S = s g: g = 2^k (fp32, one per row), the smallest with
+ *                   max|row| <= 2688 g, k within [-120, 120] (1 for a row of zeros), and s =
+ *                   max|x| / (6 g) rounded to the nearest e4m3 value, ties to even.
+ * c is x / S rounded to nearest, ties to the even code, at most 6 (0 where S is 0).  A block that
+ * holds a NaN or an infinity (SV_FP4_E4M3_16: any block of such a row) gets the scale that stands
+ * for NaN, so every product with it is NaN, and SV_ERR_BAD_INPUT is written to status.
+ * Layout: packed [rows][spec_fp4_row_bytes(H)], element i in nibble i % 2 (0: low) of byte i / 2,
+ * rows padded with zeros to 32 elements.  scales: tiles of 512 bytes, one per 128 rows and 4
+ * blocks, tile (r / 128, k / 4) row-major, byte (r % 32) * 16 + (r / 32 % 4) * 4 + k % 4 of a tile
+ * for row r's block k; rows are padded to 128 and blocks to 256 elements with scale bytes 0.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Bytes of one packed row, and of all scales of `rows` rows (0 for sizes the calls reject). */
+int64_t spec_fp4_row_bytes(int64_t H);
+size_t spec_fp4_scale_bytes(int64_t rows, int64_t H, int32_t format);
+
+/* Quantises x [rows][H] (`dtype`, ldx elements apart; any alignment its elements allow).  format:
+ * an sv_fp4_format.  row_scales: DEVICE fp32 [rows], SV_FP4_E4M3_16 only.  values (nullable): bf16
+ * [rows][H], ld_values apart: the numbers the codes stand for (each is a bf16 number, or infinite
+ * where rounding up took it past the largest one). */
+sv_status spec_quantize_fp4(const void* x, sv_dtype dtype, int64_t rows, int64_t H, int64_t ldx,
+                            int32_t format, uint8_t* packed, uint8_t* scales, float* row_scales,
+                            void* values, int64_t ld_values, int32_t* status, void* stream);
+
+/* logits[m][v] = sum over k of x[m][k] w[v][k], both operands quantised in `format` (M hidden rows
+ * and V rows of the output projection of width H; row scales with SV_FP4_E4M3_16 only), summed in
+ * fp32 on the tensor cores and rounded once to `dtype`: the rows spec_verify_token and
+ * spec_process_logits take.  Rows of logits are ld apart, 16-byte aligned as for verification;
+ * columns from V on are not written.  M and H at most 2^24, V at most 2^31 - 257.
+ * status (nullable) tells of a wait that ran out. */
+sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_scales,
+                           const float* x_row_scales, int64_t M, const uint8_t* w_packed,
+                           const uint8_t* w_scales, const float* w_row_scales, int64_t V,
+                           int64_t H, int32_t format, void* logits, sv_dtype dtype, int64_t ld,
+                           int32_t* status, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * DSpark draft side.

@@ -20,6 +20,8 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "specverify.h")
 
 SV_OK, SV_ERR_INVALID, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_BAD_INPUT, SV_ERR_TIMEOUT = range(6)
 SV_F32, SV_BF16 = 0, 1
+SV_HISTORY_OUTPUT, SV_HISTORY_PROMPT = 0, 1
+SV_FP4_E8M0_32, SV_FP4_E4M3_16 = 0, 1
 SV_MAX_DRAFT_LEN = 64
 SV_NOALLOC_SCRATCH_BYTES = 8 << 20  # scratch array of spec_verify_token_noalloc
 
@@ -80,6 +82,15 @@ def lib():
             "spec_verify_lmhead_workspace_bytes": (sz, [i32, i32, i64, i64]),
             "spec_verify_lmhead": (st, [P, P, i64, P, i64, i64, i64, P, P, P, i32, P, i32, u64,
                                         P, P, P, i64, P, P, P, P, P, sz, P]),
+            "spec_history_append": (st, [P, i64, P, i32, P, i32, i32, i32, i64, i32, P, i64, P, P,
+                                         i64, P, P]),
+            "spec_process_logits": (st, [P, i64, P, i64, st, i64, P, P, P, i32, i32, i32, P, i32,
+                                         P, i32, P, i64, P, P, i64, P, P, P, P, P, P, i64, P, i64,
+                                         i32, P, P, P]),
+            "spec_fp4_row_bytes": (i64, [i64]),
+            "spec_fp4_scale_bytes": (sz, [i64, i64, i32]),
+            "spec_quantize_fp4": (st, [P, st, i64, i64, i64, i32, P, P, P, P, i64, P, P]),
+            "spec_project_fp4": (st, [P, P, P, i64, P, P, P, i64, i64, i32, P, st, i64, P, P]),
             "dspark_schedule_rule": (st, [P, P, i32, i32, P, i32, i32, P, P, P, P, P, P, sz, P]),
             "dspark_schedule_async": (st, [P, i32, i64, P, P, i32, i32, P, i32, i32, P, P, P, P, P,
                                            P, sz, P]),
@@ -430,6 +441,200 @@ def spec_verify_token_sharded(target, draft, v_off, V_total, target_row0, draft_
     out = st["finish"](gather(race["winners"]), race["accepted_len"], draft_row0, draft_tokens,
                        out_ld or max_draft_len + 1)
     out["accept_ratio"] = race.get("accept_ratio")
+    return out
+
+
+# ---- logits before verification ----------------------------------------------------------------
+
+def _sized(t, name, *shape):
+    """Checks a tensor's shape (None: any extent)."""
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t
+
+
+def _status(status, dev):
+    if status is None:
+        return torch.zeros(1, dtype=torch.int32, device=dev)
+    return _dev(status, torch.int32)
+
+
+def _history(counts, prompt_bits, output_bits):
+    """Checks the history tensors; returns (slots, counts stride, bits stride, V)."""
+    _dev(counts, torch.int32, rows=True), _dev(prompt_bits, torch.int32, rows=True)
+    _dev(output_bits, torch.int32, rows=True)
+    n_slots, V = counts.shape
+    words = (V + 31) // 32
+    if (prompt_bits.shape[0] != n_slots or output_bits.shape[0] != n_slots
+            or prompt_bits.shape[1] < words or output_bits.shape[1] < words):
+        raise ValueError("the bit rows must be [slots, ceil(V / 32)] for counts [slots, V]")
+    if prompt_bits.stride(0) != output_bits.stride(0):
+        raise ValueError("prompt_bits and output_bits must have the same stride")
+    return n_slots, counts.stride(0), prompt_bits.stride(0), V
+
+
+def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, lens=None,
+                        prompt=False, reset=False, status=None, stream=None):
+    """Adds tokens int32 [B, n] (negative: padding; only the first lens[r] columns if given) to
+    the history of slots int32 [B] (default: row r in slot r), in place: counts int32 [S, V] and
+    the bit rows int32 [S, ceil(V / 32)] (see include/specverify.h).  `prompt` marks them as prompt
+    tokens instead of counting them; `reset` clears the listed slots first.  Returns the status."""
+    _dev(tokens, torch.int32, rows=True)
+    n_slots, ldc, ldb, V = _history(counts, prompt_bits, output_bits)
+    B, n = tokens.shape
+    if lens is not None:
+        _sized(_dev(lens, torch.int32), "lens", B)
+    if slots is not None:
+        _sized(_dev(slots, torch.int32), "slots", B)
+    elif B > n_slots:
+        raise ValueError("more rows than slots")
+    status = _status(status, tokens.device)
+    code = lib().spec_history_append(_ptr(tokens), max(tokens.stride(0), n), _ptr(lens), n,
+                                     _ptr(slots), B, int(prompt), int(reset), V, n_slots,
+                                     _ptr(counts), ldc, _ptr(prompt_bits), _ptr(output_bits), ldb,
+                                     _ptr(status), _stream(stream))
+    _check(code, "spec_history_append")
+    return status
+
+
+def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draft_tokens,
+                        first_row=0, bonus_row=True, slots=None, counts=None, prompt_bits=None,
+                        output_bits=None, repetition=None, presence=None, frequency=None,
+                        bias_start=None, bias_tokens=None, bias_values=None, mask=None,
+                        mask_row=None, out=None, status=None, stream=None):
+    """Repetition / presence / frequency penalties (fp32 [B]), logit biases (bias_start int32
+    [B + 1] into ascending bias_tokens int32 and bias_values fp32) and grammar masks (mask int32
+    [n, ceil(V / 32)] bit rows, mask_row int32 per logit row, -1: none) on the rows of a round
+    (see include/specverify.h).  Works in place unless `out` is another tensor of the same shape
+    and dtype.  Returns out."""
+    _dev(logits, rows=True), _dev(row0, torch.int64), _dev(draft_row0, torch.int64)
+    _dev(draft_len, torch.int32), _dev(draft_tokens, torch.int32)
+    dt = _dtype_code(logits)
+    V = logits.shape[1]
+    B = draft_len.numel()
+    out = logits if out is None else _dev(out, logits.dtype, rows=True)
+    if out.shape != logits.shape:
+        raise ValueError("out must have the shape of the logits")
+    if row0.numel() != B or (draft_row0 is not None and draft_row0.numel() != B):
+        raise ValueError("row0, draft_row0 and draft_len must have one entry per request")
+    n_slots = ldc = ldb = 0
+    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+        if t is not None:
+            _sized(_dev(t, torch.float32), name, B)
+    if repetition is not None or presence is not None or frequency is not None:
+        if counts is None or prompt_bits is None or output_bits is None:
+            raise ValueError("penalties need counts, prompt_bits and output_bits")
+        n_slots, ldc, ldb, hv = _history(counts, prompt_bits, output_bits)
+        if hv != V:
+            raise ValueError("the history's vocabulary differs from the logits'")
+        if slots is not None:
+            _sized(_dev(slots, torch.int32), "slots", B)
+        elif B > n_slots:
+            raise ValueError("more requests than slots")
+    n_bias = 0
+    if bias_start is not None:
+        _sized(_dev(bias_start, torch.int32), "bias_start", B + 1)
+        _dev(bias_tokens, torch.int32), _dev(bias_values, torch.float32)
+        n_bias = bias_tokens.numel()
+        if bias_values.numel() != n_bias:
+            raise ValueError("bias_tokens and bias_values must have the same length")
+    n_mask = ldm = 0
+    if mask_row is not None:
+        _sized(_dev(mask_row, torch.int32), "mask_row", logits.shape[0])
+        _dev(mask, torch.int32, rows=True)
+        n_mask, ldm = mask.shape[0], mask.stride(0)
+        if mask.shape[1] < (V + 31) // 32:
+            raise ValueError("mask rows must hold ceil(V / 32) words")
+    status = _status(status, logits.device)
+    code = lib().spec_process_logits(
+        _ptr(logits), logits.stride(0), _ptr(out), out.stride(0), dt, V, _ptr(row0),
+        _ptr(draft_row0), _ptr(draft_len), int(max_draft_len), int(first_row), int(bonus_row),
+        _ptr(draft_tokens), B, _ptr(slots), n_slots, _ptr(counts), ldc, _ptr(prompt_bits),
+        _ptr(output_bits), ldb, _ptr(repetition), _ptr(presence), _ptr(frequency),
+        _ptr(bias_start), _ptr(bias_tokens), _ptr(bias_values), n_bias, _ptr(mask), ldm, n_mask,
+        _ptr(mask_row), _ptr(status), _stream(stream))
+    _check(code, "spec_process_logits")
+    return out
+
+
+# ---- the output projection in 4 bits -------------------------------------------------------------
+
+def spec_fp4_row_bytes(H):
+    return int(lib().spec_fp4_row_bytes(H))
+
+
+def spec_fp4_scale_bytes(rows, H, fmt):
+    return int(lib().spec_fp4_scale_bytes(rows, H, fmt))
+
+
+def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=None, status=None,
+                      stream=None):
+    """Rows x [rows, H] (bf16 or fp32, any row stride) to blocks of 4-bit values in format `fmt`
+    (see include/specverify.h).  Returns {"packed", "scales", "row_scales", "rows", "H", "format",
+    "status"}, which spec_project_fp4 takes as an operand; `values`, a bf16 [rows, H] tensor, is
+    filled with the numbers the codes stand for."""
+    _dev(x, rows=True)
+    dt = _dtype_code(x)
+    rows, H = x.shape
+    dev = x.device
+    nbytes, rb = spec_fp4_scale_bytes(rows, H, fmt), spec_fp4_row_bytes(H)
+    if packed is None:
+        packed = torch.empty((rows, rb), dtype=torch.uint8, device=dev)
+    elif tuple(_dev(packed, torch.uint8).shape) != (rows, rb):
+        raise ValueError(f"packed must be [rows, {rb}]")
+    if scales is None:
+        scales = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif _dev(scales, torch.uint8).numel() != nbytes:
+        raise ValueError(f"scales must hold {nbytes} bytes")
+    if fmt == SV_FP4_E4M3_16:
+        if row_scales is None:
+            row_scales = torch.empty(rows, dtype=torch.float32, device=dev)
+        else:
+            _sized(_dev(row_scales, torch.float32), "row_scales", rows)
+    else:
+        row_scales = None
+    ldv = 0
+    if values is not None:
+        _sized(_dev(values, torch.bfloat16, rows=True), "values", rows, H)
+        ldv = max(values.stride(0), H)
+    status = _status(status, dev)
+    code = lib().spec_quantize_fp4(_ptr(x), dt, rows, H, max(x.stride(0), H), int(fmt),
+                                   _ptr(packed), _ptr(scales), _ptr(row_scales), _ptr(values), ldv,
+                                   _ptr(status), _stream(stream))
+    _check(code, "spec_quantize_fp4")
+    return {"packed": packed, "scales": scales, "row_scales": row_scales, "rows": rows, "H": H,
+            "format": int(fmt), "status": status}
+
+
+def _fp4_operand(t, name):
+    rows, H, fmt = t["rows"], t["H"], t["format"]
+    _sized(_dev(t["packed"], torch.uint8), f"{name} packed", rows, (H + 31) // 32 * 16)
+    if _dev(t["scales"], torch.uint8).numel() != spec_fp4_scale_bytes(rows, H, fmt):
+        raise ValueError(f"{name} scales do not fit [{rows}, {H}]")
+    if fmt == SV_FP4_E4M3_16:
+        _sized(_dev(t["row_scales"], torch.float32), f"{name} row_scales", rows)
+    return rows, H, fmt
+
+
+def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=None):
+    """Logits [M, V] = x w^T of two operands quantised by spec_quantize_fp4: hidden rows x [M, H]
+    and the output projection w [V, H] (see include/specverify.h).  `out` (bf16 or fp32, rows
+    16-byte aligned) is allocated in `dtype` if not given.  Returns it."""
+    M, H, fmt = _fp4_operand(x, "x")
+    V, Hw, fw = _fp4_operand(w, "w")
+    if Hw != H or fw != fmt:
+        raise ValueError("x and w must have the same width and format")
+    if out is None:
+        ld = (V + 7) // 8 * 8  # rows start on 16-byte boundaries
+        out = torch.empty((M, ld), dtype=dtype, device=x["packed"].device)[:, :V]
+    _sized(_dev(out, rows=True), "out", M, V)
+    dt = _dtype_code(out)
+    status = _status(status, out.device)
+    code = lib().spec_project_fp4(_ptr(x["packed"]), _ptr(x["scales"]), _ptr(x["row_scales"]), M,
+                                  _ptr(w["packed"]), _ptr(w["scales"]), _ptr(w["row_scales"]), V,
+                                  H, fmt, _ptr(out), dt, max(out.stride(0), V), _ptr(status),
+                                  _stream(stream))
+    _check(code, "spec_project_fp4")
     return out
 
 

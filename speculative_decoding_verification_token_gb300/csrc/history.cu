@@ -1,0 +1,157 @@
+// history.cu -- the token history that penalties are computed from (spec_history_append).
+//
+// State of a slot: how often each token was emitted (counts), and two bit rows, token v in bit
+// v % 32 of word v / 32: the tokens of the prompt and the tokens emitted (set exactly where the
+// count is positive).  Appending adds integers and sets bits, so the result does not depend on the
+// order in which the atomics land.
+#include "sv_device.cuh"
+#include "sv_host.h"
+
+namespace sv {
+namespace {
+
+struct HistParams {
+  const int32_t* tokens;
+  int64_t ld_tokens;
+  const int32_t* lens;
+  int32_t n;
+  const int32_t* slots;
+  int32_t B;
+  int32_t prompt;
+  int64_t V;
+  int32_t n_slots;
+  int32_t* counts;
+  int64_t ld_counts;
+  uint32_t* prompt_bits;
+  uint32_t* output_bits;
+  int64_t ld_bits;
+  int32_t* status;
+};
+
+constexpr int kHistThreads = 256;
+
+// Row r's slot and number of columns; a bad value of either is reported and leaves the row alone.
+__device__ __forceinline__ bool hist_row(const HistParams& p, int32_t r, int32_t& slot,
+                                         int32_t& n) {
+  slot = p.slots ? p.slots[r] : r;
+  n = p.lens ? p.lens[r] : p.n;
+  if (slot < 0 || slot >= p.n_slots || n < 0 || n > p.n) {
+    report(p.status, SV_ERR_BAD_INPUT);
+    return false;
+  }
+  return true;
+}
+
+// One thread per token.  A round appends a few hundred tokens, so the call is one launch of one
+// or two dependent loads and two atomics.
+__global__ void __launch_bounds__(kHistThreads) history_append_kernel(HistParams p) {
+  const int64_t i = int64_t(blockIdx.x) * kHistThreads + threadIdx.x;
+  if (i >= int64_t(p.B) * p.n) return;
+  const int32_t r = static_cast<int32_t>(i / p.n);
+  const int32_t t = static_cast<int32_t>(i % p.n);
+  int32_t slot, n;
+  if (!hist_row(p, r, slot, n) || t >= n) return;
+  const int32_t x = p.tokens[r * p.ld_tokens + t];
+  if (x < 0) return;  // padding
+  if (x >= p.V) {
+    report(p.status, SV_ERR_BAD_INPUT);
+    return;
+  }
+  uint32_t* word = (p.prompt ? p.prompt_bits : p.output_bits) + slot * p.ld_bits + (x >> 5);
+  atomicOr(word, 1u << (x & 31));
+  if (!p.prompt) atomicAdd(p.counts + slot * p.ld_counts + x, 1);
+}
+
+constexpr int kResetThreads = 512;
+constexpr int kResetWords = 512;  // 32-token words of a slot that one CTA owns
+
+// Clear, then append: each CTA owns kResetWords words of one slot and the counts below them, so the
+// two steps need no order between CTAs.  It clears its counts, reads the row's tokens (at most a few
+// tens of KB, from L2 for all CTAs of a slot but the first) and keeps those in its range.
+__global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams p,
+                                                                      int32_t chunks) {
+  __shared__ uint32_t s_bits[kResetWords];
+  __shared__ int32_t s_twice;
+  const int32_t r = blockIdx.x / chunks;
+  const int32_t c = blockIdx.x % chunks;
+  const int tid = threadIdx.x;
+  int32_t slot, n;
+  if (!hist_row(p, r, slot, n)) return;  // the whole CTA
+  if (tid == 0) s_twice = 0;
+  for (int w = tid; w < kResetWords; w += kResetThreads) s_bits[w] = 0;
+  __syncthreads();
+  if (p.slots)
+    for (int32_t q = tid; q < p.B; q += kResetThreads)
+      if (q != r && p.slots[q] == slot) s_twice = 1;
+  const int64_t w0 = int64_t(c) * kResetWords;
+  const int64_t words = min(int64_t(kResetWords), (p.V + 31) / 32 - w0);
+  const int64_t v0 = w0 * 32, v1 = min(p.V, v0 + int64_t(kResetWords) * 32);
+  int32_t* cnt = p.counts + slot * p.ld_counts;
+  __syncthreads();
+  if (s_twice) {  // two rows would clear and fill the same slot
+    if (tid == 0) report(p.status, SV_ERR_BAD_INPUT);
+    return;
+  }
+  if ((reinterpret_cast<uintptr_t>(cnt) & 15u) == 0) {
+    const int64_t full = v1 & ~int64_t(3);
+    for (int64_t v = v0 + 4 * tid; v < full; v += 4 * kResetThreads)
+      *reinterpret_cast<int4*>(cnt + v) = make_int4(0, 0, 0, 0);
+    for (int64_t v = full + tid; v < v1; v += kResetThreads) cnt[v] = 0;
+  } else {
+    for (int64_t v = v0 + tid; v < v1; v += kResetThreads) cnt[v] = 0;
+  }
+  __syncthreads();  // the counts are zero before this CTA's atomics reach them
+  const int32_t* row = p.tokens + r * p.ld_tokens;
+  for (int32_t t = tid; t < n; t += kResetThreads) {
+    const int32_t x = row[t];
+    if (x < 0) continue;
+    if (x >= p.V) {
+      report(p.status, SV_ERR_BAD_INPUT);
+      continue;
+    }
+    if (x < v0 || x >= v1) continue;
+    atomicOr(&s_bits[(x - v0) >> 5], 1u << (x & 31));
+    if (!p.prompt) atomicAdd(cnt + x, 1);
+  }
+  __syncthreads();
+  uint32_t* pb = p.prompt_bits + slot * p.ld_bits + w0;
+  uint32_t* ob = p.output_bits + slot * p.ld_bits + w0;
+  for (int w = tid; w < words; w += kResetThreads) {
+    pb[w] = p.prompt ? s_bits[w] : 0u;
+    ob[w] = p.prompt ? 0u : s_bits[w];
+  }
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" sv_status spec_history_append(const int32_t* tokens, int64_t ld_tokens,
+                                         const int32_t* lens, int32_t n, const int32_t* slots,
+                                         int32_t B, int32_t kind, int32_t reset, int64_t V,
+                                         int32_t n_slots, int32_t* counts, int64_t ld_counts,
+                                         uint32_t* prompt_bits, uint32_t* output_bits,
+                                         int64_t ld_bits, int32_t* status, void* stream) {
+  if (B < 0 || n < 0 || V < 1 || n_slots < 0 || ld_tokens < n || ld_counts < V ||
+      ld_bits < (V + 31) / 32 || (kind != SV_HISTORY_OUTPUT && kind != SV_HISTORY_PROMPT) ||
+      (reset != 0 && reset != 1))
+    return SV_ERR_INVALID;
+  if (V > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  if (B == 0 || (n == 0 && !reset)) return SV_OK;
+  if ((n > 0 && !tokens) || !counts || !prompt_bits || !output_bits) return SV_ERR_INVALID;
+  const int64_t chunks = ((V + 31) / 32 + kResetWords - 1) / kResetWords;
+  const int64_t blocks =
+      reset ? chunks * B : (int64_t(B) * n + kHistThreads - 1) / kHistThreads;
+  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return SV_ERR_CUDA;
+  const HistParams p = {tokens, ld_tokens, lens, n,         slots,       B,           kind,
+                        V,      n_slots,   counts, ld_counts, prompt_bits, output_bits, ld_bits,
+                        status};
+  if (reset)
+    history_reset_kernel<<<unsigned(blocks), kResetThreads, 0, s>>>(p, int32_t(chunks));
+  else
+    history_append_kernel<<<unsigned(blocks), kHistThreads, 0, s>>>(p);
+  return launch_status(cudaGetLastError());
+}
