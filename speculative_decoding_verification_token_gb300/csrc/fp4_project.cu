@@ -2,14 +2,17 @@
 // (spec_project_fp4): out[m][v] = sum_k x[m][k] w[v][k], both operands as quantised by
 // spec_quantize_fp4.
 //
-// A persistent, warp-specialised tcgen05 GEMM.  W is the A operand (128 vocabulary rows per tile,
-// TMEM lanes), the hidden rows the B operand (up to 192 rows per tile, TMEM columns), K in blocks
-// of 256 elements: 128 bytes, one row of the 128-byte swizzle.
-//   warp 0     TMA loads of the k-blocks of W and of the hidden rows, and bulk copies of their
-//              scale tiles, into a ring;
-//   warp 1     per k-block, tcgen05.cp of the scale tiles to TMEM and four block-scaled
-//              tcgen05.mma (K = 64) into one of two accumulators;
-//   warps 2-9  the epilogue: a lane quadrant and a column half each.
+// A persistent, warp-specialised tcgen05 GEMM on pairs of CTAs (cta_group::2).  W is the A operand
+// (256 vocabulary rows per tile: TMEM lanes, 128 in each CTA), the hidden rows the B operand (up to
+// 256 rows per tile: TMEM columns, half of them in each CTA's shared memory), K in blocks of 256
+// elements: 128 bytes, one row of the 128-byte swizzle.
+//   warp 0      TMA loads of this CTA's k-blocks of W, of its half of the hidden rows and of the
+//               scale tiles into a ring; both CTAs' copies complete on the leader's barrier;
+//   warp 1      in the leader, per k-block, tcgen05.cp of the scale tiles to both CTAs' TMEM and
+//               four block-scaled tcgen05.mma (K = 64) into an accumulator;
+//   warps 2-17  the epilogue: a lane quadrant and every fourth 16-column piece each, moved to
+//               registers at once so that the accumulator is free again, then through shared
+//               memory to the logits by TMA stores.
 // The tensor cores apply the block scales and add in fp32; the row scales of SV_FP4_E4M3_16 are
 // powers of two, applied to the sum in the epilogue.
 #include <algorithm>
@@ -22,9 +25,9 @@
 namespace sv {
 namespace {
 
-constexpr int kPjRows = 128;     // vocabulary rows per tile (UMMA M)
-constexpr int kPjMaxN = 192;     // hidden rows per tile at most
-constexpr int kPjEpiWarps = 8;
+constexpr int kPjRows = 128;    // vocabulary rows per CTA and tile
+constexpr int kPjMaxN = 256;    // hidden rows per tile at most
+constexpr int kPjEpiWarps = 16;
 constexpr int kPjThreads = 32 * (2 + kPjEpiWarps);
 constexpr uint32_t kPjABytes = kPjRows * 128;
 constexpr uint32_t kPjSmem = 225 * 1024;  // ring and alignment slack
@@ -32,21 +35,75 @@ constexpr int kPjMaxStages = 10;
 constexpr uint32_t kPjTmemCols = 512;
 
 struct PjParams {
-  int32_t n_vt, n_nt, nt;  // vocabulary tiles, hidden-row tiles, rows of a hidden-row tile
+  int32_t n_vt, n_nt, nt;  // tiles of 256 vocabulary rows, hidden-row tiles, their rows
   int32_t kblocks;
   int64_t H, V;
   int32_t M;
-  int32_t m_tiles;  // scale tiles of the hidden rows
+  int32_t n_acc;  // accumulators in TMEM
   int32_t stages;
   uint32_t stage_bytes, b_off, sfa_off, sfb_off;
-  const uint8_t* w_scales;
-  const uint8_t* x_scales;
+  uint32_t out_off;  // the epilogue's staging buffers, behind the ring
+  uint32_t tx_bytes;  // bytes both CTAs load per stage
+  int32_t groups;     // scale groups per row
   const float* w_row;
   const float* x_row;
   void* out;
   int64_t ld;
   int32_t* status;
 };
+
+// ---- cluster pieces ------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// The cluster-window address of `local` (a shared::cta address) in CTA `rank`.
+__device__ __forceinline__ uint32_t map_rank(uint32_t local, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// TMA loads of a CTA pair: the destination is this CTA's, `bar` the leader's barrier.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, int32_t c0,
+                                             int32_t c1, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0,
+                                             int32_t c1, int32_t c2, uint32_t bar,
+                                             uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// Arrive once on `bar` (the same offset in both CTAs) when all tcgen05 work issued so far is done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
 
 // mbar_wait with a suspend-time hint: the waiting thread sleeps until the phase completes.  Bounded:
 // after kWaitLimitNs it reports SV_ERR_TIMEOUT and gives up.
@@ -74,27 +131,60 @@ __device__ __forceinline__ bool pj_wait(uint64_t* bar, uint32_t parity, int32_t*
   return true;
 }
 
-// Shared-memory descriptor of a 512-byte scale tile (32 rows of 16 bytes, no swizzle): core
-// matrices of 8 rows by 16 bytes are 128 bytes, the stride between them.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_byte_addr) {
-  uint64_t d = 0;
-  d |= uint64_t((smem_byte_addr & 0x3FFFFu) >> 4);
-  d |= uint64_t(128 >> 4) << 32;  // stride byte offset: eight rows of 16 bytes
-  d |= uint64_t(1) << 46;         // descriptor version
+// One thread of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
+// pj_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool pj_wait_warp(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return __all_sync(0xffffffffu, pj_wait(bar, parity, status));
+}
+
+// Shared-memory descriptors by halves: the low word holds the address (>> 4) and the leading
+// offset, the high word is a constant of the layout, so that moving to another stage, tile or
+// K-step is one 32-bit addition.  Operands: 128-byte swizzle (tc.cuh).  Scale tiles: 32 rows of 16
+// bytes without swizzle, core matrices of 8 rows by 16 bytes 128 bytes apart.
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kOperandLo = 1u << 16;
+constexpr uint32_t kScaleHi = (128u >> 4) | (1u << 14);
+
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
   return d;
 }
 
 // 512 bytes of scales to four TMEM columns, the 32 lanes repeated in every lane quadrant.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+               "l"(desc_of(lo, kScaleHi))
                : "memory");
 }
 
 // Instruction descriptor of the block-scaled 4-bit kinds: e2m1 A and B (1 in bits [7,10) and
 // [10,12)), both K-major, N >> 3 in [17,23), scale type in bit 23 (1: e8m0, 0: e4m3), M >> 7 in
-// [27,29); the scale ids of B and A go to [4,6) and [29,31).
+// [27,29) (M = 256 over the pair); the scale ids of B and A go to [4,6) and [29,31).
 constexpr uint32_t pj_idesc(int32_t n, bool e8m0) {
-  return (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (e8m0 ? 1u << 23 : 0u) | (1u << 27);
+  return (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (e8m0 ? 1u << 23 : 0u) | (2u << 27);
+}
+
+// 16 columns of this thread's TMEM lane, in flight until the next tcgen05.wait::ld.
+__device__ __forceinline__ void tmem_load16_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 template <int kFmt>
@@ -105,7 +195,7 @@ __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
         "[%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(sfa), "r"(sfb)
         : "memory");
@@ -113,29 +203,68 @@ __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X "
         "[%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(sfa), "r"(sfb)
         : "memory");
   }
 }
 
-template <int kFmt, typename Out>
-__global__ void __launch_bounds__(kPjThreads, 1)
+// One k-block: the scale tiles of W and of kX tiles of the hidden rows to TMEM, then `ksteps`
+// products of K = 64.  Everything but the K-steps of the last k-block is known at compile time: a
+// single thread issues all of this, and its instructions, not the tensor cores, set the pace of
+// small tiles.
+template <int kFmt, int kX>
+__device__ __forceinline__ void k_block(uint32_t stage, uint32_t b_off, uint32_t sfa_off,
+                                        uint32_t sfb_off, uint32_t acc, uint32_t sfa,
+                                        uint32_t sfb_shift, uint32_t idesc, int32_t ksteps,
+                                        bool accumulate) {
+  constexpr int kGroups = kFmt == SV_FP4_E8M0_32 ? 2 : 4;
+  const uint32_t sfb = sfa + kGroups * 4;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    copy_scales(sfa + g * 4, stage + sfa_off + g * 32);
+#pragma unroll
+    for (int x = 0; x < kX; ++x)
+      copy_scales(sfb + (g * kX + x) * 4, stage + sfb_off + (x * kGroups + g) * 32);
+  }
+  const uint32_t a_lo = stage + kOperandLo, b_lo = a_lo + b_off;
+  const uint32_t sfbs = sfb + sfb_shift;
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    if (ks >= ksteps) break;
+    const int g = kGroups == 4 ? ks : ks >> 1;
+    const uint32_t id = kGroups == 4 ? 0u : (ks & 1) ? (2u << 4) | (2u << 29) : 0u;
+    mma_fp4<kFmt>(acc, desc_of(a_lo + ks * 2, kOperandHi), desc_of(b_lo + ks * 2, kOperandHi),
+                  idesc | id, sfa + g * 4, sfbs + g * kX * 4, accumulate || ks != 0);
+  }
+}
+
+__device__ __forceinline__ void put(float* o, float y) { *o = y; }
+__device__ __forceinline__ void put(__nv_bfloat16* o, float y) { *o = __float2bfloat16_rn(y); }
+
+template <int kFmt, int kX, typename Out>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
     project_kernel(const __grid_constant__ CUtensorMap map_w,
-                   const __grid_constant__ CUtensorMap map_x, PjParams p) {
+                   const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ CUtensorMap map_ws,
+                   const __grid_constant__ CUtensorMap map_xs,
+                   const __grid_constant__ CUtensorMap map_out, PjParams p) {
   constexpr int kGroups = kFmt == SV_FP4_E8M0_32 ? 2 : 4;  // scale groups per k-block
-  constexpr uint32_t kTileBytes = kGroups * 512;           // scales of 128 rows and one k-block
-  constexpr uint32_t kSfaCols = kGroups * 4;
-  constexpr uint32_t kSfCols = kSfaCols * 3;  // W's tile and at most two of the hidden rows'
+  constexpr uint32_t kSfCols = kGroups * 4 * (1 + kX);
+  constexpr int kPieces = kX == 1 ? 2 : 4;  // 16-column pieces per epilogue warp
+  constexpr uint32_t kOutBytes = 16 * 32 * sizeof(Out);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kPjMaxStages], empty[kPjMaxStages];
-  __shared__ uint64_t acc_full[2], acc_empty[2], drain;
+  __shared__ uint64_t full[kPjMaxStages], empty[kPjMaxStages];  // full: the leader's
+  __shared__ uint64_t acc_full[2], acc_empty[2], drain;         // acc_empty: the leader's
   __shared__ uint32_t tmem_base;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
+  const uint32_t rank = cluster_rank();
+  const int32_t pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int32_t n_items = p.n_vt * p.n_nt;
   const int32_t stages = p.stages;
   if (tid == 0) {
@@ -145,158 +274,264 @@ __global__ void __launch_bounds__(kPjThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], kPjEpiWarps);
+      mbar_init(&acc_empty[a], 2 * kPjEpiWarps);
     }
     mbar_init(&drain, 1);
     fence_barrier_init();
+    // the only report is of a wait that ran out, a second after the start at the earliest
+    if (blockIdx.x == 0 && p.status) *p.status = 0;
   }
-  if (warp == 1) tc::tmem_alloc(&tmem_base, kPjTmemCols);
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&tmem_base)),
+                 "r"(kPjTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
   tc::fence_before_sync();
   __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised before anything arrives on them
   tc::fence_after_sync();
   const uint32_t tmem = tmem_base;
   const uint32_t sf_base = tmem + kPjTmemCols - 2 * kSfCols;  // two buffers of scale columns
 
-  // Scale tiles of the hidden rows n0 .. n0 + nt - 1 that exist.
-  auto x_tiles = [&](int32_t n0) {
-    return min(p.m_tiles, (n0 + p.nt + 127) >> 7) - (n0 >> 7);
-  };
-
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t keep = tc::policy_evict_last(), once = tc::policy_evict_first();
-      const uint64_t w_policy = p.n_nt > 1 ? keep : once;
-      uint32_t it = 0;
-      bool ok = true;
-      for (int32_t item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const int32_t vt = item / p.n_nt, n0 = (item % p.n_nt) * p.nt;
-        const int32_t nx = x_tiles(n0);
-        const uint32_t bytes = kPjABytes + uint32_t(p.nt) * 128 + (1 + nx) * kTileBytes;
-        const size_t per_tile = size_t(p.kblocks) * kTileBytes;
-        const uint8_t* ws = p.w_scales + size_t(vt) * per_tile;
-        const uint8_t* xs = p.x_scales + size_t(n0 >> 7) * per_tile;
-        for (int32_t kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const uint32_t s = it % stages, use = it / stages;
-          if (use > 0 && !pj_wait(&empty[s], (use - 1) & 1, p.status)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = ring + size_t(s) * p.stage_bytes;
-          mbar_expect_tx(&full[s], bytes);
-          tc::tma_load_2d_hint(st, &map_w, kb * 128, vt * kPjRows, &full[s], w_policy);
-          tc::tma_load_2d_hint(st + p.b_off, &map_x, kb * 128, n0, &full[s], keep);
-          bulk_g2s(st + p.sfa_off, ws + size_t(kb) * kTileBytes, kTileBytes, &full[s]);
-          for (int32_t t = 0; t < nx; ++t)
-            bulk_g2s(st + p.sfb_off + t * kTileBytes, xs + t * per_tile + size_t(kb) * kTileBytes,
-                     kTileBytes, &full[s]);
+    const uint64_t keep = tc::policy_evict_last(), once = tc::policy_evict_first();
+    const uint64_t w_policy = p.n_nt > 1 ? keep : once;
+    const uint32_t ring_at = smem_addr(ring);
+    int32_t st = 0;
+    uint32_t phase = 1;  // a ring stage starts out empty
+    int32_t issued = 0;  // stages filled at least once
+    uint32_t dst = ring_at, bar = map_rank(smem_addr(&full[0]), 0);
+    const uint32_t bar0 = bar;
+    bool ok = true;
+    for (int32_t item = pair; item < n_items && ok; item += n_pairs) {
+      const int32_t vt = (item / p.n_nt) * 2 + int32_t(rank), n0 = (item % p.n_nt) * p.nt;
+      // the products take their N columns half from each CTA
+      const int32_t x0 = n0 + int32_t(rank) * (min(p.nt, (p.M - n0 + 15) & ~15) >> 1);
+      for (int32_t kb = 0; kb < p.kblocks; ++kb) {
+        if (!pj_wait_warp(&empty[st], phase, p.status)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          if (rank == 0) mbar_expect_tx(&full[st], p.tx_bytes);
+          pair_load_2d(dst, &map_w, kb * 128, vt * kPjRows, bar, w_policy);
+          pair_load_2d(dst + p.b_off, &map_x, kb * 128, x0, bar, keep);
+          pair_load_3d(dst + p.sfa_off, &map_ws, 0, kb * kGroups, vt, bar, w_policy);
+          pair_load_3d(dst + p.sfb_off, &map_xs, 0, kb * kGroups, n0 >> 7, bar, keep);
+        }
+        __syncwarp();
+        issued = max(issued, st + 1);
+        dst += p.stage_bytes;
+        bar += 8;
+        if (++st == stages) {
+          st = 0;
+          phase ^= 1;
+          dst = ring_at;
+          bar = bar0;
         }
       }
-      // the copies in flight land before the block may end
-      for (uint32_t k = it > uint32_t(stages) ? it - stages : 0; k < it; ++k)
-        pj_wait(&full[k % stages], (k / stages) & 1, p.status);
     }
+    // both CTAs' copies in flight land before either block may end: of each stage that was
+    // filled, the last fill (this round's below st, the round's before from st on)
+    if (rank == 0)
+      for (int32_t k = 0; k < issued; ++k)
+        pj_wait_warp(&full[k], k < st ? phase ^ 1 : phase, p.status);
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      int t = 0;
+    if (rank == 0) {
+      const uint32_t ring_lo = smem_addr(ring) >> 4, stage_lo = p.stage_bytes >> 4;
+      const uint32_t b_off = p.b_off >> 4, sfa_off = p.sfa_off >> 4, sfb_off = p.sfb_off >> 4;
+      const int32_t last_steps = int32_t((p.H - int64_t(p.kblocks - 1) * 256 + 63) >> 6);
+      int32_t st = 0, a = 0;
+      uint32_t phase = 0, stage = ring_lo, sfa = sf_base;
+      uint32_t acc_phase = 1;  // the accumulators start out empty
       bool ok = true;
-      for (int32_t item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++t) {
+      for (int32_t item = pair; item < n_items && ok; item += n_pairs) {
         const int32_t n0 = (item % p.n_nt) * p.nt;
-        const int32_t nx = x_tiles(n0);
-        const int32_t n = min(p.nt, (p.M - n0 + 15) & ~15);
-        const uint32_t idesc = pj_idesc(n, kFmt == SV_FP4_E8M0_32);
-        const uint32_t acc = tmem + (t & 1) * p.nt;
-        if (t >= 2 && !pj_wait(&acc_empty[t & 1], ((t >> 1) - 1) & 1, p.status)) break;
+        const uint32_t idesc =
+            pj_idesc(min(p.nt, (p.M - n0 + 15) & ~15), kFmt == SV_FP4_E8M0_32);
+        const uint32_t shift = (n0 & 127) >> 5;
+        const uint32_t acc = tmem + a * p.nt;
+        if (!pj_wait_warp(&acc_empty[a], acc_phase, p.status)) break;
         tc::fence_after_sync();
-        for (int32_t kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const uint32_t s = it % stages;
-          if (!pj_wait(&full[s], (it / stages) & 1, p.status)) {
+        for (int32_t kb = 0; kb < p.kblocks; ++kb) {
+          if (!pj_wait_warp(&full[st], phase, p.status)) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint32_t base = smem_addr(ring + size_t(s) * p.stage_bytes);
-          const uint32_t sfa = sf_base + (it & 1) * kSfCols, sfb = sfa + kSfaCols;
-#pragma unroll
-          for (int gq = 0; gq < kGroups; ++gq) {
-            copy_scales(sfa + gq * 4, scale_desc(base + p.sfa_off + gq * 512));
-            for (int32_t x = 0; x < nx; ++x)
-              copy_scales(sfb + (gq * 2 + x) * 4,
-                          scale_desc(base + p.sfb_off + x * kTileBytes + gq * 512));
+          if (elect_one()) {
+            k_block<kFmt, kX>(stage, b_off, sfa_off, sfb_off, acc, sfa, shift, idesc,
+                              kb + 1 == p.kblocks ? last_steps : 4, kb != 0);
+            pair_commit(&empty[st]);
           }
-          const int32_t ksteps = min(4, int32_t((p.H - int64_t(kb) * 256 + 63) >> 6));
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            if (ks >= ksteps) break;
-            const int gq = kGroups == 4 ? ks : ks >> 1;
-            const uint32_t id = kGroups == 4 ? 0u : uint32_t(ks & 1) * 2u;
-            mma_fp4<kFmt>(acc, tc::smem_desc_sw128(base + ks * 32),
-                          tc::smem_desc_sw128(base + p.b_off + ks * 32),
-                          idesc | (id << 4) | (id << 29), sfa + gq * 4,
-                          sfb + gq * 8 + ((n0 & 127) >> 5), (kb | ks) != 0);
+          __syncwarp();
+          sfa = sfa == sf_base ? sf_base + kSfCols : sf_base;
+          stage += stage_lo;
+          if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+            stage = ring_lo;
           }
-          tc::mma_commit(&empty[s]);
         }
-        if (ok) tc::mma_commit(&acc_full[t & 1]);
+        if (ok && elect_one()) pair_commit(&acc_full[a]);
+        __syncwarp();
+        if (++a == p.n_acc) {
+          a = 0;
+          acc_phase ^= 1;
+        }
       }
       // nothing reads shared or tensor memory once this has passed
-      tc::mma_commit(&drain);
-      pj_wait(&drain, 0, p.status);
+      if (elect_one()) pair_commit(&drain);
+      __syncwarp();
+      pj_wait_warp(&drain, 0, p.status);
     }
   } else {
     const int q = warp & 3, h = (warp - 2) >> 2;
+    const uint32_t lanes = tmem + (uint32_t(32 * q) << 16);
+    const uint32_t freed = map_rank(smem_addr(acc_empty), 0);
+    // this warp's two staging buffers of 16 rows of 32 logits
+    uint8_t* const stage0 = ring + p.out_off + (warp - 2) * 2 * kOutBytes;
     bool failed = false;
-    int t = 0;
-    for (int32_t item = blockIdx.x; item < n_items; item += gridDim.x, ++t) {
-      const int32_t vt = item / p.n_nt, n0 = (item % p.n_nt) * p.nt;
-      const int64_t v = int64_t(vt) * kPjRows + 32 * q + lane;
+    int32_t a = 0, buf = 0;
+    uint32_t phase = 0;
+    for (int32_t item = pair; item < n_items; item += n_pairs) {
+      const int32_t vt = (item / p.n_nt) * 2 + int32_t(rank), n0 = (item % p.n_nt) * p.nt;
+      const int32_t v0 = vt * kPjRows + 32 * q;
       const int32_t n = min(p.nt, p.M - n0);
-      float ws = 1.f;
-      if (kFmt == SV_FP4_E4M3_16 && v < p.V) ws = __ldg(p.w_row + v);
-      if (!failed && !pj_wait(&acc_full[t & 1], (t >> 1) & 1, p.status)) failed = true;
+      float ws = 1.f, xs[kPieces];
+      if constexpr (kFmt == SV_FP4_E4M3_16) {
+        if (v0 + lane < p.V) ws = __ldg(p.w_row + v0 + lane);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {  // lane j holds column j's row scale
+          const int32_t c = 16 * (h + 4 * i) + (lane & 15);
+          xs[i] = c < n ? __ldg(p.x_row + n0 + c) : 0.f;
+        }
+      }
+      if (!failed && !pj_wait(&acc_full[a], phase, p.status)) failed = true;
       __syncwarp();
       tc::fence_after_sync();
-      // 16-column pieces, alternating between the two warps of a quadrant
-      for (int32_t c = 16 * h; c < n; c += 32) {
-        float a[16];
-        tc::tmem_load16(tmem + (uint32_t(32 * q) << 16) + (t & 1) * p.nt + c, a);
-        if (v < p.V) {
-          Out* o = static_cast<Out*>(p.out) + int64_t(n0 + c) * p.ld + v;
+      float f[kPieces][16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c + j >= n) break;
-            float y = a[j];
-            if (kFmt == SV_FP4_E4M3_16) y = y * ws * __ldg(p.x_row + n0 + c + j);
-            if constexpr (sizeof(Out) == 2)
-              o[j * p.ld] = __float2bfloat16_rn(y);
-            else
-              o[j * p.ld] = y;
+      for (int i = 0; i < kPieces; ++i)
+        if (16 * (h + 4 * i) < n) tmem_load16_async(lanes + a * p.nt + 16 * (h + 4 * i), f[i]);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(freed + a * 8);
+      if (++a == p.n_acc) {
+        a = 0;
+        phase ^= 1;
+      }
+      if (v0 >= p.V) continue;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int32_t c = 16 * (h + 4 * i);
+        if (c >= n) break;
+        if constexpr (kFmt == SV_FP4_E4M3_16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            f[i][j] = f[i][j] * ws * __shfl_sync(0xffffffffu, xs[i], j);
+        }
+        if (v0 + 32 > p.V) {  // a TMA store clips a row at 16 bytes only: these 32 one by one
+          Out* const o = static_cast<Out*>(p.out) + int64_t(n0 + c) * p.ld + v0 + lane;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < n && v0 + lane < p.V) put(o + j * p.ld, f[i][j]);
+          continue;
+        }
+        uint8_t* const st = stage0 + buf * kOutBytes;
+        buf ^= 1;
+        tc::bulk_wait_read<1>();  // the store before the last has read this buffer
+        __syncwarp();
+        if constexpr (sizeof(Out) == 4) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(st)[j * 32 + lane] = f[i][j];
+        } else {
+          // rows j and j + 1 at once: an even lane takes (v, v + 1) of row j, an odd one
+          // (v - 1, v) of row j + 1
+          uint32_t* const o = reinterpret_cast<uint32_t*>(st) + (lane & 1) * 16 + (lane >> 1);
+          const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(f[i][j], f[i][j + 1]);
+            const uint32_t mine = *reinterpret_cast<const uint32_t*>(&two);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+            o[j * 16] = __byte_perm(mine, other, pick);
           }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (elect_one()) {
+          tc::tma_store_2d(&map_out, st, v0, n0 + c);  // clipped at M
+          tc::bulk_commit();
         }
         __syncwarp();
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[t & 1]);
     }
+    tc::bulk_wait_all();
   }
+  __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
+  cluster_sync();  // neither CTA's memory goes away while the other's work may touch it
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, kPjTmemCols);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kPjTmemCols)
+                 : "memory");
   }
 }
 
-template <int kFmt, typename Out>
-sv_status launch_project(const CUtensorMap& map_w, const CUtensorMap& map_x, const PjParams& p,
-                         int grid, cudaStream_t s) {
-  auto* kern = project_kernel<kFmt, Out>;
+struct PjMaps {
+  CUtensorMap w, x, ws, xs, out;
+};
+
+template <int kFmt, int kX, typename Out>
+sv_status launch_project(const PjMaps& m, const PjParams& p, int grid, cudaStream_t s) {
+  auto* kern = project_kernel<kFmt, kX, Out>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kPjSmem)) !=
       cudaSuccess)
     return SV_ERR_CUDA;
-  kern<<<grid, kPjThreads, kPjSmem, s>>>(map_w, map_x, p);
+  kern<<<grid, kPjThreads, kPjSmem, s>>>(m.w, m.x, m.ws, m.xs, m.out, p);
   return launch_status(cudaGetLastError());
+}
+
+template <int kFmt, int kX>
+sv_status launch_project(const PjMaps& m, const PjParams& p, sv_dtype dtype, int grid,
+                         cudaStream_t s) {
+  return dtype == SV_BF16 ? launch_project<kFmt, kX, __nv_bfloat16>(m, p, grid, s)
+                          : launch_project<kFmt, kX, float>(m, p, grid, s);
+}
+
+bool rows_map(CUtensorMap* map, const uint8_t* base, int64_t rows, uint64_t row_bytes,
+              uint32_t box_rows) {
+  const uint64_t dims[2] = {row_bytes, uint64_t(rows)};
+  const uint64_t strides[1] = {row_bytes};
+  const uint32_t box[2] = {128, box_rows};
+  return make_map(map, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
+// Scale tiles as [row tile][group][128 words]; a row tile that does not exist loads as zeros.
+bool scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int32_t groups,
+                uint32_t box_groups, uint32_t box_tiles) {
+  const uint64_t dims[3] = {128, uint64_t(groups), uint64_t((rows + 127) / 128)};
+  const uint64_t strides[2] = {512, uint64_t(groups) * 512};
+  const uint32_t box[3] = {128, box_groups, box_tiles};
+  return make_map(map, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_DATA_TYPE_UINT32);
+}
+
+bool logits_map(CUtensorMap* map, const void* out, sv_dtype dtype, int64_t M, int64_t V,
+                int64_t ld) {
+  const uint64_t dims[2] = {uint64_t(V), uint64_t(M)};
+  const uint64_t strides[1] = {uint64_t(ld) * uint64_t(elem_bytes(dtype))};
+  const uint32_t box[2] = {32, 16};
+  return make_map(map, out, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 }
 
 }  // namespace
@@ -325,7 +560,7 @@ extern "C" sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_
   p.H = H;
   p.M = int32_t(M);
   p.kblocks = int32_t((H + 255) / 256);
-  p.n_vt = int32_t((V + kPjRows - 1) / kPjRows);
+  p.n_vt = int32_t((V + 2 * kPjRows - 1) / (2 * kPjRows));
   // tiles of equal size; where there is more than one, they start on whole 64-row halves of a
   // scale tile
   p.n_nt = int32_t((M + kPjMaxN - 1) / kPjMaxN);
@@ -336,47 +571,43 @@ extern "C" sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_
     p.n_nt = int32_t((M + p.nt - 1) / p.nt);
   }
   if (int64_t(p.n_vt) * p.n_nt > INT32_MAX / 2) return SV_ERR_UNSUPPORTED;
-  p.m_tiles = int32_t((M + 127) / 128);
-  const uint32_t tile_bytes = format == SV_FP4_E8M0_32 ? 1024 : 2048;
+  const bool e8m0 = format == SV_FP4_E8M0_32;
+  const uint32_t box_groups = e8m0 ? 2 : 4;
+  const uint32_t x_tiles = p.nt > 128 ? 2 : 1;  // scale tiles that a tile's rows can lie in
+  const uint32_t sf_cols = box_groups * 4 * (1 + x_tiles);
+  p.n_acc = 2 * p.nt + 2 * sf_cols <= kPjTmemCols ? 2 : 1;
+  p.groups = fp4_groups(H, format);
   p.b_off = kPjABytes;
-  p.sfa_off = p.b_off + uint32_t(p.nt) * 128;
-  p.sfb_off = p.sfa_off + tile_bytes;
-  p.stage_bytes = (p.sfb_off + 2 * tile_bytes + 1023) / 1024 * 1024;
-  p.stages = int32_t(std::min<uint32_t>(kPjMaxStages, (kPjSmem - 1024) / p.stage_bytes));
-  p.w_scales = w_scales;
-  p.x_scales = x_scales;
+  p.sfa_off = p.b_off + uint32_t(p.nt / 2) * 128;
+  p.sfb_off = p.sfa_off + box_groups * 512;
+  const uint32_t bytes = p.sfb_off + x_tiles * box_groups * 512;
+  p.tx_bytes = 2 * bytes;
+  p.stage_bytes = (bytes + 1023) / 1024 * 1024;
+  const uint32_t out_bytes = kPjEpiWarps * 2 * 16 * 32 * uint32_t(elem_bytes(dtype));
+  p.stages =
+      int32_t(std::min<uint32_t>(kPjMaxStages, (kPjSmem - 1024 - out_bytes) / p.stage_bytes));
+  p.out_off = uint32_t(p.stages) * p.stage_bytes;
   p.w_row = w_row_scales;
   p.x_row = x_row_scales;
   p.out = logits;
   p.ld = ld;
   p.status = status;
   const int sms = device_sm_count();
-  if (sms <= 0) return SV_ERR_CUDA;
+  if (sms < 2) return SV_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
   const uint64_t row_bytes = uint64_t(spec_fp4_row_bytes(H));
-  CUtensorMap map_w, map_x;
-  {
-    const uint64_t dims[2] = {row_bytes, uint64_t(V)};
-    const uint64_t strides[1] = {row_bytes};
-    const uint32_t box[2] = {128, kPjRows};
-    if (!make_map(&map_w, w_packed, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_DATA_TYPE_UINT8))
-      return SV_ERR_CUDA;
-  }
-  {
-    const uint64_t dims[2] = {row_bytes, uint64_t(M)};
-    const uint64_t strides[1] = {row_bytes};
-    const uint32_t box[2] = {128, uint32_t(p.nt)};
-    if (!make_map(&map_x, x_packed, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_DATA_TYPE_UINT8))
-      return SV_ERR_CUDA;
-  }
-  if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return SV_ERR_CUDA;
-  const int grid = int(std::min<int64_t>(sms, int64_t(p.n_vt) * p.n_nt));
-  if (format == SV_FP4_E8M0_32)
-    return dtype == SV_BF16 ? launch_project<SV_FP4_E8M0_32, __nv_bfloat16>(map_w, map_x, p, grid, s)
-                            : launch_project<SV_FP4_E8M0_32, float>(map_w, map_x, p, grid, s);
-  return dtype == SV_BF16 ? launch_project<SV_FP4_E4M3_16, __nv_bfloat16>(map_w, map_x, p, grid, s)
-                          : launch_project<SV_FP4_E4M3_16, float>(map_w, map_x, p, grid, s);
+  PjMaps m;
+  if (!rows_map(&m.w, w_packed, V, row_bytes, kPjRows) ||
+      !rows_map(&m.x, x_packed, M, row_bytes, uint32_t(p.nt / 2)) ||
+      !scales_map(&m.ws, w_scales, V, p.groups, box_groups, 1) ||
+      !scales_map(&m.xs, x_scales, M, p.groups, box_groups, x_tiles) ||
+      !logits_map(&m.out, logits, dtype, M, V, ld))
+    return SV_ERR_CUDA;
+  const int grid = 2 * int(std::min<int64_t>(sms / 2, int64_t(p.n_vt) * p.n_nt));
+  if (e8m0)
+    return x_tiles == 1 ? launch_project<SV_FP4_E8M0_32, 1>(m, p, dtype, grid, s)
+                        : launch_project<SV_FP4_E8M0_32, 2>(m, p, dtype, grid, s);
+  return x_tiles == 1 ? launch_project<SV_FP4_E4M3_16, 1>(m, p, dtype, grid, s)
+                      : launch_project<SV_FP4_E4M3_16, 2>(m, p, dtype, grid, s);
 }
