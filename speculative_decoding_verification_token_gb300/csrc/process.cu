@@ -10,6 +10,8 @@
 //   l = allowed(v) ? l : -inf
 // computed in binary32 and rounded once to the logits' type.  An element that nothing touches is
 // left (or copied) bit for bit.
+#include <algorithm>
+
 #include "sv_device.cuh"
 #include "sv_host.h"
 
@@ -32,9 +34,9 @@ struct ProcParams {
   int32_t n_slots;
   const int32_t* counts;
   int64_t ld_counts;
-  const uint8_t* prompt_bits;
-  const uint8_t* output_bits;
-  int64_t ld_bits;  // bytes
+  const uint32_t* prompt_bits;
+  const uint32_t* output_bits;
+  int64_t ld_bits;
   const float* repetition;
   const float* presence;
   const float* frequency;
@@ -42,244 +44,413 @@ struct ProcParams {
   const int32_t* bias_tokens;
   const float* bias_values;
   int64_t n_bias;
-  const uint8_t* mask;
-  int64_t ld_mask;  // bytes
+  const uint32_t* mask;
+  int64_t ld_mask;
   int32_t n_mask;
   const int32_t* mask_row;
   int32_t* status;
+  bool reset_status;
 };
 
-constexpr int kProcThreads = 256;
-constexpr int kProcRows = 4;  // rows whose loads are in flight together
+constexpr int kProcThreads = 128;
+constexpr int kProcRows = 4;  // rows handled together
+
+// How a call moves its logits, and the bytes of a row that one CTA takes.
+enum ProcMode {
+  kCopy = 0,     // out of place: every row moves
+  kMasked = 1,   // in place with masks: banned elements are written
+  kSparse = 2    // in place without masks: only touched elements move
+};
+constexpr uint32_t proc_row_bytes(int mode) {
+  return mode == kCopy ? 4096 : 8192;
+}
 
 template <typename E>
 struct ProcElem;
 
 template <>
 struct ProcElem<float> {
-  static constexpr int kBytes = 4;
+  using T = float;
   static constexpr uint32_t kNegInf = 0xFF800000u;
-  __device__ static __forceinline__ float get(const uint4& v, int j) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    return __uint_as_float(w[j]);
-  }
-  __device__ static __forceinline__ void put(uint4& v, int j, float y) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-    w[j] = __float_as_uint(y);
-  }
+  __device__ static __forceinline__ float up(float x) { return x; }
+  __device__ static __forceinline__ float down(float y) { return y; }
 };
 
 template <>
 struct ProcElem<bf16_tag> {
-  static constexpr int kBytes = 2;
+  using T = uint16_t;
   static constexpr uint32_t kNegInf = 0xFF80FF80u;
-  __device__ static __forceinline__ float get(const uint4& v, int j) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
+  __device__ static __forceinline__ float up(uint16_t h) {
+    return __uint_as_float(uint32_t(h) << 16);
   }
-  __device__ static __forceinline__ void put(uint4& v, int j, float y) {
-    const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-    w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xFFFFu) | (h << 16)) : ((w[j >> 1] & 0xFFFF0000u) | h);
+  __device__ static __forceinline__ uint16_t down(float y) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(y));
   }
 };
 
-// The kVec bits of tokens v0 .. v0 + kVec - 1 (v0 a multiple of kVec) of a bit row.
-template <int kVec>
-__device__ __forceinline__ uint32_t bits_of(const uint8_t* row, int64_t v0) {
-  const uint32_t b = __ldg(row + (v0 >> 3));
-  return kVec == 8 ? b : (b >> (v0 & 4)) & 0xFu;
+// The elements of a 16-byte vector whose bit in `ok` is clear become -inf.
+template <typename E>
+__device__ __forceinline__ uint4 ban(uint4 x, uint32_t ok) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (sizeof(typename ProcElem<E>::T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (!(ok >> j & 1u)) w[j] = ProcElem<E>::kNegInf;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!(ok >> (2 * j) & 1u)) w[j] = (w[j] & 0xFFFF0000u) | 0xFF80u;
+      if (!(ok >> (2 * j + 1) & 1u)) w[j] = (w[j] & 0xFFFFu) | 0xFF800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA per (request, chunk of kProcThreads vectors); a thread owns one 16-byte vector of the
-// vocabulary in every row of the request, so history, counts and biases are read once for all of
-// them.  In place, a vector that nothing touches costs two bytes of bits and no logit traffic.
-template <typename E, bool kInPlace>
-__global__ void __launch_bounds__(kProcThreads) process_kernel(ProcParams p) {
+// One CTA per (request, chunk of a row), for all rows of the request: the history, biases
+// and drafted tokens of the chunk are read once.  What they touch -- a few tokens in a hundred --
+// is gathered into a list of offsets, one thread per listed token edits it in every row, and the
+// rest of the logits moves (or, in place, does not move) without passing through a register:
+//   out of place  bulk copies bring kProcRows row parts to shared memory, masks and edits work
+//                 there, bulk copies take them to `out`;
+//   in place      masks store -inf where they ban and edits touch single elements.
+template <typename E, int kMode>
+__global__ void __launch_bounds__(kProcThreads, 10)
+    process_kernel(ProcParams p) {
+  constexpr bool kInPlace = kMode != kCopy;
+  constexpr uint32_t kRowBytes = proc_row_bytes(kMode);
   using X = ProcElem<E>;
-  constexpr int kVec = 16 / X::kBytes;
-  constexpr int kChunk = kProcThreads * kVec;
+  using T = typename X::T;
+  constexpr int kVec = 16 / sizeof(T);
+  constexpr uint32_t kAll = (1u << kVec) - 1u;
+  constexpr int kChunk = kRowBytes / sizeof(T);
+  constexpr int kWords = kChunk / 32;
+  constexpr int kOwn = (kWords + kProcThreads - 1) / kProcThreads;  // bit words per thread
+  extern __shared__ __align__(128) uint8_t s_rows[];  // row parts, out of place
+  __shared__ uint32_t s_mask[kMode == kSparse ? 1 : kProcRows][kWords];
+  __shared__ uint16_t s_off[kChunk];
+  __shared__ uint32_t s_touch[kWords], s_prompt[kWords], s_out[kWords], s_bbits[kWords];
   __shared__ int32_t s_tok[SV_MAX_DRAFT_LEN], s_pos[SV_MAX_DRAFT_LEN];
-  __shared__ int32_t s_n;
-  __shared__ float s_bias[kChunk];
-  __shared__ uint32_t s_bbits[kChunk / 32];
+  __shared__ int32_t s_mrow[SV_MAX_DRAFT_LEN + 1];
+  __shared__ int32_t s_n, s_nd;
+  __shared__ uint32_t s_bias0;  // first entry of the bias list in this chunk, from b0
+  __shared__ uint64_t s_bar;
+  static_assert(kProcThreads > SV_MAX_DRAFT_LEN, "a thread for each row and drafted token");
   const int32_t r = blockIdx.x / p.chunks;
   const int32_t c = blockIdx.x % p.chunks;
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t lo = int64_t(c) * kChunk;
-  const bool first = c == 0 && tid == 0;  // reports what does not depend on the chunk
+  const int32_t n_tok = static_cast<int32_t>(min(int64_t(kChunk), p.V - lo));
+  const uint32_t full = uint32_t(n_tok) * sizeof(T) & ~15u;  // bytes in whole vectors
+  const int32_t n_vec = full >> 4, n_tail = n_tok - n_vec * kVec;
 
+  // ---- first loads: the request's parameters
   int32_t g = p.draft_len[r];
-  if (g < 0 || g > p.gmax) {
-    if (first) report(p.status, SV_ERR_BAD_INPUT);
-    g = g < 0 ? 0 : p.gmax;
-  }
-  const int32_t rows = g + p.bonus_row;
+  const int64_t row = p.row0[r];
+  const int64_t d0 = p.draft_row0 ? p.draft_row0[r] : 0;
   const float theta = p.repetition ? p.repetition[r] : 1.f;
   const float pres = p.presence ? p.presence[r] : 0.f;
   const float freq = p.frequency ? p.frequency[r] : 0.f;
-  bool pen = theta != 1.f || pres != 0.f || freq != 0.f;
-  int32_t slot = 0;
-  if (pen) {
-    slot = p.slots ? p.slots[r] : r;
-    const bool ok = theta > 0.f && theta < INFINITY && fabsf(pres) < INFINITY &&
-                    fabsf(freq) < INFINITY && slot >= 0 && slot < p.n_slots;
-    if (!ok) {
-      if (first) report(p.status, SV_ERR_BAD_INPUT);
-      pen = false;
-    }
-  }
+  const int32_t slot = p.slots ? p.slots[r] : r;
   int64_t b0 = 0, b1 = 0;
   if (p.bias_start) {
     b0 = p.bias_start[r];
     b1 = p.bias_start[r + 1];
-    if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
-      if (first) report(p.status, SV_ERR_BAD_INPUT);
-      b1 = b0 = 0;
+  }
+  for (int w = tid; w < kWords; w += kProcThreads) s_touch[w] = s_bbits[w] = 0;
+  // data errors are reported by the request's first chunk, which also resets the status of a
+  // single request's call
+  const bool first = c == 0;
+  if (tid == 0) {
+    s_n = s_nd = 0;
+    s_bias0 = ~0u;
+    if (first && p.reset_status) *p.status = 0;
+    if (!kInPlace) {
+      mbar_init(&s_bar, 1);
+      fence_barrier_init();
     }
   }
+  bool bad = g < 0 || g > p.gmax;
+  g = min(max(g, 0), p.gmax);
+  const int32_t rows = g + p.bonus_row;
+  bool pen = theta != 1.f || pres != 0.f || freq != 0.f;
+  if (pen && !(theta > 0.f && theta < INFINITY && fabsf(pres) < INFINITY &&
+               fabsf(freq) < INFINITY && slot >= 0 && slot < p.n_slots)) {
+    bad = true;
+    pen = false;
+  }
+  if (b0 < 0 || b1 < b0 || b1 > p.n_bias) {
+    bad = true;
+    b1 = b0 = 0;
+  }
+  const uint8_t* const src = p.logits + (row * p.ld + lo) * int64_t(sizeof(T));
+  uint8_t* const dst = p.out + (row * p.ld_out + lo) * int64_t(sizeof(T));
+  const int64_t src_ld = p.ld * int64_t(sizeof(T)), dst_ld = p.ld_out * int64_t(sizeof(T));
 
-  // ---- the drafted tokens and the biases of this chunk
-  if (tid == 0) s_n = 0;
-  if (tid < kChunk / 32) s_bbits[tid] = 0;
+  auto load_rows = [&](int32_t i0) {  // thread 0
+    const int32_t n = min(kProcRows, rows - i0);
+    if (full == 0) return;
+    mbar_expect_tx(&s_bar, uint32_t(n) * full);
+    for (int32_t u = 0; u < n; ++u)
+      bulk_g2s(s_rows + u * kRowBytes, src + (i0 + u) * src_ld, full, &s_bar);
+  };
+  // ---- second loads, all in flight together: row parts, bits, drafted tokens, mask rows, biases
+  if (!kInPlace && tid == 0 && p.first_row < rows) load_rows(p.first_row);
+  uint32_t pb[kOwn], ob[kOwn];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    const int w = tid + q * kProcThreads;
+    pb[q] = ob[q] = 0;
+    if (pen && w < kWords && w * 32 < n_tok) {
+      const uint32_t valid = n_tok - w * 32 >= 32 ? ~0u : (1u << (n_tok - w * 32)) - 1u;
+      pb[q] = __ldg(p.prompt_bits + slot * p.ld_bits + (lo >> 5) + w) & valid;
+      ob[q] = __ldg(p.output_bits + slot * p.ld_bits + (lo >> 5) + w) & valid;
+    }
+  }
+  const int role = kProcThreads - 1 - tid;  // the threads least busy with bits
+  const bool drafted = pen && role < g;
+  const int32_t x_draft = drafted ? p.draft_tokens[d0 + role] : -1;
+  const bool masked = kMode != kSparse && p.mask_row != nullptr;
+  int32_t mrow = -1;
+  if (masked && tid < rows - p.first_row) {
+    mrow = p.mask_row[row + p.first_row + tid];
+    if (mrow < -1 || mrow >= p.n_mask) {
+      bad = true;
+      mrow = -1;
+    }
+  }
+  constexpr int kAhead = 3;  // bias entries per thread loaded with the rest
+  int32_t bt[kAhead];
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) {
+    const int64_t k = b0 + tid + q * kProcThreads;
+    bt[q] = k < b1 ? p.bias_tokens[k] : -1;
+  }
   __syncthreads();
-  if (pen && tid < 32 && g > 0) {
-    const int64_t d0 = p.draft_row0[r];
-    int n = 0;
-    for (int32_t k0 = 0; k0 < g; k0 += 32) {
-      const int32_t k = k0 + lane;
-      const int32_t x = k < g ? p.draft_tokens[d0 + k] : -1;
-      if (k < g && (x < 0 || x >= p.V)) report(p.status, SV_ERR_BAD_INPUT);
-      const bool in = k < g && x >= lo && x < lo + kChunk && x < p.V;
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const int at = n + __popc(m & ((1u << lane) - 1u));
-        s_tok[at] = static_cast<int32_t>(x - lo);
-        s_pos[at] = k + 1;
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    const int w = tid + q * kProcThreads;
+    if (w >= kWords) break;
+    s_prompt[w] = pb[q];
+    s_out[w] = ob[q];
+    if (pb[q] | ob[q]) atomicOr(&s_touch[w], pb[q] | ob[q]);
+  }
+  if (tid <= SV_MAX_DRAFT_LEN) s_mrow[tid] = mrow;
+  if (drafted) {
+    bad |= x_draft < 0 || x_draft >= p.V;
+    const int64_t o = x_draft - lo;
+    if (o >= 0 && o < n_tok) {  // an unordered list: rows count the entries before them
+      const int at = atomicAdd(&s_nd, 1);
+      s_tok[at] = static_cast<int32_t>(o);
+      s_pos[at] = role + 1;
+      atomicOr(&s_touch[o >> 5], 1u << (o & 31));
+    }
+  }
+  auto add_bias = [&](int64_t k, int32_t x) {
+    if (first) bad |= x < 0 || x >= p.V || (k > b0 && p.bias_tokens[k - 1] >= x);
+    const int64_t o = x - lo;
+    if (o >= 0 && o < n_tok) {
+      atomicMin(&s_bias0, static_cast<uint32_t>(k - b0));
+      atomicOr(&s_bbits[o >> 5], 1u << (o & 31));
+      atomicOr(&s_touch[o >> 5], 1u << (o & 31));
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) {
+    const int64_t k = b0 + tid + q * kProcThreads;
+    if (k < b1) add_bias(k, bt[q]);
+  }
+  for (int64_t k = b0 + tid + kAhead * kProcThreads; k < b1; k += kProcThreads)
+    add_bias(k, p.bias_tokens[k]);
+  if (first && bad) report(p.status, SV_ERR_BAD_INPUT);
+  __syncthreads();
+  // The masks' words of this chunk (1 behind the vocabulary) for the batch of rows from i0 on: loads,
+  // then stores to shared memory, with other work between them.  Tells whether any mask applies.
+  constexpr int kMaskOwn = kProcRows * kWords / kProcThreads;
+  uint32_t mw[kMode == kSparse ? 1 : kMaskOwn];
+  auto load_masks = [&](int32_t i0) {
+    const int32_t* mr = s_mrow + (i0 - p.first_row);
+    const int32_t n = min(kProcRows, rows - i0);
+    bool any = false;
+#pragma unroll
+    for (int u = 0; u < kProcRows; ++u) any |= u < n && mr[u] >= 0;
+    if (!any) return false;
+#pragma unroll
+    for (int q = 0; q < kMaskOwn; ++q) {
+      const int u = (tid + q * kProcThreads) / kWords, w = (tid + q * kProcThreads) % kWords;
+      const int32_t m = u < n ? mr[u] : -1;
+      mw[q] = ~0u;
+      if (m >= 0 && w * 32 < n_tok) {
+        mw[q] = __ldg(p.mask + m * p.ld_mask + (lo >> 5) + w);
+        if (n_tok - w * 32 < 32) mw[q] |= ~0u << (n_tok - w * 32);
       }
-      n += __popc(m);
     }
-    if (lane == 0) s_n = n;
+    return true;
+  };
+  bool next_masked = false;
+  if constexpr (kMode != kSparse) {
+    if (masked && p.first_row < rows) next_masked = load_masks(p.first_row);
   }
-  for (int64_t k = b0 + tid; k < b1; k += kProcThreads) {
-    const int32_t x = p.bias_tokens[k];
-    if (c == 0 && (x < 0 || x >= p.V || (k > b0 && p.bias_tokens[k - 1] >= x)))
-      report(p.status, SV_ERR_BAD_INPUT);
-    if (x >= lo && x < lo + kChunk) {
-      s_bias[x - lo] = p.bias_values[k];
-      atomicOr(&s_bbits[(x - lo) >> 5], 1u << ((x - lo) & 31));
+  for (int w = tid; w < kWords; w += kProcThreads) {  // the list of touched offsets, in any order
+    uint32_t t = s_touch[w];
+    if (!t) continue;
+    int at = atomicAdd(&s_n, __popc(t));
+    while (t) {
+      s_off[at++] = static_cast<uint16_t>(w * 32 + __ffs(t) - 1);
+      t &= t - 1;
     }
   }
   __syncthreads();
-
-  const int64_t v0 = lo + int64_t(tid) * kVec;
-  if (v0 >= p.V) return;
-  const uint32_t valid = p.V - v0 >= kVec ? (1u << kVec) - 1u : (1u << (p.V - v0)) - 1u;
-  const bool whole = valid == (1u << kVec) - 1u;
-  uint32_t emitted = 0, seen = 0;
-  int32_t cnt[kVec];
-#pragma unroll
-  for (int j = 0; j < kVec; ++j) cnt[j] = 0;
-  if (pen) {
-    emitted = bits_of<kVec>(p.output_bits + slot * p.ld_bits, v0) & valid;
-    seen = (bits_of<kVec>(p.prompt_bits + slot * p.ld_bits, v0) & valid) | emitted;
-    if (emitted) {
-      const int32_t* cr = p.counts + slot * p.ld_counts + v0;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (emitted >> j & 1u) cnt[j] = __ldg(cr + j);
-    }
+  const int32_t n_list = s_n, nd = s_nd;
+  auto count_of = [&](int o) {
+    return s_out[o >> 5] >> (o & 31) & 1u ? __ldg(p.counts + slot * p.ld_counts + lo + o) : 0;
+  };
+  // a biased token's value: the chunk's entries are neighbours in the ascending list
+  auto bias_of = [&](int o) {
+    if (!(s_bbits[o >> 5] >> (o & 31) & 1u)) return 0.f;
+    int k = __popc(s_bbits[o >> 5] & ((1u << (o & 31)) - 1u));
+    for (int w = 0; w < o >> 5; ++w) k += __popc(s_bbits[w]);
+    return __ldg(p.bias_values + b0 + s_bias0 + k);
+  };
+  // the count and bias of this thread's first listed token, while the rows are on their way
+  int32_t count0 = 0;
+  float bias0 = 0.f;
+  if (tid < n_list) {
+    count0 = count_of(s_off[tid]);
+    bias0 = bias_of(s_off[tid]);
   }
-  const uint32_t biased =
-      (s_bbits[(tid * kVec) >> 5] >> ((tid * kVec) & 31)) & ((1u << kVec) - 1u);
-  const int n_draft = s_n;
-  int next = 0;       // drafted tokens of the chunk already counted
-  int next_bits = 0;  // the same, for the bits only (they run ahead with the loads)
-  uint32_t touched = seen | biased;
 
-  const int64_t row = p.row0[r];
+  uint32_t phase = 0;
   for (int32_t i0 = p.first_row; i0 < rows; i0 += kProcRows) {
-    uint4 x[kProcRows];
-    uint32_t ok[kProcRows], act[kProcRows];
+    const int32_t n = min(kProcRows, rows - i0);
+    const bool now_masked = next_masked;  // the same in every thread
+    if constexpr (kMode != kSparse) {
+      if (now_masked) {
 #pragma unroll
-    for (int u = 0; u < kProcRows; ++u) {
-      const int32_t i = i0 + u;
-      ok[u] = valid;
-      act[u] = 0;
-      if (i >= rows) continue;
-      if (p.mask_row) {
-        const int32_t m = p.mask_row[row + i];
-        if (m >= p.n_mask || m < -1) {
-          if (first) report(p.status, SV_ERR_BAD_INPUT);
-        } else if (m >= 0) {
-          ok[u] = bits_of<kVec>(p.mask + m * p.ld_mask, v0) & valid;
-        }
+        for (int q = 0; q < kMaskOwn; ++q)
+          (&s_mask[0][0])[tid + q * kProcThreads] = mw[q];
       }
-      while (next_bits < n_draft && s_pos[next_bits] <= i) {
-        const uint32_t j = static_cast<uint32_t>(s_tok[next_bits++] - tid * kVec);
-        if (j < uint32_t(kVec)) touched |= 1u << j;
-      }
-      act[u] = (touched & ok[u]) | (valid & ~ok[u]);
-      if ((!kInPlace || act[u]) && (ok[u] || !whole)) {
-        const uint8_t* src = p.logits + ((row + i) * p.ld + v0) * X::kBytes;
-        if (whole) {
-          x[u] = kInPlace ? *reinterpret_cast<const uint4*>(src)
-                          : __ldg(reinterpret_cast<const uint4*>(src));
-        } else {
-          x[u] = make_uint4(0, 0, 0, 0);
-          for (int j = 0; j < kVec; ++j)
-            if (valid >> j & 1u) {
-              if constexpr (X::kBytes == 4)
-                X::put(x[u], j, reinterpret_cast<const float*>(src)[j]);
-              else
-                reinterpret_cast<uint16_t*>(&x[u])[j] = reinterpret_cast<const uint16_t*>(src)[j];
-            }
-        }
-      } else {
-        x[u] = make_uint4(X::kNegInf, X::kNegInf, X::kNegInf, X::kNegInf);
-      }
+      next_masked = masked && i0 + kProcRows < rows && load_masks(i0 + kProcRows);
     }
-#pragma unroll
-    for (int u = 0; u < kProcRows; ++u) {
-      const int32_t i = i0 + u;
-      if (i >= rows) continue;
-      while (next < n_draft && s_pos[next] <= i) {
-        const uint32_t j = static_cast<uint32_t>(s_tok[next++] - tid * kVec);
-        if (j < uint32_t(kVec)) {
-          emitted |= 1u << j;
-          seen |= 1u << j;
-#pragma unroll
-          for (int q = 0; q < kVec; ++q)
-            if (uint32_t(q) == j) ++cnt[q];
-        }
+    if constexpr (!kInPlace) {
+      for (int q = tid; q < n * n_tail; q += kProcThreads) {
+        const int u = q / n_tail, j = n_vec * kVec + q % n_tail;
+        reinterpret_cast<T*>(s_rows + u * kRowBytes)[j] =
+            reinterpret_cast<const T*>(src + (i0 + u) * src_ld)[j];
       }
-      if (kInPlace && !act[u]) continue;
-      if (act[u]) {
+      if (full) mbar_wait(&s_bar, phase, p.status);
+      phase ^= 1;
+    }
+    __syncthreads();
+    // ---- masks: whole vectors, then the row's last few elements
+    if (kMode != kSparse && now_masked) {
+      auto piece = [&](int u, int v) {  // the bits of vector v
+        return s_mask[u][(v * kVec) >> 5] >> ((v * kVec) & 31) & kAll;
+      };
+      if constexpr (kInPlace) {
+        // a vector banned as a whole is stored, a partly banned one read first.  Both in one store
+        // instruction: 16-byte halves of a sector stored by two cost a read of the sector in L2 each
+        for (int v = tid; v < n_vec; v += kProcThreads) {
+          uint4 x[kProcRows];
+          uint32_t ok[kProcRows];
+          uint8_t* const at = dst + i0 * dst_ld + v * 16;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          if (!(act[u] >> j & 1u)) continue;
-          float y = X::get(x[u], j);
-          if (seen >> j & 1u) y = y > 0.f ? __fdiv_rn(y, theta) : y * theta;
-          if (emitted >> j & 1u) y = y - freq * static_cast<float>(cnt[j]) - pres;
-          if (biased >> j & 1u) y += s_bias[tid * kVec + j];
-          if (!(ok[u] >> j & 1u)) y = -INFINITY;
-          X::put(x[u], j, y);
-        }
-      }
-      uint8_t* dst = p.out + ((row + i) * p.ld_out + v0) * X::kBytes;
-      if (whole) {
-        *reinterpret_cast<uint4*>(dst) = x[u];
-      } else {
-        for (int j = 0; j < kVec; ++j)
-          if (valid >> j & 1u) {
-            if constexpr (X::kBytes == 4)
-              reinterpret_cast<uint32_t*>(dst)[j] = reinterpret_cast<const uint32_t*>(&x[u])[j];
-            else
-              reinterpret_cast<uint16_t*>(dst)[j] = reinterpret_cast<const uint16_t*>(&x[u])[j];
+          for (int u = 0; u < kProcRows; ++u) {
+            ok[u] = u < n ? piece(u, v) : kAll;
+            if (ok[u] && ok[u] != kAll) x[u] = *reinterpret_cast<const uint4*>(at + u * dst_ld);
           }
+#pragma unroll
+          for (int u = 0; u < kProcRows; ++u)
+            if (ok[u] != kAll)
+              *reinterpret_cast<uint4*>(at + u * dst_ld) =
+                  ok[u] ? ban<E>(x[u], ok[u])
+                        : make_uint4(X::kNegInf, X::kNegInf, X::kNegInf, X::kNegInf);
+        }
+        for (int q = tid; q < n * n_tail; q += kProcThreads) {
+          const int u = q / n_tail, j = n_vec * kVec + q % n_tail;
+          if (!(s_mask[u][j >> 5] >> (j & 31) & 1u))
+            reinterpret_cast<T*>(dst + (i0 + u) * dst_ld)[j] = X::down(-INFINITY);
+        }
+      } else {
+        for (int q = tid; q < n * int(kRowBytes / 16); q += kProcThreads) {
+          const int u = q / int(kRowBytes / 16), v = q % int(kRowBytes / 16);
+          const uint32_t ok = piece(u, v);
+          if (ok == kAll) continue;
+          uint4* at = reinterpret_cast<uint4*>(s_rows + u * kRowBytes) + v;
+          *at = ban<E>(*at, ok);
+        }
+      }
+      __syncthreads();
+    }
+    // ---- edits: a thread per listed token
+    for (int e = tid; e < n_list; e += kProcThreads) {
+      const int o = s_off[e];
+      const uint32_t w = o >> 5, b = 1u << (o & 31);
+      const bool in_prompt = s_prompt[w] & b, biased = s_bbits[w] & b;
+      const int32_t base = e == tid ? count0 : count_of(o);
+      const float add = e == tid ? bias0 : bias_of(o);
+      T* const at = reinterpret_cast<T*>(kInPlace ? dst + i0 * dst_ld : s_rows) + o;
+      const int64_t step = kInPlace ? p.ld_out : int64_t(kRowBytes / sizeof(T));
+      T x[kProcRows];
+#pragma unroll
+      for (int u = 0; u < kProcRows; ++u)
+        if (u < n) x[u] = at[u * step];
+#pragma unroll
+      for (int u = 0; u < kProcRows; ++u) {
+        if (u >= n || (now_masked && !(s_mask[u][w] & b))) continue;
+        int32_t cnt = base;
+        for (int k = 0; k < nd; ++k) cnt += s_tok[k] == o && s_pos[k] <= i0 + u;
+        const bool seen = in_prompt || cnt > 0;
+        if (!seen && !biased) continue;
+        float y = X::up(x[u]);
+        if (seen) y = y > 0.f ? __fdiv_rn(y, theta) : y * theta;
+        if (cnt > 0) y = y - freq * static_cast<float>(cnt) - pres;
+        if (biased) y += add;
+        at[u * step] = X::down(y);
       }
     }
+    if constexpr (!kInPlace) {
+      fence_proxy_async();  // the edits before the bulk copies that read them
+      __syncthreads();
+      for (int q = tid; q < n * n_tail; q += kProcThreads) {
+        const int u = q / n_tail, j = n_vec * kVec + q % n_tail;
+        reinterpret_cast<T*>(dst + (i0 + u) * dst_ld)[j] =
+            reinterpret_cast<const T*>(s_rows + u * kRowBytes)[j];
+      }
+      if (tid == 0 && full) {
+        for (int32_t u = 0; u < n; ++u)
+          bulk_s2g(dst + (i0 + u) * dst_ld, s_rows + u * kRowBytes, full);
+        bulk_group_commit();
+        bulk_group_wait_read();  // the rows may be overwritten, or the CTA end
+        if (i0 + kProcRows < rows) load_rows(i0 + kProcRows);
+      }
+    }
+    if (i0 + kProcRows < rows) __syncthreads();  // masks and tails of the next rows
   }
+}
+
+template <typename E, int kMode>
+sv_status launch_process(ProcParams p, int32_t B, cudaStream_t s) {
+  const int64_t chunk = proc_row_bytes(kMode) / sizeof(typename ProcElem<E>::T);
+  const int64_t chunks = (p.V + chunk - 1) / chunk;
+  if (chunks * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  // with one request a single CTA reports, and resets the status before it does
+  p.reset_status = p.status && B == 1;
+  if (p.status && B > 1 && cudaMemsetAsync(p.status, 0, sizeof(int32_t), s) != cudaSuccess)
+    return SV_ERR_CUDA;
+  p.chunks = int32_t(chunks);
+  const size_t smem =
+      kMode == kCopy
+          ? size_t(std::max(1, std::min(kProcRows, p.gmax + p.bonus_row - p.first_row))) *
+                proc_row_bytes(kMode)
+          : 0;
+  process_kernel<E, kMode><<<unsigned(chunks * B), kProcThreads, smem, s>>>(p);
+  return launch_status(cudaGetLastError());
+}
+
+template <typename E>
+sv_status launch_process(const ProcParams& p, int32_t B, cudaStream_t s) {
+  if (p.out != p.logits) return launch_process<E, kCopy>(p, B, s);
+  return p.mask_row ? launch_process<E, kMasked>(p, B, s) : launch_process<E, kSparse>(p, B, s);
 }
 
 }  // namespace
@@ -318,11 +489,9 @@ extern "C" sv_status spec_process_logits(
     return SV_ERR_INVALID;
   if (mask_row && (n_mask < 0 || (n_mask > 0 && (!mask || ld_mask < (V + 31) / 32))))
     return SV_ERR_INVALID;
-  const int64_t chunk = int64_t(kProcThreads) * (16 / eb);
-  const int64_t chunks = (V + chunk - 1) / chunk;
-  if (chunks * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  // the most CTAs any mode launches
+  if ((V + 2047 / eb) / (2048 / eb) * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return SV_ERR_CUDA;
   const ProcParams p = {static_cast<const uint8_t*>(logits),
                         ld,
                         static_cast<uint8_t*>(out),
@@ -335,14 +504,14 @@ extern "C" sv_status spec_process_logits(
                         first_row,
                         bonus_row,
                         draft_tokens,
-                        int32_t(chunks),
+                        0,
                         slots,
                         n_slots,
                         counts,
                         ld_counts,
-                        reinterpret_cast<const uint8_t*>(prompt_bits),
-                        reinterpret_cast<const uint8_t*>(output_bits),
-                        ld_bits * 4,
+                        prompt_bits,
+                        output_bits,
+                        ld_bits,
                         repetition,
                         presence,
                         frequency,
@@ -350,23 +519,11 @@ extern "C" sv_status spec_process_logits(
                         bias_tokens,
                         bias_values,
                         n_bias,
-                        reinterpret_cast<const uint8_t*>(mask),
-                        ld_mask * 4,
+                        mask,
+                        ld_mask,
                         n_mask,
                         mask_row,
-                        status};
-  const unsigned grid = unsigned(chunks * B);
-  const bool in_place = out == logits;
-  if (dtype == SV_BF16) {
-    if (in_place)
-      process_kernel<bf16_tag, true><<<grid, kProcThreads, 0, s>>>(p);
-    else
-      process_kernel<bf16_tag, false><<<grid, kProcThreads, 0, s>>>(p);
-  } else {
-    if (in_place)
-      process_kernel<float, true><<<grid, kProcThreads, 0, s>>>(p);
-    else
-      process_kernel<float, false><<<grid, kProcThreads, 0, s>>>(p);
-  }
-  return launch_status(cudaGetLastError());
+                        status,
+                        false};
+  return dtype == SV_BF16 ? launch_process<bf16_tag>(p, B, s) : launch_process<float>(p, B, s);
 }
