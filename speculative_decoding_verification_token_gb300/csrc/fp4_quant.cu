@@ -6,10 +6,13 @@
 //                   in [4, 8), above 6 it saturates).
 //   SV_FP4_E4M3_16  blocks of 16, S = s g: g = 2^k the row's scale, the smallest power of two with
 //                   row maximum <= 6 * 448 g, and s = max|x| / (6 g) rounded to the nearest e4m3.
-// c is x / S rounded to nearest, ties to the even code.  Every rounding is decided on the exact
-// quotient: a division by a power of two is exact, the other two are rounded to odd in binary32
-// (truncated, the last bit set when inexact) before the conversion rounds them, which keeps a
-// quotient from being rounded onto the middle between two codes and then away from its side.
+// c is x / S rounded to nearest, ties to the even code, decided on the exact quotient without
+// dividing: see fp4_quotients.
+//
+// A lane takes 8 neighbouring elements (16 bytes of bf16, of packed codes 4, of values 16), so that
+// every load and store of a warp is contiguous; 4 or 2 lanes share a block.
+#include <algorithm>
+
 #include "fp4.cuh"
 #include "sv_host.h"
 
@@ -29,231 +32,359 @@ struct QuantParams {
   int32_t* status;
 };
 
-constexpr int kQuantThreads = 128;
-
-template <typename E>
-struct In;
-template <>
-struct In<float> {
-  static constexpr int kBytes = 4;
-  __device__ static __forceinline__ uint32_t one(const uint8_t* p) {
-    return __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
-};
-template <>
-struct In<bf16_tag> {
-  static constexpr int kBytes = 2;
-  __device__ static __forceinline__ uint32_t one(const uint8_t* p) {
-    return uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p))) << 16;
-  }
-};
-
-// Elements e0 .. e0 + kN - 1 of a row as binary32 bit patterns, zeros past H.
-template <typename E, int kN, bool kVec>
-__device__ __forceinline__ void load_block(const uint8_t* row, int64_t e0, int64_t H,
-                                           uint32_t* v) {
-  constexpr int kPer = 16 / In<E>::kBytes;
-  if (kVec && e0 + kN <= H) {
-    const uint4* p = reinterpret_cast<const uint4*>(row + e0 * In<E>::kBytes);
-#pragma unroll
-    for (int q = 0; q < kN / kPer; ++q) {
-      float f[kPer];
-      Elem<E>::unpack(__ldg(p + q), f);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) v[q * kPer + j] = __float_as_uint(f[j]);
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < kN; ++j) v[j] = e0 + j < H ? In<E>::one(row + (e0 + j) * In<E>::kBytes) : 0u;
-}
-
-// Largest magnitude as a bit pattern: above 0x7F800000 for a NaN, so neither NaN nor infinity is
-// lost among finite values.
-template <int kN>
-__device__ __forceinline__ uint32_t amax_bits(const uint32_t* v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < kN; ++j) m = max(m, v[j] & 0x7FFFFFFFu);
-  return m;
-}
-
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// |x| / S rounded to odd, for S with few significant bits: q the nearest quotient, then one step
-// towards the exact one if it is inexact and its last bit is even.
-__device__ __forceinline__ float div_odd(float x, float S) {
-  const float q = __fdiv_rn(x, S);
-  const float d = fmaf(-q, S, x);  // exact remainder
-  uint32_t b = __float_as_uint(q);
-  if (d != 0.f && !(b & 1u)) b = d > 0.f ? b + 1u : b - 1u;
-  return __uint_as_float(b);
-}
+// Eight elements: as they lie in memory (bf16 pairs, or binary32 patterns).
+template <typename E>
+struct In;
 
-// Writes one block: codes, and the values they stand for.
-template <int kN, bool kVec>
-__device__ __forceinline__ void store_block(const QuantParams& p, int64_t r, int64_t e0,
-                                            const float* t, float S) {
-  uint32_t w[kN / 8];
-#pragma unroll
-  for (int q = 0; q < kN / 8; ++q) w[q] = fp4x8(t + 8 * q);
-  uint8_t* dst = p.packed + r * p.row_bytes + (e0 >> 1);
-  if constexpr (kN == 32) {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+template <>
+struct In<float> {
+  static constexpr int kBytes = 4, kWords = 8;
+  static constexpr bool kFew = false;  // 24 significant bits
+  __device__ static __forceinline__ void load(const uint8_t* p, uint32_t* w) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
-  if (!p.values) return;
-  uint16_t* vd = p.values + r * p.ldv + e0;
+  __device__ static __forceinline__ void load_some(const uint8_t* p, int n, uint32_t* w) {
 #pragma unroll
-  for (int q = 0; q < kN / 8; ++q) {
-    float f[8];
-    fp4x8_values(w[q], f);
-    uint32_t h[4];
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + j) : 0;
+  }
+  // Largest magnitude as a binary32 pattern: a NaN exceeds infinity, which exceeds finite values.
+  __device__ static __forceinline__ uint32_t amax(const uint32_t* w) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ static __forceinline__ float get(const uint32_t* w, int j) {
+    return __uint_as_float(w[j]);
+  }
+};
+
+template <>
+struct In<bf16_tag> {
+  static constexpr int kBytes = 2, kWords = 4;
+  static constexpr bool kFew = true;  // 8 significant bits
+  __device__ static __forceinline__ void load(const uint8_t* p, uint32_t* w) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+  __device__ static __forceinline__ void load_some(const uint8_t* p, int n, uint32_t* w) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j] * S, f[2 * j + 1] * S);  // exact
-      h[j] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    if (kVec && e0 + 8 * q + 8 <= p.H) {
-      *reinterpret_cast<uint4*>(vd + 8 * q) = make_uint4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e0 + 8 * q + j < p.H) vd[8 * q + j] = static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1)));
+      w[j] = 2 * j < n ? __ldg(h + 2 * j) : 0;
+      if (2 * j + 1 < n) w[j] |= uint32_t(__ldg(h + 2 * j + 1)) << 16;
     }
   }
-}
+  __device__ static __forceinline__ uint32_t amax(const uint32_t* w) {
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+  __device__ static __forceinline__ float get(const uint32_t* w, int j) {
+    return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
+  }
+};
 
-// Where row r's scale of block k lies.
-__device__ __forceinline__ size_t scale_at(int64_t r, int64_t k, int32_t groups) {
-  return (size_t(r >> 7) * groups + size_t(k >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 +
-         (k & 3);
-}
-
-// Blocks of 32: a thread per (row, block), the padding blocks and rows of the scale tiles included.
+// Elements 8 j .. 8 j + 7 of a row, zeros past H.
 template <typename E, bool kVec>
-__global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p) {
-  const int64_t nb = int64_t(p.groups) * 4;
-  const int64_t i = int64_t(blockIdx.x) * kQuantThreads + threadIdx.x;
-  const int64_t r = i / nb, k = i % nb;
-  if (r >= ((p.rows + 127) & ~int64_t(127))) return;
-  uint8_t* sc = p.scales + scale_at(r, k, p.groups);
-  if (r >= p.rows || k * 32 >= p.H) {
-    *sc = 0;
-    return;
-  }
-  uint32_t v[32];
-  load_block<E, 32, kVec>(p.x + r * p.ldx * In<E>::kBytes, k * 32, p.H, v);
-  const uint32_t m = amax_bits<32>(v);
-  float t[32];
-  float S;
-  if (m >= kInfBits) {
-    report(p.status, SV_ERR_BAD_INPUT);
-    *sc = 0xFF;  // the scale that stands for NaN
-    S = __uint_as_float(0x7FC00000u);
+__device__ __forceinline__ void load_vec(const uint8_t* row, int64_t j, int64_t H, uint32_t* w) {
+  const int64_t e0 = j * 8;
+  if (kVec && e0 + 8 <= H)
+    In<E>::load(row + e0 * In<E>::kBytes, w);
+  else
+    In<E>::load_some(row + e0 * In<E>::kBytes, static_cast<int>(min(int64_t(8), H - e0)), w);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Eight elements times 2^60.
+template <typename E>
+__device__ __forceinline__ void scale_up(const uint32_t* w, uint32_t* y) {
+  if constexpr (In<E>::kFew) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) t[j] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = __float_as_uint(In<E>::get(w, 2 * i) * 0x1p60f);
+      const uint32_t b = __float_as_uint(In<E>::get(w, 2 * i + 1) * 0x1p60f);
+      y[i] = (a >> 16) | (b & 0xFFFF0000u);  // exact: still 8 significant bits
+    }
   } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(w[i]) * 0x1p60f);
+  }
+}
+
+// Numbers that round to the same codes as the quotients x / S, S = s g.  The codes' borders are
+// 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.  q = x / S is first approximated (x r, r near 1 / S, off by
+// less than 2^-19) and put on the grid of multiples of 2^-13, which holds the borders.
+//   8 significant bits (bf16): a border has 3 significant bits and S has 4, so x is either S times
+//   the border or off it by at least 2^-8 of it; on the grid q is then the border itself, or at
+//   least 7 steps away on its side.
+//   24 significant bits: the sign of the exact remainder x - q' S of the grid point q' says on which
+//   side of q' the quotient lies; half a step to that side keeps it off the border.
+template <typename E>
+__device__ __forceinline__ void fp4_quotients(const uint32_t* w, float S, float r, float* t) {
+  constexpr float kGrid = 1536.f;  // one unit in the last place of 1024 .. 2048 is 2^-13
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = In<E>::get(w, j);
+    t[j] = __fadd_rn(__fmaf_rn(x, r, kGrid), -kGrid);
+    if constexpr (!In<E>::kFew) {
+      const float d = __fmaf_rn(-t[j], S, x);
+      if (d != 0.f) t[j] += copysignf(6.103515625e-05f, d);  // 2^-14
+    }
+  }
+}
+
+// The e4m3 code of a / 6, rounded to nearest, ties to even: a / 6 is rounded to odd for 24
+// significant bits (truncated, the last bit set if inexact), so that no quotient lands on the
+// middle of two codes; for 8 bits a rounding to 12 significant bits is enough (a middle times 6 has
+// at most 7, so a is it or at least 2^-8 away).
+template <typename E>
+__device__ __forceinline__ uint32_t scale_code(float a) {
+  if constexpr (In<E>::kFew) {
+    const float q = a * 0.16666667163372039794921875f;  // 1 / 6 rounded
+    return e4m3_of(__uint_as_float((__float_as_uint(q) + 0x800u) & ~0xFFFu));
+  } else {
+    const float q = __fdiv_rn(a, 6.f);
+    const float d = fmaf(-q, 6.f, a);  // exact remainder
+    uint32_t b = __float_as_uint(q);
+    if (d != 0.f && !(b & 1u)) b = d > 0.f ? b + 1u : b - 1u;
+    return e4m3_of(__uint_as_float(b));
+  }
+}
+
+// Writes the codes of elements 8 j .. 8 j + 7 and the values they stand for.
+template <bool kVec>
+__device__ __forceinline__ void store_vec(const QuantParams& p, int64_t r, int64_t j,
+                                          const float* t, float S) {
+  if (j * 4 >= p.row_bytes) return;  // past the packed row's padding
+  const uint32_t w = fp4x8(t);
+  *reinterpret_cast<uint32_t*>(p.packed + r * p.row_bytes + j * 4) = w;
+  if (!p.values || j * 8 >= p.H) return;
+  float f[8];
+  fp4x8_values(w, f);
+  uint32_t h[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * q] * S, f[2 * q + 1] * S);  // exact
+    h[q] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  uint16_t* vd = p.values + r * p.ldv + j * 8;
+  if (kVec && j * 8 + 8 <= p.H) {
+    *reinterpret_cast<uint4*>(vd) = make_uint4(h[0], h[1], h[2], h[3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (j * 8 + q < p.H) vd[q] = static_cast<uint16_t>(h[q >> 1] >> (16 * (q & 1)));
+  }
+}
+
+// Four blocks' scale bytes of row r (group gr) in one store.
+__device__ __forceinline__ void store_scales(const QuantParams& p, int64_t r, int64_t gr,
+                                             uint32_t four) {
+  *reinterpret_cast<uint32_t*>(p.scales + (size_t(r >> 7) * p.groups + size_t(gr)) * 512 +
+                               (r & 31) * 16 + ((r >> 5) & 3) * 4) = four;
+}
+
+constexpr int kQuantThreads = 256;
+
+// Blocks of 32: a warp takes kN spans of 256 elements (two scale groups) of one row; the padding
+// rows of the last scale tile get scales of zero.
+template <typename E, bool kVec, int kN>
+__global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p, int32_t spans) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (int64_t(blockIdx.x) * kQuantThreads + threadIdx.x) >> 5;
+  const int32_t per_row = (spans + kN - 1) / kN;
+  const int64_t r = warp / per_row;
+  const int32_t s0 = static_cast<int32_t>(warp % per_row) * kN;
+  if (r >= ((p.rows + 127) & ~int64_t(127))) return;
+  const uint8_t* row = p.x + r * p.ldx * In<E>::kBytes;
+  uint32_t w[kN][In<E>::kWords];
+#pragma unroll
+  for (int q = 0; q < kN; ++q) {
+#pragma unroll
+    for (int i = 0; i < In<E>::kWords; ++i) w[q][i] = 0;
+    const int64_t j = int64_t(s0 + q) * 32 + lane;
+    if (r < p.rows && j * 8 < p.H) load_vec<E, kVec>(row, j, p.H, w[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < kN; ++q) {
+    if (s0 + q >= spans) break;
+    const int64_t j = int64_t(s0 + q) * 32 + lane;
+    uint32_t m = In<E>::amax(w[q]);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const bool bad = m >= kInfBits;
     // floor(log2 m) - 2, biased; below 2^-125 (and for a block of zeros) the smallest scale
     const int32_t e = max(int32_t(m >> 23) - 2, 0);
-    *sc = static_cast<uint8_t>(e);
-    S = e ? __uint_as_float(uint32_t(e) << 23) : __uint_as_float(1u << 22);
-    const float inv = __uint_as_float(uint32_t(254 - e) << 23);  // 2^(127 - e), exact
+    uint32_t four = (bad ? 0xFFu : uint32_t(e)) << (8 * ((lane >> 2) & 3));
+    four |= __shfl_xor_sync(0xffffffffu, four, 4);
+    four |= __shfl_xor_sync(0xffffffffu, four, 8);
+    if ((lane & 15) == 0) store_scales(p, r, (s0 + q) * 2 + (lane >> 4), four);
+    if (r >= p.rows) continue;
+    if (bad) report(p.status, SV_ERR_BAD_INPUT);
+    const float S = bad ? __uint_as_float(0x7FC00000u)  // the scale 0xFF stands for NaN
+                        : e ? __uint_as_float(uint32_t(e) << 23) : __uint_as_float(1u << 22);
+    const float inv = __uint_as_float(uint32_t(254 - e) << 23);  // 2^(127 - e): exact products
+    float t[8];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) t[j] = __uint_as_float(v[j]) * inv;
+    for (int i = 0; i < 8; ++i) t[i] = bad ? 0.f : In<E>::get(w[q], i) * inv;
+    store_vec<kVec>(p, r, j, t, S);
   }
-  store_block<32, kVec>(p, r, k * 32, t, S);
 }
 
-// Blocks of 16 under a row scale: a CTA per row, two passes over it (the second from L1).
-template <typename E, bool kVec>
-__global__ void __launch_bounds__(kQuantThreads) quant_e4m3_kernel(QuantParams p) {
-  __shared__ uint32_t s_max[kQuantThreads / 32];
-  const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x;
-  const int64_t nb = int64_t(p.groups) * 4;
-  if (r >= p.rows) {
-    for (int64_t k = tid; k < nb; k += kQuantThreads) p.scales[scale_at(r, k, p.groups)] = 0;
-    return;
-  }
+// Blocks of 16 under a row scale: `warps` warps of a CTA per row, each lane with kN vectors of it in
+// registers between the row's maximum and the codes (kN = 0: any number, read twice).
+template <typename E, bool kVec, int kN>
+__global__ void __launch_bounds__(512) quant_e4m3_kernel(QuantParams p, int32_t spans,
+                                                         int32_t warps) {
+  __shared__ uint32_t s_max[16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t rows_here = (blockDim.x >> 5) / warps;
+  const int64_t r = int64_t(blockIdx.x) * rows_here + warp / warps;
+  const int32_t mine = warp % warps;
+  const bool real = r < p.rows, tile = r < ((p.rows + 127) & ~int64_t(127));
   const uint8_t* row = p.x + r * p.ldx * In<E>::kBytes;
+  constexpr int kHold = kN ? kN : 1;
+  uint32_t w[kHold][In<E>::kWords], am[kHold];
+  auto fetch = [&](int32_t q, uint32_t* x) {
+#pragma unroll
+    for (int i = 0; i < In<E>::kWords; ++i) x[i] = 0;
+    const int64_t j = (int64_t(q) * warps + mine) * 32 + lane;
+    if (real && j * 8 < p.H) load_vec<E, kVec>(row, j, p.H, x);
+  };
   uint32_t m = 0;
-  for (int64_t k = tid; k * 16 < p.H; k += kQuantThreads) {
-    uint32_t v[16];
-    load_block<E, 16, kVec>(row, k * 16, p.H, v);
-    m = max(m, amax_bits<16>(v));
+  if constexpr (kN > 0) {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) fetch(q, w[q]);
+#pragma unroll
+    for (int q = 0; q < kN; ++q) m = max(m, am[q] = In<E>::amax(w[q]));
+  } else {
+    for (int32_t q = 0; q * warps + mine < spans; ++q) {
+      fetch(q, w[0]);
+      m = max(m, In<E>::amax(w[0]));
+    }
   }
   m = __reduce_max_sync(0xffffffffu, m);
-  if ((tid & 31) == 0) s_max[tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, s_max[w]);
+  if (warps > 1) {
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    for (int i = 0; i < warps; ++i) m = max(m, s_max[warp - mine + i]);
+  }
+  if (!tile) return;
   const bool bad = m >= kInfBits;
   // 6 * 448 = 1.3125 * 2^11: the smallest k with m <= 1.3125 * 2^(11 + k)
   int32_t k2 = 0;
   if (!bad && m) {
-    const int32_t e = int32_t(m >> 23) - 127;
-    k2 = e - 11 + ((m & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+    k2 = int32_t(m >> 23) - 127 - 11 + ((m & 0x7FFFFFu) > 0x280000u ? 1 : 0);
     k2 = min(max(k2, -120), 120);
   }
   const float g = __uint_as_float(uint32_t(k2 + 127) << 23);
   const float ginv = __uint_as_float(uint32_t(127 - k2) << 23);
-  if (tid == 0) {
+  if (real && mine == 0 && lane == 0) {
     p.row_scales[r] = g;
     if (bad) report(p.status, SV_ERR_BAD_INPUT);
   }
-  for (int64_t k = tid; k < nb; k += kQuantThreads) {
-    uint8_t* sc = p.scales + scale_at(r, k, p.groups);
-    if (k * 16 >= p.H) {
-      *sc = 0;
-      // the packed row is padded to 32 elements: its second half block is zeros
-      if (k * 8 < p.row_bytes)
-        *reinterpret_cast<uint2*>(p.packed + r * p.row_bytes + k * 8) = make_uint2(0, 0);
-      continue;
-    }
-    uint32_t v[16];
-    load_block<E, 16, kVec>(row, k * 16, p.H, v);
-    float t[16];
-    uint32_t code;
-    float s;
-    if (bad) {
-      code = 0x7Fu;
-      s = __uint_as_float(0x7FC00000u);
-    } else {
-      const float a = __uint_as_float(amax_bits<16>(v)) * ginv;
-      code = e4m3_of(div_odd(a, 6.f));
-      s = e4m3_value(code);
-    }
-    const float S = s * g;
+  auto emit = [&](int32_t q, const uint32_t* x, uint32_t amax) {
+    const int32_t span = q * warps + mine;
+    if (span >= spans) return;
+    const int64_t j = int64_t(span) * 32 + lane;
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const uint32_t code = bad ? 0x7Fu : scale_code<E>(__uint_as_float(amax) * ginv);
+    uint32_t four = (real ? code : 0u) << (8 * ((lane >> 1) & 3));
+    four |= __shfl_xor_sync(0xffffffffu, four, 2);
+    four |= __shfl_xor_sync(0xffffffffu, four, 4);
+    if ((lane & 7) == 0) store_scales(p, r, span * 4 + (lane >> 3), four);
+    if (!real) return;
+    const float s = e4m3_value(code);
+    const float S = bad ? __uint_as_float(0x7FC00000u) : s * g;
+    float t[8];
+    if (bad || code == 0) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float x = __uint_as_float(v[j]);
-      t[j] = (bad || code == 0) ? 0.f : copysignf(div_odd(fabsf(x), S), x);
+      for (int i = 0; i < 8; ++i) t[i] = 0.f;
+    } else {
+      // 1 / S; at the smallest scales it overflows: there both are taken 2^60 larger (x and S stay
+      // exact, they are far below the largest number)
+      const float rs = rcp_approx(s);
+      if (k2 > -110) {
+        fp4_quotients<E>(x, S, rs * ginv, t);
+      } else {
+        uint32_t y[In<E>::kWords];
+        scale_up<E>(x, y);
+        fp4_quotients<E>(y, S * 0x1p60f, rs * (ginv * 0x1p-60f), t);
+      }
     }
-    *sc = static_cast<uint8_t>(code);
-    store_block<16, kVec>(p, r, k * 16, t, S);
+    store_vec<kVec>(p, r, j, t, S);
+  };
+  if constexpr (kN > 0) {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) emit(q, w[q], am[q]);
+  } else {
+    for (int32_t q = 0; q * warps + mine < spans; ++q) {
+      fetch(q, w[0]);
+      emit(q, w[0], In<E>::amax(w[0]));
+    }
   }
+}
+
+template <typename E, bool kVec>
+sv_status launch_e8m0(const QuantParams& p, cudaStream_t s) {
+  const int32_t spans = int32_t((p.H + 255) / 256);
+  const int64_t padded = (p.rows + 127) / 128 * 128;
+  // two spans per warp where there is enough work for the GPU, else one
+  const bool two = padded * spans >= 2 * 16384;
+  const int64_t warps = padded * (two ? (spans + 1) / 2 : spans);
+  const int64_t blocks = (warps * 32 + kQuantThreads - 1) / kQuantThreads;
+  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  if (two)
+    quant_e8m0_kernel<E, kVec, 2><<<unsigned(blocks), kQuantThreads, 0, s>>>(p, spans);
+  else
+    quant_e8m0_kernel<E, kVec, 1><<<unsigned(blocks), kQuantThreads, 0, s>>>(p, spans);
+  return launch_status(cudaGetLastError());
+}
+
+template <typename E, bool kVec>
+sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
+  constexpr int kMost = In<E>::kFew ? 5 : 3;  // vectors a lane holds
+  const int32_t spans = int32_t((p.H + 255) / 256);
+  const int64_t padded = (p.rows + 127) / 128 * 128;
+  // the fewest warps per row that hold it; more where the rows alone would leave the GPU idle
+  int32_t warps = 1;
+  while (warps < 16 && (warps * kMost < spans || (warps < spans && p.rows * warps < 2048)))
+    warps *= 2;
+  const int threads = 32 * std::max(warps, 8);
+  const int64_t blocks = (padded + threads / 32 / warps - 1) / (threads / 32 / warps);
+  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  const unsigned grid = unsigned(blocks);
+  switch ((spans + warps - 1) / warps) {
+    case 1: quant_e4m3_kernel<E, kVec, 1><<<grid, threads, 0, s>>>(p, spans, warps); break;
+    case 2: quant_e4m3_kernel<E, kVec, 2><<<grid, threads, 0, s>>>(p, spans, warps); break;
+    case 3: quant_e4m3_kernel<E, kVec, 3><<<grid, threads, 0, s>>>(p, spans, warps); break;
+    case 4:
+      quant_e4m3_kernel<E, kVec, kMost == 5 ? 4 : 0><<<grid, threads, 0, s>>>(p, spans, warps);
+      break;
+    case 5:
+      quant_e4m3_kernel<E, kVec, kMost == 5 ? 5 : 0><<<grid, threads, 0, s>>>(p, spans, warps);
+      break;
+    default: quant_e4m3_kernel<E, kVec, 0><<<grid, threads, 0, s>>>(p, spans, warps);
+  }
+  return launch_status(cudaGetLastError());
 }
 
 template <typename E>
 sv_status launch_quant(const QuantParams& p, int32_t format, bool vec, cudaStream_t s) {
-  const int64_t padded = (p.rows + 127) / 128 * 128;
-  if (format == SV_FP4_E8M0_32) {
-    const int64_t blocks = (padded * p.groups * 4 + kQuantThreads - 1) / kQuantThreads;
-    if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-    if (vec)
-      quant_e8m0_kernel<E, true><<<unsigned(blocks), kQuantThreads, 0, s>>>(p);
-    else
-      quant_e8m0_kernel<E, false><<<unsigned(blocks), kQuantThreads, 0, s>>>(p);
-  } else {
-    if (padded > INT32_MAX) return SV_ERR_UNSUPPORTED;
-    if (vec)
-      quant_e4m3_kernel<E, true><<<unsigned(padded), kQuantThreads, 0, s>>>(p);
-    else
-      quant_e4m3_kernel<E, false><<<unsigned(padded), kQuantThreads, 0, s>>>(p);
-  }
-  return launch_status(cudaGetLastError());
+  if (format == SV_FP4_E8M0_32)
+    return vec ? launch_e8m0<E, true>(p, s) : launch_e8m0<E, false>(p, s);
+  return vec ? launch_e4m3<E, true>(p, s) : launch_e4m3<E, false>(p, s);
 }
 
 }  // namespace
