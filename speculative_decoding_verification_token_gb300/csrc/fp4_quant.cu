@@ -134,12 +134,15 @@ template <typename E>
 __device__ __forceinline__ void fp4_quotients(const uint32_t* w, float S, float r, float* t) {
   constexpr float kGrid = 1536.f;  // one unit in the last place of 1024 .. 2048 is 2^-13
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float x = In<E>::get(w, j);
-    t[j] = __fadd_rn(__fmaf_rn(x, r, kGrid), -kGrid);
+  for (int j = 0; j < 8; j += 2) {
+    const float2 x = make_float2(In<E>::get(w, j), In<E>::get(w, j + 1));
+    const float2 q = add2(fma2(x, splat2(r), splat2(kGrid)), splat2(-kGrid));
+    t[j] = q.x;
+    t[j + 1] = q.y;
     if constexpr (!In<E>::kFew) {
-      const float d = __fmaf_rn(-t[j], S, x);
-      if (d != 0.f) t[j] += copysignf(6.103515625e-05f, d);  // 2^-14
+      const float2 d = fma2(make_float2(-q.x, -q.y), splat2(S), x);
+      if (d.x != 0.f) t[j] += copysignf(6.103515625e-05f, d.x);  // 2^-14
+      if (d.y != 0.f) t[j + 1] += copysignf(6.103515625e-05f, d.y);
     }
   }
 }
@@ -175,7 +178,8 @@ __device__ __forceinline__ void store_vec(const QuantParams& p, int64_t r, int64
   uint32_t h[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * q] * S, f[2 * q + 1] * S);  // exact
+    const float2 v = mul2(make_float2(f[2 * q], f[2 * q + 1]), splat2(S));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);  // exact
     h[q] = *reinterpret_cast<const uint32_t*>(&b);
   }
   uint16_t* vd = p.values + r * p.ldv + j * 8;
@@ -244,8 +248,9 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
 
 // Blocks of 16 under a row scale: `warps` warps of a CTA per row, each lane with kN vectors of it in
 // registers between the row's maximum and the codes (kN = 0: any number, read twice).
-template <typename E, bool kVec, int kN>
-__global__ void __launch_bounds__(512) quant_e4m3_kernel(QuantParams p, int32_t spans,
+template <typename E, bool kVec, int kN, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
+    quant_e4m3_kernel(QuantParams p, int32_t spans,
                                                          int32_t warps) {
   __shared__ uint32_t s_max[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -361,22 +366,24 @@ sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
   int32_t warps = 1;
   while (warps < 16 && (warps * kMost < spans || (warps < spans && p.rows * warps < 2048)))
     warps *= 2;
-  const int threads = 32 * std::max(warps, 8);
+  const int threads = warps <= 4 ? 128 : 512;
   const int64_t blocks = (padded + threads / 32 / warps - 1) / (threads / 32 / warps);
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  const unsigned grid = unsigned(blocks);
-  switch ((spans + warps - 1) / warps) {
-    case 1: quant_e4m3_kernel<E, kVec, 1><<<grid, threads, 0, s>>>(p, spans, warps); break;
-    case 2: quant_e4m3_kernel<E, kVec, 2><<<grid, threads, 0, s>>>(p, spans, warps); break;
-    case 3: quant_e4m3_kernel<E, kVec, 3><<<grid, threads, 0, s>>>(p, spans, warps); break;
-    case 4:
-      quant_e4m3_kernel<E, kVec, kMost == 5 ? 4 : 0><<<grid, threads, 0, s>>>(p, spans, warps);
-      break;
-    case 5:
-      quant_e4m3_kernel<E, kVec, kMost == 5 ? 5 : 0><<<grid, threads, 0, s>>>(p, spans, warps);
-      break;
-    default: quant_e4m3_kernel<E, kVec, 0><<<grid, threads, 0, s>>>(p, spans, warps);
-  }
+  const int32_t hold = (spans + warps - 1) / warps;
+  auto go = [&](auto* narrow, auto* wide) {
+    if (threads == 128)
+      narrow<<<unsigned(blocks), 128, 0, s>>>(p, spans, warps);
+    else
+      wide<<<unsigned(blocks), 512, 0, s>>>(p, spans, warps);
+  };
+  if (hold == 1)
+    go(quant_e4m3_kernel<E, kVec, 1, 128>, quant_e4m3_kernel<E, kVec, 1, 512>);
+  else if (hold == 2)
+    go(quant_e4m3_kernel<E, kVec, 2, 128>, quant_e4m3_kernel<E, kVec, 2, 512>);
+  else if (hold <= kMost)
+    go(quant_e4m3_kernel<E, kVec, kMost, 128>, quant_e4m3_kernel<E, kVec, kMost, 512>);
+  else
+    go(quant_e4m3_kernel<E, kVec, 0, 128>, quant_e4m3_kernel<E, kVec, 0, 512>);
   return launch_status(cudaGetLastError());
 }
 
