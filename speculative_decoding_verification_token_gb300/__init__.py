@@ -47,6 +47,8 @@ def declared_functions():
 def lib():
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:  # set once, complete
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -142,8 +144,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without the stream object (3 us of a short call)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_code(t):
@@ -445,32 +449,74 @@ def spec_verify_token_sharded(target, draft, v_off, V_total, target_row0, draft_
 
 
 # ---- logits before verification ----------------------------------------------------------------
+# These calls are short, so that checking their arguments counts: one condition per tensor, and
+# _refuse finds out what is wrong with one that fails it.
 
-def _sized(t, name, *shape):
-    """Checks a tensor's shape (None: any extent)."""
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return t
+def _refuse(t, name, dtype, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _status(status, dev):
+def _device_of(t, name):
+    """Index of the device a call works on: the tensor's, which must be the current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (
+            t.get_device() != torch._C._cuda_getDevice()):
+        _refuse(t, name, None, "")
+    return t.get_device()
+
+
+def _vec(t, name, dtype, n, dev):
+    """Pointer of a contiguous tensor [n] on device `dev` (n None: any length); None stays None."""
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev
+            or t.dtype != dtype or (n is not None and t.shape != (n,)) or not t.is_contiguous()):
+        _refuse(t, name, dtype, "contiguous" if n is None else f"contiguous [{n}]")
+    return t.data_ptr()
+
+
+def _mat(t, name, dtype, dev, rows=None, cols=None):
+    """Pointer of a 2-D tensor with unit column stride on device `dev`, of at least `cols` columns
+    and exactly `rows` rows if given."""
+    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev
+            or t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)
+            or (rows is not None and t.shape[0] != rows)
+            or (cols is not None and t.shape[1] < cols)):
+        _refuse(t, name, dtype, f"[{rows or 'rows'}, {cols or 'columns'}] with unit column stride")
+    return t.data_ptr()
+
+
+def _ld(t, multiple=1):
+    """Row stride of a 2-D tensor; a single row's says nothing and may be any `multiple`."""
+    if t.shape[0] > 1:
+        return t.stride(0)
+    return (max(t.stride(0), t.shape[1]) + multiple - 1) // multiple * multiple
+
+
+def _status_ptr(status, dev):
     if status is None:
-        return torch.zeros(1, dtype=torch.int32, device=dev)
-    return _dev(status, torch.int32)
+        status = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
+    return status, _vec(status, "status", torch.int32, None, dev)
 
 
-def _history(counts, prompt_bits, output_bits):
-    """Checks the history tensors; returns (slots, counts stride, bits stride, V)."""
-    _dev(counts, torch.int32, rows=True), _dev(prompt_bits, torch.int32, rows=True)
-    _dev(output_bits, torch.int32, rows=True)
+def _history(counts, prompt_bits, output_bits, dev):
+    """Checks the history tensors; returns (counts, prompt bits, output bits, slots, strides, V)."""
+    c = _mat(counts, "counts", torch.int32, dev)
     n_slots, V = counts.shape
     words = (V + 31) // 32
-    if (prompt_bits.shape[0] != n_slots or output_bits.shape[0] != n_slots
-            or prompt_bits.shape[1] < words or output_bits.shape[1] < words):
-        raise ValueError("the bit rows must be [slots, ceil(V / 32)] for counts [slots, V]")
-    if prompt_bits.stride(0) != output_bits.stride(0):
+    pb = _mat(prompt_bits, "prompt_bits", torch.int32, dev, n_slots, words)
+    ob = _mat(output_bits, "output_bits", torch.int32, dev, n_slots, words)
+    ldb = _ld(prompt_bits)
+    if _ld(output_bits) != ldb:
         raise ValueError("prompt_bits and output_bits must have the same stride")
-    return n_slots, counts.stride(0), prompt_bits.stride(0), V
+    return c, pb, ob, n_slots, _ld(counts), ldb, V
 
 
 def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, lens=None,
@@ -479,20 +525,17 @@ def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, le
     the history of slots int32 [B] (default: row r in slot r), in place: counts int32 [S, V] and
     the bit rows int32 [S, ceil(V / 32)] (see include/specverify.h).  `prompt` marks them as prompt
     tokens instead of counting them; `reset` clears the listed slots first.  Returns the status."""
-    _dev(tokens, torch.int32, rows=True)
-    n_slots, ldc, ldb, V = _history(counts, prompt_bits, output_bits)
+    dev = _device_of(tokens, "tokens")
+    tk = _mat(tokens, "tokens", torch.int32, dev)
+    c, pb, ob, n_slots, ldc, ldb, V = _history(counts, prompt_bits, output_bits, dev)
     B, n = tokens.shape
-    if lens is not None:
-        _sized(_dev(lens, torch.int32), "lens", B)
-    if slots is not None:
-        _sized(_dev(slots, torch.int32), "slots", B)
-    elif B > n_slots:
+    if slots is None and B > n_slots:
         raise ValueError("more rows than slots")
-    status = _status(status, tokens.device)
-    code = lib().spec_history_append(_ptr(tokens), max(tokens.stride(0), n), _ptr(lens), n,
-                                     _ptr(slots), B, int(prompt), int(reset), V, n_slots,
-                                     _ptr(counts), ldc, _ptr(prompt_bits), _ptr(output_bits), ldb,
-                                     _ptr(status), _stream(stream))
+    status, st = _status_ptr(status, dev)
+    code = lib().spec_history_append(
+        tk, _ld(tokens), _vec(lens, "lens", torch.int32, B, dev), n,
+        _vec(slots, "slots", torch.int32, B, dev), B, int(prompt), int(reset), V, n_slots, c, ldc,
+        pb, ob, ldb, st, _stream(stream))
     _check(code, "spec_history_append")
     return status
 
@@ -507,57 +550,62 @@ def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draf
     [n, ceil(V / 32)] bit rows, mask_row int32 per logit row, -1: none) on the rows of a round
     (see include/specverify.h).  Works in place unless `out` is another tensor of the same shape
     and dtype.  Returns out."""
-    _dev(logits, rows=True), _dev(row0, torch.int64), _dev(draft_row0, torch.int64)
-    _dev(draft_len, torch.int32), _dev(draft_tokens, torch.int32)
+    dev = _device_of(logits, "logits")
     dt = _dtype_code(logits)
-    V = logits.shape[1]
+    lg = _mat(logits, "logits", logits.dtype, dev)
+    rows, V = logits.shape
     B = draft_len.numel()
-    out = logits if out is None else _dev(out, logits.dtype, rows=True)
-    if out.shape != logits.shape:
-        raise ValueError("out must have the shape of the logits")
-    if row0.numel() != B or (draft_row0 is not None and draft_row0.numel() != B):
-        raise ValueError("row0, draft_row0 and draft_len must have one entry per request")
+    if out is None:
+        out, ot = logits, lg
+    else:
+        ot = _mat(out, "out", logits.dtype, dev, rows, V)
+        if out.shape[1] != V:
+            raise ValueError("out must have the shape of the logits")
+    f32, i32, i64 = torch.float32, torch.int32, torch.int64
+    rep = _vec(repetition, "repetition", f32, B, dev)
+    pres = _vec(presence, "presence", f32, B, dev)
+    freq = _vec(frequency, "frequency", f32, B, dev)
+    c = pb = ob = sl = None
     n_slots = ldc = ldb = 0
-    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
-        if t is not None:
-            _sized(_dev(t, torch.float32), name, B)
-    if repetition is not None or presence is not None or frequency is not None:
+    if rep is not None or pres is not None or freq is not None:
         if counts is None or prompt_bits is None or output_bits is None:
             raise ValueError("penalties need counts, prompt_bits and output_bits")
-        n_slots, ldc, ldb, hv = _history(counts, prompt_bits, output_bits)
+        c, pb, ob, n_slots, ldc, ldb, hv = _history(counts, prompt_bits, output_bits, dev)
         if hv != V:
             raise ValueError("the history's vocabulary differs from the logits'")
-        if slots is not None:
-            _sized(_dev(slots, torch.int32), "slots", B)
-        elif B > n_slots:
+        sl = _vec(slots, "slots", i32, B, dev)
+        if slots is None and B > n_slots:
             raise ValueError("more requests than slots")
+    bs = _vec(bias_start, "bias_start", i32, B + 1, dev)
+    bt = bv = None
     n_bias = 0
-    if bias_start is not None:
-        _sized(_dev(bias_start, torch.int32), "bias_start", B + 1)
-        _dev(bias_tokens, torch.int32), _dev(bias_values, torch.float32)
+    if bs is not None:
+        bt = _vec(bias_tokens, "bias_tokens", i32, None, dev)
+        if bt is None or bias_values is None:
+            raise ValueError("bias_start needs bias_tokens and bias_values")
         n_bias = bias_tokens.numel()
-        if bias_values.numel() != n_bias:
-            raise ValueError("bias_tokens and bias_values must have the same length")
+        bv = _vec(bias_values, "bias_values", f32, n_bias, dev)
+    mr = _vec(mask_row, "mask_row", i32, rows, dev)
+    mk = None
     n_mask = ldm = 0
-    if mask_row is not None:
-        _sized(_dev(mask_row, torch.int32), "mask_row", logits.shape[0])
-        _dev(mask, torch.int32, rows=True)
-        n_mask, ldm = mask.shape[0], mask.stride(0)
-        if mask.shape[1] < (V + 31) // 32:
-            raise ValueError("mask rows must hold ceil(V / 32) words")
-    status = _status(status, logits.device)
+    if mr is not None:
+        mk = _mat(mask, "mask", i32, dev, None, (V + 31) // 32)
+        n_mask, ldm = mask.shape[0], _ld(mask)
+    status, st = _status_ptr(status, dev)
     code = lib().spec_process_logits(
-        _ptr(logits), logits.stride(0), _ptr(out), out.stride(0), dt, V, _ptr(row0),
-        _ptr(draft_row0), _ptr(draft_len), int(max_draft_len), int(first_row), int(bonus_row),
-        _ptr(draft_tokens), B, _ptr(slots), n_slots, _ptr(counts), ldc, _ptr(prompt_bits),
-        _ptr(output_bits), ldb, _ptr(repetition), _ptr(presence), _ptr(frequency),
-        _ptr(bias_start), _ptr(bias_tokens), _ptr(bias_values), n_bias, _ptr(mask), ldm, n_mask,
-        _ptr(mask_row), _ptr(status), _stream(stream))
+        lg, _ld(logits, 8), ot, _ld(out, 8), dt, V, _vec(row0, "row0", i64, B, dev),
+        _vec(draft_row0, "draft_row0", i64, B, dev), _vec(draft_len, "draft_len", i32, B, dev),
+        int(max_draft_len), int(first_row), int(bonus_row),
+        _vec(draft_tokens, "draft_tokens", i32, None, dev), B, sl, n_slots, c, ldc, pb, ob, ldb,
+        rep, pres, freq, bs, bt, bv, n_bias, mk, ldm, n_mask, mr, st, _stream(stream))
     _check(code, "spec_process_logits")
     return out
 
 
 # ---- the output projection in 4 bits -------------------------------------------------------------
+
+_FP4_BLOCK = {SV_FP4_E8M0_32: 32, SV_FP4_E4M3_16: 16}
+
 
 def spec_fp4_row_bytes(H):
     return int(lib().spec_fp4_row_bytes(H))
@@ -567,72 +615,89 @@ def spec_fp4_scale_bytes(rows, H, fmt):
     return int(lib().spec_fp4_scale_bytes(rows, H, fmt))
 
 
+def _fp4_sizes(rows, H, fmt):
+    """(packed bytes of a row, bytes of all scales): 128-row tiles, 256-element spans."""
+    return (H + 31) // 32 * 16, (rows + 127) // 128 * ((H + 255) // 256) * (32768 // _FP4_BLOCK[fmt])
+
+
 def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=None, status=None,
                       stream=None):
     """Rows x [rows, H] (bf16 or fp32, any row stride) to blocks of 4-bit values in format `fmt`
     (see include/specverify.h).  Returns {"packed", "scales", "row_scales", "rows", "H", "format",
     "status"}, which spec_project_fp4 takes as an operand; `values`, a bf16 [rows, H] tensor, is
     filled with the numbers the codes stand for."""
-    _dev(x, rows=True)
+    dev = _device_of(x, "x")
     dt = _dtype_code(x)
+    xp = _mat(x, "x", x.dtype, dev)
     rows, H = x.shape
-    dev = x.device
-    nbytes, rb = spec_fp4_scale_bytes(rows, H, fmt), spec_fp4_row_bytes(H)
+    if fmt not in _FP4_BLOCK:
+        raise ValueError("fmt must be SV_FP4_E8M0_32 or SV_FP4_E4M3_16")
+    rb, nbytes = _fp4_sizes(rows, H, fmt)
     if packed is None:
-        packed = torch.empty((rows, rb), dtype=torch.uint8, device=dev)
-    elif tuple(_dev(packed, torch.uint8).shape) != (rows, rb):
-        raise ValueError(f"packed must be [rows, {rb}]")
+        packed = torch.empty((rows, rb), dtype=torch.uint8, device=x.device)
+    elif packed.shape != (rows, rb):
+        raise ValueError(f"packed must be [{rows}, {rb}]")
     if scales is None:
-        scales = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    elif _dev(scales, torch.uint8).numel() != nbytes:
+        scales = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    elif scales.numel() != nbytes:
         raise ValueError(f"scales must hold {nbytes} bytes")
+    rs = None
     if fmt == SV_FP4_E4M3_16:
         if row_scales is None:
-            row_scales = torch.empty(rows, dtype=torch.float32, device=dev)
-        else:
-            _sized(_dev(row_scales, torch.float32), "row_scales", rows)
+            row_scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rs = _vec(row_scales, "row_scales", torch.float32, rows, dev)
     else:
         row_scales = None
-    ldv = 0
+    vp, ldv = None, 0
     if values is not None:
-        _sized(_dev(values, torch.bfloat16, rows=True), "values", rows, H)
-        ldv = max(values.stride(0), H)
-    status = _status(status, dev)
-    code = lib().spec_quantize_fp4(_ptr(x), dt, rows, H, max(x.stride(0), H), int(fmt),
-                                   _ptr(packed), _ptr(scales), _ptr(row_scales), _ptr(values), ldv,
-                                   _ptr(status), _stream(stream))
+        vp, ldv = _mat(values, "values", torch.bfloat16, dev, rows, H), _ld(values)
+        if values.shape[1] != H:
+            raise ValueError("values must have the shape of x")
+    status, st = _status_ptr(status, dev)
+    u8 = torch.uint8
+    code = lib().spec_quantize_fp4(xp, dt, rows, H, _ld(x), fmt,
+                                   _vec(packed, "packed", u8, None, dev),
+                                   _vec(scales, "scales", u8, None, dev), rs, vp, ldv, st,
+                                   _stream(stream))
     _check(code, "spec_quantize_fp4")
     return {"packed": packed, "scales": scales, "row_scales": row_scales, "rows": rows, "H": H,
-            "format": int(fmt), "status": status}
+            "format": fmt, "status": status}
 
 
-def _fp4_operand(t, name):
+def _fp4_operand(t, name, dev):
+    """(packed, scales, row scales, rows, H, format) of an operand, checked."""
     rows, H, fmt = t["rows"], t["H"], t["format"]
-    _sized(_dev(t["packed"], torch.uint8), f"{name} packed", rows, (H + 31) // 32 * 16)
-    if _dev(t["scales"], torch.uint8).numel() != spec_fp4_scale_bytes(rows, H, fmt):
-        raise ValueError(f"{name} scales do not fit [{rows}, {H}]")
+    if fmt not in _FP4_BLOCK:
+        raise ValueError(f"{name}: unknown format {fmt}")
+    rb, nbytes = _fp4_sizes(rows, H, fmt)
+    packed, scales = t["packed"], t["scales"]
+    if packed.shape != (rows, rb) or scales.numel() != nbytes:
+        raise ValueError(f"{name}: packed and scales do not fit [{rows}, {H}]")
+    rs = None
     if fmt == SV_FP4_E4M3_16:
-        _sized(_dev(t["row_scales"], torch.float32), f"{name} row_scales", rows)
-    return rows, H, fmt
+        rs = _vec(t["row_scales"], name + " row_scales", torch.float32, rows, dev)
+    return (_vec(packed, name + " packed", torch.uint8, None, dev),
+            _vec(scales, name + " scales", torch.uint8, None, dev), rs, rows, H, fmt)
 
 
 def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=None):
     """Logits [M, V] = x w^T of two operands quantised by spec_quantize_fp4: hidden rows x [M, H]
     and the output projection w [V, H] (see include/specverify.h).  `out` (bf16 or fp32, rows
     16-byte aligned) is allocated in `dtype` if not given.  Returns it."""
-    M, H, fmt = _fp4_operand(x, "x")
-    V, Hw, fw = _fp4_operand(w, "w")
+    dev = _device_of(x["packed"], "x packed")
+    xp, xs, xr, M, H, fmt = _fp4_operand(x, "x", dev)
+    wp, ws, wr, V, Hw, fw = _fp4_operand(w, "w", dev)
     if Hw != H or fw != fmt:
         raise ValueError("x and w must have the same width and format")
     if out is None:
         ld = (V + 7) // 8 * 8  # rows start on 16-byte boundaries
         out = torch.empty((M, ld), dtype=dtype, device=x["packed"].device)[:, :V]
-    _sized(_dev(out, rows=True), "out", M, V)
     dt = _dtype_code(out)
-    status = _status(status, out.device)
-    code = lib().spec_project_fp4(_ptr(x["packed"]), _ptr(x["scales"]), _ptr(x["row_scales"]), M,
-                                  _ptr(w["packed"]), _ptr(w["scales"]), _ptr(w["row_scales"]), V,
-                                  H, fmt, _ptr(out), dt, max(out.stride(0), V), _ptr(status),
+    op = _mat(out, "out", out.dtype, dev, M, V)
+    if out.shape[1] != V:
+        raise ValueError(f"out must be [{M}, {V}]")
+    status, st = _status_ptr(status, dev)
+    code = lib().spec_project_fp4(xp, xs, xr, M, wp, ws, wr, V, H, fmt, op, dt, _ld(out, 8), st,
                                   _stream(stream))
     _check(code, "spec_project_fp4")
     return out

@@ -292,6 +292,26 @@ def test_process_without_penalties(sv):
     assert torch.equal(y, want)
 
 
+def test_single_row_of_odd_width(sv):
+    """A lone row's stride says nothing: [1, 1001] is as good as a padded row."""
+    x = torch.randn((1, 1001), device="cuda")
+    row0 = torch.zeros(1, dtype=torch.int64, device="cuda")
+    ln = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mask = torch.full((1, 32), -1, dtype=torch.int32, device="cuda")
+    mask[0, 31] = 0  # tokens 992 .. 1000 banned
+    y = sv.spec_process_logits(x, row0, None, ln, 0, None, mask=mask, mask_row=ln,
+                               out=torch.zeros_like(x))
+    assert torch.equal(y[:, :992], x[:, :992]) and torch.isneginf(y[:, 992:]).all()
+    w = sv.spec_quantize_fp4(torch.randn((1001, 96), device="cuda"), 0)
+    h = sv.spec_quantize_fp4(torch.randn((2, 96), device="cuda"), 0)
+    one = sv.spec_quantize_fp4(torch.zeros((1, 96), device="cuda"), 0)
+    one["packed"].copy_(h["packed"][:1])
+    one["scales"].copy_(h["scales"])
+    out = torch.full((1, 1001), 7.0, device="cuda")
+    sv.spec_project_fp4(one, w, out=out)
+    assert torch.equal(out, sv.spec_project_fp4(h, w, dtype=torch.float32)[:1])
+
+
 def test_process_parts_of_the_penalties(sv):
     """Each of the three penalties may be left out."""
     c = _case(8, 3, 4, 777, torch.float32)
