@@ -476,28 +476,28 @@ def _vec(t, name, dtype, n, dev):
     """Pointer of a contiguous tensor [n] on device `dev` (n None: any length); None stays None."""
     if t is None:
         return None
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev
-            or t.dtype != dtype or (n is not None and t.shape != (n,)) or not t.is_contiguous()):
-        _refuse(t, name, dtype, "contiguous" if n is None else f"contiguous [{n}]")
-    return t.data_ptr()
+    try:
+        if (t.get_device() == dev and t.dtype == dtype and t.is_contiguous()
+                and (n is None or t.shape == (n,))):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, "contiguous" if n is None else f"contiguous [{n}]")
 
 
-def _mat(t, name, dtype, dev, rows=None, cols=None):
-    """Pointer of a 2-D tensor with unit column stride on device `dev`, of at least `cols` columns
-    and exactly `rows` rows if given."""
-    if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev
-            or t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)
-            or (rows is not None and t.shape[0] != rows)
-            or (cols is not None and t.shape[1] < cols)):
-        _refuse(t, name, dtype, f"[{rows or 'rows'}, {cols or 'columns'}] with unit column stride")
-    return t.data_ptr()
-
-
-def _ld(t, multiple=1):
-    """Row stride of a 2-D tensor; a single row's says nothing and may be any `multiple`."""
-    if t.shape[0] > 1:
-        return t.stride(0)
-    return (max(t.stride(0), t.shape[1]) + multiple - 1) // multiple * multiple
+def _mat(t, name, dtype, dev, rows=None, cols=1):
+    """(pointer, row stride) of a 2-D tensor with unit column stride on device `dev`, of at least
+    `cols` columns and exactly `rows` rows if given.  A single row's stride says nothing: the next
+    multiple of 8 will do."""
+    try:
+        n, m = t.shape
+        ld, step = t.stride()
+        if (t.get_device() == dev and t.dtype == dtype and (step == 1 or m <= 1) and m >= cols
+                and (rows is None or n == rows)):
+            return t.data_ptr(), ld if n > 1 else (max(ld, m) + 7) // 8 * 8
+    except (AttributeError, ValueError):
+        pass
+    _refuse(t, name, dtype, f"[{rows or 'rows'}, {cols} or more] with unit column stride")
 
 
 def _status_ptr(status, dev):
@@ -508,15 +508,15 @@ def _status_ptr(status, dev):
 
 def _history(counts, prompt_bits, output_bits, dev):
     """Checks the history tensors; returns (counts, prompt bits, output bits, slots, strides, V)."""
-    c = _mat(counts, "counts", torch.int32, dev)
+    i32 = torch.int32
+    c, ldc = _mat(counts, "counts", i32, dev)
     n_slots, V = counts.shape
     words = (V + 31) // 32
-    pb = _mat(prompt_bits, "prompt_bits", torch.int32, dev, n_slots, words)
-    ob = _mat(output_bits, "output_bits", torch.int32, dev, n_slots, words)
-    ldb = _ld(prompt_bits)
-    if _ld(output_bits) != ldb:
+    pb, ldb = _mat(prompt_bits, "prompt_bits", i32, dev, n_slots, words)
+    ob, ldo = _mat(output_bits, "output_bits", i32, dev, n_slots, words)
+    if ldo != ldb:
         raise ValueError("prompt_bits and output_bits must have the same stride")
-    return c, pb, ob, n_slots, _ld(counts), ldb, V
+    return c, pb, ob, n_slots, ldc, ldb, V
 
 
 def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, lens=None,
@@ -526,14 +526,14 @@ def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, le
     the bit rows int32 [S, ceil(V / 32)] (see include/specverify.h).  `prompt` marks them as prompt
     tokens instead of counting them; `reset` clears the listed slots first.  Returns the status."""
     dev = _device_of(tokens, "tokens")
-    tk = _mat(tokens, "tokens", torch.int32, dev)
+    tk, ldt = _mat(tokens, "tokens", torch.int32, dev, cols=0)
     c, pb, ob, n_slots, ldc, ldb, V = _history(counts, prompt_bits, output_bits, dev)
     B, n = tokens.shape
     if slots is None and B > n_slots:
         raise ValueError("more rows than slots")
     status, st = _status_ptr(status, dev)
     code = lib().spec_history_append(
-        tk, _ld(tokens), _vec(lens, "lens", torch.int32, B, dev), n,
+        tk, ldt, _vec(lens, "lens", torch.int32, B, dev), n,
         _vec(slots, "slots", torch.int32, B, dev), B, int(prompt), int(reset), V, n_slots, c, ldc,
         pb, ob, ldb, st, _stream(stream))
     _check(code, "spec_history_append")
@@ -552,13 +552,13 @@ def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draf
     and dtype.  Returns out."""
     dev = _device_of(logits, "logits")
     dt = _dtype_code(logits)
-    lg = _mat(logits, "logits", logits.dtype, dev)
+    lg, ld = _mat(logits, "logits", logits.dtype, dev)
     rows, V = logits.shape
     B = draft_len.numel()
     if out is None:
-        out, ot = logits, lg
+        out, ot, ldo = logits, lg, ld
     else:
-        ot = _mat(out, "out", logits.dtype, dev, rows, V)
+        ot, ldo = _mat(out, "out", logits.dtype, dev, rows, V)
         if out.shape[1] != V:
             raise ValueError("out must have the shape of the logits")
     f32, i32, i64 = torch.float32, torch.int32, torch.int64
@@ -589,11 +589,11 @@ def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draf
     mk = None
     n_mask = ldm = 0
     if mr is not None:
-        mk = _mat(mask, "mask", i32, dev, None, (V + 31) // 32)
-        n_mask, ldm = mask.shape[0], _ld(mask)
+        mk, ldm = _mat(mask, "mask", i32, dev, None, (V + 31) // 32)
+        n_mask = mask.shape[0]
     status, st = _status_ptr(status, dev)
     code = lib().spec_process_logits(
-        lg, _ld(logits, 8), ot, _ld(out, 8), dt, V, _vec(row0, "row0", i64, B, dev),
+        lg, ld, ot, ldo, dt, V, _vec(row0, "row0", i64, B, dev),
         _vec(draft_row0, "draft_row0", i64, B, dev), _vec(draft_len, "draft_len", i32, B, dev),
         int(max_draft_len), int(first_row), int(bonus_row),
         _vec(draft_tokens, "draft_tokens", i32, None, dev), B, sl, n_slots, c, ldc, pb, ob, ldb,
@@ -628,7 +628,7 @@ def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=
     filled with the numbers the codes stand for."""
     dev = _device_of(x, "x")
     dt = _dtype_code(x)
-    xp = _mat(x, "x", x.dtype, dev)
+    xp, ldx = _mat(x, "x", x.dtype, dev)
     rows, H = x.shape
     if fmt not in _FP4_BLOCK:
         raise ValueError("fmt must be SV_FP4_E8M0_32 or SV_FP4_E4M3_16")
@@ -650,12 +650,12 @@ def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=
         row_scales = None
     vp, ldv = None, 0
     if values is not None:
-        vp, ldv = _mat(values, "values", torch.bfloat16, dev, rows, H), _ld(values)
+        vp, ldv = _mat(values, "values", torch.bfloat16, dev, rows, H)
         if values.shape[1] != H:
             raise ValueError("values must have the shape of x")
     status, st = _status_ptr(status, dev)
     u8 = torch.uint8
-    code = lib().spec_quantize_fp4(xp, dt, rows, H, _ld(x), fmt,
+    code = lib().spec_quantize_fp4(xp, dt, rows, H, ldx, fmt,
                                    _vec(packed, "packed", u8, None, dev),
                                    _vec(scales, "scales", u8, None, dev), rs, vp, ldv, st,
                                    _stream(stream))
@@ -693,11 +693,11 @@ def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=N
         ld = (V + 7) // 8 * 8  # rows start on 16-byte boundaries
         out = torch.empty((M, ld), dtype=dtype, device=x["packed"].device)[:, :V]
     dt = _dtype_code(out)
-    op = _mat(out, "out", out.dtype, dev, M, V)
+    op, ld = _mat(out, "out", out.dtype, dev, M, V)
     if out.shape[1] != V:
         raise ValueError(f"out must be [{M}, {V}]")
     status, st = _status_ptr(status, dev)
-    code = lib().spec_project_fp4(xp, xs, xr, M, wp, ws, wr, V, H, fmt, op, dt, _ld(out, 8), st,
+    code = lib().spec_project_fp4(xp, xs, xr, M, wp, ws, wr, V, H, fmt, op, dt, ld, st,
                                   _stream(stream))
     _check(code, "spec_project_fp4")
     return out

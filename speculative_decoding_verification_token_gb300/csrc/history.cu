@@ -28,7 +28,7 @@ struct HistParams {
   int32_t* status;
 };
 
-constexpr int kHistThreads = 256;
+constexpr int kHistThreads = 256;  // of a CTA, where there are several
 
 // Row r's slot and number of columns; a bad value of either is reported and leaves the row alone.
 __device__ __forceinline__ bool hist_row(const HistParams& p, int32_t r, int32_t& slot,
@@ -42,16 +42,21 @@ __device__ __forceinline__ bool hist_row(const HistParams& p, int32_t r, int32_t
   return true;
 }
 
-// One thread per token.  A round appends a few hundred tokens, so the call is one launch of one
-// or two dependent loads and two atomics.
-__global__ void __launch_bounds__(kHistThreads) history_append_kernel(HistParams p) {
-  const int64_t i = int64_t(blockIdx.x) * kHistThreads + threadIdx.x;
+// One thread per token: a round appends a few hundred, so the call is one launch of one or two
+// dependent loads and two atomics.  A single CTA (one = true) resets the status itself, which
+// saves the short call a second operation on the stream.
+__global__ void __launch_bounds__(1024) history_append_kernel(HistParams p, bool one) {
+  if (one) {
+    if (threadIdx.x == 0 && p.status) *p.status = 0;
+    __syncthreads();
+  }
+  const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= int64_t(p.B) * p.n) return;
   const int32_t r = static_cast<int32_t>(i / p.n);
   const int32_t t = static_cast<int32_t>(i % p.n);
+  const int32_t x = p.tokens[r * p.ld_tokens + t];
   int32_t slot, n;
   if (!hist_row(p, r, slot, n) || t >= n) return;
-  const int32_t x = p.tokens[r * p.ld_tokens + t];
   if (x < 0) return;  // padding
   if (x >= p.V) {
     report(p.status, SV_ERR_BAD_INPUT);
@@ -62,8 +67,9 @@ __global__ void __launch_bounds__(kHistThreads) history_append_kernel(HistParams
   if (!p.prompt) atomicAdd(p.counts + slot * p.ld_counts + x, 1);
 }
 
-constexpr int kResetThreads = 512;
-constexpr int kResetWords = 512;  // 32-token words of a slot that one CTA owns
+constexpr int kResetThreads = 256;
+constexpr int kResetWords = 256;  // 32-token words of a slot that one CTA owns
+constexpr int kResetAhead = 8;    // tokens a thread has in flight
 
 // Clear, then append: each CTA owns kResetWords words of one slot and the counts below them, so the
 // two steps need no order between CTAs.  It clears its counts, reads the row's tokens (at most a few
@@ -71,27 +77,33 @@ constexpr int kResetWords = 512;  // 32-token words of a slot that one CTA owns
 __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams p,
                                                                       int32_t chunks) {
   __shared__ uint32_t s_bits[kResetWords];
-  __shared__ int32_t s_twice;
   const int32_t r = blockIdx.x / chunks;
   const int32_t c = blockIdx.x % chunks;
   const int tid = threadIdx.x;
   int32_t slot, n;
   if (!hist_row(p, r, slot, n)) return;  // the whole CTA
-  if (tid == 0) s_twice = 0;
-  for (int w = tid; w < kResetWords; w += kResetThreads) s_bits[w] = 0;
-  __syncthreads();
+  const int32_t* row = p.tokens + r * p.ld_tokens;
+  int32_t x[kResetAhead];
+  auto fetch = [&](int32_t t0) {
+#pragma unroll
+    for (int q = 0; q < kResetAhead; ++q) {
+      const int32_t t = t0 + tid + q * kResetThreads;
+      x[q] = t < n ? __ldg(row + t) : -1;
+    }
+  };
+  fetch(0);
+  int32_t twice = 0;
   if (p.slots)
-    for (int32_t q = tid; q < p.B; q += kResetThreads)
-      if (q != r && p.slots[q] == slot) s_twice = 1;
-  const int64_t w0 = int64_t(c) * kResetWords;
-  const int64_t words = min(int64_t(kResetWords), (p.V + 31) / 32 - w0);
-  const int64_t v0 = w0 * 32, v1 = min(p.V, v0 + int64_t(kResetWords) * 32);
-  int32_t* cnt = p.counts + slot * p.ld_counts;
-  __syncthreads();
-  if (s_twice) {  // two rows would clear and fill the same slot
+    for (int32_t q = tid; q < p.B; q += kResetThreads) twice |= q != r && p.slots[q] == slot;
+  static_assert(kResetWords == kResetThreads, "a word per thread");
+  s_bits[tid] = 0;
+  if (__syncthreads_or(twice)) {  // two rows would clear and fill the same slot
     if (tid == 0) report(p.status, SV_ERR_BAD_INPUT);
     return;
   }
+  const int64_t w0 = int64_t(c) * kResetWords;
+  const int64_t v0 = w0 * 32, v1 = min(p.V, v0 + int64_t(kResetWords) * 32);
+  int32_t* cnt = p.counts + slot * p.ld_counts;
   if ((reinterpret_cast<uintptr_t>(cnt) & 15u) == 0) {
     const int64_t full = v1 & ~int64_t(3);
     for (int64_t v = v0 + 4 * tid; v < full; v += 4 * kResetThreads)
@@ -100,25 +112,23 @@ __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams
   } else {
     for (int64_t v = v0 + tid; v < v1; v += kResetThreads) cnt[v] = 0;
   }
-  __syncthreads();  // the counts are zero before this CTA's atomics reach them
-  const int32_t* row = p.tokens + r * p.ld_tokens;
-  for (int32_t t = tid; t < n; t += kResetThreads) {
-    const int32_t x = row[t];
-    if (x < 0) continue;
-    if (x >= p.V) {
-      report(p.status, SV_ERR_BAD_INPUT);
-      continue;
+  if (!p.prompt) __syncthreads();  // the counts are zero before this CTA's atomics reach them
+  for (int32_t t0 = 0; t0 < n; t0 += kResetAhead * kResetThreads) {
+    if (t0) fetch(t0);
+#pragma unroll
+    for (int q = 0; q < kResetAhead; ++q) {
+      if (x[q] >= p.V) report(p.status, SV_ERR_BAD_INPUT);
+      if (x[q] < v0 || x[q] >= v1) continue;
+      const uint32_t b = 1u << (x[q] & 31);
+      uint32_t* word = &s_bits[(x[q] - v0) >> 5];
+      if (!(*reinterpret_cast<volatile uint32_t*>(word) & b)) atomicOr(word, b);
+      if (!p.prompt) atomicAdd(cnt + x[q], 1);
     }
-    if (x < v0 || x >= v1) continue;
-    atomicOr(&s_bits[(x - v0) >> 5], 1u << (x & 31));
-    if (!p.prompt) atomicAdd(cnt + x, 1);
   }
   __syncthreads();
-  uint32_t* pb = p.prompt_bits + slot * p.ld_bits + w0;
-  uint32_t* ob = p.output_bits + slot * p.ld_bits + w0;
-  for (int w = tid; w < words; w += kResetThreads) {
-    pb[w] = p.prompt ? s_bits[w] : 0u;
-    ob[w] = p.prompt ? 0u : s_bits[w];
+  if (w0 + tid < (p.V + 31) / 32) {
+    p.prompt_bits[slot * p.ld_bits + w0 + tid] = p.prompt ? s_bits[tid] : 0u;
+    p.output_bits[slot * p.ld_bits + w0 + tid] = p.prompt ? 0u : s_bits[tid];
   }
 }
 
@@ -145,13 +155,17 @@ extern "C" sv_status spec_history_append(const int32_t* tokens, int64_t ld_token
       reset ? chunks * B : (int64_t(B) * n + kHistThreads - 1) / kHistThreads;
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return SV_ERR_CUDA;
+  const bool one = !reset && int64_t(B) * n <= 1024;
+  if (status && !one && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess)
+    return SV_ERR_CUDA;
   const HistParams p = {tokens, ld_tokens, lens, n,         slots,       B,           kind,
                         V,      n_slots,   counts, ld_counts, prompt_bits, output_bits, ld_bits,
                         status};
   if (reset)
     history_reset_kernel<<<unsigned(blocks), kResetThreads, 0, s>>>(p, int32_t(chunks));
+  else if (one)
+    history_append_kernel<<<1, (B * n + 31) / 32 * 32, 0, s>>>(p, true);
   else
-    history_append_kernel<<<unsigned(blocks), kHistThreads, 0, s>>>(p);
+    history_append_kernel<<<unsigned(blocks), kHistThreads, 0, s>>>(p, false);
   return launch_status(cudaGetLastError());
 }
