@@ -27,6 +27,7 @@ SV_NOALLOC_SCRATCH_BYTES = 8 << 20  # scratch array of spec_verify_token_noalloc
 
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the _fastcall module, once the library is loaded
 
 
 class SpecVerifyError(RuntimeError):
@@ -105,8 +106,21 @@ def lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
+        _bind_fastcall(L)
         _lib = L
         return L
+
+
+def _bind_fastcall(L):
+    """Gives the marshalling module the entry points' addresses.  A library built without it (the
+    module file is missing) is called through ctypes alone."""
+    global _fast
+    if not os.path.exists(os.path.join(_HERE, "_fastcall.so")):
+        return
+    from . import _fastcall
+    _fastcall.bind(*(C.cast(getattr(L, name), C.c_void_p).value for name in (
+        "spec_history_append", "spec_process_logits", "spec_quantize_fp4", "spec_project_fp4")))
+    _fast = _fastcall
 
 
 def status_string(code):
@@ -449,8 +463,20 @@ def spec_verify_token_sharded(target, draft, v_off, V_total, target_row0, draft_
 
 
 # ---- logits before verification ----------------------------------------------------------------
-# These calls are short, so that checking their arguments counts: one condition per tensor, and
-# _refuse finds out what is wrong with one that fails it.
+# These calls are short, so that checking their arguments counts: _fastcall does it in C++ and makes
+# the call, and declines all that is not plain -- the checks below then find out what it is.
+
+def _quick(name, args, stream):
+    """The call made by _fastcall: True if it was, False if the checks below have to see it."""
+    if _lib is None:
+        lib()
+    if _fast is None:
+        return False
+    code = getattr(_fast, name)(*args, None if stream is None else stream.cuda_stream)
+    if code > 0:
+        raise SpecVerifyError(code, "spec_" + name)
+    return code == 0
+
 
 def _refuse(t, name, dtype, shape):
     if not isinstance(t, torch.Tensor):
@@ -525,6 +551,9 @@ def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, le
     the history of slots int32 [B] (default: row r in slot r), in place: counts int32 [S, V] and
     the bit rows int32 [S, ceil(V / 32)] (see include/specverify.h).  `prompt` marks them as prompt
     tokens instead of counting them; `reset` clears the listed slots first.  Returns the status."""
+    if status is not None and _quick("history_append", (
+            tokens, counts, prompt_bits, output_bits, slots, lens, prompt, reset, status), stream):
+        return status
     dev = _device_of(tokens, "tokens")
     tk, ldt = _mat(tokens, "tokens", torch.int32, dev, cols=0)
     c, pb, ob, n_slots, ldc, ldb, V = _history(counts, prompt_bits, output_bits, dev)
@@ -550,17 +579,21 @@ def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draf
     [n, ceil(V / 32)] bit rows, mask_row int32 per logit row, -1: none) on the rows of a round
     (see include/specverify.h).  Works in place unless `out` is another tensor of the same shape
     and dtype.  Returns out."""
+    if out is None:
+        out = logits
+    if status is not None and _quick("process_logits", (
+            logits, row0, draft_row0, draft_len, max_draft_len, draft_tokens, first_row, bonus_row,
+            slots, counts, prompt_bits, output_bits, repetition, presence, frequency, bias_start,
+            bias_tokens, bias_values, mask, mask_row, out, status), stream):
+        return out
     dev = _device_of(logits, "logits")
     dt = _dtype_code(logits)
     lg, ld = _mat(logits, "logits", logits.dtype, dev)
     rows, V = logits.shape
     B = draft_len.numel()
-    if out is None:
-        out, ot, ldo = logits, lg, ld
-    else:
-        ot, ldo = _mat(out, "out", logits.dtype, dev, rows, V)
-        if out.shape[1] != V:
-            raise ValueError("out must have the shape of the logits")
+    ot, ldo = _mat(out, "out", logits.dtype, dev, rows, V)
+    if out.shape[1] != V:
+        raise ValueError("out must have the shape of the logits")
     f32, i32, i64 = torch.float32, torch.int32, torch.int64
     rep = _vec(repetition, "repetition", f32, B, dev)
     pres = _vec(presence, "presence", f32, B, dev)
@@ -626,6 +659,11 @@ def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=
     (see include/specverify.h).  Returns {"packed", "scales", "row_scales", "rows", "H", "format",
     "status"}, which spec_project_fp4 takes as an operand; `values`, a bf16 [rows, H] tensor, is
     filled with the numbers the codes stand for."""
+    if status is not None and packed is not None and scales is not None and _quick("quantize_fp4", (
+            x, fmt, packed, scales, row_scales, values, status), stream):
+        return {"packed": packed, "scales": scales,
+                "row_scales": row_scales if fmt == SV_FP4_E4M3_16 else None, "rows": x.shape[0],
+                "H": x.shape[1], "format": fmt, "status": status}
     dev = _device_of(x, "x")
     dt = _dtype_code(x)
     xp, ldx = _mat(x, "x", x.dtype, dev)
@@ -684,6 +722,11 @@ def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=N
     """Logits [M, V] = x w^T of two operands quantised by spec_quantize_fp4: hidden rows x [M, H]
     and the output projection w [V, H] (see include/specverify.h).  `out` (bf16 or fp32, rows
     16-byte aligned) is allocated in `dtype` if not given.  Returns it."""
+    if status is not None and out is not None and x["H"] == w["H"] and (
+            x["format"] == w["format"]) and _quick("project_fp4", (
+            x["packed"], x["scales"], x["row_scales"], x["rows"], w["packed"], w["scales"],
+            w["row_scales"], w["rows"], x["H"], x["format"], out, status), stream):
+        return out
     dev = _device_of(x["packed"], "x packed")
     xp, xs, xr, M, H, fmt = _fp4_operand(x, "x", dev)
     wp, ws, wr, V, Hw, fw = _fp4_operand(w, "w", dev)

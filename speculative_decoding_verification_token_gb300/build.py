@@ -2,6 +2,8 @@
 
 Each translation unit is compiled by its own nvcc process (in parallel), then linked with the
 shared CUDA runtime so that the library uses the runtime already loaded by the host process.
+Beside it the host compiler builds ``_fastcall.so``, the Python module that marshals the short
+calls' arguments (csrc/fastcall.cpp).
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -37,7 +40,42 @@ def _deps():
     return files
 
 
+def build_fastcall(force: bool = False) -> str:
+    """The marshalling module, against the installed torch's headers."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "fastcall.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "specverify.h")),
+                 os.path.getmtime(torch.__file__))
+    if not force and os.path.exists(FASTCALL) and os.path.getmtime(FASTCALL) >= newest:
+        return FASTCALL
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = FASTCALL + f".{os.getpid()}.tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, src,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {src}:\n{res.stderr}")
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    with cf.ThreadPoolExecutor(1) as ex:  # beside the CUDA sources
+        fast = ex.submit(build_fastcall, force)
+        lib = build_library(force, verbose)
+        fast.result()
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     newest = max(os.path.getmtime(f) for f in _deps())
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
         return LIB
