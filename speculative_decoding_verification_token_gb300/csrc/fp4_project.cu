@@ -278,8 +278,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
     }
     mbar_init(&drain, 1);
     fence_barrier_init();
-    // the only report is of a wait that ran out, a second after the start at the earliest
-    if (blockIdx.x == 0 && p.status) *p.status = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -288,6 +286,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  // programmatic dependent of the work before it: all above ran beside that work's end, and nothing
+  // it wrote (or that still reads the logits) is touched before this
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the only report is of a wait that ran out, a second after the start at the earliest
+  if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = 0;
   tc::fence_before_sync();
   __syncthreads();
   cluster_sync();  // the peer's barriers are initialised before anything arrives on them
@@ -494,8 +498,17 @@ sv_status launch_project(const PjMaps& m, const PjParams& p, int grid, cudaStrea
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kPjSmem)) !=
       cudaSuccess)
     return SV_ERR_CUDA;
-  kern<<<grid, kPjThreads, kPjSmem, s>>>(m.w, m.x, m.ws, m.xs, m.out, p);
-  return launch_status(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kPjThreads);
+  cfg.dynamicSmemBytes = kPjSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, m.w, m.x, m.ws, m.xs, m.out, p));
 }
 
 template <int kFmt, int kX>
