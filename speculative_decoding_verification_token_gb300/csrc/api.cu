@@ -57,6 +57,17 @@ int resident_ctas(const void* kernel, int threads, size_t smem) {
 }
 
 namespace {
+__global__ void reset_status_kernel(int32_t* status) {
+  dependent_start();
+  *status = SV_OK;
+}
+}  // namespace
+
+sv_status reset_status(int32_t* status, cudaStream_t s) {
+  return status ? launch_dependent(reset_status_kernel, 1, 1, 0, s, status) : SV_OK;
+}
+
+namespace {
 struct ProfileState {
   bool enabled = false;
   bool created = false;

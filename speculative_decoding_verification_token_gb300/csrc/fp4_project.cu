@@ -288,8 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
   }
   // programmatic dependent of the work before it: all above ran beside that work's end, and nothing
   // it wrote (or that still reads the logits) is touched before this
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependent_start();
   // the only report is of a wait that ran out, a second after the start at the earliest
   if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = 0;
   tc::fence_before_sync();
@@ -498,17 +497,8 @@ sv_status launch_project(const PjMaps& m, const PjParams& p, int grid, cudaStrea
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kPjSmem)) !=
       cudaSuccess)
     return SV_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kPjThreads);
-  cfg.dynamicSmemBytes = kPjSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, kern, m.w, m.x, m.ws, m.xs, m.out, p));
+  return launch_dependent(kern, unsigned(grid), kPjThreads, kPjSmem, s, m.w, m.x, m.ws, m.xs, m.out,
+                          p);
 }
 
 template <int kFmt, int kX>

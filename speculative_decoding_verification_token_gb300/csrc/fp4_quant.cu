@@ -205,6 +205,7 @@ constexpr int kQuantThreads = 256;
 // rows of the last scale tile get scales of zero.
 template <typename E, bool kVec, int kN>
 __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p, int32_t spans) {
+  dependent_start();
   const int lane = threadIdx.x & 31;
   const int64_t warp = (int64_t(blockIdx.x) * kQuantThreads + threadIdx.x) >> 5;
   const int32_t per_row = (spans + kN - 1) / kN;
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
     quant_e4m3_kernel(QuantParams p, int32_t spans,
                                                          int32_t warps) {
   __shared__ uint32_t s_max[16];
+  dependent_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t rows_here = (blockDim.x >> 5) / warps;
   const int64_t r = int64_t(blockIdx.x) * rows_here + warp / warps;
@@ -350,11 +352,8 @@ sv_status launch_e8m0(const QuantParams& p, cudaStream_t s) {
   const int64_t warps = padded * (two ? (spans + 1) / 2 : spans);
   const int64_t blocks = (warps * 32 + kQuantThreads - 1) / kQuantThreads;
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  if (two)
-    quant_e8m0_kernel<E, kVec, 2><<<unsigned(blocks), kQuantThreads, 0, s>>>(p, spans);
-  else
-    quant_e8m0_kernel<E, kVec, 1><<<unsigned(blocks), kQuantThreads, 0, s>>>(p, spans);
-  return launch_status(cudaGetLastError());
+  return launch_dependent(two ? quant_e8m0_kernel<E, kVec, 2> : quant_e8m0_kernel<E, kVec, 1>,
+                          unsigned(blocks), kQuantThreads, 0, s, p, spans);
 }
 
 template <typename E, bool kVec>
@@ -371,20 +370,14 @@ sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
   const int32_t hold = (spans + warps - 1) / warps;
   auto go = [&](auto* narrow, auto* wide) {
-    if (threads == 128)
-      narrow<<<unsigned(blocks), 128, 0, s>>>(p, spans, warps);
-    else
-      wide<<<unsigned(blocks), 512, 0, s>>>(p, spans, warps);
+    return launch_dependent(threads == 128 ? narrow : wide, unsigned(blocks), unsigned(threads), 0, s,
+                            p, spans, warps);
   };
-  if (hold == 1)
-    go(quant_e4m3_kernel<E, kVec, 1, 128>, quant_e4m3_kernel<E, kVec, 1, 512>);
-  else if (hold == 2)
-    go(quant_e4m3_kernel<E, kVec, 2, 128>, quant_e4m3_kernel<E, kVec, 2, 512>);
-  else if (hold <= kMost)
-    go(quant_e4m3_kernel<E, kVec, kMost, 128>, quant_e4m3_kernel<E, kVec, kMost, 512>);
-  else
-    go(quant_e4m3_kernel<E, kVec, 0, 128>, quant_e4m3_kernel<E, kVec, 0, 512>);
-  return launch_status(cudaGetLastError());
+  if (hold == 1) return go(quant_e4m3_kernel<E, kVec, 1, 128>, quant_e4m3_kernel<E, kVec, 1, 512>);
+  if (hold == 2) return go(quant_e4m3_kernel<E, kVec, 2, 128>, quant_e4m3_kernel<E, kVec, 2, 512>);
+  if (hold <= kMost)
+    return go(quant_e4m3_kernel<E, kVec, kMost, 128>, quant_e4m3_kernel<E, kVec, kMost, 512>);
+  return go(quant_e4m3_kernel<E, kVec, 0, 128>, quant_e4m3_kernel<E, kVec, 0, 512>);
 }
 
 template <typename E>
@@ -424,7 +417,8 @@ extern "C" sv_status spec_quantize_fp4(const void* x, sv_dtype dtype, int64_t ro
   const bool vec = aligned16(x) && (ldx * eb) % 16 == 0 &&
                    (!values || (aligned16(values) && ld_values % 8 == 0));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return SV_ERR_CUDA;
+  const sv_status reset = reset_status(status, s);
+  if (reset != SV_OK) return reset;
   const QuantParams p = {static_cast<const uint8_t*>(x),
                          rows,
                          H,

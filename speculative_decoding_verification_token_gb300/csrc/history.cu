@@ -46,6 +46,7 @@ __device__ __forceinline__ bool hist_row(const HistParams& p, int32_t r, int32_t
 // dependent loads and two atomics.  A single CTA (one = true) resets the status itself, which
 // saves the short call a second operation on the stream.
 __global__ void __launch_bounds__(1024) history_append_kernel(HistParams p, bool one) {
+  dependent_start();
   if (one) {
     if (threadIdx.x == 0 && p.status) *p.status = 0;
     __syncthreads();
@@ -77,6 +78,7 @@ constexpr int kResetAhead = 8;    // tokens a thread has in flight
 __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams p,
                                                                       int32_t chunks) {
   __shared__ uint32_t s_bits[kResetWords];
+  dependent_start();
   const int32_t r = blockIdx.x / chunks;
   const int32_t c = blockIdx.x % chunks;
   const int tid = threadIdx.x;
@@ -132,6 +134,77 @@ __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams
   }
 }
 
+constexpr int kPromptThreads = 512;
+constexpr int kPromptWords = 8192;   // words of prompt bits one CTA collects: 262144 tokens
+constexpr int kPromptAhead = 16;     // tokens a thread has in flight
+constexpr int kClearTokens = 16384;  // counts one CTA clears
+
+// A slot's history replaced by a prompt.  The prompt touches no counts, so clearing them and
+// collecting the tokens need no order: of each slot's CTAs the first `marks` read the tokens, once,
+// and write the bit rows whole, the others clear 64 KB of counts each.  (The kernel above takes
+// 12.8 us for 32 prompts of up to 8192 tokens and V = 129280: its CTAs each read all tokens.)
+__global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistParams p,
+                                                                        int32_t marks,
+                                                                        int32_t ctas) {
+  __shared__ uint32_t s_bits[kPromptWords];
+  dependent_start();
+  const int32_t r = blockIdx.x / ctas;
+  const int32_t c = blockIdx.x % ctas;
+  const int tid = threadIdx.x;
+  int32_t slot, n;
+  if (!hist_row(p, r, slot, n)) return;  // the whole CTA
+  int32_t twice = 0;
+  if (p.slots)
+    for (int32_t q = tid; q < p.B; q += kPromptThreads) twice |= q != r && p.slots[q] == slot;
+  if (c >= marks) {
+    if (__syncthreads_or(twice)) return;
+    const int64_t v0 = int64_t(c - marks) * kClearTokens, v1 = min(p.V, v0 + kClearTokens);
+    int32_t* cnt = p.counts + slot * p.ld_counts;
+    const int64_t full = (reinterpret_cast<uintptr_t>(cnt) & 15u) ? v0 : v1 & ~int64_t(3);
+    for (int64_t v = v0 + 4 * tid; v < full; v += 4 * kPromptThreads)
+      *reinterpret_cast<int4*>(cnt + v) = make_int4(0, 0, 0, 0);
+    for (int64_t v = full + tid; v < v1; v += kPromptThreads) cnt[v] = 0;
+    return;
+  }
+  const int32_t* row = p.tokens + r * p.ld_tokens;
+  const int64_t w0 = int64_t(c) * kPromptWords;
+  const int32_t words =
+      static_cast<int32_t>(min(int64_t(kPromptWords), (p.V + 31) / 32 - w0));
+  const int64_t v0 = w0 * 32, v1 = min(p.V, v0 + int64_t(kPromptWords) * 32);
+  int32_t x[kPromptAhead];
+  auto fetch = [&](int32_t t0) {
+#pragma unroll
+    for (int q = 0; q < kPromptAhead; ++q) {
+      const int32_t t = t0 + tid + q * kPromptThreads;
+      x[q] = t < n ? __ldg(row + t) : -1;
+    }
+  };
+  fetch(0);
+  for (int w = tid; w < words; w += kPromptThreads) s_bits[w] = 0;
+  if (__syncthreads_or(twice)) {
+    if (tid == 0) report(p.status, SV_ERR_BAD_INPUT);
+    return;
+  }
+  for (int32_t t0 = 0; t0 < n; t0 += kPromptAhead * kPromptThreads) {
+    if (t0) fetch(t0);
+#pragma unroll
+    for (int q = 0; q < kPromptAhead; ++q) {
+      if (x[q] >= p.V) report(p.status, SV_ERR_BAD_INPUT);
+      if (x[q] < v0 || x[q] >= v1) continue;
+      const uint32_t b = 1u << (x[q] & 31);
+      uint32_t* word = &s_bits[(x[q] - v0) >> 5];
+      if (!(*reinterpret_cast<volatile uint32_t*>(word) & b)) atomicOr(word, b);  // often there
+    }
+  }
+  __syncthreads();
+  uint32_t* pb = p.prompt_bits + slot * p.ld_bits + w0;
+  uint32_t* ob = p.output_bits + slot * p.ld_bits + w0;
+  for (int w = tid; w < words; w += kPromptThreads) {
+    pb[w] = s_bits[w];
+    ob[w] = 0;
+  }
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -150,22 +223,29 @@ extern "C" sv_status spec_history_append(const int32_t* tokens, int64_t ld_token
   if (V > INT32_MAX) return SV_ERR_UNSUPPORTED;
   if (B == 0 || (n == 0 && !reset)) return SV_OK;
   if ((n > 0 && !tokens) || !counts || !prompt_bits || !output_bits) return SV_ERR_INVALID;
-  const int64_t chunks = ((V + 31) / 32 + kResetWords - 1) / kResetWords;
+  const bool fill = reset && kind == SV_HISTORY_PROMPT;
+  const int64_t marks = ((V + 31) / 32 + kPromptWords - 1) / kPromptWords;
+  const int64_t chunks = fill ? marks + (V + kClearTokens - 1) / kClearTokens
+                              : ((V + 31) / 32 + kResetWords - 1) / kResetWords;
   const int64_t blocks =
       reset ? chunks * B : (int64_t(B) * n + kHistThreads - 1) / kHistThreads;
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool one = !reset && int64_t(B) * n <= 1024;
-  if (status && !one && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess)
-    return SV_ERR_CUDA;
+  if (!one) {
+    const sv_status st = reset_status(status, s);
+    if (st != SV_OK) return st;
+  }
   const HistParams p = {tokens, ld_tokens, lens, n,         slots,       B,           kind,
                         V,      n_slots,   counts, ld_counts, prompt_bits, output_bits, ld_bits,
                         status};
+  if (fill)
+    return launch_dependent(history_prompt_kernel, unsigned(blocks), kPromptThreads, 0, s, p,
+                            int32_t(marks), int32_t(chunks));
   if (reset)
-    history_reset_kernel<<<unsigned(blocks), kResetThreads, 0, s>>>(p, int32_t(chunks));
-  else if (one)
-    history_append_kernel<<<1, (B * n + 31) / 32 * 32, 0, s>>>(p, true);
-  else
-    history_append_kernel<<<unsigned(blocks), kHistThreads, 0, s>>>(p, false);
-  return launch_status(cudaGetLastError());
+    return launch_dependent(history_reset_kernel, unsigned(blocks), kResetThreads, 0, s, p,
+                            int32_t(chunks));
+  if (one)
+    return launch_dependent(history_append_kernel, 1u, unsigned(B * n + 31) / 32 * 32, 0, s, p, true);
+  return launch_dependent(history_append_kernel, unsigned(blocks), kHistThreads, 0, s, p, false);
 }

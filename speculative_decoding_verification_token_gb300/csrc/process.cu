@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   const uint32_t full = uint32_t(n_tok) * sizeof(T) & ~15u;  // bytes in whole vectors
   const int32_t n_vec = full >> 4, n_tail = n_tok - n_vec * kVec;
 
+  dependent_start();
   // ---- first loads: the request's parameters
   int32_t g = p.draft_len[r];
   const int64_t row = p.row0[r];
@@ -435,16 +436,17 @@ sv_status launch_process(ProcParams p, int32_t B, cudaStream_t s) {
   if (chunks * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
   // with one request a single CTA reports, and resets the status before it does
   p.reset_status = p.status && B == 1;
-  if (p.status && B > 1 && cudaMemsetAsync(p.status, 0, sizeof(int32_t), s) != cudaSuccess)
-    return SV_ERR_CUDA;
+  if (!p.reset_status) {
+    const sv_status st = reset_status(p.status, s);
+    if (st != SV_OK) return st;
+  }
   p.chunks = int32_t(chunks);
   const size_t smem =
       kMode == kCopy
           ? size_t(std::max(1, std::min(kProcRows, p.gmax + p.bonus_row - p.first_row))) *
                 proc_row_bytes(kMode)
           : 0;
-  process_kernel<E, kMode><<<unsigned(chunks * B), kProcThreads, smem, s>>>(p);
-  return launch_status(cudaGetLastError());
+  return launch_dependent(process_kernel<E, kMode>, unsigned(chunks * B), kProcThreads, smem, s, p);
 }
 
 template <typename E>

@@ -128,6 +128,14 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
   return old;
 }
 
+// ---- programmatic dependent launches (sv_host.h, launch_dependent) --------------------------------
+// Lets the next kernel start beside this one, then waits until the work before this one is done and
+// visible; everything a kernel shares with other work comes after it.
+__device__ __forceinline__ void dependent_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---- status word ---------------------------------------------------------------------------
 __device__ __forceinline__ void report(int32_t* status, int32_t code) {
   if (status) atomicCAS(status, 0, code);

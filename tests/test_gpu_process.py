@@ -36,7 +36,8 @@ def _history_state(rng, S, V):
 @pytest.mark.parametrize("reset", [False, True])
 @pytest.mark.parametrize("prompt", [False, True])
 @pytest.mark.parametrize("B,n,V", [(1, 1, 1), (3, 6, 31), (5, 17, 1000), (7, 2000, 16385),
-                                   (2, 33, 151936), (64, 6, 33)])
+                                   (2, 33, 151936), (64, 6, 33), (3, 9000, 40001),
+                                   (2, 500, 262145)])
 def test_history_append(sv, B, n, V, prompt, reset):
     rng = np.random.default_rng(B * 1000 + n + V)
     S = B + 2
@@ -387,6 +388,49 @@ def test_empty_mask_is_reported_by_verification(sv):
     assert torch.isneginf(t[1]).all() and torch.isfinite(t[0]).all() and torch.isfinite(t[2]).all()
     out = sv.spec_verify_token(t, d, row0, row0, ln, g, tok, 0)
     assert int(out["status"]) == sv.SV_ERR_BAD_INPUT
+
+
+def test_calls_captured_behind_memsets_and_copies(sv):
+    """Programmatic dependents whose predecessor in the captured stream is no kernel."""
+    V = 517
+    i32 = dict(dtype=torch.int32, device="cuda")
+    counts, pb, ob = torch.zeros((1, V), **i32), torch.zeros((1, 17), **i32), torch.zeros((1, 17), **i32)
+    tok, st = torch.tensor([[3, 3, 9]], **i32), torch.zeros(1, **i32)
+    src = torch.randn((1, 520), device="cuda")
+    x = torch.zeros_like(src)
+    row0, ln = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(1, **i32)
+    rep = torch.full((1,), 2.0, device="cuda")
+    h = torch.randn((5, 64), device="cuda")
+    out = torch.zeros((5, 8), device="cuda")
+    wq = sv.spec_quantize_fp4(torch.randn((8, 64), device="cuda"), 0)
+    hq = sv.spec_quantize_fp4(h, 0)
+    kw = dict(counts=counts, prompt_bits=pb, output_bits=ob, status=st)
+
+    def step():
+        counts.zero_(), ob.zero_()
+        sv.spec_history_append(tok, **kw)
+        x.copy_(src)
+        sv.spec_process_logits(x[:, :V], row0, row0, ln, 0, tok[0], repetition=rep, **kw)
+        hq["packed"].copy_(hq["packed"].clone())
+        out.zero_()
+        sv.spec_project_fp4(hq, wq, out=out, status=st)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (counts, ob, x, out)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        for t in (counts, ob, x, out):
+            t.fill_(1)
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip((counts, ob, x, out), want))
+    assert counts[0, 3] == 2 and x[0, 3] == (src[0, 3] / 2 if src[0, 3] > 0 else src[0, 3] * 2)
 
 
 def test_process_and_history_in_a_graph(sv):
