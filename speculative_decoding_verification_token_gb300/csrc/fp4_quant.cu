@@ -90,11 +90,14 @@ struct In<bf16_tag> {
   }
 };
 
+// How far vectors may be trusted: 0, rows on any element boundary; 1, rows 16-byte aligned; 2, and
+// H a multiple of 256, so that no vector needs a check.
+//
 // Elements 8 j .. 8 j + 7 of a row, zeros past H.
-template <typename E, bool kVec>
+template <typename E, int kAlign>
 __device__ __forceinline__ void load_vec(const uint8_t* row, int64_t j, int64_t H, uint32_t* w) {
   const int64_t e0 = j * 8;
-  if (kVec && e0 + 8 <= H)
+  if (kAlign == 2 || (kAlign == 1 && e0 + 8 <= H))
     In<E>::load(row + e0 * In<E>::kBytes, w);
   else
     In<E>::load_some(row + e0 * In<E>::kBytes, static_cast<int>(min(int64_t(8), H - e0)), w);
@@ -165,45 +168,64 @@ __device__ __forceinline__ uint32_t scale_code(float a) {
   }
 }
 
-// Writes the codes of elements 8 j .. 8 j + 7 and the values they stand for.
-template <bool kVec>
-__device__ __forceinline__ void store_vec(const QuantParams& p, int64_t r, int64_t j,
-                                          const float* t, float S) {
-  if (j * 4 >= p.row_bytes) return;  // past the packed row's padding
-  const uint32_t w = fp4x8(t);
-  *reinterpret_cast<uint32_t*>(p.packed + r * p.row_bytes + j * 4) = w;
-  if (!p.values || j * 8 >= p.H) return;
+// The values that eight codes stand for, as bf16 pairs (exact).
+__device__ __forceinline__ uint4 fp4x8_bf16(uint32_t codes, float S) {
   float f[8];
-  fp4x8_values(w, f);
+  fp4x8_values(codes, f);
   uint32_t h[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const float2 v = mul2(make_float2(f[2 * q], f[2 * q + 1]), splat2(S));
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);  // exact
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
     h[q] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  uint16_t* vd = p.values + r * p.ldv + j * 8;
-  if (kVec && j * 8 + 8 <= p.H) {
-    *reinterpret_cast<uint4*>(vd) = make_uint4(h[0], h[1], h[2], h[3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (j * 8 + q < p.H) vd[q] = static_cast<uint16_t>(h[q >> 1] >> (16 * (q & 1)));
-  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// Four blocks' scale bytes of row r (group gr) in one store.
-__device__ __forceinline__ void store_scales(const QuantParams& p, int64_t r, int64_t gr,
-                                             uint32_t four) {
-  *reinterpret_cast<uint32_t*>(p.scales + (size_t(r >> 7) * p.groups + size_t(gr)) * 512 +
-                               (r & 31) * 16 + ((r >> 5) & 3) * 4) = four;
+// Where a lane's vectors of one row go: vector j0 of the row, later ones at multiples of 32 from it.
+struct RowOut {
+  uint8_t* packed;
+  uint8_t* values;  // null: not asked for
+  uint8_t* scales;  // of the group that vector j0 lies in (kPerGroup vectors to a group)
+};
+
+template <int kPerGroup>
+__device__ __forceinline__ RowOut row_out(const QuantParams& p, int64_t r, int64_t j0) {
+  RowOut o;
+  o.packed = p.packed + r * p.row_bytes + j0 * 4;
+  o.values = p.values ? reinterpret_cast<uint8_t*>(p.values + r * p.ldv + j0 * 8) : nullptr;
+  o.scales = p.scales + (size_t(r >> 7) * p.groups + size_t(j0) / kPerGroup) * 512 + (r & 31) * 16 +
+             ((r >> 5) & 3) * 4;
+  return o;
+}
+
+// Codes and values of the vector `ahead` spans of 32 vectors behind the row's first; `left` elements
+// of the row from it on (kAlign 2: no end in sight), `room` bytes of the packed row.
+template <int kAlign>
+__device__ __forceinline__ void store_vec(const RowOut& o, int64_t ahead, const float* t, float S,
+                                          int64_t left, int64_t room) {
+  if (kAlign < 2 && room <= 0) return;  // past the packed row's padding
+  const uint32_t w = fp4x8(t);
+  *reinterpret_cast<uint32_t*>(o.packed + ahead * 128) = w;
+  if (!o.values || (kAlign < 2 && left <= 0)) return;
+  const uint4 h = fp4x8_bf16(w, S);
+  uint8_t* vd = o.values + ahead * 512;
+  if (kAlign == 2 || (kAlign == 1 && left >= 8)) {
+    *reinterpret_cast<uint4*>(vd) = h;
+  } else {
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < left)
+        reinterpret_cast<uint16_t*>(vd)[q] = static_cast<uint16_t>(hw[q >> 1] >> (16 * (q & 1)));
+  }
 }
 
 constexpr int kQuantThreads = 256;
 
 // Blocks of 32: a warp takes kN spans of 256 elements (two scale groups) of one row; the padding
 // rows of the last scale tile get scales of zero.
-template <typename E, bool kVec, int kN>
+template <typename E, int kAlign, int kN>
 __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p, int32_t spans) {
   dependent_start();
   const int lane = threadIdx.x & 31;
@@ -212,19 +234,21 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
   const int64_t r = warp / per_row;
   const int32_t s0 = static_cast<int32_t>(warp % per_row) * kN;
   if (r >= ((p.rows + 127) & ~int64_t(127))) return;
+  const bool real = r < p.rows;
+  const int64_t j0 = int64_t(s0) * 32 + lane;
   const uint8_t* row = p.x + r * p.ldx * In<E>::kBytes;
   uint32_t w[kN][In<E>::kWords];
 #pragma unroll
   for (int q = 0; q < kN; ++q) {
 #pragma unroll
     for (int i = 0; i < In<E>::kWords; ++i) w[q][i] = 0;
-    const int64_t j = int64_t(s0 + q) * 32 + lane;
-    if (r < p.rows && j * 8 < p.H) load_vec<E, kVec>(row, j, p.H, w[q]);
+    const int64_t j = j0 + q * 32;
+    if (real && s0 + q < spans && (kAlign == 2 || j * 8 < p.H)) load_vec<E, kAlign>(row, j, p.H, w[q]);
   }
+  const RowOut o = row_out<16>(p, r, j0);
 #pragma unroll
   for (int q = 0; q < kN; ++q) {
     if (s0 + q >= spans) break;
-    const int64_t j = int64_t(s0 + q) * 32 + lane;
     uint32_t m = In<E>::amax(w[q]);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -234,8 +258,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
     uint32_t four = (bad ? 0xFFu : uint32_t(e)) << (8 * ((lane >> 2) & 3));
     four |= __shfl_xor_sync(0xffffffffu, four, 4);
     four |= __shfl_xor_sync(0xffffffffu, four, 8);
-    if ((lane & 15) == 0) store_scales(p, r, (s0 + q) * 2 + (lane >> 4), four);
-    if (r >= p.rows) continue;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(o.scales + q * 1024) = four;
+    if (!real) continue;
     if (bad) report(p.status, SV_ERR_BAD_INPUT);
     const float S = bad ? __uint_as_float(0x7FC00000u)  // the scale 0xFF stands for NaN
                         : e ? __uint_as_float(uint32_t(e) << 23) : __uint_as_float(1u << 22);
@@ -243,31 +267,33 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = bad ? 0.f : In<E>::get(w[q], i) * inv;
-    store_vec<kVec>(p, r, j, t, S);
+    const int64_t j = j0 + q * 32;
+    store_vec<kAlign>(o, q, t, S, p.H - j * 8, p.row_bytes - j * 4);
   }
 }
 
 // Blocks of 16 under a row scale: `warps` warps of a CTA per row, each lane with kN vectors of it in
 // registers between the row's maximum and the codes (kN = 0: any number, read twice).
-template <typename E, bool kVec, int kN, int kThreads>
+template <typename E, int kAlign, int kN, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
-    quant_e4m3_kernel(QuantParams p, int32_t spans,
-                                                         int32_t warps) {
+    quant_e4m3_kernel(QuantParams p, int32_t spans, int32_t warps) {
   __shared__ uint32_t s_max[16];
   dependent_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t rows_here = (blockDim.x >> 5) / warps;
+  const int32_t rows_here = (kThreads >> 5) / warps;
   const int64_t r = int64_t(blockIdx.x) * rows_here + warp / warps;
   const int32_t mine = warp % warps;
   const bool real = r < p.rows, tile = r < ((p.rows + 127) & ~int64_t(127));
+  const int64_t j0 = int64_t(mine) * 32 + lane;
   const uint8_t* row = p.x + r * p.ldx * In<E>::kBytes;
   constexpr int kHold = kN ? kN : 1;
   uint32_t w[kHold][In<E>::kWords], am[kHold];
   auto fetch = [&](int32_t q, uint32_t* x) {
 #pragma unroll
     for (int i = 0; i < In<E>::kWords; ++i) x[i] = 0;
-    const int64_t j = (int64_t(q) * warps + mine) * 32 + lane;
-    if (real && j * 8 < p.H) load_vec<E, kVec>(row, j, p.H, x);
+    const int64_t j = j0 + int64_t(q) * warps * 32;
+    if (real && (kAlign == 2 ? q * warps + mine < spans : j * 8 < p.H))
+      load_vec<E, kAlign>(row, j, p.H, x);
   };
   uint32_t m = 0;
   if constexpr (kN > 0) {
@@ -288,6 +314,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
     for (int i = 0; i < warps; ++i) m = max(m, s_max[warp - mine + i]);
   }
   if (!tile) return;
+  const RowOut o = row_out<8>(p, r, j0);
+  if (!real) {  // a padding row of the last scale tile
+    for (int32_t q = 0; q * warps + mine < spans; ++q)
+      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(o.scales + int64_t(q) * warps * 2048) = 0;
+    return;
+  }
   const bool bad = m >= kInfBits;
   // 6 * 448 = 1.3125 * 2^11: the smallest k with m <= 1.3125 * 2^(11 + k)
   int32_t k2 = 0;
@@ -297,40 +329,38 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
   }
   const float g = __uint_as_float(uint32_t(k2 + 127) << 23);
   const float ginv = __uint_as_float(uint32_t(127 - k2) << 23);
-  if (real && mine == 0 && lane == 0) {
+  if (mine == 0 && lane == 0) {
     p.row_scales[r] = g;
     if (bad) report(p.status, SV_ERR_BAD_INPUT);
   }
+  const uint32_t byte = 8 * ((lane >> 1) & 3);
   auto emit = [&](int32_t q, const uint32_t* x, uint32_t amax) {
-    const int32_t span = q * warps + mine;
-    if (span >= spans) return;
-    const int64_t j = int64_t(span) * 32 + lane;
+    if (q * warps + mine >= spans) return;
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     const uint32_t code = bad ? 0x7Fu : scale_code<E>(__uint_as_float(amax) * ginv);
-    uint32_t four = (real ? code : 0u) << (8 * ((lane >> 1) & 3));
+    uint32_t four = code << byte;
     four |= __shfl_xor_sync(0xffffffffu, four, 2);
     four |= __shfl_xor_sync(0xffffffffu, four, 4);
-    if ((lane & 7) == 0) store_scales(p, r, span * 4 + (lane >> 3), four);
-    if (!real) return;
+    if ((lane & 7) == 0)
+      *reinterpret_cast<uint32_t*>(o.scales + int64_t(q) * warps * 2048) = four;
     const float s = e4m3_value(code);
     const float S = bad ? __uint_as_float(0x7FC00000u) : s * g;
+    const float rs = code ? rcp_approx(s) : 0.f;  // a block of zero scale has codes of zero
     float t[8];
-    if (bad || code == 0) {
+    if (bad) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = 0.f;
+    } else if (k2 > -110) {
+      fp4_quotients<E>(x, S, rs * ginv, t);
     } else {
-      // 1 / S; at the smallest scales it overflows: there both are taken 2^60 larger (x and S stay
-      // exact, they are far below the largest number)
-      const float rs = rcp_approx(s);
-      if (k2 > -110) {
-        fp4_quotients<E>(x, S, rs * ginv, t);
-      } else {
-        uint32_t y[In<E>::kWords];
-        scale_up<E>(x, y);
-        fp4_quotients<E>(y, S * 0x1p60f, rs * (ginv * 0x1p-60f), t);
-      }
+      // 1 / S would overflow at the smallest scales: both are taken 2^60 larger (x and S stay exact,
+      // they are far below the largest number)
+      uint32_t y[In<E>::kWords];
+      scale_up<E>(x, y);
+      fp4_quotients<E>(y, S * 0x1p60f, rs * (ginv * 0x1p-60f), t);
     }
-    store_vec<kVec>(p, r, j, t, S);
+    const int64_t j = j0 + int64_t(q) * warps * 32;
+    store_vec<kAlign>(o, int64_t(q) * warps, t, S, p.H - j * 8, p.row_bytes - j * 4);
   };
   if constexpr (kN > 0) {
 #pragma unroll
@@ -343,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
   }
 }
 
-template <typename E, bool kVec>
+template <typename E, int kAlign>
 sv_status launch_e8m0(const QuantParams& p, cudaStream_t s) {
   const int32_t spans = int32_t((p.H + 255) / 256);
   const int64_t padded = (p.rows + 127) / 128 * 128;
@@ -352,13 +382,13 @@ sv_status launch_e8m0(const QuantParams& p, cudaStream_t s) {
   const int64_t warps = padded * (two ? (spans + 1) / 2 : spans);
   const int64_t blocks = (warps * 32 + kQuantThreads - 1) / kQuantThreads;
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  return launch_dependent(two ? quant_e8m0_kernel<E, kVec, 2> : quant_e8m0_kernel<E, kVec, 1>,
+  return launch_dependent(two ? quant_e8m0_kernel<E, kAlign, 2> : quant_e8m0_kernel<E, kAlign, 1>,
                           unsigned(blocks), kQuantThreads, 0, s, p, spans);
 }
 
-template <typename E, bool kVec>
+template <typename E, int kAlign>
 sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
-  constexpr int kMost = In<E>::kFew ? 5 : 3;  // vectors a lane holds
+  constexpr int kMost = kAlign == 0 ? 1 : In<E>::kFew ? 5 : 3;  // vectors a lane holds
   const int32_t spans = int32_t((p.H + 255) / 256);
   const int64_t padded = (p.rows + 127) / 128 * 128;
   // the fewest warps per row that hold it; more where the rows alone would leave the GPU idle
@@ -373,18 +403,27 @@ sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
     return launch_dependent(threads == 128 ? narrow : wide, unsigned(blocks), unsigned(threads), 0, s,
                             p, spans, warps);
   };
-  if (hold == 1) return go(quant_e4m3_kernel<E, kVec, 1, 128>, quant_e4m3_kernel<E, kVec, 1, 512>);
-  if (hold == 2) return go(quant_e4m3_kernel<E, kVec, 2, 128>, quant_e4m3_kernel<E, kVec, 2, 512>);
-  if (hold <= kMost)
-    return go(quant_e4m3_kernel<E, kVec, kMost, 128>, quant_e4m3_kernel<E, kVec, kMost, 512>);
-  return go(quant_e4m3_kernel<E, kVec, 0, 128>, quant_e4m3_kernel<E, kVec, 0, 512>);
+  if (hold == 1)
+    return go(quant_e4m3_kernel<E, kAlign, 1, 128>, quant_e4m3_kernel<E, kAlign, 1, 512>);
+  if constexpr (kMost > 1) {
+    if (hold == 2)
+      return go(quant_e4m3_kernel<E, kAlign, 2, 128>, quant_e4m3_kernel<E, kAlign, 2, 512>);
+    if (hold <= kMost)
+      return go(quant_e4m3_kernel<E, kAlign, kMost, 128>, quant_e4m3_kernel<E, kAlign, kMost, 512>);
+  }
+  return go(quant_e4m3_kernel<E, kAlign, 0, 128>, quant_e4m3_kernel<E, kAlign, 0, 512>);
 }
 
 template <typename E>
 sv_status launch_quant(const QuantParams& p, int32_t format, bool vec, cudaStream_t s) {
+  const int align = !vec ? 0 : p.H % 256 ? 1 : 2;
   if (format == SV_FP4_E8M0_32)
-    return vec ? launch_e8m0<E, true>(p, s) : launch_e8m0<E, false>(p, s);
-  return vec ? launch_e4m3<E, true>(p, s) : launch_e4m3<E, false>(p, s);
+    return align == 0   ? launch_e8m0<E, 0>(p, s)
+           : align == 1 ? launch_e8m0<E, 1>(p, s)
+                        : launch_e8m0<E, 2>(p, s);
+  return align == 0   ? launch_e4m3<E, 0>(p, s)
+         : align == 1 ? launch_e4m3<E, 1>(p, s)
+                      : launch_e4m3<E, 2>(p, s);
 }
 
 }  // namespace
