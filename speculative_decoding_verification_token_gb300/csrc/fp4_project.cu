@@ -96,6 +96,22 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* ma
       : "memory");
 }
 
+// Tiles towards L2 ahead of their loads.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // Arrive once on `bar` (the same offset in both CTAs) when all tcgen05 work issued so far is done.
 __device__ __forceinline__ void pair_commit(uint64_t* bar) {
   asm volatile(
@@ -286,8 +302,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  // programmatic dependent of the work before it: all above ran beside that work's end, and nothing
-  // it wrote (or that still reads the logits) is touched before this
+  // Programmatic dependent of the work before it: all above ran beside that work's end, and nothing
+  // it wrote (or that still reads the logits) is touched before dependent_start.  W's first tiles
+  // are on their way to L2 meanwhile; should that work still write W, its writes meet them there.
+  if (warp == 0 && elect_one()) {
+    const int32_t vt = (pair / p.n_nt) * 2 + int32_t(rank);
+    for (int32_t kb = 0; kb < min(stages, p.kblocks); ++kb) {
+      prefetch_2d(&map_w, kb * 128, vt * kPjRows);
+      prefetch_3d(&map_ws, 0, kb * kGroups, vt);
+    }
+  }
+  __syncwarp();
   dependent_start();
   // the only report is of a wait that ran out, a second after the start at the earliest
   if (blockIdx.x == 0 && tid == 0 && p.status) *p.status = 0;
