@@ -183,6 +183,56 @@ def test_project_same_tensor_and_reruns(sv):
         assert torch.equal(sv.spec_project_fp4(q, q, dtype=torch.float32), y)
 
 
+def test_project_right_behind_a_new_w(sv):
+    """W quantised and multiplied back to back, ever another one, without a wait in between: the
+    product must not see the W before."""
+    g = torch.Generator("cuda").manual_seed(2)
+    V, H = 20000, 1024
+    xs = torch.randn((40, H), generator=g, device="cuda").to(torch.bfloat16)
+    w = [torch.randn((V, H), generator=g, device="cuda").to(torch.bfloat16) for _ in range(4)]
+    x = sv.spec_quantize_fp4(xs, 0)
+    alone = []
+    for t in w:
+        q = sv.spec_quantize_fp4(t, 0)
+        torch.cuda.synchronize()
+        alone.append(sv.spec_project_fp4(x, q, dtype=torch.float32))
+        torch.cuda.synchronize()
+    packed, scales = torch.empty_like(q["packed"]), torch.empty_like(q["scales"])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.empty_like(alone[0]) for _ in range(40)]
+    for k, o in enumerate(outs):
+        q = sv.spec_quantize_fp4(w[k % 4], 0, packed=packed, scales=scales, status=st)
+        sv.spec_project_fp4(x, q, out=o, status=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, alone[k % 4]) for k, o in enumerate(outs))
+
+
+def test_offsets_past_32_bits(sv):
+    """Hidden rows, packed rows and logits that lie more than 4 GiB into their tensors."""
+    g = torch.Generator("cuda").manual_seed(6)
+    x = torch.zeros((140000, 16384), dtype=torch.bfloat16, device="cuda")  # 4.6 GB
+    x[-3:] = torch.randn((3, 16384), generator=g, device="cuda")
+    for fmt in (0, 1):
+        q = sv.spec_quantize_fp4(x, fmt)
+        part = sv.spec_quantize_fp4(x[-96:].contiguous(), fmt)  # rows 139904 .. 139999, a whole tile
+        assert torch.equal(q["packed"][-96:], part["packed"])
+        assert 139904 % 128 == 0 and torch.equal(q["scales"][-part["scales"].numel():], part["scales"])
+        assert q["packed"][:-3].count_nonzero() == 0
+        del q
+    del x
+    M, V, H = 17000, 131072, 32
+    h = sv.spec_quantize_fp4(torch.randn((M, H), generator=g, device="cuda"), 0)
+    w = sv.spec_quantize_fp4(torch.randn((V, H), generator=g, device="cuda"), 0)
+    y = sv.spec_project_fp4(h, w)  # 4.5 GB
+    some = torch.tensor([0, 255, 256, 9000, 16383, 16384, 16999], device="cuda")
+    few = sv.spec_quantize_fp4(torch.zeros((7, H), device="cuda"), 0)
+    few["packed"].copy_(h["packed"][some])
+    sc, _ = plain.scale_bytes(h["scales"].cpu().numpy(), M, 1)
+    at = torch.arange(7) * 16
+    few["scales"][at.cuda()] = torch.from_numpy(sc[some.cpu().numpy(), 0]).cuda()
+    assert torch.equal(y[some], sv.spec_project_fp4(few, w))
+
+
 def test_chain_to_verification(sv, orc):
     """The operators as they are used: hidden rows and W quantised, logits from the product, the
     history's penalties and masks in place on target and draft rows, verification, and the verified

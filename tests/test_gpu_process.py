@@ -293,6 +293,54 @@ def test_process_without_penalties(sv):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+def test_process_everything_seen(sv, in_place):
+    """Every token of the vocabulary in the history and in the bias list: lists as long as a chunk."""
+    c = _case(21, 2, 3, 9000, torch.bfloat16, 9000, True, ragged=False)
+    c["counts"][:] = 1 + np.arange(9000) % 5
+    c["output"][:] = True
+    start = np.array([0, 9000, 18000], np.int32)
+    c["bias"] = (start, np.tile(np.arange(9000, dtype=np.int32), 2),
+                 np.linspace(-2, 2, 18000).astype(np.float32))
+    _run(sv, c, in_place)
+
+
+def test_same_history_for_several_requests(sv):
+    """Requests may share a slot; its history is only read."""
+    c = _case(22, 5, 2, 1500, torch.float32)
+    c["slots"][:] = 3
+    _run(sv, c, True)
+
+
+def test_offsets_past_32_bits(sv):
+    """Rows, counts and tokens that lie more than 4 GiB into their tensors."""
+    V, rows, S = 131072, 17000, 8400
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.zeros((rows, V), dtype=torch.bfloat16, device="cuda")  # 4.5 GB
+    counts = torch.zeros((S, V), **i32)                              # 4.4 GB
+    pb, ob = torch.zeros((S, V // 32), **i32), torch.zeros((S, V // 32), **i32)
+    slots = torch.tensor([S - 1], **i32)
+    tok = torch.tensor([[V - 1, 7, V - 1]], **i32)
+    st = sv.spec_history_append(tok, counts, pb, ob, slots=slots)
+    assert int(st) == 0 and counts[S - 1, V - 1] == 2 and counts[S - 1, 7] == 1
+    assert counts[:S - 1].count_nonzero() == 0
+    x[rows - 1] = 4.0
+    kw = dict(slots=slots, counts=counts, prompt_bits=pb, output_bits=ob,
+              frequency=torch.ones(1, device="cuda"))
+    row0 = torch.tensor([rows - 1], device="cuda")
+    zero = torch.zeros(1, **i32)
+    out = torch.zeros_like(x)
+    sv.spec_process_logits(x, row0, None, zero, 0, None, out=out, **kw)
+    sv.spec_process_logits(x, row0, None, zero, 0, None, **kw)
+    want = torch.full((V,), 4.0, dtype=torch.bfloat16, device="cuda")
+    want[V - 1], want[7] = 2.0, 3.0
+    assert torch.equal(x[rows - 1], want) and torch.equal(out[rows - 1], want)
+    assert x[:rows - 1].count_nonzero() == 0 and out[:rows - 1].count_nonzero() == 0
+    st = sv.spec_history_append(tok, counts, pb, ob, slots=slots, prompt=True, reset=True)
+    assert int(st) == 0 and counts[S - 1].count_nonzero() == 0 and ob.count_nonzero() == 0
+    assert pb[S - 1, 0] == 1 << 7 and pb[S - 1, V // 32 - 1] == -2**31
+
+
 def test_single_row_of_odd_width(sv):
     """A lone row's stride says nothing: [1, 1001] is as good as a padded row."""
     x = torch.randn((1, 1001), device="cuda")
