@@ -48,10 +48,7 @@ struct In<float> {
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
-  __device__ static __forceinline__ void load_some(const uint8_t* p, int n, uint32_t* w) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = j < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + j) : 0;
-  }
+  using Raw = uint32_t;
   // Largest magnitude as a binary32 pattern: a NaN exceeds infinity, which exceeds finite values.
   __device__ static __forceinline__ uint32_t amax(const uint32_t* w) {
     uint32_t m = 0;
@@ -72,14 +69,7 @@ struct In<bf16_tag> {
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
   }
-  __device__ static __forceinline__ void load_some(const uint8_t* p, int n, uint32_t* w) {
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = 2 * j < n ? __ldg(h + 2 * j) : 0;
-      if (2 * j + 1 < n) w[j] |= uint32_t(__ldg(h + 2 * j + 1)) << 16;
-    }
-  }
+  using Raw = uint16_t;
   __device__ static __forceinline__ uint32_t amax(const uint32_t* w) {
     const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
                                 __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
@@ -92,15 +82,63 @@ struct In<bf16_tag> {
 
 // How far vectors may be trusted: 0, rows on any element boundary; 1, rows 16-byte aligned; 2, and
 // H a multiple of 256, so that no vector needs a check.
-//
-// Elements 8 j .. 8 j + 7 of a row, zeros past H.
-template <typename E, int kAlign>
-__device__ __forceinline__ void load_vec(const uint8_t* row, int64_t j, int64_t H, uint32_t* w) {
-  const int64_t e0 = j * 8;
-  if (kAlign == 2 || (kAlign == 1 && e0 + 8 <= H))
-    In<E>::load(row + e0 * In<E>::kBytes, w);
-  else
-    In<E>::load_some(row + e0 * In<E>::kBytes, static_cast<int>(min(int64_t(8), H - e0)), w);
+
+// One warp loads kN spans of 256 elements (span[q] < 0: none) of a row, each lane 8 neighbouring
+// elements of every span, zeros past H.  Rows off the 16-byte boundary (kAlign 0) come element by
+// element, neighbours to neighbouring lanes, and change hands in shared memory (`stage`, kN spans):
+// five times the rate of lanes that load their own 8 (5000 x 8191 FIGURE).
+template <typename E, int kAlign, int kN, typename Span>
+__device__ __forceinline__ void load_spans(const uint8_t* row, int64_t H, int lane, Span&& span,
+                                           typename In<E>::Raw* stage,
+                                           uint32_t (*w)[In<E>::kWords]) {
+  using Raw = typename In<E>::Raw;
+  if constexpr (kAlign == 0) {
+    Raw raw[kN][8];
+#pragma unroll
+    for (int q = 0; q < kN; ++q) {
+      const int64_t e0 = span(q) * 256;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t e = e0 + i * 32 + lane;
+        raw[q][i] = e0 >= 0 && e < H ? __ldg(reinterpret_cast<const Raw*>(row) + e) : Raw(0);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < kN; ++q)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) stage[q * 256 + i * 32 + lane] = raw[q][i];
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < kN; ++q)
+#pragma unroll
+      for (int i = 0; i < In<E>::kWords; i += 4) {
+        const uint4 v = *(reinterpret_cast<const uint4*>(stage + q * 256 + lane * 8) + i / 4);
+        w[q][i] = v.x, w[q][i + 1] = v.y, w[q][i + 2] = v.z, w[q][i + 3] = v.w;
+      }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) {
+      const int64_t e0 = span(q) * 256 + lane * 8;
+      if (e0 >= 0 && (kAlign == 2 || e0 + 8 <= H)) {
+        In<E>::load(row + e0 * In<E>::kBytes, w[q]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < In<E>::kWords; ++i) w[q][i] = 0;
+        if (e0 >= 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (e0 + j >= H) continue;
+            const uint32_t x = __ldg(reinterpret_cast<const Raw*>(row) + e0 + j);
+            if constexpr (sizeof(Raw) == 4)
+              w[q][j] = x;
+            else
+              w[q][j >> 1] |= x << (16 * (j & 1));
+          }
+        }
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -200,17 +238,26 @@ __device__ __forceinline__ RowOut row_out(const QuantParams& p, int64_t r, int64
 }
 
 // Codes and values of the vector `ahead` spans of 32 vectors behind the row's first; `left` elements
-// of the row from it on (kAlign 2: no end in sight), `room` bytes of the packed row.
+// of the row from it on, `room` bytes of the packed row (kAlign 2: no end in sight).  The whole warp
+// takes part; with kAlign 0 values change hands in `stage` as elements do when they are loaded.
 template <int kAlign>
 __device__ __forceinline__ void store_vec(const RowOut& o, int64_t ahead, const float* t, float S,
-                                          int64_t left, int64_t room) {
-  if (kAlign < 2 && room <= 0) return;  // past the packed row's padding
+                                          int64_t left, int64_t room, int lane, uint16_t* stage) {
   const uint32_t w = fp4x8(t);
-  *reinterpret_cast<uint32_t*>(o.packed + ahead * 128) = w;
-  if (!o.values || (kAlign < 2 && left <= 0)) return;
+  if (kAlign == 2 || room > 0) *reinterpret_cast<uint32_t*>(o.packed + ahead * 128) = w;
+  if (!o.values) return;
   const uint4 h = fp4x8_bf16(w, S);
   uint8_t* vd = o.values + ahead * 512;
-  if (kAlign == 2 || (kAlign == 1 && left >= 8)) {
+  if constexpr (kAlign == 0) {
+    __syncwarp();
+    *reinterpret_cast<uint4*>(stage + lane * 8) = h;
+    __syncwarp();
+    uint16_t* const first = reinterpret_cast<uint16_t*>(vd) - lane * 8;  // the span's first element
+    const int64_t there = left + lane * 8;                               // elements from it on
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 32 + lane < there) first[i * 32 + lane] = stage[i * 32 + lane];
+  } else if (kAlign == 2 || left >= 8) {
     *reinterpret_cast<uint4*>(vd) = h;
   } else {
     const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
@@ -236,15 +283,13 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
   if (r >= ((p.rows + 127) & ~int64_t(127))) return;
   const bool real = r < p.rows;
   const int64_t j0 = int64_t(s0) * 32 + lane;
-  const uint8_t* row = p.x + r * p.ldx * In<E>::kBytes;
+  __shared__ __align__(16) typename In<E>::Raw
+      s_stage[kAlign == 0 ? kQuantThreads / 32 : 1][kAlign == 0 ? kN * 256 : 8];
+  auto* const stage = s_stage[kAlign == 0 ? threadIdx.x >> 5 : 0];
   uint32_t w[kN][In<E>::kWords];
-#pragma unroll
-  for (int q = 0; q < kN; ++q) {
-#pragma unroll
-    for (int i = 0; i < In<E>::kWords; ++i) w[q][i] = 0;
-    const int64_t j = j0 + q * 32;
-    if (real && s0 + q < spans && (kAlign == 2 || j * 8 < p.H)) load_vec<E, kAlign>(row, j, p.H, w[q]);
-  }
+  load_spans<E, kAlign, kN>(
+      p.x + r * p.ldx * In<E>::kBytes, p.H, lane,
+      [&](int q) { return real && s0 + q < spans ? int64_t(s0 + q) : int64_t(-1); }, stage, w);
   const RowOut o = row_out<16>(p, r, j0);
 #pragma unroll
   for (int q = 0; q < kN; ++q) {
@@ -268,7 +313,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = bad ? 0.f : In<E>::get(w[q], i) * inv;
     const int64_t j = j0 + q * 32;
-    store_vec<kAlign>(o, q, t, S, p.H - j * 8, p.row_bytes - j * 4);
+    store_vec<kAlign>(o, q, t, S, p.H - j * 8, p.row_bytes - j * 4, lane,
+                      reinterpret_cast<uint16_t*>(stage));
   }
 }
 
@@ -287,23 +333,27 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
   const int64_t j0 = int64_t(mine) * 32 + lane;
   const uint8_t* row = p.x + r * p.ldx * In<E>::kBytes;
   constexpr int kHold = kN ? kN : 1;
+  __shared__ __align__(16) typename In<E>::Raw
+      s_stage[kAlign == 0 ? kThreads / 32 : 1][kAlign == 0 ? kHold * 256 : 8];
+  auto* const stage = s_stage[kAlign == 0 ? warp : 0];
   uint32_t w[kHold][In<E>::kWords], am[kHold];
-  auto fetch = [&](int32_t q, uint32_t* x) {
-#pragma unroll
-    for (int i = 0; i < In<E>::kWords; ++i) x[i] = 0;
-    const int64_t j = j0 + int64_t(q) * warps * 32;
-    if (real && (kAlign == 2 ? q * warps + mine < spans : j * 8 < p.H))
-      load_vec<E, kAlign>(row, j, p.H, x);
+  auto fetch = [&](int32_t q0) {  // kHold spans from q0 on
+    load_spans<E, kAlign, kHold>(
+        row, p.H, lane,
+        [&](int q) {
+          const int32_t span = (q0 + q) * warps + mine;
+          return real && span < spans ? int64_t(span) : int64_t(-1);
+        },
+        stage, w);
   };
   uint32_t m = 0;
   if constexpr (kN > 0) {
-#pragma unroll
-    for (int q = 0; q < kN; ++q) fetch(q, w[q]);
+    fetch(0);
 #pragma unroll
     for (int q = 0; q < kN; ++q) m = max(m, am[q] = In<E>::amax(w[q]));
   } else {
     for (int32_t q = 0; q * warps + mine < spans; ++q) {
-      fetch(q, w[0]);
+      fetch(q);
       m = max(m, In<E>::amax(w[0]));
     }
   }
@@ -360,14 +410,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
       fp4_quotients<E>(y, S * 0x1p60f, rs * (ginv * 0x1p-60f), t);
     }
     const int64_t j = j0 + int64_t(q) * warps * 32;
-    store_vec<kAlign>(o, int64_t(q) * warps, t, S, p.H - j * 8, p.row_bytes - j * 4);
+    store_vec<kAlign>(o, int64_t(q) * warps, t, S, p.H - j * 8, p.row_bytes - j * 4, lane,
+                      reinterpret_cast<uint16_t*>(stage));
   };
   if constexpr (kN > 0) {
 #pragma unroll
     for (int q = 0; q < kN; ++q) emit(q, w[q], am[q]);
   } else {
     for (int32_t q = 0; q * warps + mine < spans; ++q) {
-      fetch(q, w[0]);
+      fetch(q);
       emit(q, w[0], In<E>::amax(w[0]));
     }
   }
@@ -388,7 +439,7 @@ sv_status launch_e8m0(const QuantParams& p, cudaStream_t s) {
 
 template <typename E, int kAlign>
 sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
-  constexpr int kMost = kAlign == 0 ? 1 : In<E>::kFew ? 5 : 3;  // vectors a lane holds
+  constexpr int kMost = kAlign == 0 ? 2 : In<E>::kFew ? 5 : 3;  // vectors a lane holds
   const int32_t spans = int32_t((p.H + 255) / 256);
   const int64_t padded = (p.rows + 127) / 128 * 128;
   // the fewest warps per row that hold it; more where the rows alone would leave the GPU idle
@@ -405,12 +456,10 @@ sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
   };
   if (hold == 1)
     return go(quant_e4m3_kernel<E, kAlign, 1, 128>, quant_e4m3_kernel<E, kAlign, 1, 512>);
-  if constexpr (kMost > 1) {
-    if (hold == 2)
-      return go(quant_e4m3_kernel<E, kAlign, 2, 128>, quant_e4m3_kernel<E, kAlign, 2, 512>);
-    if (hold <= kMost)
-      return go(quant_e4m3_kernel<E, kAlign, kMost, 128>, quant_e4m3_kernel<E, kAlign, kMost, 512>);
-  }
+  if (hold == 2)
+    return go(quant_e4m3_kernel<E, kAlign, 2, 128>, quant_e4m3_kernel<E, kAlign, 2, 512>);
+  if (hold <= kMost)
+    return go(quant_e4m3_kernel<E, kAlign, kMost, 128>, quant_e4m3_kernel<E, kAlign, kMost, 512>);
   return go(quant_e4m3_kernel<E, kAlign, 0, 128>, quant_e4m3_kernel<E, kAlign, 0, 512>);
 }
 

@@ -29,7 +29,8 @@ struct ProcParams {
   const int32_t* draft_len;
   int32_t gmax, first_row, bonus_row;
   const int32_t* draft_tokens;
-  int32_t chunks;
+  int32_t chunks, splits;  // CTAs per request: chunks of the row times groups of rows
+  int32_t group_rows;
   const int32_t* slots;
   int32_t n_slots;
   const int32_t* counts;
@@ -142,15 +143,17 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   extern __shared__ __align__(128) uint8_t s_rows[];  // row parts, out of place
   __shared__ uint32_t s_mask[kMode == kSparse ? 1 : kProcRows][kWords];
   __shared__ uint16_t s_off[kChunk];
-  __shared__ uint32_t s_touch[kWords], s_prompt[kWords], s_out[kWords], s_bbits[kWords];
+  __shared__ uint32_t s_touch[kWords], s_prompt[kWords], s_out[kWords], s_bbits[kWords],
+      s_drafted[kWords];
   __shared__ int32_t s_tok[SV_MAX_DRAFT_LEN], s_pos[SV_MAX_DRAFT_LEN];
   __shared__ int32_t s_mrow[SV_MAX_DRAFT_LEN + 1];
   __shared__ int32_t s_n, s_nd;
   __shared__ uint32_t s_bias0;  // first entry of the bias list in this chunk, from b0
   __shared__ uint64_t s_bar;
   static_assert(kProcThreads > SV_MAX_DRAFT_LEN, "a thread for each row and drafted token");
-  const int32_t r = blockIdx.x / p.chunks;
-  const int32_t c = blockIdx.x % p.chunks;
+  const int32_t r = blockIdx.x / (p.chunks * p.splits);
+  const int32_t c = blockIdx.x / p.splits % p.chunks;
+  const int32_t group = blockIdx.x % p.splits;
   const int tid = threadIdx.x;
   const int64_t lo = int64_t(c) * kChunk;
   const int32_t n_tok = static_cast<int32_t>(min(int64_t(kChunk), p.V - lo));
@@ -171,10 +174,10 @@ __global__ void __launch_bounds__(kProcThreads, 10)
     b0 = p.bias_start[r];
     b1 = p.bias_start[r + 1];
   }
-  for (int w = tid; w < kWords; w += kProcThreads) s_touch[w] = s_bbits[w] = 0;
-  // data errors are reported by the request's first chunk, which also resets the status of a
-  // single request's call
-  const bool first = c == 0;
+  for (int w = tid; w < kWords; w += kProcThreads) s_touch[w] = s_bbits[w] = s_drafted[w] = 0;
+  // data errors are reported by the request's first CTA, which also resets the status of a single
+  // request's call
+  const bool first = c == 0 && group == 0;
   if (tid == 0) {
     s_n = s_nd = 0;
     s_bias0 = ~0u;
@@ -186,7 +189,10 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   }
   bool bad = g < 0 || g > p.gmax;
   g = min(max(g, 0), p.gmax);
-  const int32_t rows = g + p.bonus_row;
+  // rows of the request, and those of this CTA's group
+  const int32_t all_rows = g + p.bonus_row;
+  const int32_t row_a = p.first_row + group * p.group_rows;
+  const int32_t rows = min(all_rows, row_a + p.group_rows);
   bool pen = theta != 1.f || pres != 0.f || freq != 0.f;
   if (pen && !(theta > 0.f && theta < INFINITY && fabsf(pres) < INFINITY &&
                fabsf(freq) < INFINITY && slot >= 0 && slot < p.n_slots)) {
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
       bulk_g2s(s_rows + u * kRowBytes, src + (i0 + u) * src_ld, full, &s_bar);
   };
   // ---- second loads, all in flight together: row parts, bits, drafted tokens, mask rows, biases
-  if (!kInPlace && tid == 0 && p.first_row < rows) load_rows(p.first_row);
+  if (!kInPlace && tid == 0 && row_a < rows) load_rows(row_a);
   uint32_t pb[kOwn], ob[kOwn];
 #pragma unroll
   for (int q = 0; q < kOwn; ++q) {
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   const int32_t x_draft = drafted ? p.draft_tokens[d0 + role] : -1;
   const bool masked = kMode != kSparse && p.mask_row != nullptr;
   int32_t mrow = -1;
-  if (masked && tid < rows - p.first_row) {
+  if (masked && tid < all_rows - p.first_row) {
     mrow = p.mask_row[row + p.first_row + tid];
     if (mrow < -1 || mrow >= p.n_mask) {
       bad = true;
@@ -258,6 +264,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
       s_tok[at] = static_cast<int32_t>(o);
       s_pos[at] = role + 1;
       atomicOr(&s_touch[o >> 5], 1u << (o & 31));
+      atomicOr(&s_drafted[o >> 5], 1u << (o & 31));
     }
   }
   auto add_bias = [&](int64_t k, int32_t x) {
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   };
   bool next_masked = false;
   if constexpr (kMode != kSparse) {
-    if (masked && p.first_row < rows) next_masked = load_masks(p.first_row);
+    if (masked && row_a < rows) next_masked = load_masks(row_a);
   }
   for (int w = tid; w < kWords; w += kProcThreads) {  // the list of touched offsets, in any order
     uint32_t t = s_touch[w];
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   }
 
   uint32_t phase = 0;
-  for (int32_t i0 = p.first_row; i0 < rows; i0 += kProcRows) {
+  for (int32_t i0 = row_a; i0 < rows; i0 += kProcRows) {
     const int32_t n = min(kProcRows, rows - i0);
     const bool now_masked = next_masked;  // the same in every thread
     if constexpr (kMode != kSparse) {
@@ -400,6 +407,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
       const int o = s_off[e];
       const uint32_t w = o >> 5, b = 1u << (o & 31);
       const bool in_prompt = s_prompt[w] & b, biased = s_bbits[w] & b;
+      const int drafts = s_drafted[w] & b ? nd : 0;
       const int32_t base = e == tid ? count0 : count_of(o);
       const float add = e == tid ? bias0 : bias_of(o);
       T* const at = reinterpret_cast<T*>(kInPlace ? dst + i0 * dst_ld : s_rows) + o;
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
       for (int u = 0; u < kProcRows; ++u) {
         if (u >= n || (now_masked && !(s_mask[u][w] & b))) continue;
         int32_t cnt = base;
-        for (int k = 0; k < nd; ++k) cnt += s_tok[k] == o && s_pos[k] <= i0 + u;
+        for (int k = 0; k < drafts; ++k) cnt += s_tok[k] == o && s_pos[k] <= i0 + u;
         const bool seen = in_prompt || cnt > 0;
         if (!seen && !biased) continue;
         float y = X::up(x[u]);
@@ -447,6 +455,16 @@ sv_status launch_process(ProcParams p, int32_t B, cudaStream_t s) {
   const int64_t chunk = proc_row_bytes(kMode) / sizeof(typename ProcElem<E>::T);
   const int64_t chunks = (p.V + chunk - 1) / chunk;
   if (chunks * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return SV_ERR_CUDA;
+  // One CTA takes all rows of a chunk, unless that leaves SMs with fewer than four CTAs: then groups
+  // of kProcRows rows go to CTAs of their own, each with the lists built anew (1 request of 17 rows
+  // of 152000, masked in place: FIGURE).
+  const int64_t most = std::max(1, p.gmax + p.bonus_row - p.first_row);
+  const int64_t batches = (most + kProcRows - 1) / kProcRows;
+  const int64_t splits = std::min(batches, std::max<int64_t>(1, 4 * sms / (chunks * B)));
+  p.group_rows = int32_t((batches + splits - 1) / splits) * kProcRows;
+  p.splits = int32_t((most + p.group_rows - 1) / p.group_rows);
   // with one request a single CTA reports, and resets the status before it does
   p.reset_status = p.status && B == 1;
   if (!p.reset_status) {
@@ -459,7 +477,8 @@ sv_status launch_process(ProcParams p, int32_t B, cudaStream_t s) {
           ? size_t(std::max(1, std::min(kProcRows, p.gmax + p.bonus_row - p.first_row))) *
                 proc_row_bytes(kMode)
           : 0;
-  return launch_dependent(process_kernel<E, kMode>, unsigned(chunks * B), kProcThreads, smem, s, p);
+  return launch_dependent(process_kernel<E, kMode>, unsigned(chunks * B * p.splits), kProcThreads, smem, s,
+                          p);
 }
 
 template <typename E>
@@ -505,7 +524,7 @@ extern "C" sv_status spec_process_logits(
   if (mask_row && (n_mask < 0 || (n_mask > 0 && (!mask || ld_mask < (V + 31) / 32))))
     return SV_ERR_INVALID;
   // the most CTAs any mode launches
-  if ((V + 2047 / eb) / (2048 / eb) * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  if ((V + 4095 / eb) / (4096 / eb) * B > INT32_MAX / 32) return SV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const ProcParams p = {static_cast<const uint8_t*>(logits),
                         ld,
@@ -519,6 +538,8 @@ extern "C" sv_status spec_process_logits(
                         first_row,
                         bonus_row,
                         draft_tokens,
+                        0,
+                        1,
                         0,
                         slots,
                         n_slots,
