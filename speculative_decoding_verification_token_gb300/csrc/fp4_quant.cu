@@ -270,6 +270,9 @@ __device__ __forceinline__ void store_vec(const RowOut& o, int64_t ahead, const 
 
 constexpr int kQuantThreads = 256;
 
+// Latency bounds the hidden rows of a round: 384 x 2560 take 4.7 us a call, most of it the two
+// launches.
+//
 // Blocks of 32: a warp takes kN spans of 256 elements (two scale groups) of one row; the padding
 // rows of the last scale tile get scales of zero.
 template <typename E, int kAlign, int kN>
@@ -318,6 +321,10 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
   }
 }
 
+// Memory and issue slots bound it alike: 151936 x 2560 bf16 with values take 262 us, 6.8 TB/s (the
+// rate of a copy) at 74% of the issue slots.  A persistent form with the next row in registers took
+// 368: 112 registers leave too few warps.
+//
 // Blocks of 16 under a row scale: `warps` warps of a CTA per row, each lane with kN vectors of it in
 // registers between the row's maximum and the codes (kN = 0: any number, read twice).
 template <typename E, int kAlign, int kN, int kThreads>

@@ -43,8 +43,9 @@ __device__ __forceinline__ bool hist_row(const HistParams& p, int32_t r, int32_t
 }
 
 // One thread per token: a round appends a few hundred, so the call is one launch of one or two
-// dependent loads and two atomics.  A single CTA (one = true) resets the status itself, which
-// saves the short call a second operation on the stream.
+// dependent loads and two atomics, and the launch is what it costs (64 x 6 tokens: 2.7 us a call in
+// a loop, host time included).  A single CTA (one = true) resets the status itself, which saves the
+// short call a second launch.
 __global__ void __launch_bounds__(1024) history_append_kernel(HistParams p, bool one) {
   dependent_start();
   if (one) {
@@ -141,8 +142,9 @@ constexpr int kClearTokens = 16384;  // counts one CTA clears
 
 // A slot's history replaced by a prompt.  The prompt touches no counts, so clearing them and
 // collecting the tokens need no order: of each slot's CTAs the first `marks` read the tokens, once,
-// and write the bit rows whole, the others clear 64 KB of counts each.  (The kernel above takes
-// 12.8 us for 32 prompts of up to 8192 tokens and V = 129280: its CTAs each read all tokens.)
+// and write the bit rows whole, the others clear 64 KB of counts each.  32 prompts of up to 8192
+// tokens, V = 129280: 6.7 us a call, of which the 18 MB written would take 2.7; the rest is launches
+// and the tokens' latency (with the kernel above, whose CTAs each read all tokens, 9.5).
 __global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistParams p,
                                                                         int32_t marks,
                                                                         int32_t ctas) {
