@@ -3,8 +3,9 @@
  *
  * The library turns target and draft logits into verified tokens (token-level and block
  * verification, also with the vocabulary split across ranks, or straight from hidden states
- * through an output projection), drafts a block with DSpark's Markov head, and schedules how much
- * of each drafted block to verify.  Every call is one or more hand-written CUDA kernels for sm_103a launched on the
+ * through an output projection), makes and processes those logits (4-bit output projection;
+ * penalties, biases and masks under the requests' token history), drafts a block with DSpark's
+ * Markov head, and schedules how much of each drafted block to verify.  Every call is one or more hand-written CUDA kernels for sm_103a launched on the
  * caller's stream.
  *
  * Conventions for every entry point
@@ -344,7 +345,8 @@ sv_status spec_history_append(const int32_t* tokens, int64_t ld_tokens, const in
  *   mask_row: DEVICE int32, indexed like the logit rows (nullable: no masks): the row of
  *     mask uint32 [n_mask][ld_mask] that applies, or -1 for none; bit 1 allows a token.  A mask
  *     that allows nothing leaves a row of -inf, which verification reports.
- * Values out of the ranges above, draft lengths outside [0, max_draft_len], drafted tokens outside
+ * The rows of different requests must be different rows; slots, masks and drafted tokens may be
+ * shared.  Values out of the ranges above, draft lengths outside [0, max_draft_len], drafted tokens outside
  * [0, V) (where penalties read them) and lists that do not ascend write SV_ERR_BAD_INPUT to status.
  * Rows are 16-byte aligned as for verification.  V at most 2^31 - 4097. */
 sv_status spec_process_logits(const void* logits, int64_t ld, void* out, int64_t ld_out,
