@@ -464,18 +464,11 @@ def spec_verify_token_sharded(target, draft, v_off, V_total, target_row0, draft_
 
 # ---- logits before verification ----------------------------------------------------------------
 # These calls are short, so that checking their arguments counts: _fastcall does it in C++ and makes
-# the call, and declines all that is not plain -- the checks below then find out what it is.
+# the call, and declines (-1) all that is not plain -- the checks below then find out what it is.
 
-def _quick(name, args, stream):
-    """The call made by _fastcall: True if it was, False if the checks below have to see it."""
-    if _lib is None:
-        lib()
-    if _fast is None:
-        return False
-    code = getattr(_fast, name)(*args, None if stream is None else stream.cuda_stream)
-    if code > 0:
-        raise SpecVerifyError(code, "spec_" + name)
-    return code == 0
+def _load_fast():
+    lib()
+    return _fast
 
 
 def _refuse(t, name, dtype, shape):
@@ -551,9 +544,13 @@ def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, le
     the history of slots int32 [B] (default: row r in slot r), in place: counts int32 [S, V] and
     the bit rows int32 [S, ceil(V / 32)] (see include/specverify.h).  `prompt` marks them as prompt
     tokens instead of counting them; `reset` clears the listed slots first.  Returns the status."""
-    if status is not None and _quick("history_append", (
-            tokens, counts, prompt_bits, output_bits, slots, lens, prompt, reset, status), stream):
-        return status
+    if status is not None and (_fast or _load_fast()):
+        code = _fast.history_append(tokens, counts, prompt_bits, output_bits, slots, lens, prompt,
+                                    reset, status, stream)
+        if code == 0:
+            return status
+        if code > 0:
+            raise SpecVerifyError(code, "spec_history_append")
     dev = _device_of(tokens, "tokens")
     tk, ldt = _mat(tokens, "tokens", torch.int32, dev, cols=0)
     c, pb, ob, n_slots, ldc, ldb, V = _history(counts, prompt_bits, output_bits, dev)
@@ -581,11 +578,15 @@ def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draf
     and dtype.  Returns out."""
     if out is None:
         out = logits
-    if status is not None and _quick("process_logits", (
+    if status is not None and (_fast or _load_fast()):
+        code = _fast.process_logits(
             logits, row0, draft_row0, draft_len, max_draft_len, draft_tokens, first_row, bonus_row,
             slots, counts, prompt_bits, output_bits, repetition, presence, frequency, bias_start,
-            bias_tokens, bias_values, mask, mask_row, out, status), stream):
-        return out
+            bias_tokens, bias_values, mask, mask_row, out, status, stream)
+        if code == 0:
+            return out
+        if code > 0:
+            raise SpecVerifyError(code, "spec_process_logits")
     dev = _device_of(logits, "logits")
     dt = _dtype_code(logits)
     lg, ld = _mat(logits, "logits", logits.dtype, dev)
@@ -659,11 +660,15 @@ def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=
     (see include/specverify.h).  Returns {"packed", "scales", "row_scales", "rows", "H", "format",
     "status"}, which spec_project_fp4 takes as an operand; `values`, a bf16 [rows, H] tensor, is
     filled with the numbers the codes stand for."""
-    if status is not None and packed is not None and scales is not None and _quick("quantize_fp4", (
-            x, fmt, packed, scales, row_scales, values, status), stream):
-        return {"packed": packed, "scales": scales,
-                "row_scales": row_scales if fmt == SV_FP4_E4M3_16 else None, "rows": x.shape[0],
-                "H": x.shape[1], "format": fmt, "status": status}
+    if status is not None and packed is not None and scales is not None and (_fast or _load_fast()):
+        code = _fast.quantize_fp4(x, fmt, packed, scales, row_scales, values, status, stream)
+        if code == 0:
+            rows, H = x.shape
+            return {"packed": packed, "scales": scales,
+                    "row_scales": row_scales if fmt == SV_FP4_E4M3_16 else None, "rows": rows,
+                    "H": H, "format": fmt, "status": status}
+        if code > 0:
+            raise SpecVerifyError(code, "spec_quantize_fp4")
     dev = _device_of(x, "x")
     dt = _dtype_code(x)
     xp, ldx = _mat(x, "x", x.dtype, dev)
@@ -722,11 +727,15 @@ def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=N
     """Logits [M, V] = x w^T of two operands quantised by spec_quantize_fp4: hidden rows x [M, H]
     and the output projection w [V, H] (see include/specverify.h).  `out` (bf16 or fp32, rows
     16-byte aligned) is allocated in `dtype` if not given.  Returns it."""
-    if status is not None and out is not None and x["H"] == w["H"] and (
-            x["format"] == w["format"]) and _quick("project_fp4", (
-            x["packed"], x["scales"], x["row_scales"], x["rows"], w["packed"], w["scales"],
-            w["row_scales"], w["rows"], x["H"], x["format"], out, status), stream):
-        return out
+    if status is not None and out is not None and (_fast or _load_fast()) and (
+            x["H"] == w["H"] and x["format"] == w["format"]):
+        code = _fast.project_fp4(x["packed"], x["scales"], x["row_scales"], x["rows"], w["packed"],
+                                 w["scales"], w["row_scales"], w["rows"], x["H"], x["format"], out,
+                                 status, stream)
+        if code == 0:
+            return out
+        if code > 0:
+            raise SpecVerifyError(code, "spec_project_fp4")
     dev = _device_of(x["packed"], "x packed")
     xp, xs, xr, M, H, fmt = _fp4_operand(x, "x", dev)
     wp, ws, wr, V, Hw, fw = _fp4_operand(w, "w", dev)

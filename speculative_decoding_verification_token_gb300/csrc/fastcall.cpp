@@ -88,10 +88,18 @@ struct Call {
     }
     return v;
   }
-  // the stream's number, or None for the current stream
+  // a torch stream, or None for the current one
   void* stream(PyObject* o) {
     if (o == Py_None) return ok ? c10::cuda::getCurrentCUDAStream(dev).stream() : nullptr;
-    return reinterpret_cast<void*>(num(o));
+    PyObject* number = PyObject_GetAttrString(o, "cuda_stream");
+    if (!number) {
+      PyErr_Clear();
+      ok = false;
+      return nullptr;
+    }
+    void* s = reinterpret_cast<void*>(num(number));
+    Py_DECREF(number);
+    return s;
   }
 };
 

@@ -373,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
       }
     }
     // both CTAs' copies in flight land before either block may end: of each stage that was
-    // filled, the last fill (this round's below st, the round's before from st on)
+    // filled, the last fill (of this turn of the ring below st, of the one before from st on)
     if (rank == 0)
       for (int32_t k = 0; k < issued; ++k)
         pj_wait_warp(&full[k], k < st ? phase ^ 1 : phase, p.status);

@@ -59,15 +59,22 @@ def _calls(sv, stream=None):
 
 
 def test_same_as_python_checks(sv, monkeypatch):
-    made = []
-    real = sv._quick
-    monkeypatch.setattr(sv, "_quick", lambda *a: made.append(real(*a)) or made[-1])
-    quick = _calls(sv)
-    assert made == [True] * 6  # every call went through the module
+    codes = []
+
+    class Spy:
+        def __getattr__(self, name):
+            real = getattr(sv._fastcall, name)
+            return lambda *a: codes.append(real(*a)) or codes[-1]
+
+    with monkeypatch.context() as m:
+        m.setattr(sv, "_fast", Spy())
+        quick = _calls(sv)
+    assert codes == [0] * 6  # every call went through the module
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     on_side = _calls(sv, side)
     monkeypatch.setattr(sv, "_fast", None)
+    monkeypatch.setattr(sv, "_load_fast", lambda: None)
     slow = _calls(sv)
     for a, b, c in zip(quick, slow, on_side):
         assert torch.equal(a, b) and torch.equal(a, c)
