@@ -135,9 +135,9 @@ __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams
   }
 }
 
-constexpr int kPromptThreads = 512;
+constexpr int kPromptThreads = 1024;
 constexpr int kPromptWords = 8192;   // words of prompt bits one CTA collects: 262144 tokens
-constexpr int kPromptAhead = 16;     // tokens a thread has in flight
+constexpr int kPromptAhead = 8;      // tokens a thread has in flight
 constexpr int kClearTokens = 16384;  // counts one CTA clears
 
 // A slot's history replaced by a prompt.  The prompt touches no counts, so clearing them and
@@ -153,6 +153,16 @@ __global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistPara
   const int32_t r = blockIdx.x / ctas;
   const int32_t c = blockIdx.x % ctas;
   const int tid = threadIdx.x;
+  const int32_t* row = p.tokens + r * p.ld_tokens;
+  int32_t x[kPromptAhead];
+  auto fetch = [&](int32_t t0) {
+#pragma unroll
+    for (int q = 0; q < kPromptAhead; ++q) {
+      const int32_t t = t0 + tid + q * kPromptThreads;
+      x[q] = t < p.n ? __ldg(row + t) : -1;
+    }
+  };
+  if (c < marks) fetch(0);  // beside the row's slot and length; columns behind the length are dropped
   int32_t slot, n;
   if (!hist_row(p, r, slot, n)) return;  // the whole CTA
   int32_t twice = 0;
@@ -168,20 +178,10 @@ __global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistPara
     for (int64_t v = full + tid; v < v1; v += kPromptThreads) cnt[v] = 0;
     return;
   }
-  const int32_t* row = p.tokens + r * p.ld_tokens;
   const int64_t w0 = int64_t(c) * kPromptWords;
   const int32_t words =
       static_cast<int32_t>(min(int64_t(kPromptWords), (p.V + 31) / 32 - w0));
   const int64_t v0 = w0 * 32, v1 = min(p.V, v0 + int64_t(kPromptWords) * 32);
-  int32_t x[kPromptAhead];
-  auto fetch = [&](int32_t t0) {
-#pragma unroll
-    for (int q = 0; q < kPromptAhead; ++q) {
-      const int32_t t = t0 + tid + q * kPromptThreads;
-      x[q] = t < n ? __ldg(row + t) : -1;
-    }
-  };
-  fetch(0);
   for (int w = tid; w < words; w += kPromptThreads) s_bits[w] = 0;
   if (__syncthreads_or(twice)) {
     if (tid == 0) report(p.status, SV_ERR_BAD_INPUT);
@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistPara
     if (t0) fetch(t0);
 #pragma unroll
     for (int q = 0; q < kPromptAhead; ++q) {
+      if (t0 + tid + q * kPromptThreads >= n) continue;
       if (x[q] >= p.V) report(p.status, SV_ERR_BAD_INPUT);
       if (x[q] < v0 || x[q] >= v1) continue;
       const uint32_t b = 1u << (x[q] & 31);
