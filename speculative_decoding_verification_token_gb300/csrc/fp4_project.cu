@@ -214,6 +214,14 @@ __device__ __forceinline__ void tmem_load16_async(uint32_t taddr, float* v) {
       : "memory");
 }
 
+// Uses of v stay behind the wait before this.
+__device__ __forceinline__ void tmem_landed(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                 "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
+}
+
 template <int kFmt>
 __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -456,6 +464,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
       for (int i = 0; i < kPieces; ++i)
         if (16 * (h + 4 * i) < n) tmem_load16_async(lanes + a * p.nt + 16 * (h + 4 * i), f[i]);
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) tmem_landed(f[i]);
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive_cluster(freed + a * 8);
