@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
       if constexpr (kInPlace) {
         // A vector banned as a whole is stored, a partly banned one read first.  Both in one store
         // instruction: halves of a 32-byte sector stored by two take five times as long in all.
-        // (Masked rows through shared memory by bulk copies: 83 us for these 73.)
+        // (Masked rows through shared memory by bulk copies took 83 us where this then took 73.)
         for (int v = tid; v < n_vec; v += kProcThreads) {
           uint4 x[kProcRows];
           uint32_t ok[kProcRows];
