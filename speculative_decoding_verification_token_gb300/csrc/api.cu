@@ -3,8 +3,7 @@
 #include <chrono>
 #include <mutex>
 
-#include "sv_device.cuh"
-#include "sv_host.h"
+#include "dependent.cuh"
 
 namespace sv {
 

@@ -28,8 +28,8 @@
 //   - the accumulator is emptied at once and stored by TMA (355 -> 199, with the item before).
 #include <algorithm>
 
+#include "dependent.cuh"
 #include "fp4.cuh"
-#include "sv_host.h"
 #include "tc.cuh"
 #include "tmap.h"
 
@@ -105,6 +105,14 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* ma
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
+}
+
+__device__ __forceinline__ void store_2d(const CUtensorMap* map, const void* src, int32_t c0,
+                                         int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1)
+               : "memory");
 }
 
 // Tiles towards L2 ahead of their loads.
@@ -513,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
         fence_proxy_async();
         __syncwarp();
         if (elect_one()) {
-          tc::tma_store_2d(&map_out, st, v0, n0 + c);  // clipped at M
+          store_2d(&map_out, st, v0, n0 + c);  // clipped at M
           tc::bulk_commit();
         }
         __syncwarp();
@@ -554,12 +562,31 @@ sv_status launch_project(const PjMaps& m, const PjParams& p, sv_dtype dtype, int
                           : launch_project<kFmt, kX, float>(m, p, grid, s);
 }
 
+// A tensor map of `type` elements; dims[0] is the contiguous one, strides in bytes for dims 1 ..;
+// what lies outside loads as zero.
+bool typed_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+               CUtensorMapDataType type) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+  }
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return fn(map, type, rank, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool rows_map(CUtensorMap* map, const uint8_t* base, int64_t rows, uint64_t row_bytes,
               uint32_t box_rows) {
   const uint64_t dims[2] = {row_bytes, uint64_t(rows)};
   const uint64_t strides[1] = {row_bytes};
   const uint32_t box[2] = {128, box_rows};
-  return make_map(map, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+  return typed_map(map, base, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
@@ -569,7 +596,7 @@ bool scales_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int32_t gro
   const uint64_t dims[3] = {128, uint64_t(groups), uint64_t((rows + 127) / 128)};
   const uint64_t strides[2] = {512, uint64_t(groups) * 512};
   const uint32_t box[3] = {128, box_groups, box_tiles};
-  return make_map(map, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+  return typed_map(map, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_DATA_TYPE_UINT32);
 }
 
@@ -578,7 +605,7 @@ bool logits_map(CUtensorMap* map, const void* out, sv_dtype dtype, int64_t M, in
   const uint64_t dims[2] = {uint64_t(V), uint64_t(M)};
   const uint64_t strides[1] = {uint64_t(ld) * uint64_t(elem_bytes(dtype))};
   const uint32_t box[2] = {32, 16};
-  return make_map(map, out, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+  return typed_map(map, out, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
                   dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 }

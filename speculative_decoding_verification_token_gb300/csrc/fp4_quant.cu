@@ -13,8 +13,8 @@
 // every load and store of a warp is contiguous; 4 or 2 lanes share a block.
 #include <algorithm>
 
+#include "dependent.cuh"
 #include "fp4.cuh"
-#include "sv_host.h"
 
 namespace sv {
 namespace {

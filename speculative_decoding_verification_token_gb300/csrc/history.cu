@@ -4,8 +4,7 @@
 // v % 32 of word v / 32: the tokens of the prompt and the tokens emitted (set exactly where the
 // count is positive).  Appending adds integers and sets bits, so the result does not depend on the
 // order in which the atomics land.
-#include "sv_device.cuh"
-#include "sv_host.h"
+#include "dependent.cuh"
 
 namespace sv {
 namespace {

@@ -12,8 +12,7 @@
 // left (or copied) bit for bit.
 #include <algorithm>
 
-#include "sv_device.cuh"
-#include "sv_host.h"
+#include "dependent.cuh"
 
 namespace sv {
 namespace {

@@ -34,27 +34,4 @@ inline sv_status launch_status(cudaError_t e) {
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
-// Launches `kernel` as a programmatic dependent: it may start while the kernel before it on the
-// stream ends, and waits for that (griddepcontrol.wait) before it touches what others wrote or read.
-template <typename... KArgs, typename... Args>
-inline sv_status launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned threads,
-                                  size_t smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, kernel, args...));
-}
-
-// Sets the status word (if any) to SV_OK ahead of kernels launched by launch_dependent: a kernel
-// that starts and ends beside them, where a memset would sit between two of them (quantising 384
-// rows of 2560 6.1 -> 4.8 us a call).
-sv_status reset_status(int32_t* status, cudaStream_t s);
-
 }  // namespace sv

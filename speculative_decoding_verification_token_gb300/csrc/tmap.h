@@ -1,5 +1,5 @@
 // tmap.h -- tensor maps (cuTensorMapEncodeTiled, reached through the runtime's driver entry
-// point) for the operands of the tcgen05 GEMMs.
+// point) for the bf16 operands of the tcgen05 GEMMs.
 #pragma once
 
 #include <cuda.h>
@@ -30,12 +30,11 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// Tensor map of bf16 elements (or of another type) with 128-byte swizzle; dims[0] is the contiguous one, strides in bytes for
+// bf16 tensor map with 128-byte swizzle; dims[0] is the contiguous one, strides in bytes for
 // dims 1.. ; out-of-range elements load as zero and are skipped by stores.
 bool make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
               const uint64_t* strides, const uint32_t* box,
-              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
-              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   cuuint64_t d[3], st[2];
@@ -45,7 +44,7 @@ bool make_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims
     bx[i] = box[i];
   }
   for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-  return fn(map, type, rank, const_cast<void*>(base), d, st, bx, es,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, bx, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
