@@ -398,7 +398,9 @@ sv_status spec_quantize_fp4(const void* x, sv_dtype dtype, int64_t rows, int64_t
  * fp32 on the tensor cores and rounded once to `dtype`: the rows spec_verify_token and
  * spec_process_logits take.  Rows of logits are ld apart, 16-byte aligned as for verification;
  * columns from V on are not written.  M and H at most 2^24, V at most 2^31 - 257.
- * status (nullable) tells of a wait that ran out. */
+ * status (nullable) tells of a wait that ran out.  w_packed and w_scales must be accessible from the
+ * call on: their first tiles are sent to L2 while the work before the call ends (their contents are
+ * read in stream order). */
 sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_scales,
                            const float* x_row_scales, int64_t M, const uint8_t* w_packed,
                            const uint8_t* w_scales, const float* w_row_scales, int64_t V,

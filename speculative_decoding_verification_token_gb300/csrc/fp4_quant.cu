@@ -270,7 +270,7 @@ __device__ __forceinline__ void store_vec(const RowOut& o, int64_t ahead, const 
 
 constexpr int kQuantThreads = 256;
 
-// Latency bounds the hidden rows of a round: 384 x 2560 take 4.7 us a call, most of it the two
+// Latency bounds the hidden rows of a round: 384 x 2560 take 4.4 us a call, most of it the two
 // launches.
 //
 // Blocks of 32: a warp takes kN spans of 256 elements (two scale groups) of one row; the padding

@@ -142,7 +142,7 @@ constexpr int kClearTokens = 16384;  // counts one CTA clears
 // A slot's history replaced by a prompt.  The prompt touches no counts, so clearing them and
 // collecting the tokens need no order: of each slot's CTAs the first `marks` read the tokens, once,
 // and write the bit rows whole, the others clear 64 KB of counts each.  32 prompts of up to 8192
-// tokens, V = 129280: 6.7 us a call, of which the 18 MB written would take 2.7; the rest is launches
+// tokens, V = 129280: 6.4 us a call, of which the 18 MB written would take 2.7; the rest is launches
 // and the tokens' latency (with the kernel above, whose CTAs each read all tokens, 9.5).
 __global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistParams p,
                                                                         int32_t marks,

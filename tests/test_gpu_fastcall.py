@@ -104,3 +104,82 @@ def test_declined_arguments_are_refused_by_name(sv):
         sv.spec_process_logits(x, torch.zeros(2, dtype=torch.int64, device="cuda"), None, mk(2), 0,
                                None, status=st)
     assert e.value.code == sv.SV_ERR_UNSUPPORTED
+
+
+def test_wrong_arguments_of_the_other_calls(sv):
+    """Shapes, types and devices that do not fit, with and without the marshalling module."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    z = lambda *n: torch.zeros(n, **i32)  # noqa: E731
+    f = lambda *n: torch.zeros(n, device="cuda")  # noqa: E731
+    L = lambda *n: torch.zeros(n, dtype=torch.int64, device="cuda")  # noqa: E731
+    B, V = 2, 64
+    good = dict(logits=f(2, V), row0=torch.arange(2, device="cuda"), draft_row0=L(2), draft_len=z(2),
+                max_draft_len=0, draft_tokens=z(1), counts=z(2, V), prompt_bits=z(2, 2),
+                output_bits=z(2, 2), repetition=f(2) + 1, status=z(1))
+    sv.spec_process_logits(**good)
+    bad = [(dict(logits=f(2, V).half()), TypeError), (dict(logits=f(2, V).cpu()), ValueError),
+           (dict(row0=z(2)), TypeError), (dict(row0=L(3)), ValueError),
+           (dict(draft_row0=L(1)), ValueError), (dict(draft_tokens=L(1)), TypeError),
+           (dict(draft_len=z(2).float()), TypeError), (dict(repetition=f(3)), ValueError),
+           (dict(presence=f(2).double()), TypeError), (dict(counts=z(2, V + 1)), ValueError),
+           (dict(counts=None), ValueError), (dict(counts=z(1, V), prompt_bits=z(1, 2),
+                                                  output_bits=z(1, 2)), ValueError),
+           (dict(slots=z(1)), ValueError), (dict(bias_start=z(2)), ValueError),
+           (dict(bias_start=z(3), bias_tokens=z(1)), ValueError),
+           (dict(bias_start=z(3), bias_tokens=z(2), bias_values=f(1)), ValueError),
+           (dict(mask_row=z(3), mask=z(1, 2)), ValueError),
+           (dict(mask_row=z(2), mask=z(1, 1)), ValueError), (dict(mask_row=z(2)), TypeError),
+           (dict(out=f(2, V + 8)), ValueError), (dict(out=f(1, V)), ValueError),
+           (dict(out=f(2, V).bfloat16()), TypeError)]
+    for change, error in bad:
+        for status in (good["status"], None):
+            with pytest.raises(error):
+                sv.spec_process_logits(**{**good, **change, "status": status})
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    x = f(5, 100)
+    for kw, error in [(dict(fmt=2), ValueError), (dict(packed=torch.zeros((5, 63), **u8)), ValueError),
+                      (dict(scales=torch.zeros(7, **u8)), ValueError),
+                      (dict(fmt=1, row_scales=f(4)), ValueError), (dict(values=f(5, 100)), TypeError),
+                      (dict(values=f(5, 108).bfloat16()), ValueError), (dict(x=x.half()), TypeError),
+                      (dict(x=x.t()), ValueError), (dict(x=x[0]), ValueError)]:
+        with pytest.raises(error):
+            sv.spec_quantize_fp4(**{**dict(x=x, fmt=0), **kw})
+    q = {fmt: sv.spec_quantize_fp4(x, fmt) for fmt in (0, 1)}
+    other = sv.spec_quantize_fp4(f(5, 99), 0)
+    st = z(1)
+    for a, b, kw, error in [
+            (q[0], q[1], {}, ValueError), (q[0], other, {}, ValueError),
+            (q[0], q[0], dict(out=f(5, 8)), ValueError), (q[0], q[0], dict(out=f(4, 5)), ValueError),
+            (q[0], q[0], dict(out=torch.zeros((5, 8), **i32)[:, :5]), TypeError),
+            (q[0], {**q[0], "scales": q[0]["scales"][:512]}, {}, ValueError),
+            (q[0], {**q[0], "packed": q[0]["packed"][:4]}, {}, ValueError),
+            (q[1], {**q[1], "row_scales": f(4)}, {}, ValueError),
+            (q[1], {**q[1], "row_scales": None}, {}, (TypeError, ValueError, sv.SpecVerifyError))]:
+        for status in (st, None):
+            with pytest.raises(error):
+                sv.spec_project_fp4(a, b, **{**dict(out=f(5, 8)[:, :5]), **kw}, status=status)
+
+
+def test_two_host_threads_on_two_streams(sv):
+    """Calls from two threads at once, each on its stream and tensors: the results of calls alone."""
+    import threading
+    want = _calls(sv)
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                got[k] = [_calls(sv) for _ in range(10)]
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for runs in got.values():
+        for run in runs:
+            assert all(torch.equal(a, b) for a, b in zip(run, want))
