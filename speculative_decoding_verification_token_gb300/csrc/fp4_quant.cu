@@ -32,6 +32,15 @@ struct QuantParams {
   int32_t* status;
 };
 
+// A CTA that is alone first resets the status, which saves a few rows a second launch, and clears the
+// one tile row of scales there is, padding rows and all.
+__device__ __forceinline__ void begin_alone(const QuantParams& p) {
+  if (threadIdx.x == 0 && p.status) *p.status = 0;
+  for (int32_t i = threadIdx.x; i < p.groups * 32; i += blockDim.x)
+    reinterpret_cast<uint4*>(p.scales)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();  // the rows' scales come after
+}
+
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 // Eight elements: as they lie in memory (bf16 pairs, or binary32 patterns).
@@ -275,50 +284,56 @@ constexpr int kQuantThreads = 256;
 //
 // Blocks of 32: a warp takes kN spans of 256 elements (two scale groups) of one row; the padding
 // rows of the last scale tile get scales of zero.
-template <typename E, int kAlign, int kN>
-__global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p, int32_t spans) {
+template <typename E, int kAlign, int kN, int kThreads>
+__global__ void __launch_bounds__(kThreads) quant_e8m0_kernel(QuantParams p, int32_t spans) {
+  constexpr bool kAlone = kThreads == 1024;
   dependent_start();
+  if constexpr (kAlone) begin_alone(p);
   const int lane = threadIdx.x & 31;
-  const int64_t warp = (int64_t(blockIdx.x) * kQuantThreads + threadIdx.x) >> 5;
   const int32_t per_row = (spans + kN - 1) / kN;
-  const int64_t r = warp / per_row;
-  const int32_t s0 = static_cast<int32_t>(warp % per_row) * kN;
-  if (r >= ((p.rows + 127) & ~int64_t(127))) return;
-  const bool real = r < p.rows;
-  const int64_t j0 = int64_t(s0) * 32 + lane;
   __shared__ __align__(16) typename In<E>::Raw
-      s_stage[kAlign == 0 ? kQuantThreads / 32 : 1][kAlign == 0 ? kN * 256 : 8];
+      s_stage[kAlign == 0 ? kThreads / 32 : 1][kAlign == 0 ? kN * 256 : 8];
+  static_assert(sizeof(s_stage) <= 48 * 1024);
   auto* const stage = s_stage[kAlign == 0 ? threadIdx.x >> 5 : 0];
-  uint32_t w[kN][In<E>::kWords];
-  load_spans<E, kAlign, kN>(
-      p.x + r * p.ldx * In<E>::kBytes, p.H, lane,
-      [&](int q) { return real && s0 + q < spans ? int64_t(s0 + q) : int64_t(-1); }, stage, w);
-  const RowOut o = row_out<16>(p, r, j0);
+  int64_t warp = (int64_t(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  do {
+    const int64_t r = warp / per_row;
+    const int32_t s0 = static_cast<int32_t>(warp % per_row) * kN;
+    if (r >= (kAlone ? p.rows : (p.rows + 127) & ~int64_t(127))) break;
+    const bool real = r < p.rows;
+    const int64_t j0 = int64_t(s0) * 32 + lane;
+    uint32_t w[kN][In<E>::kWords];
+    load_spans<E, kAlign, kN>(
+        p.x + r * p.ldx * In<E>::kBytes, p.H, lane,
+        [&](int q) { return real && s0 + q < spans ? int64_t(s0 + q) : int64_t(-1); }, stage, w);
+    const RowOut o = row_out<16>(p, r, j0);
 #pragma unroll
-  for (int q = 0; q < kN; ++q) {
-    if (s0 + q >= spans) break;
-    uint32_t m = In<E>::amax(w[q]);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const bool bad = m >= kInfBits;
-    // floor(log2 m) - 2, biased; below 2^-125 (and for a block of zeros) the smallest scale
-    const int32_t e = max(int32_t(m >> 23) - 2, 0);
-    uint32_t four = (bad ? 0xFFu : uint32_t(e)) << (8 * ((lane >> 2) & 3));
-    four |= __shfl_xor_sync(0xffffffffu, four, 4);
-    four |= __shfl_xor_sync(0xffffffffu, four, 8);
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(o.scales + q * 1024) = four;
-    if (!real) continue;
-    if (bad) report(p.status, SV_ERR_BAD_INPUT);
-    const float S = bad ? __uint_as_float(0x7FC00000u)  // the scale 0xFF stands for NaN
-                        : e ? __uint_as_float(uint32_t(e) << 23) : __uint_as_float(1u << 22);
-    const float inv = __uint_as_float(uint32_t(254 - e) << 23);  // 2^(127 - e): exact products
-    float t[8];
+    for (int q = 0; q < kN; ++q) {
+      if (s0 + q >= spans) break;
+      uint32_t m = In<E>::amax(w[q]);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const bool bad = m >= kInfBits;
+      // floor(log2 m) - 2, biased; below 2^-125 (and for a block of zeros) the smallest scale
+      const int32_t e = max(int32_t(m >> 23) - 2, 0);
+      uint32_t four = (bad ? 0xFFu : uint32_t(e)) << (8 * ((lane >> 2) & 3));
+      four |= __shfl_xor_sync(0xffffffffu, four, 4);
+      four |= __shfl_xor_sync(0xffffffffu, four, 8);
+      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(o.scales + q * 1024) = four;
+      if (!real) continue;
+      if (bad) report(p.status, SV_ERR_BAD_INPUT);
+      const float S = bad ? __uint_as_float(0x7FC00000u)  // the scale 0xFF stands for NaN
+                          : e ? __uint_as_float(uint32_t(e) << 23) : __uint_as_float(1u << 22);
+      const float inv = __uint_as_float(uint32_t(254 - e) << 23);  // 2^(127 - e): exact products
+      float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = bad ? 0.f : In<E>::get(w[q], i) * inv;
-    const int64_t j = j0 + q * 32;
-    store_vec<kAlign>(o, q, t, S, p.H - j * 8, p.row_bytes - j * 4, lane,
-                      reinterpret_cast<uint16_t*>(stage));
-  }
+      for (int i = 0; i < 8; ++i) t[i] = bad ? 0.f : In<E>::get(w[q], i) * inv;
+      const int64_t j = j0 + q * 32;
+      store_vec<kAlign>(o, q, t, S, p.H - j * 8, p.row_bytes - j * 4, lane,
+                        reinterpret_cast<uint16_t*>(stage));
+    }
+    warp += kThreads / 32;
+  } while (kAlone);
 }
 
 // Memory and issue slots bound it alike: 151936 x 2560 bf16 with values take 262 us, 6.8 TB/s (the
@@ -330,10 +345,11 @@ __global__ void __launch_bounds__(kQuantThreads) quant_e8m0_kernel(QuantParams p
 template <typename E, int kAlign, int kN, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
     quant_e4m3_kernel(QuantParams p, int32_t spans, int32_t warps) {
-  __shared__ uint32_t s_max[16];
+  __shared__ uint32_t s_max[kThreads / 32];
   dependent_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t rows_here = (kThreads >> 5) / warps;
+  if constexpr (kThreads == 1024) begin_alone(p);
   const int64_t r = int64_t(blockIdx.x) * rows_here + warp / warps;
   const int32_t mine = warp % warps;
   const bool real = r < p.rows, tile = r < ((p.rows + 127) & ~int64_t(127));
@@ -342,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
   constexpr int kHold = kN ? kN : 1;
   __shared__ __align__(16) typename In<E>::Raw
       s_stage[kAlign == 0 ? kThreads / 32 : 1][kAlign == 0 ? kHold * 256 : 8];
+  static_assert(sizeof(s_stage) + sizeof(s_max) <= 48 * 1024);
   auto* const stage = s_stage[kAlign == 0 ? warp : 0];
   uint32_t w[kHold][In<E>::kWords], am[kHold];
   auto fetch = [&](int32_t q0) {  // kHold spans from q0 on
@@ -440,7 +457,14 @@ sv_status launch_e8m0(const QuantParams& p, cudaStream_t s) {
   const int64_t warps = padded * (two ? (spans + 1) / 2 : spans);
   const int64_t blocks = (warps * 32 + kQuantThreads - 1) / kQuantThreads;
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  return launch_dependent(two ? quant_e8m0_kernel<E, kAlign, 2> : quant_e8m0_kernel<E, kAlign, 1>,
+  // Few spans go to one CTA and one launch (us a call, bf16 with values: 2 x 2560 3.0, 6 x 2560 3.5; 8
+  // x 2560, 80 spans, 4.4 and 16 x 2560 6.8, where two launches take 4.4 for all of them).
+  if (p.rows * spans <= 64)
+    return launch_dependent(quant_e8m0_kernel<E, kAlign, 1, 1024>, 1, 1024, 0, s, p, spans);
+  const sv_status reset = reset_status(p.status, s);
+  if (reset != SV_OK) return reset;
+  return launch_dependent(two ? quant_e8m0_kernel<E, kAlign, 2, kQuantThreads>
+                              : quant_e8m0_kernel<E, kAlign, 1, kQuantThreads>,
                           unsigned(blocks), kQuantThreads, 0, s, p, spans);
 }
 
@@ -453,6 +477,20 @@ sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
   int32_t warps = 1;
   while (warps < 16 && (warps * kMost < spans || (warps < spans && p.rows * warps < 2048)))
     warps *= 2;
+  // Few spans go to one CTA and one launch (us a call, with values: 2 x 2560 3.0, 8 x 2560 bf16 3.8, 6 x
+  // 2560 fp32 4.3; 16 x 2560 5.1 and 7.5, where two launches take 4.4 for all of them).
+  int32_t each = 1;  // warps per row of that CTA: 32 over the next power of two of the rows
+  while (each * 2 * p.rows <= 32) each *= 2;
+  constexpr int kHeld = kAlign == 0 && !In<E>::kFew ? 1 : kMost;  // its staging fits in 48 KB
+  if (p.rows <= 32 && p.rows * spans <= (In<E>::kFew ? 80 : 48) && spans <= kHeld * each) {
+    const int32_t hold = (spans + each - 1) / each;
+    return launch_dependent(hold == 1   ? quant_e4m3_kernel<E, kAlign, 1, 1024>
+                            : hold == 2 ? quant_e4m3_kernel<E, kAlign, kHeld < 2 ? 1 : 2, 1024>
+                                        : quant_e4m3_kernel<E, kAlign, kHeld, 1024>,
+                            1, 1024, 0, s, p, spans, each);
+  }
+  const sv_status reset = reset_status(p.status, s);
+  if (reset != SV_OK) return reset;
   const int threads = warps <= 4 ? 128 : 512;
   const int64_t blocks = (padded + threads / 32 / warps - 1) / (threads / 32 / warps);
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
@@ -512,8 +550,6 @@ extern "C" sv_status spec_quantize_fp4(const void* x, sv_dtype dtype, int64_t ro
   const bool vec = aligned16(x) && (ldx * eb) % 16 == 0 &&
                    (!values || (aligned16(values) && ld_values % 8 == 0));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const sv_status reset = reset_status(status, s);
-  if (reset != SV_OK) return reset;
   const QuantParams p = {static_cast<const uint8_t*>(x),
                          rows,
                          H,

@@ -125,6 +125,38 @@ def test_quantize_reports_non_finite(sv, fmt, bad):
     assert torch.isnan(y[2]).all() and torch.isfinite(y[[0, 1, 3, 4]]).all()
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("rows,H", [(1, 16), (3, 2560), (6, 2560), (17, 500), (32, 256), (64, 256),
+                                    (65, 256), (300, 700), (20, 500), (30, 300), (1, 8192)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_quantize_status_is_of_the_call(sv, fmt, rows, H, dtype, shift):
+    """The status of a call with a NaN, then of one without, in one word and without a wait; and the
+    codes are those of a larger batch (whose CTAs are others).  With a shift no row is aligned."""
+    buf = torch.zeros((rows, H + shift), dtype=dtype, device="cuda")
+    buf[:, shift:] = _rows(rows, H, dtype, rows + H).cuda()
+    x = buf[:, shift:]
+    st = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    q = sv.spec_quantize_fp4(x, fmt, status=st)
+    bad = buf.clone()[:, shift:]
+    bad[rows - 1, H - 1] = float("nan")
+    seen = []
+    for t in (bad, x, bad, bad, x):
+        sv.spec_quantize_fp4(t, fmt, packed=torch.empty_like(q["packed"]),
+                             scales=torch.empty_like(q["scales"]),
+                             row_scales=None if fmt == 0 else torch.empty_like(q["row_scales"]),
+                             status=st)
+        seen.append(st.clone())
+    assert [int(s) for s in seen] == [sv.SV_ERR_BAD_INPUT, 0, sv.SV_ERR_BAD_INPUT,
+                                      sv.SV_ERR_BAD_INPUT, 0]
+    many = sv.spec_quantize_fp4(torch.cat([x, torch.randn((1000, H), device="cuda").to(dtype)]), fmt)
+    assert torch.equal(many["packed"][:rows], q["packed"])
+    n = -(-H // plain.BLOCK[fmt])
+    a, clear = plain.scale_bytes(q["scales"].cpu().numpy(), rows, n)
+    b, _ = plain.scale_bytes(many["scales"].cpu().numpy(), rows + 1000, n)
+    assert clear and (a == b[:rows]).all()
+
+
 # ---- the product ---------------------------------------------------------------------------------
 
 def _project(sv, M, V, H, fmt, dtype, spread, seed, ld=None):
