@@ -315,7 +315,8 @@ sv_status spec_verify_lmhead(const void* target_hidden, const void* draft_hidden
  * be listed several times.  Counts are added modulo 2^32.
  * A slot outside [0, n_slots), a length outside [0, n], a token >= V, or a slot listed twice with
  * reset writes SV_ERR_BAD_INPUT to status; that row or token is left out.  Slots that are not
- * listed keep their history.  The result does not depend on the order of the rows. */
+ * listed keep their history.  The result does not depend on the order of the rows.  n at most
+ * 2^31 - 8193. */
 sv_status spec_history_append(const int32_t* tokens, int64_t ld_tokens, const int32_t* lens,
                               int32_t n, const int32_t* slots, int32_t B, int32_t kind,
                               int32_t reset, int64_t V, int32_t n_slots, int32_t* counts,
@@ -388,7 +389,8 @@ size_t spec_fp4_scale_bytes(int64_t rows, int64_t H, int32_t format);
 /* Quantises x [rows][H] (`dtype`, ldx elements apart; any alignment its elements allow).  format:
  * an sv_fp4_format.  row_scales: DEVICE fp32 [rows], SV_FP4_E4M3_16 only.  values (nullable): bf16
  * [rows][H], ld_values apart: the numbers the codes stand for (each is a bf16 number, or infinite
- * where rounding up took it past the largest one). */
+ * where rounding up took it past the largest one).  values may be x itself (bf16, ld_values = ldx:
+ * each element is replaced by its value); no other overlap of inputs and outputs is allowed. */
 sv_status spec_quantize_fp4(const void* x, sv_dtype dtype, int64_t rows, int64_t H, int64_t ldx,
                             int32_t format, uint8_t* packed, uint8_t* scales, float* row_scales,
                             void* values, int64_t ld_values, int32_t* status, void* stream);

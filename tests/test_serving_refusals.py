@@ -34,6 +34,8 @@ def test_history_refusals(sv):
     assert call(ptr=None) == sv.SV_ERR_INVALID
     assert call(V=2**31, ldc=2**31, ldb=2**26) == sv.SV_ERR_UNSUPPORTED
     assert call(B=2**30, n=2**12, ld=2**12) == sv.SV_ERR_UNSUPPORTED  # more blocks than a grid holds
+    assert call(n=2**31 - 8192, ld=2**31) == sv.SV_ERR_UNSUPPORTED
+    assert call(n=2**31 - 1, ld=2**31, reset=1) == sv.SV_ERR_UNSUPPORTED
     assert call(B=0) == sv.SV_OK and call(n=0, ld=0) == sv.SV_OK      # nothing to do
 
 
