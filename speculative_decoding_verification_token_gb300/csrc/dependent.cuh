@@ -8,7 +8,8 @@
 namespace sv {
 
 // Lets the next kernel start beside this one, then waits until the work before this one is done and
-// visible; everything a kernel shares with other work comes after it.
+// visible; everything a kernel shares with other work comes after it.  The loads that follow are
+// ordinary ones: the read-only path wants memory that nobody writes while the kernel is resident.
 __device__ __forceinline__ void dependent_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -457,11 +457,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
       const int32_t n = min(p.nt, p.M - n0);
       float ws = 1.f, xs[kPieces];
       if constexpr (kFmt == SV_FP4_E4M3_16) {
-        if (v0 + lane < p.V) ws = __ldg(p.w_row + v0 + lane);
+        if (v0 + lane < p.V) ws = p.w_row[v0 + lane];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {  // lane j holds column j's row scale
           const int32_t c = 16 * (h + 4 * i) + (lane & 15);
-          xs[i] = c < n ? __ldg(p.x_row + n0 + c) : 0.f;
+          xs[i] = c < n ? p.x_row[n0 + c] : 0.f;
         }
       }
       if (!failed && !pj_wait(&acc_full[a], phase, p.status)) failed = true;

@@ -52,8 +52,8 @@ struct In<float> {
   static constexpr int kBytes = 4, kWords = 8;
   static constexpr bool kFew = false;  // 24 significant bits
   __device__ static __forceinline__ void load(const uint8_t* p, uint32_t* w) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint4 b = reinterpret_cast<const uint4*>(p)[1];
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
@@ -75,7 +75,7 @@ struct In<bf16_tag> {
   static constexpr int kBytes = 2, kWords = 4;
   static constexpr bool kFew = true;  // 8 significant bits
   __device__ static __forceinline__ void load(const uint8_t* p, uint32_t* w) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
   }
   using Raw = uint16_t;
@@ -109,7 +109,7 @@ __device__ __forceinline__ void load_spans(const uint8_t* row, int64_t H, int la
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t e = e0 + i * 32 + lane;
-        raw[q][i] = e0 >= 0 && e < H ? __ldg(reinterpret_cast<const Raw*>(row) + e) : Raw(0);
+        raw[q][i] = e0 >= 0 && e < H ? reinterpret_cast<const Raw*>(row)[e] : Raw(0);
       }
     }
     __syncwarp();
@@ -138,7 +138,7 @@ __device__ __forceinline__ void load_spans(const uint8_t* row, int64_t H, int la
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (e0 + j >= H) continue;
-            const uint32_t x = __ldg(reinterpret_cast<const Raw*>(row) + e0 + j);
+            const uint32_t x = reinterpret_cast<const Raw*>(row)[e0 + j];
             if constexpr (sizeof(Raw) == 4)
               w[q][j] = x;
             else

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams
 #pragma unroll
     for (int q = 0; q < kResetAhead; ++q) {
       const int32_t t = t0 + tid + q * kResetThreads;
-      x[q] = t < n ? __ldg(row + t) : -1;
+      x[q] = t < n ? row[t] : -1;
     }
   };
   fetch(0);
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistPara
 #pragma unroll
     for (int q = 0; q < kPromptAhead; ++q) {
       const int32_t t = t0 + tid + q * kPromptThreads;
-      x[q] = t < p.n ? __ldg(row + t) : -1;
+      x[q] = t < p.n ? row[t] : -1;
     }
   };
   if (c < marks) fetch(0);  // beside the row's slot and length; columns behind the length are dropped
@@ -222,7 +222,7 @@ extern "C" sv_status spec_history_append(const int32_t* tokens, int64_t ld_token
       ld_bits < (V + 31) / 32 || (kind != SV_HISTORY_OUTPUT && kind != SV_HISTORY_PROMPT) ||
       (reset != 0 && reset != 1))
     return SV_ERR_INVALID;
-  if (V > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  if (V > INT32_MAX || n > INT32_MAX - 8192) return SV_ERR_UNSUPPORTED;
   if (B == 0 || (n == 0 && !reset)) return SV_OK;
   if ((n > 0 && !tokens) || !counts || !prompt_bits || !output_bits) return SV_ERR_INVALID;
   const bool fill = reset && kind == SV_HISTORY_PROMPT;

@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kProcThreads, 10)
     pb[q] = ob[q] = 0;
     if (pen && w < kWords && w * 32 < n_tok) {
       const uint32_t valid = n_tok - w * 32 >= 32 ? ~0u : (1u << (n_tok - w * 32)) - 1u;
-      pb[q] = __ldg(p.prompt_bits + slot * p.ld_bits + (lo >> 5) + w) & valid;
-      ob[q] = __ldg(p.output_bits + slot * p.ld_bits + (lo >> 5) + w) & valid;
+      pb[q] = p.prompt_bits[slot * p.ld_bits + (lo >> 5) + w] & valid;
+      ob[q] = p.output_bits[slot * p.ld_bits + (lo >> 5) + w] & valid;
     }
   }
   const int role = kProcThreads - 1 - tid;  // the threads least busy with bits
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
       const int32_t m = u < n ? mr[u] : -1;
       mw[q] = ~0u;
       if (m >= 0 && w * 32 < n_tok) {
-        mw[q] = __ldg(p.mask + m * p.ld_mask + (lo >> 5) + w);
+        mw[q] = p.mask[m * p.ld_mask + (lo >> 5) + w];
         if (n_tok - w * 32 < 32) mw[q] |= ~0u << (n_tok - w * 32);
       }
     }
@@ -330,14 +330,14 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   __syncthreads();
   const int32_t n_list = s_n, nd = s_nd;
   auto count_of = [&](int o) {
-    return s_out[o >> 5] >> (o & 31) & 1u ? __ldg(p.counts + slot * p.ld_counts + lo + o) : 0;
+    return s_out[o >> 5] >> (o & 31) & 1u ? p.counts[slot * p.ld_counts + lo + o] : 0;
   };
   // a biased token's value: the chunk's entries are neighbours in the ascending list
   auto bias_of = [&](int o) {
     if (!(s_bbits[o >> 5] >> (o & 31) & 1u)) return 0.f;
     int k = __popc(s_bbits[o >> 5] & ((1u << (o & 31)) - 1u));
     for (int w = 0; w < o >> 5; ++w) k += __popc(s_bbits[w]);
-    return __ldg(p.bias_values + b0 + s_bias0 + k);
+    return p.bias_values[b0 + s_bias0 + k];
   };
   // the count and bias of this thread's first listed token, while the rows are on their way
   int32_t count0 = 0;

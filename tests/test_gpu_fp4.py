@@ -157,6 +157,22 @@ def test_quantize_status_is_of_the_call(sv, fmt, rows, H, dtype, shift):
     assert clear and (a == b[:rows]).all()
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("rows,H", [(2, 2560), (20, 500), (300, 700), (130, 2560), (5, 70001)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_quantize_values_over_x(sv, fmt, rows, H, shift):
+    """values = x: the elements become the numbers their codes stand for."""
+    buf = torch.zeros((rows, H + shift + 7), dtype=torch.bfloat16, device="cuda")
+    buf[:, shift:shift + H] = _rows(rows, H, torch.bfloat16, rows + H).cuda()
+    x, before = buf[:, shift:shift + H], buf.clone()
+    y = torch.empty((rows, H), dtype=torch.bfloat16, device="cuda")
+    want = sv.spec_quantize_fp4(x, fmt, values=y)
+    got = sv.spec_quantize_fp4(x, fmt, values=x)
+    assert torch.equal(x, y) and torch.equal(got["packed"], want["packed"])
+    before[:, shift:shift + H] = y
+    assert torch.equal(buf, before)  # nothing beside the rows changed
+
+
 # ---- the product ---------------------------------------------------------------------------------
 
 def _project(sv, M, V, H, fmt, dtype, spread, seed, ld=None):
