@@ -55,7 +55,7 @@ struct ProcParams {
 constexpr int kProcThreads = 128;
 constexpr int kProcRows = 4;  // rows handled together
 
-// How a call moves its logits, and the bytes of a row that one CTA takes.
+// How a call moves its logits, and the bytes of a row that one CTA takes where there are many.
 enum ProcMode {
   kCopy = 0,     // out of place: every row moves
   kMasked = 1,   // in place with masks: banned elements are written
@@ -134,11 +134,10 @@ __device__ __forceinline__ uint4 ban(uint4 x, uint32_t ok) {
 // the 256 ragged requests that take 120).  In place it is sectors: a banned or edited element costs
 // the 32 or 64 bytes around it, read and written, so that 512 masked rows of 129280 (2% allowed) and
 // the edits of 512 others move 340 MB for 144 MB of elements: 62 us.
-template <typename E, int kMode>
+template <typename E, int kMode, uint32_t kRowBytes>
 __global__ void __launch_bounds__(kProcThreads, 10)
     process_kernel(ProcParams p) {
   constexpr bool kInPlace = kMode != kCopy;
-  constexpr uint32_t kRowBytes = proc_row_bytes(kMode);
   using X = ProcElem<E>;
   using T = typename X::T;
   constexpr int kVec = 16 / sizeof(T);
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   __syncthreads();
   // The masks' words of this chunk (1 behind the vocabulary) for the batch of rows from i0 on: loads,
   // then stores to shared memory, with other work between them.  Tells whether any mask applies.
-  constexpr int kMaskOwn = kProcRows * kWords / kProcThreads;
+  constexpr int kMaskOwn = (kProcRows * kWords + kProcThreads - 1) / kProcThreads;
   uint32_t mw[kMode == kSparse ? 1 : kMaskOwn];
   auto load_masks = [&](int32_t i0) {
     const int32_t* mr = s_mrow + (i0 - p.first_row);
@@ -355,7 +354,8 @@ __global__ void __launch_bounds__(kProcThreads, 10)
       if (now_masked) {
 #pragma unroll
         for (int q = 0; q < kMaskOwn; ++q)
-          (&s_mask[0][0])[tid + q * kProcThreads] = mw[q];
+          if (tid + q * kProcThreads < kProcRows * kWords)
+            (&s_mask[0][0])[tid + q * kProcThreads] = mw[q];
       }
       next_masked = masked && i0 + kProcRows < rows && load_masks(i0 + kProcRows);
     }
@@ -457,13 +457,10 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   }
 }
 
-template <typename E, int kMode>
-sv_status launch_process(ProcParams p, int32_t B, cudaStream_t s) {
-  const int64_t chunk = proc_row_bytes(kMode) / sizeof(typename ProcElem<E>::T);
+template <typename E, int kMode, uint32_t kRowBytes>
+sv_status launch_process(ProcParams p, int32_t B, int sms, cudaStream_t s) {
+  constexpr int64_t chunk = kRowBytes / sizeof(typename ProcElem<E>::T);
   const int64_t chunks = (p.V + chunk - 1) / chunk;
-  if (chunks * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  const int sms = device_sm_count();
-  if (sms <= 0) return SV_ERR_CUDA;
   // One CTA takes all rows of a chunk, unless that leaves SMs with fewer than twelve CTAs: then groups
   // of kProcRows rows go to CTAs of their own, each with the lists built anew (1 request of 17 rows
   // of 152000, masked in place: 23.6 -> 7.5 us; 256 requests of 17 rows of 1000: 59 -> 29; with four
@@ -480,13 +477,26 @@ sv_status launch_process(ProcParams p, int32_t B, cudaStream_t s) {
     if (st != SV_OK) return st;
   }
   p.chunks = int32_t(chunks);
-  const size_t smem =
-      kMode == kCopy
-          ? size_t(std::max(1, std::min(kProcRows, p.gmax + p.bonus_row - p.first_row))) *
-                proc_row_bytes(kMode)
-          : 0;
-  return launch_dependent(process_kernel<E, kMode>, unsigned(chunks * B * p.splits), kProcThreads, smem, s,
-                          p);
+  const size_t smem = kMode == kCopy ? std::min<int64_t>(kProcRows, most) * kRowBytes : 0;
+  return launch_dependent(process_kernel<E, kMode, kRowBytes>, unsigned(chunks * B * p.splits),
+                          kProcThreads, smem, s, p);
+}
+
+template <typename E, int kMode>
+sv_status launch_process(const ProcParams& p, int32_t B, cudaStream_t s) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return SV_ERR_CUDA;
+  // Parts of 1 KB while they make one wave (eight CTAs an SM), so that long lists of touched tokens
+  // are spread as far as they go: 9 requests of 5 rows of 8217 bf16 with 6382 tokens of history and
+  // 300 biases, masked in place, 26.3 -> 7.9 us; 2 of 14 rows of 1709 fp32 13.7 -> 6.3; 8 of 5 rows of
+  // 32000 7.1 -> 6.2.  Beyond a wave every part's own lists cost more: 13 rows of 113249 fp32 (11.7
+  // CTAs an SM) 5.2 -> 5.8.
+  constexpr int64_t kFew = 1024 / sizeof(typename ProcElem<E>::T);
+  const int64_t most = std::max(1, p.gmax + p.bonus_row - p.first_row);
+  const int64_t batches = (most + kProcRows - 1) / kProcRows;
+  if ((p.V + kFew - 1) / kFew * B * batches <= int64_t(8) * sms)
+    return launch_process<E, kMode, 1024>(p, B, sms, s);
+  return launch_process<E, kMode, proc_row_bytes(kMode)>(p, B, sms, s);
 }
 
 template <typename E>

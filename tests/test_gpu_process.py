@@ -265,6 +265,16 @@ def test_process_serving_size(sv, dtype):
     _run(sv, c, False, ld=151936)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("B,gamma,V,bias,masked", [
+    (70, 5, 9000, 4000, True), (330, 4, 1003, 30, True), (140, 0, 20000, 17, False),
+    (60, 20, 4097, 0, True)])
+def test_process_many_requests(sv, B, gamma, V, bias, masked, dtype, in_place):
+    """More parts of rows than SMs can hold at once."""
+    _run(sv, _case(B + 10 * gamma + V, B, gamma, V, dtype, bias, masked), in_place)
+
+
 @pytest.mark.parametrize("in_place", [True, False])
 def test_process_draft_side_and_single_rows(sv, in_place):
     """Draft rows (no bonus row), one row of an autoregressive draft, and requests without any
