@@ -49,8 +49,12 @@ struct ProcParams {
   int32_t n_mask;
   const int32_t* mask_row;
   int32_t* status;
-  bool reset_status;
+  // Who resets the status and reports: each request's first CTA reports, after a kernel that resets
+  // it; with kSingle the only request's first CTA does both; with kChecker CTA 0, which does nothing
+  // else, does both for all requests.
+  int32_t reports;
 };
+enum { kFirst = 0, kSingle = 1, kChecker = 2 };
 
 constexpr int kProcThreads = 128;
 constexpr int kProcRows = 4;  // rows handled together
@@ -64,6 +68,8 @@ enum ProcMode {
 constexpr uint32_t proc_row_bytes(int mode) {
   return mode == kCopy ? 4096 : 8192;
 }
+
+constexpr uint32_t kSmallRowBytes = 1024;  // where there are few
 
 template <typename E>
 struct ProcElem;
@@ -120,6 +126,63 @@ __device__ __forceinline__ uint4 ban(uint4 x, uint32_t ok) {
                     (x.z & m[2]) | (kInf & ~m[2]), (x.w & m[3]) | (kInf & ~m[3]));
 }
 
+// All of a small call's requests checked by one CTA, a thread for each row and bias entry: saves the
+// call the launch that would reset the status.
+__device__ __forceinline__ void check_requests(const ProcParams& p, int32_t B, bool masked) {
+  dependent_start();
+  if (threadIdx.x == 0) *p.status = 0;
+  bool bad = false;
+  const int32_t per = p.gmax + 1;
+  for (int32_t j = threadIdx.x; j < B * per; j += kProcThreads) {
+    const int32_t i = j % per;
+    const int32_t r = j / per, g = p.draft_len[r], slot = p.slots ? p.slots[r] : r;
+    const float theta = p.repetition ? p.repetition[r] : 1.f;
+    const float pres = p.presence ? p.presence[r] : 0.f;
+    const float freq = p.frequency ? p.frequency[r] : 0.f;
+    bool pen = theta != 1.f || pres != 0.f || freq != 0.f;
+    if (pen && !(theta > 0.f && theta < INFINITY && fabsf(pres) < INFINITY &&
+                 fabsf(freq) < INFINITY && slot >= 0 && slot < p.n_slots)) {
+      bad = true;
+      pen = false;
+    }
+    bad |= g < 0 || g > p.gmax;
+    const int32_t drafts = min(max(g, 0), p.gmax);
+    if (pen && i < drafts) {
+      const int32_t x = p.draft_tokens[p.draft_row0[r] + i];
+      bad |= x < 0 || x >= p.V;
+    }
+    if (masked && i >= p.first_row && i < drafts + p.bonus_row) {
+      const int32_t m = p.mask_row[p.row0[r] + i];
+      bad |= m < -1 || m >= p.n_mask;
+    }
+    if (p.bias_start) {
+      const int32_t b0 = p.bias_start[r], b1 = p.bias_start[r + 1];
+      bad |= b0 < 0 || b1 < b0 || b1 > p.n_bias;
+    }
+  }
+  if (p.bias_start) {  // the lists follow one another: neighbours ascend unless a list starts there
+    const int64_t k0 = max(int64_t(p.bias_start[0]), int64_t(0));
+    const int64_t k1 = min(int64_t(p.bias_start[B]), p.n_bias);
+    for (int64_t k = k0 + threadIdx.x; k < k1; k += kProcThreads) {
+      const int32_t x = p.bias_tokens[k];
+      bad |= x < 0 || x >= p.V;
+      if (k > k0 && p.bias_tokens[k - 1] >= x) {
+        int32_t r = 0;  // the first list that starts at k or behind it
+        for (int32_t end = B; r < end;) {
+          const int32_t mid = (r + end) >> 1;
+          if (p.bias_start[mid] < k)
+            r = mid + 1;
+          else
+            end = mid;
+        }
+        bad |= r == B || p.bias_start[r] != k;
+      }
+    }
+  }
+  __syncthreads();
+  if (bad) report(p.status, SV_ERR_BAD_INPUT);
+}
+
 // One CTA per (request, chunk of a row), for all rows of the request: the history, biases
 // and drafted tokens of the chunk are read once.  What they touch -- a few tokens in a hundred --
 // is gathered into a list of offsets, one thread per listed token edits it in every row, and the
@@ -156,15 +219,23 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   __shared__ uint32_t s_bias0;  // first entry of the bias list in this chunk, from b0
   __shared__ uint64_t s_bar;
   static_assert(kProcThreads > SV_MAX_DRAFT_LEN, "a thread for each row and drafted token");
-  const int32_t r = blockIdx.x / (p.chunks * p.splits);
-  const int32_t c = blockIdx.x / p.splits % p.chunks;
-  const int32_t group = blockIdx.x % p.splits;
+  constexpr bool kSmall = kRowBytes == kSmallRowBytes;
+  // (one dimension: with a grid of three, which needs no division, 128 requests in place took 65 us
+  // where they take 62, and the ragged ones 122 for 120)
+  const uint32_t part = blockIdx.x - (kSmall && p.reports == kChecker ? 1u : 0u);
+  const int32_t r = part / (p.chunks * p.splits);
+  const int32_t c = part / p.splits % p.chunks;
+  const int32_t group = part % p.splits;
   const int tid = threadIdx.x;
   const int64_t lo = int64_t(c) * kChunk;
   const int32_t n_tok = static_cast<int32_t>(min(int64_t(kChunk), p.V - lo));
   const uint32_t full = uint32_t(n_tok) * sizeof(T) & ~15u;  // bytes in whole vectors
   const int32_t n_vec = full >> 4, n_tail = n_tok - n_vec * kVec;
 
+  if (kSmall && part == ~0u) {
+    check_requests(p, int32_t(gridDim.x - 1) / (p.chunks * p.splits), kMode != kSparse && p.mask_row);
+    return;
+  }
   dependent_start();
   // ---- first loads: the request's parameters
   int32_t g = p.draft_len[r];
@@ -180,13 +251,11 @@ __global__ void __launch_bounds__(kProcThreads, 10)
     b1 = p.bias_start[r + 1];
   }
   for (int w = tid; w < kWords; w += kProcThreads) s_touch[w] = s_bbits[w] = s_drafted[w] = 0;
-  // data errors are reported by the request's first CTA, which also resets the status of a single
-  // request's call
-  const bool first = c == 0 && group == 0;
+  const bool first = c == 0 && group == 0 && !(kSmall && p.reports == kChecker);
   if (tid == 0) {
     s_n = s_nd = 0;
     s_bias0 = ~0u;
-    if (first && p.reset_status) *p.status = 0;
+    if (first && p.reports == kSingle && p.status) *p.status = 0;
     if (!kInPlace) {
       mbar_init(&s_bar, 1);
       fence_barrier_init();
@@ -470,16 +539,23 @@ sv_status launch_process(ProcParams p, int32_t B, int sms, cudaStream_t s) {
   const int64_t splits = std::min(batches, std::max<int64_t>(1, 12 * sms / (chunks * B)));
   p.group_rows = int32_t((batches + splits - 1) / splits) * kProcRows;
   p.splits = int32_t((most + p.group_rows - 1) / p.group_rows);
-  // with one request a single CTA reports, and resets the status before it does
-  p.reset_status = p.status && B == 1;
-  if (!p.reset_status) {
+  p.chunks = int32_t(chunks);
+  // CTA 0 checks a call of at most 512 rows and 1024 bias entries (fewer with many requests, whose
+  // lists' ends have to be looked up) while the others are at work (8 requests of 5 rows of 32000
+  // 7.1 -> 4.8 us, 21 of 17 rows of 4298 6.6 -> 4.7); a larger call would wait for it (256 requests
+  // with 4 biases each 6.4 -> 10.3).
+  const bool few = int64_t(B) * (p.gmax + 1) <= 512 &&
+                   (!p.bias_start || p.n_bias + 8 * int64_t(B) <= 1024);
+  p.reports = B == 1 || !p.status ? kSingle
+              : kRowBytes == kSmallRowBytes && few ? kChecker
+                                                   : kFirst;
+  if (p.reports == kFirst) {
     const sv_status st = reset_status(p.status, s);
     if (st != SV_OK) return st;
   }
-  p.chunks = int32_t(chunks);
   const size_t smem = kMode == kCopy ? std::min<int64_t>(kProcRows, most) * kRowBytes : 0;
-  return launch_dependent(process_kernel<E, kMode, kRowBytes>, unsigned(chunks * B * p.splits),
-                          kProcThreads, smem, s, p);
+  const unsigned ctas = unsigned(chunks * B * p.splits) + (p.reports == kChecker);
+  return launch_dependent(process_kernel<E, kMode, kRowBytes>, ctas, kProcThreads, smem, s, p);
 }
 
 template <typename E, int kMode>
@@ -489,13 +565,13 @@ sv_status launch_process(const ProcParams& p, int32_t B, cudaStream_t s) {
   // Parts of 1 KB while they make one wave (eight CTAs an SM), so that long lists of touched tokens
   // are spread as far as they go: 9 requests of 5 rows of 8217 bf16 with 6382 tokens of history and
   // 300 biases, masked in place, 26.3 -> 7.9 us; 2 of 14 rows of 1709 fp32 13.7 -> 6.3; 8 of 5 rows of
-  // 32000 7.1 -> 6.2.  Beyond a wave every part's own lists cost more: 13 rows of 113249 fp32 (11.7
-  // CTAs an SM) 5.2 -> 5.8.
-  constexpr int64_t kFew = 1024 / sizeof(typename ProcElem<E>::T);
+  // 32000 7.1 -> 6.2 (the status reset by a launch of its own).  Beyond a wave every part's own lists
+  // cost more: 13 rows of 113249 fp32 (11.7 CTAs an SM) 5.2 -> 5.8.
+  constexpr int64_t kFew = kSmallRowBytes / sizeof(typename ProcElem<E>::T);
   const int64_t most = std::max(1, p.gmax + p.bonus_row - p.first_row);
   const int64_t batches = (most + kProcRows - 1) / kProcRows;
   if ((p.V + kFew - 1) / kFew * B * batches <= int64_t(8) * sms)
-    return launch_process<E, kMode, 1024>(p, B, sms, s);
+    return launch_process<E, kMode, kSmallRowBytes>(p, B, sms, s);
   return launch_process<E, kMode, proc_row_bytes(kMode)>(p, B, sms, s);
 }
 
@@ -578,6 +654,6 @@ extern "C" sv_status spec_process_logits(
                         n_mask,
                         mask_row,
                         status,
-                        false};
+                        kFirst};
   return dtype == SV_BF16 ? launch_process<bf16_tag>(p, B, s) : launch_process<float>(p, B, s);
 }

@@ -432,6 +432,47 @@ def test_process_bad_data_is_reported(sv):
     assert status(mask_row=i(*([99] * 10))) == bad and status(mask_row=i(*([-2] * 10))) == bad
 
 
+@pytest.mark.parametrize("first_row,bonus", [(0, True), (0, False), (2, True)])
+@pytest.mark.parametrize("B", [3, 40, 64, 100, 130])
+def test_process_bad_data_of_one_request(sv, B, first_row, bonus):
+    """Each value of one request that can be wrong, in batches of several sizes; a word that held
+    something else before; lists that descend from one request to the next are none."""
+    c = _case(B, B, 3, 100, torch.float32, 4, True, ragged=False, first_row=first_row, bonus=bonus)
+    start, toks, _ = c["bias"]
+    n = len(toks)
+    r = int(np.argmax(start[1:] - start[:-1] >= 2))  # a request with two biases at least
+    assert start[r + 1] - start[r] >= 2
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def status(stale, name=None, at=0, value=0):
+        buf, args, kw = _device_args(c, 104)
+        d = dict(draft_len=args[2], draft_tokens=args[4], **{k: v for k, v in kw.items()
+                                                               if torch.is_tensor(v)})
+        if name:
+            d[name][at] = value
+        st.fill_(stale)
+        sv.spec_process_logits(buf[:, :100], *args, status=st, **kw)
+        return int(st)
+
+    bad = sv.SV_ERR_BAD_INPUT
+    k = int(start[r])
+    row = int(c["row0"][r]) + first_row
+    for name, at, value in (
+            ("slots", r, -1), ("slots", r, B + 1), ("draft_len", r, -1), ("draft_len", r, 4),
+            ("draft_tokens", int(c["draft_row0"][r]) + 2, 100),
+            ("draft_tokens", int(c["draft_row0"][r]), -1), ("repetition", r, 0.0),
+            ("repetition", r, float("nan")), ("presence", r, float("inf")),
+            ("frequency", r, float("nan")), ("bias_start", 0, -1), ("bias_start", B, n + 1),
+            ("bias_start", r, k + 9), ("bias_tokens", k, -1), ("bias_tokens", k + 1, 100),
+            ("bias_tokens", k + 1, int(toks[k])), ("mask_row", row, -2),
+            ("mask_row", row, len(c["mask"])), ("mask_row", row + 2 - first_row, -2)):
+        assert status(0, name, at, value) == bad, (name, at, value)
+    assert status(bad) == 0 and status(0) == 0
+    # a row that the request does not have is not looked at
+    if not bonus:
+        assert status(7, "mask_row", int(c["row0"][r]) + 3, -2) == 0
+
+
 def test_empty_mask_is_reported_by_verification(sv):
     """A mask that allows nothing leaves a row of -inf; spec_verify_token reports it."""
     V, g = 256, 2
