@@ -106,10 +106,14 @@ __device__ __forceinline__ void load_spans(const uint8_t* row, int64_t H, int la
 #pragma unroll
     for (int q = 0; q < kN; ++q) {
       const int64_t e0 = span(q) * 256;
+      const Raw* const from = reinterpret_cast<const Raw*>(row) + e0 + lane;
+      const int32_t there = e0 < 0 ? 0 : int32_t(min(H - e0, int64_t(256)));
+      if (there == 256) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t e = e0 + i * 32 + lane;
-        raw[q][i] = e0 >= 0 && e < H ? reinterpret_cast<const Raw*>(row)[e] : Raw(0);
+        for (int i = 0; i < 8; ++i) raw[q][i] = from[i * 32];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[q][i] = i * 32 + lane < there ? from[i * 32] : Raw(0);
       }
     }
     __syncwarp();
@@ -261,11 +265,16 @@ __device__ __forceinline__ void store_vec(const RowOut& o, int64_t ahead, const 
     __syncwarp();
     *reinterpret_cast<uint4*>(stage + lane * 8) = h;
     __syncwarp();
-    uint16_t* const first = reinterpret_cast<uint16_t*>(vd) - lane * 8;  // the span's first element
-    const int64_t there = left + lane * 8;                               // elements from it on
+    uint16_t* const to = reinterpret_cast<uint16_t*>(vd) - lane * 7;  // the span's element `lane`
+    const int32_t there = int32_t(min(left + lane * 8, int64_t(256)));  // elements of the span
+    if (there == 256) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i * 32 + lane < there) first[i * 32 + lane] = stage[i * 32 + lane];
+      for (int i = 0; i < 8; ++i) to[i * 32] = stage[i * 32 + lane];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * 32 + lane < there) to[i * 32] = stage[i * 32 + lane];
+    }
   } else if (kAlign == 2 || left >= 8) {
     *reinterpret_cast<uint4*>(vd) = h;
   } else {
