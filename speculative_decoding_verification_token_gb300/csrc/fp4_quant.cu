@@ -345,6 +345,12 @@ __global__ void __launch_bounds__(kThreads) quant_e8m0_kernel(QuantParams p, int
   } while (kAlone);
 }
 
+// Whether the staging of kN vectors a lane fits in 48 KB with a CTA of `threads`.
+template <typename E, int kAlign, int kN>
+constexpr bool staging_fits(int threads) {
+  return kAlign != 0 || threads / 32 * (kN * 256 * In<E>::kBytes + 4) <= 48 * 1024;
+}
+
 // Memory and issue slots bound it alike: 151936 x 2560 bf16 with values take 262 us, 6.8 TB/s (the
 // rate of a copy) at 74% of the issue slots.  A persistent form with the next row in registers took
 // 368: 112 registers leave too few warps.
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) quant_e8m0_kernel(QuantParams p, int
 // Blocks of 16 under a row scale: `warps` warps of a CTA per row, each lane with kN vectors of it in
 // registers between the row's maximum and the codes (kN = 0: any number, read twice).
 template <typename E, int kAlign, int kN, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1)
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     quant_e4m3_kernel(QuantParams p, int32_t spans, int32_t warps) {
   __shared__ uint32_t s_max[kThreads / 32];
   dependent_start();
@@ -477,20 +483,38 @@ sv_status launch_e8m0(const QuantParams& p, cudaStream_t s) {
                           unsigned(blocks), kQuantThreads, 0, s, p, spans);
 }
 
+// `warps` warps to a row, CTAs of 128 threads or a row.
+template <typename E, int kAlign, int kN>
+sv_status launch_e4m3(const QuantParams& p, int32_t spans, int32_t warps, cudaStream_t s) {
+  const int32_t threads = warps <= 4 ? 128 : warps * 32;
+  const int64_t rows = (p.rows + 127) / 128 * 128, here = threads / 32 / warps;
+  const int64_t blocks = (rows + here - 1) / here;
+  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  auto* kernel = quant_e4m3_kernel<E, kAlign, kN, 128>;
+  if (threads == 256) kernel = quant_e4m3_kernel<E, kAlign, kN, 256>;
+  if constexpr (staging_fits<E, kAlign, kN>(512)) {
+    if (threads == 512) kernel = quant_e4m3_kernel<E, kAlign, kN, 512>;
+  } else if (threads == 512) {
+    return SV_ERR_UNSUPPORTED;  // not asked for below
+  }
+  return launch_dependent(kernel, unsigned(blocks), unsigned(threads), 0, s, p, spans, warps);
+}
+
 template <typename E, int kAlign>
 sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
-  constexpr int kMost = kAlign == 0 ? 2 : In<E>::kFew ? 5 : 3;  // vectors a lane holds
+  constexpr int kMost = In<E>::kFew ? 5 : 4;  // vectors a lane holds
   const int32_t spans = int32_t((p.H + 255) / 256);
-  const int64_t padded = (p.rows + 127) / 128 * 128;
   // the fewest warps per row that hold it; more where the rows alone would leave the GPU idle
   int32_t warps = 1;
   while (warps < 16 && (warps * kMost < spans || (warps < spans && p.rows * warps < 2048)))
     warps *= 2;
   // Few spans go to one CTA and one launch (us a call, with values: 2 x 2560 3.0, 8 x 2560 bf16 3.8, 6 x
   // 2560 fp32 4.3; 16 x 2560 5.1 and 7.5, where two launches take 4.4 for all of them).
+  constexpr int kHeld = staging_fits<E, kAlign, kMost>(1024) ? kMost
+                        : staging_fits<E, kAlign, 2>(1024)   ? 2
+                                                             : 1;
   int32_t each = 1;  // warps per row of that CTA: 32 over the next power of two of the rows
   while (each * 2 * p.rows <= 32) each *= 2;
-  constexpr int kHeld = kAlign == 0 && !In<E>::kFew ? 1 : kMost;  // its staging fits in 48 KB
   if (p.rows <= 32 && p.rows * spans <= (In<E>::kFew ? 80 : 48) && spans <= kHeld * each) {
     const int32_t hold = (spans + each - 1) / each;
     return launch_dependent(hold == 1   ? quant_e4m3_kernel<E, kAlign, 1, 1024>
@@ -500,21 +524,18 @@ sv_status launch_e4m3(const QuantParams& p, cudaStream_t s) {
   }
   const sv_status reset = reset_status(p.status, s);
   if (reset != SV_OK) return reset;
-  const int threads = warps <= 4 ? 128 : 512;
-  const int64_t blocks = (padded + threads / 32 / warps - 1) / (threads / 32 / warps);
-  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  // a kernel for each number of vectors: in one for up to five or three of them the others' turns
+  // cost, and with fewer held rows need CTAs of eight warps or more (40000 x 4096 fp32 223 -> 157 us,
+  // 100000 x 1025 bf16 197 -> 113, 20000 x 7168 bf16 131 -> 116)
   const int32_t hold = (spans + warps - 1) / warps;
-  auto go = [&](auto* narrow, auto* wide) {
-    return launch_dependent(threads == 128 ? narrow : wide, unsigned(blocks), unsigned(threads), 0, s,
-                            p, spans, warps);
-  };
-  if (hold == 1)
-    return go(quant_e4m3_kernel<E, kAlign, 1, 128>, quant_e4m3_kernel<E, kAlign, 1, 512>);
-  if (hold == 2)
-    return go(quant_e4m3_kernel<E, kAlign, 2, 128>, quant_e4m3_kernel<E, kAlign, 2, 512>);
-  if (hold <= kMost)
-    return go(quant_e4m3_kernel<E, kAlign, kMost, 128>, quant_e4m3_kernel<E, kAlign, kMost, 512>);
-  return go(quant_e4m3_kernel<E, kAlign, 0, 128>, quant_e4m3_kernel<E, kAlign, 0, 512>);
+  if (hold == 1) return launch_e4m3<E, kAlign, 1>(p, spans, warps, s);
+  if (hold == 2) return launch_e4m3<E, kAlign, 2>(p, spans, warps, s);
+  if (warps < 16 || staging_fits<E, kAlign, kMost>(512)) {
+    if (hold == 3) return launch_e4m3<E, kAlign, 3>(p, spans, warps, s);
+    if (hold == 4) return launch_e4m3<E, kAlign, 4>(p, spans, warps, s);
+    if (hold <= kMost) return launch_e4m3<E, kAlign, kMost>(p, spans, warps, s);
+  }
+  return launch_e4m3<E, kAlign, 0>(p, spans, warps, s);
 }
 
 template <typename E>

@@ -75,6 +75,38 @@ def test_quantize(sv, rows, H, dtype, kind, fmt):
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("H", [200, 500, 700, 1024, 1200, 2561, 3800, 5000, 5121, 7168, 8200, 10000,
+                               10241, 16000, 20480, 20481])
+def test_quantize_rows_of_every_length(sv, H, shift, dtype, fmt):
+    """So many rows that each is held by as few warps as can; five of them against the plain form."""
+    rows = 2100
+    buf = torch.zeros((rows, H + 9), dtype=dtype, device="cuda")
+    x = buf[:, shift:shift + H]
+    x[:] = torch.randn((rows, H), device="cuda", generator=torch.Generator("cuda").manual_seed(H))
+    few = _rows(5, H, dtype, H)
+    x[:5] = few.cuda()
+    x[-5:] = few.cuda()
+    wide = torch.full((rows, H + 9), 5.0, dtype=torch.bfloat16, device="cuda")
+    v = wide[:, shift:shift + H]
+    q = sv.spec_quantize_fp4(x, fmt, values=v)
+    small = torch.empty((5, H), dtype=torch.bfloat16, device="cuda")
+    want = sv.spec_quantize_fp4(few.cuda(), fmt, values=small)
+    _check_quantized(want, small, few, fmt)
+    n = -(-H // plain.BLOCK[fmt])
+    got_scales, clear = plain.scale_bytes(q["scales"].cpu().numpy(), rows, n)
+    want_scales, _ = plain.scale_bytes(want["scales"].cpu().numpy(), 5, n)
+    assert clear
+    for part in (slice(0, 5), slice(rows - 5, rows)):
+        assert torch.equal(q["packed"][part], want["packed"]) and torch.equal(v[part], small)
+        assert (got_scales[part] == want_scales).all()
+        if fmt == 1:
+            assert torch.equal(q["row_scales"][part], want["row_scales"])
+    assert (wide[:, :shift] == 5).all() and (wide[:, shift + H:] == 5).all()
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
 def test_quantize_strided_rows(sv, fmt):
     """Rows of a wider tensor (aligned and not), values into a wider tensor, guards kept."""
     for lead, width in ((8, 1024), (3, 1001)):
