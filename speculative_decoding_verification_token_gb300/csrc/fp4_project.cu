@@ -17,11 +17,13 @@
 // powers of two, applied to the sum in the epilogue.
 //
 // Few rows are bound by reading W: 6 rows of 2560 on V = 151936 take 33 us, 6.3 TB/s.  384 rows with
-// fp32 logits (207 MB read, 233 MB written) take 84 us, 5.2 TB/s.  1024 rows of 4096 on
+// fp32 logits (207 MB read, 233 MB written) take 81 us, 5.4 TB/s.  1024 rows of 4096 on
 // V = 129280: 192 us, 5.6 PFLOP/s (204 to 209 once the power cap holds the SMs at 1.77 GHz), the
-// tensor pipe 60% active.  Taken apart at 1024 x 2560 on V = 151936 (160 us): without the products
-// 137, without the loads 131, without the stores 131, so that none bounds it alone; all three share
-// the shared memory's bandwidth.  What made the difference on the way:
+// tensor pipe 60% active.  Wide tiles are bound by the ring: a stage's way round is longer than the
+// products of the stages that fit (see where they are counted).  At 1024 x 2560 on V = 151936 (163 us)
+// half of the hidden rows' loads left out give 158, the scale copies left out 163, two of four
+// products left out and no loads but the scales' 101, with 40 us of products.  Scales copied a
+// k-block ahead, with both k-blocks waited for, took 180.  What made the difference on the way:
 //   - the issuing warps stay converged around elect.sync; in a branch on lane 0 each product took
 //     125 ns to issue (6 rows 48 us, loads or not);
 //   - pairs of CTAs: half of the hidden rows per SM (1024 rows of 4096: 432 -> 355 us);
@@ -54,6 +56,7 @@ struct PjParams {
   int32_t stages;
   uint32_t stage_bytes, b_off, sfa_off, sfb_off;
   uint32_t out_off;  // the epilogue's staging buffers, behind the ring
+  int32_t out_bufs;  // of them per warp, 1 or 2
   uint32_t tx_bytes;  // bytes both CTAs load per stage
   int32_t groups;     // scale groups per row
   const float* w_row;
@@ -446,8 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
     const int q = warp & 3, h = (warp - 2) >> 2;
     const uint32_t lanes = tmem + (uint32_t(32 * q) << 16);
     const uint32_t freed = map_rank(smem_addr(acc_empty), 0);
-    // this warp's two staging buffers of 16 rows of 32 logits
-    uint8_t* const stage0 = ring + p.out_off + (warp - 2) * 2 * kOutBytes;
+    // this warp's staging buffers of 16 rows of 32 logits
+    const bool two = p.out_bufs == 2;
+    uint8_t* const stage0 = ring + p.out_off + (warp - 2) * p.out_bufs * kOutBytes;
     bool failed = false;
     int32_t a = 0, buf = 0;
     uint32_t phase = 0;
@@ -499,8 +503,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
           continue;
         }
         uint8_t* const st = stage0 + buf * kOutBytes;
-        buf ^= 1;
-        tc::bulk_wait_read<1>();  // the store before the last has read this buffer
+        if (two) {
+          buf ^= 1;
+          tc::bulk_wait_read<1>();  // the store before the last has read this buffer
+        } else {
+          tc::bulk_wait_read<0>();
+        }
         __syncwarp();
         if constexpr (sizeof(Out) == 4) {
 #pragma unroll
@@ -664,9 +672,19 @@ extern "C" sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_
   const uint32_t bytes = p.sfb_off + x_tiles * box_groups * 512;
   p.tx_bytes = 2 * bytes;
   p.stage_bytes = (bytes + 1023) / 1024 * 1024;
-  const uint32_t out_bytes = kPjEpiWarps * 2 * 16 * 32 * uint32_t(elem_bytes(dtype));
-  p.stages =
-      int32_t(std::min<uint32_t>(kPjMaxStages, (kPjSmem - 1024 - out_bytes) / p.stage_bytes));
+  // A stage is away for 1.6 us or more, from the products that free it to the arrival of its next
+  // copies, and the products of five stages take 1.3 (256 rows), so every stage counts (1024 rows of
+  // 2560: 206 us with three, 175 with four, 164 with five).  Wide tiles give up their second staging
+  // buffers where that makes room for a stage: 384 rows with fp32 logits 84.6 -> 81.2 us (e4m3 93.8 ->
+  // 85.7), 1024 rows of 4096 241 -> 227.  A single tile with five stages and up to 128 rows do better
+  // with both (160 rows 52.1 for 54.7, 128 rows 49.5 for 52.4).
+  const uint32_t out_bytes = kPjEpiWarps * 16 * 32 * uint32_t(elem_bytes(dtype));
+  auto stages_with = [&](uint32_t bufs) {
+    return std::min<uint32_t>(kPjMaxStages, (kPjSmem - 1024 - bufs * out_bytes) / p.stage_bytes);
+  };
+  const bool wide = p.nt > 128 && (p.n_nt > 1 || stages_with(2) < 5);
+  p.out_bufs = wide && stages_with(1) > stages_with(2) ? 1 : 2;
+  p.stages = int32_t(stages_with(uint32_t(p.out_bufs)));
   p.out_off = uint32_t(p.stages) * p.stage_bytes;
   p.w_row = w_row_scales;
   p.x_row = x_row_scales;
