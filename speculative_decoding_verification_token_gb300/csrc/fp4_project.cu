@@ -21,8 +21,8 @@
 // V = 129280: 192 us, 5.6 PFLOP/s (204 to 209 once the power cap holds the SMs at 1.77 GHz), the
 // tensor pipe 60% active.  Wide tiles are bound by the ring: a stage's way round is longer than the
 // products of the stages that fit (see where they are counted).  At 1024 x 2560 on V = 151936 (163 us)
-// half of the hidden rows' loads left out give 158, the scale copies left out 163, two of four
-// products left out and no loads but the scales' 101, with 40 us of products.  Scales copied a
+// the hidden rows loaded for the first tile only give 158, the scale copies left out 163, two of four
+// products left out with no loads but the scales' 101, with 40 us of products.  Scales copied a
 // k-block ahead, with both k-blocks waited for, took 180.  What made the difference on the way:
 //   - the issuing warps stay converged around elect.sync; in a branch on lane 0 each product took
 //     125 ns to issue (6 rows 48 us, loads or not);
