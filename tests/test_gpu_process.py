@@ -97,6 +97,38 @@ def test_history_bad_data_is_reported(sv):
             assert counts.sum() == 1  # the good row's token
 
 
+@pytest.mark.parametrize("prompt", [False, True])
+@pytest.mark.parametrize("V,n", [(50, 1), (1000, 700), (40001, 9000), (300000, 20)])
+def test_history_of_one_row_replaced(sv, V, n, prompt):
+    """Status of calls with one row, good and bad, over what the word held before."""
+    W = (V + 31) // 32
+    mk = lambda *s: torch.full(s, 3, dtype=torch.int32, device="cuda")  # noqa: E731
+    good = torch.randint(0, V, (1, n), dtype=torch.int32, device="cuda")
+    for at, value, ln, slot, want in ((0, None, n, 1, 0), (n - 1, V, n, 1, 1), (0, None, n + 1, 1, 2),
+                                      (0, None, -1, 1, 2), (0, None, n, 2, 2), (n - 1, V, n - 1, 0, 0)):
+        counts, pb, ob = mk(2, V), mk(2, W), mk(2, W)
+        tok = good.clone()
+        if value is not None:
+            tok[0, at] = value
+        for stale in (0, sv.SV_ERR_BAD_INPUT):
+            st = torch.full((1,), stale, dtype=torch.int32, device="cuda")
+            sv.spec_history_append(tok, counts, pb, ob, prompt=prompt, reset=True, status=st,
+                                   slots=torch.tensor([slot], dtype=torch.int32, device="cuda"),
+                                   lens=torch.tensor([ln], dtype=torch.int32, device="cuda"))
+            assert int(st) == (sv.SV_ERR_BAD_INPUT if want else 0)
+        if want == 2:  # the row is left out
+            assert (counts == 3).all() and (pb == 3).all() and (ob == 3).all()
+            continue
+        x = tok[0, :ln].cpu().numpy()
+        c = np.bincount(x[x < V], minlength=V)
+        bits = plain.bool_to_bits((c > 0)[None])
+        zero = np.zeros_like(bits)
+        assert (counts[slot].cpu().numpy() == (0 if prompt else c)).all()
+        assert (pb[slot].cpu().numpy() == (bits if prompt else zero)[0]).all()
+        assert (ob[slot].cpu().numpy() == (zero if prompt else bits)[0]).all()
+        assert (counts[1 - slot] == 3).all() and (pb[1 - slot] == 3).all()
+
+
 def test_history_reset_without_tokens(sv):
     V = 100
     counts = torch.ones((2, V), dtype=torch.int32, device="cuda")
