@@ -253,6 +253,25 @@ def test_project_many_tiles(sv):
         assert (np.abs(got - want) <= (64 + H / 64) * 2.0 ** -23 * mag).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("M,H", [(512, 1000), (600, 2560), (700, 4096), (300, 1600)])
+def test_project_rows_do_not_depend_on_the_batch(sv, M, H, fmt, dtype):
+    """Several tiles per vocabulary tile and more of those than CTAs: the rows of smaller batches (of
+    one tile, whose figures are tested above), bit for bit: each sum is formed in the order of K."""
+    g = torch.Generator("cuda").manual_seed(M + H)
+    V = 50001
+    x = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    w = sv.spec_quantize_fp4(torch.randn((V, H), generator=g, device="cuda").to(torch.bfloat16), fmt)
+    out = torch.full((M, V + 7), 3.0, dtype=dtype, device="cuda")
+    y = sv.spec_project_fp4(sv.spec_quantize_fp4(x, fmt), w, out=out[:, :V])
+    for a in range(0, M, 128):
+        part = sv.spec_quantize_fp4(x[a:a + 128], fmt)
+        assert torch.equal(y[a:a + 128], sv.spec_project_fp4(part, w, out=torch.empty(
+            (part["rows"], V + 7), dtype=dtype, device="cuda")[:, :V]))
+    assert (out[:, V:] == 3).all()
+
+
 def test_project_same_tensor_and_reruns(sv):
     """Both operands the same tensor; the same bits from every run."""
     x = torch.randn((150, 640), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
