@@ -50,11 +50,11 @@ struct ProcParams {
   const int32_t* mask_row;
   int32_t* status;
   // Who resets the status and reports: each request's first CTA reports, after a kernel that resets
-  // it; with kSingle the only request's first CTA does both; with kChecker CTA 0, which does nothing
+  // it; with kSingle the only request's first CTA does both; with kApart CTA 0, which does nothing
   // else, does both for all requests.
   int32_t reports;
 };
-enum { kFirst = 0, kSingle = 1, kChecker = 2 };
+enum { kFirst = 0, kSingle = 1, kApart = 2 };
 
 constexpr int kProcThreads = 128;
 constexpr int kProcRows = 4;  // rows handled together
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
   constexpr bool kSmall = kRowBytes == kSmallRowBytes;
   // (one dimension: with a grid of three, which needs no division, 128 requests in place took 65 us
   // where they take 62, and the ragged ones 122 for 120)
-  const uint32_t part = blockIdx.x - (kSmall && p.reports == kChecker ? 1u : 0u);
+  const uint32_t part = blockIdx.x - (kSmall && p.reports == kApart ? 1u : 0u);
   const int32_t r = part / (p.chunks * p.splits);
   const int32_t c = part / p.splits % p.chunks;
   const int32_t group = part % p.splits;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kProcThreads, 10)
     b1 = p.bias_start[r + 1];
   }
   for (int w = tid; w < kWords; w += kProcThreads) s_touch[w] = s_bbits[w] = s_drafted[w] = 0;
-  const bool first = c == 0 && group == 0 && !(kSmall && p.reports == kChecker);
+  const bool first = c == 0 && group == 0 && !(kSmall && p.reports == kApart);
   if (tid == 0) {
     s_n = s_nd = 0;
     s_bias0 = ~0u;
@@ -547,14 +547,14 @@ sv_status launch_process(ProcParams p, int32_t B, int sms, cudaStream_t s) {
   const bool few = int64_t(B) * (p.gmax + 1) <= 512 &&
                    (!p.bias_start || p.n_bias + 8 * int64_t(B) <= 1024);
   p.reports = B == 1 || !p.status ? kSingle
-              : kRowBytes == kSmallRowBytes && few ? kChecker
+              : kRowBytes == kSmallRowBytes && few ? kApart
                                                    : kFirst;
   if (p.reports == kFirst) {
     const sv_status st = reset_status(p.status, s);
     if (st != SV_OK) return st;
   }
   const size_t smem = kMode == kCopy ? std::min<int64_t>(kProcRows, most) * kRowBytes : 0;
-  const unsigned ctas = unsigned(chunks * B * p.splits) + (p.reports == kChecker);
+  const unsigned ctas = unsigned(chunks * B * p.splits) + (p.reports == kApart);
   return launch_dependent(process_kernel<E, kMode, kRowBytes>, ctas, kProcThreads, smem, s, p);
 }
 
