@@ -18,7 +18,7 @@
 //
 // Few rows are bound by reading W: 6 rows of 2560 on V = 151936 take 33 us, 6.3 TB/s.  384 rows with
 // fp32 logits (207 MB read, 233 MB written) take 81 us, 5.4 TB/s.  1024 rows of 4096 on
-// V = 129280: 192 us, 5.6 PFLOP/s (204 to 209 once the power cap holds the SMs at 1.77 GHz), the
+// V = 129280: 192 us, 5.6 PFLOP/s (204 to 211 once the power cap holds the SMs at 1.77 GHz), the
 // tensor pipe 60% active.  Wide tiles are bound by the ring: a stage's way round is longer than the
 // products of the stages that fit (see where they are counted).  At 1024 x 2560 on V = 151936 (163 us)
 // the hidden rows loaded for the first tile only give 158, the scale copies left out 163, two of four
