@@ -575,10 +575,10 @@ def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draf
     [B + 1] into ascending bias_tokens int32 and bias_values fp32) and grammar masks (mask int32
     [n, ceil(V / 32)] bit rows, mask_row int32 per logit row, -1: none) on the rows of a round
     (see include/specverify.h).  Works in place unless `out` is another tensor of the same shape
-    and dtype.  Returns out."""
+    and dtype.  Returns out.  Data errors go to `status`; without one they go unreported."""
     if out is None:
         out = logits
-    if status is not None and (_fast or _load_fast()):
+    if _fast or _load_fast():
         code = _fast.process_logits(
             logits, row0, draft_row0, draft_len, max_draft_len, draft_tokens, first_row, bonus_row,
             slots, counts, prompt_bits, output_bits, repetition, presence, frequency, bias_start,
@@ -625,7 +625,7 @@ def spec_process_logits(logits, row0, draft_row0, draft_len, max_draft_len, draf
     if mr is not None:
         mk, ldm = _mat(mask, "mask", i32, dev, None, (V + 31) // 32)
         n_mask = mask.shape[0]
-    status, st = _status_ptr(status, dev)
+    st = _vec(status, "status", torch.int32, None, dev)
     code = lib().spec_process_logits(
         lg, ld, ot, ldo, dt, V, _vec(row0, "row0", i64, B, dev),
         _vec(draft_row0, "draft_row0", i64, B, dev), _vec(draft_len, "draft_len", i32, B, dev),
@@ -726,8 +726,9 @@ def _fp4_operand(t, name, dev):
 def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=None):
     """Logits [M, V] = x w^T of two operands quantised by spec_quantize_fp4: hidden rows x [M, H]
     and the output projection w [V, H] (see include/specverify.h).  `out` (bf16 or fp32, rows
-    16-byte aligned) is allocated in `dtype` if not given.  Returns it."""
-    if status is not None and out is not None and (_fast or _load_fast()) and (
+    16-byte aligned) is allocated in `dtype` if not given.  Returns it.  A wait that ran out is
+    written to `status`; without one it goes unreported."""
+    if out is not None and (_fast or _load_fast()) and (
             x["H"] == w["H"] and x["format"] == w["format"]):
         code = _fast.project_fp4(x["packed"], x["scales"], x["row_scales"], x["rows"], w["packed"],
                                  w["scales"], w["row_scales"], w["rows"], x["H"], x["format"], out,
@@ -748,7 +749,7 @@ def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=N
     op, ld = _mat(out, "out", out.dtype, dev, M, V)
     if out.shape[1] != V:
         raise ValueError(f"out must be [{M}, {V}]")
-    status, st = _status_ptr(status, dev)
+    st = _vec(status, "status", torch.int32, None, dev)
     code = lib().spec_project_fp4(xp, xs, xr, M, wp, ws, wr, V, H, fmt, op, dt, ld, st,
                                   _stream(stream))
     _check(code, "spec_project_fp4")
