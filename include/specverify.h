@@ -23,6 +23,8 @@
  *     row, q(x) = 0 for the drafted token x, a drafted length outside [0, max_draft_len]) are
  *     written to the optional DEVICE word `status` (reset to SV_OK by each call; the first error
  *     found is kept).  Outputs are then undefined.  `status` is NULL -> data errors go unreported.
+ *     (Verification, sampling and drafting launch nothing, not even the reset, where there is
+ *     nothing to do: B = 0, or no draft to sample.)
  *   - A device-side wait that exceeds its bound writes SV_ERR_TIMEOUT to `status`.
  *   - Logits may hold -inf (masked tokens); such tokens are never emitted.
  *   - Rows are `ld` elements apart; the row base addresses must be 16-byte aligned, i.e. the logit

@@ -633,7 +633,8 @@ extern "C" sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_
   if (format != SV_FP4_E8M0_32 && format != SV_FP4_E4M3_16) return SV_ERR_INVALID;
   if (M < 0 || V < 1 || H < 1 || ld < V) return SV_ERR_INVALID;
   if (V > INT32_MAX - 256 || M > (1 << 24) || H > (1 << 24)) return SV_ERR_UNSUPPORTED;
-  if (M == 0) return SV_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) return reset_status(status, s);
   if (!x_packed || !x_scales || !w_packed || !w_scales || !logits) return SV_ERR_INVALID;
   if (format == SV_FP4_E4M3_16 && (!x_row_scales || !w_row_scales)) return SV_ERR_INVALID;
   if (!aligned16(x_packed) || !aligned16(x_scales) || !aligned16(w_packed) ||
@@ -691,7 +692,6 @@ extern "C" sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_
   p.out = logits;
   p.ld = ld;
   p.status = status;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
 
   const uint64_t row_bytes = uint64_t(spec_fp4_row_bytes(H));
   PjMaps m;

@@ -570,7 +570,8 @@ extern "C" sv_status spec_quantize_fp4(const void* x, sv_dtype dtype, int64_t ro
   if (format != SV_FP4_E8M0_32 && format != SV_FP4_E4M3_16) return SV_ERR_INVALID;
   if (rows < 0 || H < 1 || ldx < H || (values && ld_values < H)) return SV_ERR_INVALID;
   if (H > INT32_MAX || rows > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  if (rows == 0) return SV_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) return reset_status(status, s);
   if (!x || !packed || !scales || (format == SV_FP4_E4M3_16 && !row_scales))
     return SV_ERR_INVALID;
   const int eb = elem_bytes(dtype);
@@ -579,7 +580,6 @@ extern "C" sv_status spec_quantize_fp4(const void* x, sv_dtype dtype, int64_t ro
     return SV_ERR_UNSUPPORTED;
   const bool vec = aligned16(x) && (ldx * eb) % 16 == 0 &&
                    (!values || (aligned16(values) && ld_values % 8 == 0));
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const QuantParams p = {static_cast<const uint8_t*>(x),
                          rows,
                          H,

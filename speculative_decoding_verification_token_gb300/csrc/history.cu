@@ -237,7 +237,8 @@ extern "C" sv_status spec_history_append(const int32_t* tokens, int64_t ld_token
       (reset != 0 && reset != 1))
     return SV_ERR_INVALID;
   if (V > INT32_MAX || n > INT32_MAX - 8192) return SV_ERR_UNSUPPORTED;
-  if (B == 0 || (n == 0 && !reset)) return SV_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (B == 0 || (n == 0 && !reset)) return reset_status(status, s);  // nothing else to do
   if ((n > 0 && !tokens) || !counts || !prompt_bits || !output_bits) return SV_ERR_INVALID;
   const bool fill = reset && kind == SV_HISTORY_PROMPT;
   const int64_t marks = ((V + 31) / 32 + kPromptWords - 1) / kPromptWords;
@@ -246,7 +247,6 @@ extern "C" sv_status spec_history_append(const int32_t* tokens, int64_t ld_token
   const int64_t blocks =
       reset ? chunks * B : (int64_t(B) * n + kHistThreads - 1) / kHistThreads;
   if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool one = !reset && int64_t(B) * n <= 1024, one_row = reset && B == 1;
   if (!one && !one_row) {
     const sv_status st = reset_status(status, s);

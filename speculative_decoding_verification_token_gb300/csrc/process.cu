@@ -605,7 +605,8 @@ extern "C" sv_status spec_process_logits(
   const int eb = elem_bytes(dtype);
   if (!aligned16(logits) || !aligned16(out) || (ld * eb) % 16 || (ld_out * eb) % 16)
     return SV_ERR_UNSUPPORTED;
-  if (B == 0) return SV_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (B == 0) return reset_status(status, s);
   if (!row0 || !draft_len) return SV_ERR_INVALID;
   if (repetition || presence || frequency) {
     if (!counts || !prompt_bits || !output_bits || n_slots < 1 || ld_counts < V ||
@@ -619,7 +620,6 @@ extern "C" sv_status spec_process_logits(
     return SV_ERR_INVALID;
   // the most CTAs any mode launches
   if ((V + 4095 / eb) / (4096 / eb) * B > INT32_MAX / 32) return SV_ERR_UNSUPPORTED;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const ProcParams p = {static_cast<const uint8_t*>(logits),
                         ld,
                         static_cast<uint8_t*>(out),

@@ -47,3 +47,30 @@ def test_no_status_is_made_that_nobody_can_read(sv, marshalled, monkeypatch):
     assert _allocations(lambda: sv.spec_project_fp4(q, q, out=y)) == 0
     assert torch.isneginf(x[0]).all() and torch.isfinite(x[1]).all()
     assert torch.equal(y, sv.spec_project_fp4(q, q, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("marshalled", [True, False])
+def test_a_call_with_nothing_to_do_resets_the_status(sv, marshalled, monkeypatch):
+    if not marshalled:
+        monkeypatch.setattr(sv, "_fast", None)
+        monkeypatch.setattr(sv, "_load_fast", lambda: None)
+    st = _i32(1)
+    hist = dict(counts=_i32(2, 40), prompt_bits=_i32(2, 2), output_bits=_i32(2, 2), status=st)
+    none = torch.zeros(0, dtype=torch.int64, device="cuda")
+    x = torch.randn((3, 64), device="cuda")
+    calls = [lambda: sv.spec_history_append(_i32(2, 0), **hist),  # no columns
+             lambda: sv.spec_history_append(_i32(0, 5), **hist),  # no rows
+             lambda: sv.spec_history_append(_i32(0, 5), reset=True, **hist),
+             lambda: sv.spec_process_logits(x, none, none, _i32(0), 4, _i32(1), status=st)]
+    for fmt in (sv.SV_FP4_E8M0_32, sv.SV_FP4_E4M3_16):
+        w = sv.spec_quantize_fp4(x, fmt)
+        e = sv.spec_quantize_fp4(x[:0], fmt)
+        rs = e["row_scales"]
+        calls += [lambda fmt=fmt, e=e, rs=rs: sv.spec_quantize_fp4(
+                      x[:0], fmt, packed=e["packed"], scales=e["scales"], row_scales=rs, status=st),
+                  lambda e=e, w=w: sv.spec_project_fp4(e, w, out=torch.zeros((0, 8), device="cuda")[:, :3],
+                                                       status=st)]
+    for k, call in enumerate(calls):
+        st.fill_(sv.SV_ERR_BAD_INPUT)
+        call()
+        assert int(st) == sv.SV_OK, k
