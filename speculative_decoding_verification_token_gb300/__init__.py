@@ -519,9 +519,27 @@ def _mat(t, name, dtype, dev, rows=None, cols=1):
     _refuse(t, name, dtype, f"[{rows or 'rows'}, {cols} or more] with unit column stride")
 
 
-def _status_ptr(status, dev):
+def _empty(shape, dtype, dev, stream):
+    """A tensor of the call's own, not filled, on device `dev`.  Given `stream`, it is that stream's:
+    its memory is not in use by work that the stream has still to wait for, and is not given away
+    before the call has written it.  It outlives the current stream's work too, for a caller who
+    goes on with it there."""
+    device = torch.device("cuda", dev)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def _status_ptr(status, dev, stream):
+    """The status word of a call that returns it, and its pointer; every call resets it."""
     if status is None:
-        status = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", dev))
+        status = _empty(1, torch.int32, dev, stream)
     return status, _vec(status, "status", torch.int32, None, dev)
 
 
@@ -557,7 +575,7 @@ def spec_history_append(tokens, counts, prompt_bits, output_bits, slots=None, le
     B, n = tokens.shape
     if slots is None and B > n_slots:
         raise ValueError("more rows than slots")
-    status, st = _status_ptr(status, dev)
+    status, st = _status_ptr(status, dev, stream)
     code = lib().spec_history_append(
         tk, ldt, _vec(lens, "lens", torch.int32, B, dev), n,
         _vec(slots, "slots", torch.int32, B, dev), B, int(prompt), int(reset), V, n_slots, c, ldc,
@@ -677,17 +695,17 @@ def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=
         raise ValueError("fmt must be SV_FP4_E8M0_32 or SV_FP4_E4M3_16")
     rb, nbytes = _fp4_sizes(rows, H, fmt)
     if packed is None:
-        packed = torch.empty((rows, rb), dtype=torch.uint8, device=x.device)
+        packed = _empty((rows, rb), torch.uint8, dev, stream)
     elif packed.shape != (rows, rb):
         raise ValueError(f"packed must be [{rows}, {rb}]")
     if scales is None:
-        scales = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        scales = _empty(nbytes, torch.uint8, dev, stream)
     elif scales.numel() != nbytes:
         raise ValueError(f"scales must hold {nbytes} bytes")
     rs = None
     if fmt == SV_FP4_E4M3_16:
         if row_scales is None:
-            row_scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+            row_scales = _empty(rows, torch.float32, dev, stream)
         rs = _vec(row_scales, "row_scales", torch.float32, rows, dev)
     else:
         row_scales = None
@@ -696,7 +714,7 @@ def spec_quantize_fp4(x, fmt, packed=None, scales=None, row_scales=None, values=
         vp, ldv = _mat(values, "values", torch.bfloat16, dev, rows, H)
         if values.shape[1] != H:
             raise ValueError("values must have the shape of x")
-    status, st = _status_ptr(status, dev)
+    status, st = _status_ptr(status, dev, stream)
     u8 = torch.uint8
     code = lib().spec_quantize_fp4(xp, dt, rows, H, ldx, fmt,
                                    _vec(packed, "packed", u8, None, dev),
@@ -744,7 +762,7 @@ def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=N
         raise ValueError("x and w must have the same width and format")
     if out is None:
         ld = (V + 7) // 8 * 8  # rows start on 16-byte boundaries
-        out = torch.empty((M, ld), dtype=dtype, device=x["packed"].device)[:, :V]
+        out = _empty((M, ld), dtype, dev, stream)[:, :V]
     dt = _dtype_code(out)
     op, ld = _mat(out, "out", out.dtype, dev, M, V)
     if out.shape[1] != V:
