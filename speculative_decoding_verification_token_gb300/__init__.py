@@ -2,12 +2,14 @@
 
 The functions below carry the names of the C entry points declared in ``include/specverify.h`` and
 do argument marshalling only: every step runs in the library's CUDA kernels.  Tensors must live on
-the current CUDA device; outputs that are not supplied are allocated with torch.  The library is
-loaded on first use and its absence raises -- there is no other implementation to fall back to.
+the current CUDA device; outputs that are not supplied are allocated with torch, for the stream that
+the call runs on.  The library is loaded on first use and its absence raises -- there is no other
+implementation to fall back to.
 """
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 import threading
@@ -164,6 +166,38 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _torch_stream(stream):
+    """The torch stream of any object with a cuda_stream."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _on_its_stream(call):
+    """A call with a parameter `stream` whose own tensors -- outputs, status, workspace -- belong
+    to the stream it runs on: their memory is not in use by work that the stream has still to wait
+    for, and their fills are in order with the kernels.  Results are kept for the current stream
+    too, for a caller who goes on with them there."""
+    at = call.__code__.co_varnames.index("stream")
+
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if len(args) > at:
+            args, stream = args[:at] + (None,) + args[at + 1:], args[at]
+        if stream is None:
+            return call(*args, **kw)
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(_torch_stream(stream)):
+            out = call(*args, **kw)
+        results = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,)
+        for t in results:
+            if t is not None:
+                t.record_stream(here)
+        return out
+
+    return run
+
+
 def _dtype_code(t):
     if t.dtype == torch.bfloat16:
         return SV_BF16
@@ -193,9 +227,12 @@ _ws_cache = {}
 
 
 def workspace(nbytes, device=None):
-    """A cached device buffer of at least `nbytes` bytes (256-byte aligned, from torch)."""
+    """A cached device buffer of at least `nbytes` bytes (256-byte aligned, from torch), one for each
+    host thread and stream: calls on two streams must not share their scratch.  A larger request
+    replaces it, so a captured graph that outlives that wants a workspace of its own."""
     device = torch.device(device or torch.cuda.current_device())
-    key = (device.index, threading.get_ident())
+    index = torch.cuda.current_device() if device.index is None else device.index
+    key = (index, threading.get_ident(), torch._C._cuda_getCurrentRawStream(index))
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -257,6 +294,7 @@ def _verify(block, target, draft, target_row0, draft_row0, draft_len, max_draft_
     return out
 
 
+@_on_its_stream
 def spec_verify_token(target, draft, target_row0, draft_row0, draft_len, max_draft_len,
                       draft_tokens, seed, request_ids=None, out_ld=None, want_ratio=True,
                       status=None, workspace=None, stream=None):
@@ -265,6 +303,7 @@ def spec_verify_token(target, draft, target_row0, draft_row0, draft_len, max_dra
                    draft_tokens, seed, request_ids, out_ld, want_ratio, status, workspace, stream)
 
 
+@_on_its_stream
 def spec_verify_block(target, draft, target_row0, draft_row0, draft_len, max_draft_len,
                       draft_tokens, seed, request_ids=None, out_ld=None, want_rows=True,
                       status=None, workspace=None, stream=None):
@@ -277,6 +316,7 @@ def spec_verify_lmhead_workspace_bytes(B, max_draft_len, V, H):
     return int(lib().spec_verify_lmhead_workspace_bytes(B, max_draft_len, V, H))
 
 
+@_on_its_stream
 def spec_verify_lmhead(target_hidden, draft_hidden, W, target_row0, draft_row0, draft_len,
                        max_draft_len, draft_tokens, seed, request_ids=None, out_ld=None,
                        want_ratio=True, status=None, workspace=None, stream=None):
@@ -320,6 +360,7 @@ def spec_verify_lmhead(target_hidden, draft_hidden, W, target_row0, draft_row0, 
             "accept_ratio": ratio, "recomputed": recomputed, "status": status}
 
 
+@_on_its_stream
 def spec_sample_draft(draft, draft_row0, draft_len, max_draft_len, seed, request_ids=None,
                       draft_tokens=None, status=None, workspace=None, stream=None):
     """Sample draft tokens from q for every drafted row; returns the token tensor (by draft row)."""
@@ -345,6 +386,7 @@ def spec_sample_draft(draft, draft_row0, draft_len, max_draft_len, seed, request
 
 # ---- vocabulary-sharded verification ------------------------------------------------------------
 
+@_on_its_stream
 def spec_verify_shard_stats(target, draft, v_off, V_total, target_row0, draft_row0, draft_len,
                             max_draft_len, draft_tokens, status=None, workspace=None, stream=None):
     """This shard's statistics of every drafted row pair and the drafted tokens' logits (-inf
@@ -373,6 +415,7 @@ def spec_verify_shard_stats(target, draft, v_off, V_total, target_row0, draft_ro
     return stats, tok
 
 
+@_on_its_stream
 def spec_verify_shard_merge(stats_all, tok_all, stream=None):
     """Statistics of every shard ([n, rows, 4]) merged in shard order; drafted-token logits
     ([n, rows, 2]) from the shard that holds each token."""
@@ -386,6 +429,7 @@ def spec_verify_shard_merge(stats_all, tok_all, stream=None):
     return stats, tok
 
 
+@_on_its_stream
 def spec_verify_shard_race(target, draft, v_off, V_total, target_row0, draft_row0, draft_len,
                            max_draft_len, draft_tokens, seed, stats, tok, request_ids=None,
                            want_ratio=True, status=None, workspace=None, stream=None):
@@ -414,6 +458,7 @@ def spec_verify_shard_race(target, draft, v_off, V_total, target_row0, draft_row
     return {"accepted_len": acc, "winners": winners, "accept_ratio": ratio, "status": status}
 
 
+@_on_its_stream
 def spec_verify_shard_finish(winners_all, accepted_len, draft_row0, draft_tokens, out_ld,
                              status=None, stream=None):
     """The largest winner over the shards ([n, B, 2]) and the request outputs."""
@@ -528,9 +573,7 @@ def _empty(shape, dtype, dev, stream):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     here = torch.cuda.current_stream()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream)):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(here)
     return t
@@ -780,6 +823,7 @@ def dspark_markov_workspace_bytes(B, K, V, R):
     return int(lib().dspark_markov_workspace_bytes(B, K, V, R))
 
 
+@_on_its_stream
 def dspark_markov_draft(backbone, U, Wt, anchor, conf_scores, sts_T, seed, request_ids=None,
                         want_logits=True, want_stats=True, status=None, workspace=None,
                         stream=None):
@@ -827,6 +871,7 @@ SV_STOP_ARGMAX = 1
 SV_STOP_FIXED_DEPTH = 2
 
 
+@_on_its_stream
 def dspark_schedule(cond_accept, max_len, sps, B_max, want_survival=True, status=None,
                     workspace=None, stream=None, rule=SV_STOP_FIRST_DROP):
     """Hardware-aware prefix scheduler.  cond_accept fp32 [N, K]; sps fp64 [B_max + 1]; rule:
@@ -852,6 +897,7 @@ def dspark_schedule(cond_accept, max_len, sps, B_max, want_survival=True, status
             "status": status}
 
 
+@_on_its_stream
 def dspark_schedule_async(conf_ring, round_, cond_prior, max_len, sps, B_max, rule=SV_STOP_FIRST_DROP,
                           want_survival=True, status=None, workspace=None, stream=None):
     """Round `round_` scheduled with the confidences of round `round_` - 2: conf_ring fp32
@@ -880,6 +926,7 @@ def dspark_schedule_async(conf_ring, round_, cond_prior, max_len, sps, B_max, ru
             "status": status}
 
 
+@_on_its_stream
 def dspark_acceptance_update(sel_len, accepted_len, trials, accepts, decay=1.0, prior_a=1.0,
                              prior_b=1.0, alpha=None, cond_accept_out=None, status=None,
                              stream=None):
@@ -905,6 +952,7 @@ def dspark_acceptance_update(sel_len, accepted_len, trials, accepts, decay=1.0, 
     return {"alpha": alpha, "cond_accept": cond_accept_out, "status": status}
 
 
+@_on_its_stream
 def dspark_sts_fit(scores, sel_len, accepted_len, iters=30, beta_min=1.0 / 16, beta_max=16.0,
                    nbins=15, status=None, stream=None):
     """Per-position temperatures of the confidence head fitted to verified outcomes (scores fp32
