@@ -14,7 +14,8 @@
 //               registers at once so that the accumulator is free again, then through shared
 //               memory to the logits by TMA stores.
 // The tensor cores apply the block scales and add in fp32; the row scales of SV_FP4_E4M3_16 are
-// powers of two, applied to the sum in the epilogue.
+// powers of two, applied to the sum in the epilogue (with kMinRow, kMaxRow, so that neither alone
+// takes it out of binary32's range).
 //
 // Few rows are bound by reading W: 6 rows of 2560 on V = 151936 take 33 us, 6.3 TB/s.  384 rows with
 // fp32 logits (207 MB read, 233 MB written) take 81 us, 5.4 TB/s.  1024 rows of 4096 on
@@ -46,6 +47,13 @@ constexpr uint32_t kPjABytes = kPjRows * 128;
 constexpr uint32_t kPjSmem = 225 * 1024;  // ring and alignment slack
 constexpr int kPjMaxStages = 10;
 constexpr uint32_t kPjTmemCols = 512;
+
+// Row scales of W between which a sum f of products may be multiplied by them first and by the row
+// scale of the hidden row then.  f is 0 or 2^-20 <= |f| < 2^47 (codes of 0.5 under two scales of
+// 2^-9, and 2^24 products of 2688^2), so f * w is a normal number and exact, and the second product
+// rounds the logit once.  Other row scales (2^-120 .. 2^117 are possible) go through binary64; real
+// weights never do.
+constexpr float kMinRow = 0x1p-100f, kMaxRow = 0x1p64f;
 
 struct PjParams {
   int32_t n_vt, n_nt, nt;  // tiles of 256 vocabulary rows, hidden-row tiles, their rows
@@ -486,14 +494,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPjThreads, 1)
         phase ^= 1;
       }
       if (v0 >= p.V) continue;
+      const bool plain_rows =
+          kFmt != SV_FP4_E4M3_16 || __all_sync(0xffffffffu, ws >= kMinRow && ws <= kMaxRow);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int32_t c = 16 * (h + 4 * i);
         if (c >= n) break;
         if constexpr (kFmt == SV_FP4_E4M3_16) {
+          if (plain_rows) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            f[i][j] = f[i][j] * ws * __shfl_sync(0xffffffffu, xs[i], j);
+            for (int j = 0; j < 16; ++j)
+              f[i][j] = f[i][j] * ws * __shfl_sync(0xffffffffu, xs[i], j);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              f[i][j] = static_cast<float>(double(f[i][j]) * double(ws) *
+                                           double(__shfl_sync(0xffffffffu, xs[i], j)));
+          }
         }
         if (v0 + 32 > p.V) {  // a TMA store clips a row at 16 bytes only: these 32 one by one
           Out* const o = static_cast<Out*>(p.out) + int64_t(n0 + c) * p.ld + v0 + lane;
