@@ -594,7 +594,7 @@ def _history(counts, prompt_bits, output_bits, dev):
     words = (V + 31) // 32
     pb, ldb = _mat(prompt_bits, "prompt_bits", i32, dev, n_slots, words)
     ob, ldo = _mat(output_bits, "output_bits", i32, dev, n_slots, words)
-    if ldo != ldb:
+    if ldo != ldb and n_slots > 1:
         raise ValueError("prompt_bits and output_bits must have the same stride")
     return c, pb, ob, n_slots, ldc, ldb, V
 

@@ -118,8 +118,8 @@ History history(Call& c, PyObject* counts, PyObject* prompt, PyObject* output) {
   h.prompt = c.mat<uint32_t>(prompt, at::kInt, &rows, &cols, &h.ldb);
   c.ok = c.ok && rows == h.n_slots && cols >= (h.V + 31) / 32;
   h.output = c.mat<uint32_t>(output, at::kInt, &rows, &cols, &ld);
-  c.ok = c.ok && rows == h.n_slots && cols >= (h.V + 31) / 32 && ld == h.ldb &&
-         h.n_slots <= INT32_MAX;
+  c.ok = c.ok && rows == h.n_slots && cols >= (h.V + 31) / 32 &&
+         (ld == h.ldb || h.n_slots == 1) && h.n_slots <= INT32_MAX;
   return h;
 }
 
