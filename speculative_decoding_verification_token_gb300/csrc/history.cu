@@ -84,9 +84,10 @@ constexpr int kResetThreads = 256;
 constexpr int kResetWords = 256;  // 32-token words of a slot that one CTA owns
 constexpr int kResetAhead = 8;    // tokens a thread has in flight
 
-// Clear, then append: each CTA owns kResetWords words of one slot and the counts below them, so the
-// two steps need no order between CTAs.  It clears its counts, reads the row's tokens (at most a few
-// tens of KB, from L2 for all CTAs of a slot but the first) and keeps those in its range.
+// Clear, then append emitted tokens (prompts: history_prompt_kernel): each CTA owns kResetWords words
+// of one slot and the counts below them, so the two steps need no order between CTAs.  It clears its
+// counts, reads the row's tokens (at most a few tens of KB, from L2 for all CTAs of a slot but the
+// first) and keeps those in its range.
 __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams p,
                                                                       int32_t chunks) {
   __shared__ uint32_t s_bits[kResetWords];
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams
   } else {
     for (int64_t v = v0 + tid; v < v1; v += kResetThreads) cnt[v] = 0;
   }
-  if (!p.prompt) __syncthreads();  // the counts are zero before this CTA's atomics reach them
+  __syncthreads();  // the counts are zero before this CTA's atomics reach them
   for (int32_t t0 = 0; t0 < n; t0 += kResetAhead * kResetThreads) {
     if (t0) fetch(t0);
 #pragma unroll
@@ -137,13 +138,13 @@ __global__ void __launch_bounds__(kResetThreads) history_reset_kernel(HistParams
       const uint32_t b = 1u << (x[q] & 31);
       uint32_t* word = &s_bits[(x[q] - v0) >> 5];
       if (!(*reinterpret_cast<volatile uint32_t*>(word) & b)) atomicOr(word, b);
-      if (!p.prompt) atomicAdd(cnt + x[q], 1);
+      atomicAdd(cnt + x[q], 1);
     }
   }
   __syncthreads();
   if (w0 + tid < (p.V + 31) / 32) {
-    p.prompt_bits[slot * p.ld_bits + w0 + tid] = p.prompt ? s_bits[tid] : 0u;
-    p.output_bits[slot * p.ld_bits + w0 + tid] = p.prompt ? 0u : s_bits[tid];
+    p.prompt_bits[slot * p.ld_bits + w0 + tid] = 0u;
+    p.output_bits[slot * p.ld_bits + w0 + tid] = s_bits[tid];
   }
 }
 
