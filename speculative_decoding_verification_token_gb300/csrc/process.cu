@@ -629,7 +629,7 @@ extern "C" sv_status spec_process_logits(
                         draft_row0,
                         draft_len,
                         max_draft_len,
-                        first_row,
+                        std::min(first_row, max_draft_len + 1),  // no row is that far
                         bonus_row,
                         draft_tokens,
                         0,
