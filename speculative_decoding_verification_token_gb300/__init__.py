@@ -10,14 +10,18 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import importlib
+import importlib.machinery
 import os
 import re
 import threading
+import warnings
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
+FASTCALL_PATH = os.path.join(_HERE, "_fastcall" + importlib.machinery.EXTENSION_SUFFIXES[0])
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "specverify.h")
 
 SV_OK, SV_ERR_INVALID, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_BAD_INPUT, SV_ERR_TIMEOUT = range(6)
@@ -114,15 +118,19 @@ def lib():
 
 
 def _bind_fastcall(L):
-    """Gives the marshalling module the entry points' addresses.  A library built without it (the
-    module file is missing) is called through ctypes alone."""
+    """Gives the marshalling module the entry points' addresses.  Where it is missing, or does not
+    load, the library is called through ctypes alone."""
     global _fast
-    if not os.path.exists(os.path.join(_HERE, "_fastcall.so")):
+    if not os.path.exists(FASTCALL_PATH):
         return
-    from . import _fastcall
-    _fastcall.bind(*(C.cast(getattr(L, name), C.c_void_p).value for name in (
+    try:
+        module = importlib.import_module("._fastcall", __name__)
+    except ImportError as e:
+        warnings.warn(f"_fastcall is not used, it does not load ({e}): build again", RuntimeWarning)
+        return
+    module.bind(*(C.cast(getattr(L, name), C.c_void_p).value for name in (
         "spec_history_append", "spec_process_logits", "spec_quantize_fp4", "spec_project_fp4")))
-    _fast = _fastcall
+    _fast = module
 
 
 def status_string(code):
