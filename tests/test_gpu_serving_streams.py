@@ -134,3 +134,45 @@ def test_captured_on_a_stream_beside_the_capturing_one(sv):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert [int(t) for t in st] == [sv.SV_OK] * 3 + [sv.SV_ERR_BAD_INPUT] * 2
+
+
+@pytest.mark.parametrize("marshalled", [True, False])
+def test_every_tensor_given(sv, marshalled, monkeypatch):
+    """All outputs and the status given, inputs made before: the calls on a side stream, behind long
+    work there, equal those on the current one."""
+    if not marshalled:
+        monkeypatch.setattr(sv, "_fast", None)
+        monkeypatch.setattr(sv, "_load_fast", lambda: None)
+
+    def outputs(s):
+        rows, V, H = s["rows"], s["V"], s["H"]
+        u8 = dict(dtype=torch.uint8, device="cuda")
+        n = [sv.spec_fp4_scale_bytes(k, H, 1) for k in (V, rows)]
+        return dict(status=torch.full((1,), 9, dtype=torch.int32, device="cuda"),
+                    w=dict(packed=torch.zeros((V, H // 2), **u8), scales=torch.zeros(n[0], **u8),
+                           row_scales=torch.zeros(V, device="cuda")),
+                    x=dict(packed=torch.zeros((rows, H // 2), **u8), scales=torch.zeros(n[1], **u8),
+                           row_scales=torch.zeros(rows, device="cuda")),
+                    y=torch.zeros((rows, 1016), device="cuda")[:, :V])
+
+    def run(s, o, stream):
+        kw = dict(status=o["status"], stream=stream)
+        h = dict(counts=s["counts"], prompt_bits=s["pb"], output_bits=s["ob"])
+        sv.spec_history_append(s["tok"], **h, **kw)
+        wq = sv.spec_quantize_fp4(s["w"], 1, **o["w"], **kw)
+        xq = sv.spec_quantize_fp4(s["x"], 1, **o["x"], **kw)
+        sv.spec_project_fp4(xq, wq, out=o["y"], **kw)
+        sv.spec_process_logits(o["y"], s["row0"], None, s["zero"], 0, None, repetition=s["rep"],
+                               **h, **kw)
+        return [o["status"], o["y"], s["counts"], s["ob"], *o["w"].values(), *o["x"].values()]
+
+    ins = [_inputs(), _inputs()]
+    outs = [outputs(s) for s in ins]
+    want = run(ins[0], outs[0], None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10_000_000)
+    got = run(ins[1], outs[1], side)
+    torch.cuda.synchronize()
+    assert int(got[0]) == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
