@@ -17,12 +17,12 @@
 // powers of two, applied to the sum in the epilogue (with kMinRow, kMaxRow, so that neither alone
 // takes it out of binary32's range).
 //
-// Few rows are bound by reading W: 6 rows of 2560 on V = 151936 take 33 us, 6.3 TB/s.  384 rows with
-// fp32 logits (207 MB read, 233 MB written) take 81 us, 5.4 TB/s.  1024 rows of 4096 on
-// V = 129280: 192 us, 5.6 PFLOP/s (204 to 211 once the power cap holds the SMs at 1.77 GHz), the
-// tensor pipe 60% active.  Wide tiles are bound by the ring: a stage's way round is longer than the
-// products of the stages that fit (see where they are counted).  At 1024 x 2560 on V = 151936 (163 us)
-// the hidden rows loaded for the first tile only give 158, the scale copies left out 163, two of four
+// Few rows are bound by reading W: 6 rows of 2560 on V = 151936 take 33.6 us, 6.2 TB/s.  384 rows with
+// fp32 logits (207 MB read, 233 MB written) take 82 us, 5.4 TB/s.  1024 rows of 4096 on V = 129280 take
+// 209 us in a loop of calls, 5.2 PFLOP/s, where the power cap holds the SMs at 1.77 GHz (the first
+// hundred calls, at 2.07 GHz, 192); the tensor pipe is 62% active.  Wide tiles are bound by the ring: a
+// stage's way round is longer than the products of the stages that fit (see where they are counted).
+// At 1024 x 2560 on V = 151936, e8m0 (163 us), the hidden rows loaded for the first tile only give 158, the scale copies left out 163, two of four
 // products left out with no loads but the scales' 101, with 40 us of products.  Scales copied a
 // k-block ahead, with both k-blocks waited for, took 180.  What made the difference on the way:
 //   - the issuing warps stay converged around elect.sync; in a branch on lane 0 each product took
@@ -694,7 +694,7 @@ extern "C" sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_
   // copies, and the products of five stages take 1.3 (256 rows), so every stage counts (1024 rows of
   // 2560: 206 us with three, 175 with four, 164 with five).  Wide tiles give up their second staging
   // buffers where that makes room for a stage: 384 rows with fp32 logits 84.6 -> 81.2 us (e4m3 93.8 ->
-  // 85.7), 1024 rows of 4096 241 -> 227.  A single tile with five stages and up to 128 rows do better
+  // 85.7), 1024 rows of 4096 6% less.  A single tile with five stages and up to 128 rows do better
   // with both (160 rows 52.1 for 54.7, 128 rows 49.5 for 52.4).
   const uint32_t out_bytes = kPjEpiWarps * 16 * 32 * uint32_t(elem_bytes(dtype));
   auto stages_with = [&](uint32_t bufs) {

@@ -288,7 +288,7 @@ __device__ __forceinline__ void store_vec(const RowOut& o, int64_t ahead, const 
 
 constexpr int kQuantThreads = 256;
 
-// Latency bounds the hidden rows of a round: 384 x 2560 take 4.4 us a call, most of it the two
+// Latency bounds the hidden rows of a round: 384 x 2560 take 4.3 to 4.8 us a call, most of it the two
 // launches.
 //
 // Blocks of 32: a warp takes kN spans of 256 elements (two scale groups) of one row; the padding
@@ -351,7 +351,7 @@ constexpr bool staging_fits(int threads) {
   return kAlign != 0 || threads / 32 * (kN * 256 * In<E>::kBytes + 4) <= 48 * 1024;
 }
 
-// Memory and issue slots bound it alike: 151936 x 2560 bf16 with values take 262 us, 6.8 TB/s (the
+// Memory and issue slots bound it alike: 151936 x 2560 bf16 with values take 263 us, 6.8 TB/s (the
 // rate of a copy) at 74% of the issue slots.  A persistent form with the next row in registers took
 // 368: 112 registers leave too few warps.
 //

@@ -54,7 +54,7 @@ __device__ __forceinline__ int32_t* reset_reports(const HistParams& p, int32_t c
 }
 
 // One thread per token: a round appends a few hundred, so the call is one launch of one or two
-// dependent loads and two atomics, and the launch is what it costs (64 x 6 tokens: 2.7 us a call in
+// dependent loads and two atomics, and the launch is what it costs (64 x 6 tokens: 2.5 us a call in
 // a loop, host time included).  A single CTA (one = true) resets the status itself, which saves the
 // short call a second launch.
 __global__ void __launch_bounds__(1024) history_append_kernel(HistParams p, bool one) {
@@ -156,8 +156,10 @@ constexpr int kClearTokens = 16384;  // counts one CTA clears
 // A slot's history replaced by a prompt.  The prompt touches no counts, so clearing them and
 // collecting the tokens need no order: of each slot's CTAs the first `marks` read the tokens, once,
 // and write the bit rows whole, the others clear 64 KB of counts each.  32 prompts of up to 8192
-// tokens, V = 129280: 6.4 us a call, of which the 18 MB written would take 2.7; the rest is launches
-// and the tokens' latency (with the kernel above, whose CTAs each read all tokens, 9.5).
+// tokens, V = 129280: 6.3 us a call, of which the 18 MB written would take 2.7; the rest is the two
+// launches and the CTAs that mark, whose 32 warps compete for their SM's issue slots ("not selected"
+// leads the stalls, then the tokens' latency; with the kernel above, whose CTAs each read all tokens,
+// 9.5).
 __global__ void __launch_bounds__(kPromptThreads) history_prompt_kernel(HistParams p,
                                                                         int32_t marks,
                                                                         int32_t ctas) {

@@ -191,10 +191,10 @@ __device__ __forceinline__ void check_requests(const ProcParams& p, int32_t B, b
 //                 there, bulk copies take them to `out`;
 //   in place      masks store -inf where they ban and edits touch single elements.
 // Memory traffic bounds it where rows move: 384 rows of 151936 bf16 with histories of up to 2000
-// tokens and 300 biases take 41.3 us, 5.7 TB/s of logits (without histories and biases 37); a CTA
+// tokens and 300 biases take 41.5 us, 5.7 TB/s of logits (without histories and biases 37); a CTA
 // is a chain of four dependent loads (parameters; bits and tokens; counts and mask words; rows), so
 // ten small CTAs an SM, four rows each time, do better than fewer with more rows (eight: 165 us for
-// the 256 ragged requests that take 120).  In place it is sectors: a banned or edited element costs
+// the 256 ragged requests that take 118).  In place it is sectors: a banned or edited element costs
 // the 32 or 64 bytes around it, read and written, so that 512 masked rows of 129280 (2% allowed) and
 // the edits of 512 others move 340 MB for 144 MB of elements: 62 us.
 template <typename E, int kMode, uint32_t kRowBytes>
