@@ -199,7 +199,7 @@ def _on_its_stream(call):
             out = call(*args, **kw)
         results = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,)
         for t in results:
-            if t is not None:
+            if t is not None and t.is_cuda:  # not an output of the caller's in pinned host memory
                 t.record_stream(here)
         return out
 

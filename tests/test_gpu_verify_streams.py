@@ -115,3 +115,22 @@ def test_stream_as_a_positional_argument(sv):
     torch.cuda.synchronize()
     got = sv.dspark_schedule(*args, side, sv.SV_STOP_ARGMAX)
     _same(got, want)
+
+
+def test_an_output_in_pinned_host_memory(sv):
+    """What the caller gives may lie in host memory that the device can write."""
+    N, K = 5, 3
+    i32 = dict(dtype=torch.int32, device="cuda")
+    sel, acc = torch.full((N,), K, **i32), torch.tensor([0, 1, 2, 3, 3], **i32)
+
+    def update(out, stream):
+        n = [torch.zeros(K, dtype=torch.float64, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        r = sv.dspark_acceptance_update(sel, acc, *n, cond_accept_out=out, stream=stream)
+        torch.cuda.synchronize()
+        assert int(r["status"]) == 0
+        return r["cond_accept"]
+
+    want = update(torch.zeros((N, K), device="cuda"), None)
+    got = update(torch.zeros((N, K)).pin_memory(), torch.cuda.Stream())
+    assert not got.is_cuda and torch.equal(got, want.cpu())
