@@ -85,6 +85,9 @@ typedef enum { SV_FP4_E8M0_32 = 0, SV_FP4_E4M3_16 = 1 } sv_fp4_format;
 /* Largest drafted length per request accepted by the verify calls and the Markov head. */
 #define SV_MAX_DRAFT_LEN 64
 
+/* Most rows of a request (its root and its drafts) where they form a tree. */
+#define SV_MAX_TREE_ROWS 128
+
 /* Human-readable name of a status code (static string). */
 const char* sv_status_string(sv_status status);
 
@@ -410,6 +413,112 @@ sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_scales,
                            const uint8_t* w_scales, const float* w_row_scales, int64_t V,
                            int64_t H, int32_t format, void* logits, sv_dtype dtype, int64_t ld,
                            int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * A round over a paged key/value cache: the rows that verification scores, made by a target whose
+ * drafts may form a tree.  No page covers these calls; they are what an engine runs around the ones
+ * above: append and attention in every layer, then (for trees) sampled tokens, accept and keep.
+ *
+ * Cache, all DEVICE, owned by the caller: k_cache and v_cache bf16, element d of head h of place t
+ * of page g at g * page_stride + t * token_stride + h * head_stride + d (both caches alike).
+ * Place j of request r lies in page page_table[r * ld_pages + j / page_size] (int32), at j %
+ * page_size; a request has max_pages columns of the table.  ctx_len[r] (int32): the places filled
+ * by earlier rounds.
+ *
+ * Rows: request r's are row0[r] + i, i = 0 .. n - 1, n = draft_len[r] + bonus_row, among n_rows
+ * rows in all.  bonus_row = 1: row 0 is the last emitted token and row i the i-th draft (the target
+ * rows of verification); 0: drafts or a prompt alone.  Row i's place is ctx_len[r] + i.
+ * parents (nullable, int32, indexed like the rows): row i hangs from row parents[row0[r] + i] < i
+ * of the request, or from the context (-1); NULL: a chain, row i from row i - 1.  A row's position
+ * is ctx_len[r] + its depth (0 below the context), and it sees the context, its ancestors and
+ * itself.  With parents n is at most SV_MAX_TREE_ROWS; chains may be longer (prompts).
+ * Lengths out of range (draft_len outside [0, max_draft_len], rows outside the n_rows, places past
+ * the table), pages outside [0, n_pages), parents outside [-1, i): SV_ERR_BAD_INPUT in status.  No
+ * call reads or writes outside the arrays it is given for them.
+ * Rows, heads, tokens and pages are 16-byte aligned (bases and strides).
+ * ------------------------------------------------------------------------------------------- */
+
+/* Keys and values of a round's rows written to the cache, queries to q_out (bf16), each rounded
+ * once.  q, k, v: `dtype`, row r's head h at r * ld + h * head stride.  cos_sin (nullable: no
+ * rotation): fp32 [n_positions][ld_cos_sin], the cosines of a position's rot / 2 angles, then their
+ * sines; the first `rot` elements of every head of q and k turn by them, a' = a cos - b sin, b' =
+ * a sin + b cos (binary32) with pairs (a, b) at (e, e + rot / 2), or at (2 e, 2 e + 1) if adjacent =
+ * 1.  A position outside [0, n_positions) is SV_ERR_BAD_INPUT.
+ * q and q_out may be NULL (n_heads = 0), and q_out may be q itself (bf16, equal strides).  Places
+ * other than the rows' are not written.  Different rows must have different places.
+ * D and rot multiples of 16, rot <= D <= 256. */
+sv_status spec_cache_append(const void* q, int64_t ldq, int64_t q_head, const void* k, int64_t ldk,
+                            int64_t k_head, const void* v, int64_t ldv, int64_t v_head,
+                            sv_dtype dtype, int64_t n_rows, int32_t n_heads, int32_t n_kv_heads,
+                            int32_t D, const float* cos_sin, int64_t ld_cos_sin,
+                            int64_t n_positions, int32_t rot, int32_t adjacent,
+                            const int64_t* row0, const int32_t* draft_len, int32_t max_draft_len,
+                            int32_t bonus_row, const int32_t* parents, int32_t B,
+                            const int32_t* ctx_len, const int32_t* page_table, int64_t ld_pages,
+                            int32_t max_pages, void* q_out, int64_t ldqo, int64_t qo_head,
+                            void* k_cache, void* v_cache, int64_t n_pages, int32_t page_size,
+                            int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                            int32_t* status, void* stream);
+
+/* Workspace bytes of spec_tree_attention (0 for sizes the call rejects). */
+size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t max_draft_len, int32_t bonus_row,
+                                           int32_t n_heads, int32_t n_kv_heads, int32_t D);
+
+/* Attention of a round's rows over the cache, their own places included (spec_cache_append first).
+ * For row i and query head h, over the places j that the row sees, with the key head h / (n_heads /
+ * n_kv_heads):   x_j = scale q . k_j,   out = sum_j e^(x_j) v_j / sum_j e^(x_j),
+ * lse (nullable, fp32 [n_rows][ld_lse]) = log sum_j e^(x_j).
+ * q and out: bf16 as for spec_cache_append.  Products are taken in bf16 with fp32 sums; e^(x_j - m)
+ * is rounded to bf16 for its product with v_j, and added up in fp32 for the denominator.  Places
+ * that a row does not see do not reach its result, whatever they hold, NaN included.  Rows that
+ * belong to no request are not written.  n_heads a multiple of n_kv_heads, at most 128 times it;
+ * D 64 or 128; page_size a power of two, at least 8; scale finite. */
+sv_status spec_tree_attention(const void* q, int64_t ldq, int64_t q_head, int64_t n_rows,
+                              int32_t n_heads, int32_t n_kv_heads, int32_t D, float scale,
+                              const int64_t* row0, const int32_t* draft_len,
+                              int32_t max_draft_len, int32_t bonus_row, const int32_t* parents,
+                              int32_t B, const int32_t* ctx_len, const int32_t* page_table,
+                              int64_t ld_pages, int32_t max_pages, const void* k_cache,
+                              const void* v_cache, int64_t n_pages, int32_t page_size,
+                              int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                              void* out, int64_t ldo, int64_t o_head, float* lse, int64_t ld_lse,
+                              int32_t* status, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Verification of a tree of drafts by tokens sampled from the target.  sampled (DEVICE int32,
+ * indexed like the rows) holds one token drawn from each row's distribution (spec_sample_draft on
+ * the target rows with a seed of its own, or their argmax); row i > 0 of request r is the drafted
+ * token draft_tokens[draft_row0[r] + i - 1].  From row 0 the walk goes to the child whose token was
+ * sampled at the row it stands on (the lowest such child), until there is none; the token sampled
+ * there ends the round.  Every token emitted is thus a sample of the target's distribution behind
+ * the tokens before it, whatever was drafted.
+ * Outputs: accepted_len[B], out_tokens[B][out_ld] (out_ld >= max_draft_len + 1) and correction_token
+ * (nullable) as for spec_verify_token; path (nullable) int32 [B][ld_path] (ld_path >=
+ * max_draft_len): the accepted rows, then -1.  Columns of out_tokens from max_draft_len + 1 on, and
+ * of path from max_draft_len on, are not written.  A negative sampled token on the way is
+ * SV_ERR_BAD_INPUT.  max_draft_len below SV_MAX_TREE_ROWS. */
+sv_status spec_tree_accept(const int32_t* sampled, const int32_t* draft_tokens,
+                           const int32_t* parents, const int64_t* row0, const int64_t* draft_row0,
+                           const int32_t* draft_len, int32_t max_draft_len, int32_t B,
+                           int64_t n_rows, int64_t n_drafts, int32_t* accepted_len,
+                           int32_t* out_tokens, int64_t out_ld, int32_t* correction_token,
+                           int32_t* path, int64_t ld_path, int32_t* status, void* stream);
+
+/* The accepted rows' keys and values moved behind the context, in place: for i < accepted_len[r]
+ * place ctx_len[r] + path[r][i] goes to place ctx_len[r] + 1 + i, in each of n_layers caches
+ * layer_stride elements apart; place ctx_len[r] (row 0) stays.  path (int32 [B][ld_path], n_path
+ * columns, fewer than SV_MAX_TREE_ROWS): strictly ascending from 1 or more; NULL: a chain, whose
+ * entries lie in place.  new_len (nullable, not ctx_len itself) = ctx_len + 1 + accepted_len, the
+ * next round's ctx_len.  Other places keep what they hold, the rejected rows' among them.
+ * accepted_len outside [0, n_path] or a path that does not ascend: SV_ERR_BAD_INPUT, that request
+ * is left out.  Requests must not share the pages of their own rows.  D a multiple of 8. */
+sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t* path, int64_t ld_path,
+                          int32_t n_path, int32_t B, const int32_t* ctx_len,
+                          const int32_t* page_table, int64_t ld_pages, int32_t max_pages,
+                          void* k_cache, void* v_cache, int32_t n_layers, int64_t layer_stride,
+                          int64_t n_pages, int32_t page_size, int64_t page_stride,
+                          int64_t token_stride, int64_t head_stride, int32_t n_kv_heads, int32_t D,
+                          int32_t* new_len, int32_t* status, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * DSpark draft side.

@@ -12,6 +12,7 @@ import ctypes as C
 import functools
 import importlib
 import importlib.machinery
+import math
 import os
 import re
 import threading
@@ -29,6 +30,7 @@ SV_F32, SV_BF16 = 0, 1
 SV_HISTORY_OUTPUT, SV_HISTORY_PROMPT = 0, 1
 SV_FP4_E8M0_32, SV_FP4_E4M3_16 = 0, 1
 SV_MAX_DRAFT_LEN = 64
+SV_MAX_TREE_ROWS = 128
 SV_NOALLOC_SCRATCH_BYTES = 8 << 20  # scratch array of spec_verify_token_noalloc
 
 _lock = threading.Lock()
@@ -100,6 +102,17 @@ def lib():
             "spec_fp4_scale_bytes": (sz, [i64, i64, i32]),
             "spec_quantize_fp4": (st, [P, st, i64, i64, i64, i32, P, P, P, P, i64, P, P]),
             "spec_project_fp4": (st, [P, P, P, i64, P, P, P, i64, i64, i32, P, st, i64, P, P]),
+            "spec_cache_append": (st, [P, i64, i64, P, i64, i64, P, i64, i64, st, i64, i32, i32, i32,
+                                       P, i64, i64, i32, i32, P, P, i32, i32, P, i32, P, P, i64,
+                                       i32, P, i64, i64, P, P, i64, i32, i64, i64, i64, P, P]),
+            "spec_tree_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
+            "spec_tree_attention": (st, [P, i64, i64, i64, i32, i32, i32, C.c_float, P, P, i32, i32,
+                                         P, i32, P, P, i64, i32, P, P, i64, i32, i64, i64, i64, P,
+                                         i64, i64, P, i64, P, P, sz, P]),
+            "spec_tree_accept": (st, [P, P, P, P, P, P, i32, i32, i64, i64, P, P, i64, P, P, i64, P,
+                                      P]),
+            "spec_cache_keep": (st, [P, P, i64, i32, i32, P, P, i64, i32, P, P, i32, i64, i64, i32,
+                                     i64, i64, i64, i32, i32, P, P, P]),
             "dspark_schedule_rule": (st, [P, P, i32, i32, P, i32, i32, P, P, P, P, P, P, sz, P]),
             "dspark_schedule_async": (st, [P, i32, i64, P, P, i32, i32, P, i32, i32, P, P, P, P, P,
                                            P, sz, P]),
@@ -823,6 +836,195 @@ def spec_project_fp4(x, w, out=None, dtype=torch.bfloat16, status=None, stream=N
                                   _stream(stream))
     _check(code, "spec_project_fp4")
     return out
+
+
+# ---- a round over a paged key/value cache ---------------------------------------------------------
+
+def _heads(t, name, dtype, dev, rows=None, heads=None, D=None):
+    """(pointer, row stride, head stride) of a tensor [rows, heads, D] whose last axis is dense.  The
+    stride of an axis of one says nothing: one that fits the checks will do."""
+    try:
+        n, h, d = t.shape
+        ld, hs, step = t.stride()
+        if (t.get_device() == dev and t.dtype == dtype and (step == 1 or d <= 1)
+                and (rows is None or n == rows) and (heads is None or h == heads)
+                and (D is None or d == D)):
+            return t.data_ptr(), ld if n > 1 else h * d, hs if h > 1 else d
+    except (AttributeError, ValueError):
+        pass
+    _refuse(t, name, dtype, f"[{rows or 'rows'}, {heads or 'heads'}, {D or 'D'}] with a dense last axis")
+
+
+def _caches(k_cache, v_cache, dev, layers=False):
+    """(k pointer, v pointer, layers, layer stride, pages, page size, page stride, place stride,
+    head stride, heads, D) of caches [pages, page size, heads, D], or [layers, ...], alike."""
+    try:
+        shape, st = k_cache.shape, k_cache.stride()
+        if (v_cache.shape == shape and k_cache.get_device() == v_cache.get_device() == dev
+                and k_cache.dtype == v_cache.dtype == torch.bfloat16
+                and len(shape) in ((4, 5) if layers else (4,)) and (st[-1] == 1 or shape[-1] <= 1)):
+            if v_cache.stride() == st:
+                one = len(shape) == 4
+                # (the strides of an axis of one say nothing)
+                ls, ps, ts, hs = (s if n > 1 else 0 for s, n in
+                                  zip(((0,) + st if one else st)[:4], ((1,) + shape if one else shape)))
+                return (k_cache.data_ptr(), v_cache.data_ptr(), 1 if one else shape[0], ls, shape[-4],
+                        shape[-3], ps, ts, hs, shape[-2], shape[-1])
+            raise ValueError("k_cache and v_cache must have the same strides")
+    except AttributeError:
+        pass
+    _refuse(k_cache, "k_cache, v_cache", torch.bfloat16,
+            "[%spages, page size, heads, D], alike, with a dense last axis" %
+            ("(layers,) " if layers else ""))
+
+
+def spec_cache_append(q, k, v, k_cache, v_cache, page_table, ctx_len, row0, draft_len,
+                      max_draft_len, cos_sin=None, adjacent=False, parents=None, bonus_row=True,
+                      q_out=None, status=None, stream=None):
+    """A round's keys and values k, v [rows, kv heads, D] (bf16 or fp32) to the paged caches bf16
+    [pages, page size, kv heads, D], and its queries q [rows, heads, D] (or None) to q_out (bf16; q
+    itself works in place), queries and keys rotated by cos_sin fp32 [positions, rot] (cosines, then
+    sines; pairs (2 e, 2 e + 1) if `adjacent`, else (e, e + rot / 2)).  page_table int32 [B, pages of
+    a request], ctx_len int32 [B]; row0, draft_len, bonus_row as in spec_process_logits; parents
+    int32 [rows] if the rows form trees (see include/specverify.h).  Returns q_out.  Data errors go
+    to `status`; without one they go unreported."""
+    dev = _device_of(k, "k")
+    dt = _dtype_code(k)
+    kp, ldk, hk = _heads(k, "k", k.dtype, dev)
+    rows, n_kv, D = k.shape
+    vp, ldv, hv = _heads(v, "v", k.dtype, dev, rows, n_kv, D)
+    kc, vc, _, _, pages, page, ps, ts, hs, ch, cd = _caches(k_cache, v_cache, dev)
+    if ch != n_kv or cd != D:
+        raise ValueError("k and the caches must have the same heads and D")
+    qp = op = None
+    n_heads = ldq = hq = ldo = ho = 0
+    if q is not None:
+        qp, ldq, hq = _heads(q, "q", k.dtype, dev, rows, None, D)
+        n_heads = q.shape[1]
+        if q_out is None:
+            q_out = _empty((rows, n_heads, D), torch.bfloat16, dev, stream)
+        op, ldo, ho = _heads(q_out, "q_out", torch.bfloat16, dev, rows, n_heads, D)
+    cs, ldcs, positions, rot = None, 0, 0, 0
+    if cos_sin is not None:
+        cs, ldcs = _mat(cos_sin, "cos_sin", torch.float32, dev)
+        positions, rot = cos_sin.shape
+    i32, i64 = torch.int32, torch.int64
+    B = draft_len.numel()
+    pt, ldp = _mat(page_table, "page_table", i32, dev, B, 0)
+    code = lib().spec_cache_append(
+        qp, ldq, hq, kp, ldk, hk, vp, ldv, hv, dt, rows, n_heads, n_kv, D, cs, ldcs, positions, rot,
+        int(adjacent), _vec(row0, "row0", i64, B, dev), _vec(draft_len, "draft_len", i32, B, dev),
+        int(max_draft_len), int(bonus_row), _vec(parents, "parents", i32, rows, dev), B,
+        _vec(ctx_len, "ctx_len", i32, B, dev), pt, ldp, page_table.shape[1], op, ldo, ho, kc, vc,
+        pages, page, ps, ts, hs, _vec(status, "status", i32, None, dev), _stream(stream))
+    _check(code, "spec_cache_append")
+    return q_out
+
+
+def spec_tree_attention_workspace_bytes(B, max_draft_len, bonus_row, n_heads, n_kv_heads, D):
+    return int(lib().spec_tree_attention_workspace_bytes(B, max_draft_len, int(bonus_row), n_heads,
+                                                         n_kv_heads, D))
+
+
+@_on_its_stream
+def spec_tree_attention(q, k_cache, v_cache, page_table, ctx_len, row0, draft_len, max_draft_len,
+                        parents=None, bonus_row=True, scale=None, out=None, lse=None, status=None,
+                        workspace=None, stream=None):
+    """Attention of a round's rows q bf16 [rows, heads, D] over the paged caches (their own places
+    included: spec_cache_append first): every row sees its request's context, its ancestors by
+    `parents` (None: the rows before it) and itself (see include/specverify.h).  scale: 1 / sqrt(D)
+    if not given.  lse fp32 [rows, heads] takes the logarithms of the denominators.  Returns out
+    (bf16, as q).  Data errors go to `status`; without one they go unreported."""
+    dev = _device_of(q, "q")
+    bf16, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+    qp, ldq, hq = _heads(q, "q", bf16, dev)
+    rows, n_heads, D = q.shape
+    kc, vc, _, _, pages, page, ps, ts, hs, n_kv, cd = _caches(k_cache, v_cache, dev)
+    if cd != D:
+        raise ValueError("q and the caches must have the same D")
+    if out is None:
+        out = torch.empty((rows, n_heads, D), dtype=bf16, device=q.device)
+    op, ldo, ho = _heads(out, "out", bf16, dev, rows, n_heads, D)
+    lp, ldl = None, 0
+    if lse is not None:
+        lp, ldl = _mat(lse, "lse", torch.float32, dev, rows, n_heads)
+    B = draft_len.numel()
+    pt, ldp = _mat(page_table, "page_table", i32, dev, B, 0)
+    if workspace is None:
+        workspace = globals()["workspace"](spec_tree_attention_workspace_bytes(
+            B, int(max_draft_len), bonus_row, n_heads, n_kv, D), q.device)
+    wp = _vec(workspace, "workspace", torch.uint8, None, dev)
+    code = lib().spec_tree_attention(
+        qp, ldq, hq, rows, n_heads, n_kv, D, 1.0 / math.sqrt(D) if scale is None else float(scale),
+        _vec(row0, "row0", i64, B, dev), _vec(draft_len, "draft_len", i32, B, dev),
+        int(max_draft_len), int(bonus_row), _vec(parents, "parents", i32, rows, dev), B,
+        _vec(ctx_len, "ctx_len", i32, B, dev), pt, ldp, page_table.shape[1], kc, vc, pages, page, ps,
+        ts, hs, op, ldo, ho, lp, ldl, _vec(status, "status", i32, None, dev), wp,
+        workspace.numel(), _stream(stream))
+    _check(code, "spec_tree_attention")
+    return out
+
+
+def spec_tree_accept(sampled, draft_tokens, parents, row0, draft_row0, draft_len, max_draft_len,
+                     accepted_len=None, out_tokens=None, path=None, correction=None, status=None,
+                     stream=None):
+    """Verification of trees of drafts by tokens sampled from the target's rows (sampled int32
+    [rows]; see include/specverify.h): the walk from row 0 to the children that were sampled.
+    parents int32 [rows], None: chains.  Returns a dict: accepted_len [B], out_tokens
+    [B, max_draft_len + 1] and correction [B] as spec_verify_token's, path [B, max_draft_len] (the
+    accepted rows, then -1), status."""
+    dev = _device_of(sampled, "sampled")
+    i32, i64 = torch.int32, torch.int64
+    B = draft_len.numel()
+    g = int(max_draft_len)
+    if accepted_len is None:
+        accepted_len = _empty(B, i32, dev, stream)
+    if out_tokens is None:
+        out_tokens = _empty((B, g + 1), i32, dev, stream)
+    if path is None:
+        path = _empty((B, g), i32, dev, stream)
+    if correction is None:
+        correction = _empty(B, i32, dev, stream)
+    rows, n_drafts = sampled.numel(), draft_tokens.numel()
+    status, st = _status_ptr(status, dev, stream)
+    ot, ldo = _mat(out_tokens, "out_tokens", i32, dev, B, g + 1)
+    pp, ldp = _mat(path, "path", i32, dev, B, g)
+    code = lib().spec_tree_accept(
+        _vec(sampled, "sampled", i32, None, dev), _vec(draft_tokens, "draft_tokens", i32, None, dev),
+        _vec(parents, "parents", i32, rows, dev), _vec(row0, "row0", i64, B, dev),
+        _vec(draft_row0, "draft_row0", i64, B, dev), _vec(draft_len, "draft_len", i32, B, dev), g, B,
+        rows, n_drafts, _vec(accepted_len, "accepted_len", i32, B, dev), ot, ldo,
+        _vec(correction, "correction", i32, B, dev), pp, ldp, st, _stream(stream))
+    _check(code, "spec_tree_accept")
+    return {"accepted_len": accepted_len, "out_tokens": out_tokens, "path": path,
+            "correction": correction, "status": status}
+
+
+def spec_cache_keep(k_cache, v_cache, page_table, ctx_len, accepted_len, path, new_len=None,
+                    status=None, stream=None):
+    """The accepted rows' entries moved behind the context in the caches bf16 [pages, page size, kv
+    heads, D] or [layers, pages, ...], in place: place ctx_len + path[:, i] to ctx_len + 1 + i for
+    i < accepted_len (see include/specverify.h).  path int32 [B, n], or None for chains.  Returns
+    new_len int32 [B] = ctx_len + 1 + accepted_len, the next round's ctx_len.  Data errors go to
+    `status`; without one they go unreported."""
+    dev = _device_of(accepted_len, "accepted_len")
+    i32 = torch.int32
+    B = accepted_len.numel()
+    kc, vc, layers, ls, pages, page, ps, ts, hs, n_kv, D = _caches(k_cache, v_cache, dev, True)
+    pt, ldt = _mat(page_table, "page_table", i32, dev, B, 0)
+    pp, ldp, n_path = None, 0, 2**31 - 1
+    if path is not None:
+        pp, ldp = _mat(path, "path", i32, dev, B, 0)
+        n_path = path.shape[1]
+    if new_len is None:
+        new_len = _empty(B, i32, dev, stream)
+    code = lib().spec_cache_keep(
+        _vec(accepted_len, "accepted_len", i32, B, dev), pp, ldp, n_path, B,
+        _vec(ctx_len, "ctx_len", i32, B, dev), pt, ldt, page_table.shape[1], kc, vc, layers, ls, pages,
+        page, ps, ts, hs, n_kv, D, _vec(new_len, "new_len", i32, B, dev),
+        _vec(status, "status", i32, None, dev), _stream(stream))
+    _check(code, "spec_cache_keep")
+    return new_len
 
 
 # ---- DSpark draft side ------------------------------------------------------------------------

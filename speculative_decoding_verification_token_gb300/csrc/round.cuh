@@ -1,0 +1,66 @@
+// round.cuh -- a round's rows over a paged key/value cache, as spec_cache_append,
+// spec_tree_attention and spec_cache_keep take them.
+#pragma once
+
+#include "dependent.cuh"
+
+namespace sv {
+
+struct RoundParams {
+  const int64_t* row0;
+  const int32_t* draft_len;
+  const int32_t* parents;  // null: chains
+  const int32_t* ctx_len;
+  const int32_t* page_table;
+  int64_t ld_pages;
+  int64_t n_rows;
+  int64_t n_pages;
+  int32_t B, max_draft_len, bonus_row;
+  int32_t max_pages, page_size;
+};
+
+// The caches: element strides, the same in both.
+struct CacheParams {
+  __nv_bfloat16 *k, *v;
+  int64_t page_stride, token_stride, head_stride;
+};
+
+struct Request {
+  int64_t first;  // row of the request's row 0
+  int32_t n;      // rows
+  int32_t ctx;    // places filled before
+};
+
+// Request r's sizes; false if any is out of range: the request is then left alone.
+__device__ __forceinline__ bool round_request(const RoundParams& p, int32_t r, Request& q) {
+  const int32_t drafts = p.draft_len[r];
+  q.ctx = p.ctx_len[r];
+  q.first = p.row0[r];
+  q.n = drafts + p.bonus_row;
+  const bool ok = drafts >= 0 && drafts <= p.max_draft_len && q.ctx >= 0 && q.first >= 0 &&
+                  q.first <= p.n_rows && q.n <= p.n_rows - q.first &&
+                  int64_t(q.ctx) + q.n <=
+                      min(int64_t(p.max_pages) * p.page_size, int64_t(INT32_MAX));
+  if (!ok) q.n = 0;
+  return ok;
+}
+
+// Page of place `at`; -1 where the table names none.
+__device__ __forceinline__ int32_t round_page(const RoundParams& p, int32_t r, int32_t at) {
+  const int32_t g = p.page_table[r * p.ld_pages + at / p.page_size];
+  return g >= 0 && g < p.n_pages ? g : -1;
+}
+
+// Host side: what the calls over the cache check alike.
+inline bool round_sizes_ok(int32_t max_draft_len, int32_t bonus_row, int32_t B, int64_t n_rows,
+                           int64_t ld_pages, int32_t max_pages, int64_t n_pages,
+                           int32_t page_size) {
+  return max_draft_len >= 0 && (bonus_row == 0 || bonus_row == 1) && B >= 0 && n_rows >= 0 &&
+         max_pages >= 0 && ld_pages >= max_pages && n_pages >= 0 && page_size >= 1;
+}
+
+inline bool aligned_bf16(const void* p, int64_t a, int64_t b, int64_t c) {
+  return aligned16(p) && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
+}
+
+}  // namespace sv
