@@ -1,101 +1,1004 @@
 // tree_attention.cu -- attention of a round's rows over the paged cache (spec_tree_attention).
 //
-// A CTA per (row, query head): its warps share the keys out, each keeps a running maximum, sum and
-// output, and they are joined at the end.
+// The rows of a request are few and its keys many, so a tile puts the keys where a matrix instruction
+// is wide and the rows where it is narrow: with K a tile of 128 places, Q the rows of all query heads of
+// one key head (kN columns: token i, head g in column i G + g) and V the tile's values,
+//   S^T = K Q^T   (128 x kN, TMEM lane = place, column = row),
+//   P^T = 2^(scale log2(e) S^T - m)   in bf16 to shared memory,
+//   O^T += V^T P^T   (D x kN, lane = element of the head).
+// K and V go in as they lie in the cache (K with its elements, V with its places along the contraction);
+// a row costs a 16th of the narrowest instruction, where it would be padded to 128 the other way round.
+//   warps 0-3  softmax: a place a thread.  m is a bound of the columns' maxima that is raised only when
+//              a score passes it by more than 8 (P then reaches 2^8, in 16 bits as exact as 1), so that
+//              nearly every tile costs no reduction over the places; the sums of P stay with the places
+//              and are added over them at the end;
+//   warp 4     TMA loads of K and V, page by page, into a ring;
+//   warp 5     tcgen05.mma: S of a tile ahead of the product with V of the one before;
+//   warp 6     the next work item: its sizes, its rows' queries, and for trees who sees whom.
+// The work -- (request, key head, row tile, key tile) -- is one list, cut into equal runs for a
+// persistent CTA on every SM, wherever the cuts fall; what a cut leaves in parts goes to the workspace
+// and is joined by a second kernel.
 #include "round.cuh"
+#include "tc.cuh"
+#include "tmap.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace sv {
 namespace {
 
+constexpr int kTile = 128;        // places of a tile
+constexpr int kAttnThreads = 256;
+constexpr int kSoftWarps = 4;
+constexpr uint32_t kAttnSmem = 232448 - 1024;  // dynamic shared memory of a CTA, less what is static
+constexpr float kSlack = 8.f;     // log2 of what P may reach before m is raised
+
 struct AttnParams {
   RoundParams rd;
-  CacheParams cache;
-  const __nv_bfloat16* q;
+  const __nv_bfloat16 *q, *v_cache;
+  int64_t page_stride, token_stride, head_stride;
   int64_t ldq, q_head;
-  int32_t n_heads, group, D;
+  int32_t n_heads, n_kv, group;
+  int32_t tokens;    // tokens of a row tile
+  int32_t box_rows;  // places of a TMA box
+  int32_t stages;
   float scale2;  // scale * log2(e)
   __nv_bfloat16* out;
   int64_t ldo, o_head;
   float* lse;
   int64_t ld_lse;
   int32_t* status;
+  uint8_t* ws;
 };
 
-constexpr int kAttnWarps = 4;
+// A cut item: what the joining kernel needs of it, left by the CTA that its first part lies in.
+struct Cut {
+  int64_t total;      // tiles of the whole call
+  int64_t first_row;  // the row tile's first row
+  int32_t columns, head, last, valid;
+};
+
+// Workspace: per CTA its error, its cut, and two parts (0: of an item begun before it, 1: of one it
+// begins) of kN x (D + 2) binary32: [kN][D] sums, [kN] maxima, [kN] denominators.
+struct WsLayout {
+  size_t cuts, parts, part_floats, bytes;
+};
+__host__ __device__ inline WsLayout ws_layout(int ctas, int n, int d) {
+  WsLayout w;
+  w.cuts = (size_t(ctas) * 4 + 255) / 256 * 256;
+  w.parts = w.cuts + (size_t(ctas) * sizeof(Cut) + 255) / 256 * 256;
+  w.part_floats = size_t(n) * (d + 2);
+  w.bytes = w.parts + size_t(ctas) * 2 * w.part_floats * 4;
+  return w;
+}
+
+// ---- the list of work ------------------------------------------------------------------------------
+
+__device__ __forceinline__ int32_t tiles_of(const Request& q, int32_t rt, int32_t tokens) {
+  return int32_t((int64_t(q.ctx) + min(q.n, (rt + 1) * tokens) + kTile - 1) / kTile);
+}
+
+// Tiles of one key head of a request (its row tiles together).
+__device__ __forceinline__ int64_t tiles_of_head(const Request& q, int32_t tokens) {
+  int64_t t = 0;
+  for (int32_t rt = 0; rt * tokens < q.n; ++rt) t += tiles_of(q, rt, tokens);
+  return t;
+}
+
+struct Span {
+  int64_t total, begin, end;  // tiles of the call, of this CTA
+  int64_t before;             // tiles before request `r`
+  int32_t r;                  // the request that `begin` lies in
+};
+
+// All threads: this CTA's run of the list.
+__device__ void find_span(const AttnParams& p, Span& span, int64_t* warp_sums, int32_t* err) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kAttnThreads / 32;
+  int64_t running = 0, mine = 0, before = 0;
+  // pass 0 adds everything up, pass 1 finds the place; one chunk of requests needs only the first's sums
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) {
+      if (tid == 0) {
+        span.total = running;
+        span.begin = running * blockIdx.x / gridDim.x;
+        span.end = running * (blockIdx.x + 1) / gridDim.x;
+      }
+      __syncthreads();
+      if (span.begin == span.end) return;
+      running = 0;
+    }
+    for (int32_t r0 = 0; r0 < p.rd.B; r0 += kAttnThreads) {
+      const int32_t r = r0 + tid;
+      if (pass == 0 || p.rd.B > kAttnThreads) {
+        mine = 0;
+        if (r < p.rd.B) {
+          Request q;
+          if (!round_request(p.rd, r, q) && blockIdx.x == 0) report(err, SV_ERR_BAD_INPUT);
+          mine = tiles_of_head(q, p.tokens) * p.n_kv;
+        }
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        __syncthreads();
+        if (lane == 31) warp_sums[warp] = upto;
+        __syncthreads();
+        before = upto - mine;
+        for (int w = 0; w < warp; ++w) before += warp_sums[w];
+      }
+      if (pass == 1 && mine > 0) {
+        const int64_t a = running + before;
+        if (a <= span.begin && span.begin < a + mine) {
+          span.before = a;
+          span.r = r;
+        }
+      }
+      for (int w = 0; w < kWarps; ++w) running += warp_sums[w];
+    }
+  }
+  __syncthreads();
+}
+
+// ---- small pieces ----------------------------------------------------------------------------------
+
+__device__ __forceinline__ bool try_wait_for(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return done != 0;
+}
+
+// Wait for phase `parity`, asleep; gives up after kWaitLimitNs and reports it.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t* err) {
+  if (try_wait_for(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!try_wait_for(bar, parity)) {
+    if (global_ns() - t0 > kWaitLimitNs) {
+      report(err, SV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// The same by a whole warp: one answer.
+__device__ __forceinline__ bool wait_for_warp(uint64_t* bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, err));
+}
+
+__device__ __forceinline__ bool elect() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
+// Barrier of the softmax warps that also tells whether `x` held in any thread.
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, 1, 128, q;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(uint32_t(x))
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void soft_sync() { named_sync(1, 32 * kSoftWarps); }
+
+// Largest value of a warp (NaN left out).
+__device__ __forceinline__ float warp_top(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar)),
+      "l"(policy)
+      : "memory");
+}
+
+// 16 bytes to shared memory, zeros if not `take` (the address must be valid all the same).
+__device__ __forceinline__ void async_copy16(void* dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+
+// Shared-memory descriptors of 128-byte swizzled operands by halves (low word: address >> 4 and leading
+// offset, high word: stride offset 1024, version 1, swizzle).  Operands whose rows run along the
+// contraction (K, Q) leave the leading offset unused; in those whose rows run along M or N (V, P: a row
+// of 64 elements a place) it is the distance between groups of 64, and eight places are 1024 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kAlongK = 1u << 16;
+constexpr uint32_t kAcross = (16384u >> 4) << 16;  // groups of 64: 128 places of 128 bytes
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+  return d;
+}
+
+// C columns of this thread's TMEM lane.
+template <int C>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
+  if constexpr (C == 16) tc::tmem_load16(taddr, v);
+  else tc::tmem_load32(taddr, v);
+}
+
+template <int C>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const float* v) {
+#pragma unroll
+  for (int j = 0; j < C; j += 16)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr + j),
+        "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]), "f"(v[j + 5]),
+        "f"(v[j + 6]), "f"(v[j + 7]), "f"(v[j + 8]), "f"(v[j + 9]), "f"(v[j + 10]), "f"(v[j + 11]),
+        "f"(v[j + 12]), "f"(v[j + 13]), "f"(v[j + 14]), "f"(v[j + 15])
+        : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Sums over the lanes of C columns a lane: column lane % C's sum in every lane.
+template <int C>
+__device__ __forceinline__ float column_sums(float* v) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (C == 16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], 16);
+  }
+#pragma unroll
+  for (int o = C / 2; o > 0; o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float give = upper ? v[j] : v[j + o], keep = upper ? v[j + o] : v[j];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ bool not_finite2(uint32_t w) {  // either half of a bf16 pair
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// A work item as the warps of a CTA share it.
+struct Item {
+  int64_t first_row;  // row of the tile's first token
+  int32_t r, head, columns;
+  int32_t base0;   // places below it are seen by every column
+  int32_t end;     // places from it on by none
+  int32_t t0, t1;  // its key tiles in this CTA
+  int32_t whole, begins;
+  int32_t stop;    // no item: the list is at its end
+};
+
+template <int kD, int kN>
+struct AttnShared {
+  static constexpr uint32_t kSlot = kTile * kD * 2;
+  static constexpr uint32_t kQBytes = kN * kD * 2;
+  static constexpr uint32_t kPBytes = (kN + 63) / 64 * 16384;
+  static constexpr int kWords = (kN + 31) / 32;
+  struct Small {
+    uint64_t full[16], empty[16], item_full[2], item_empty[2], s_full[2], p_full, p_free, drain;
+    int64_t col_off[2][kN];  // of a column's output
+    Item item[2];
+    Span span;
+    int64_t warp_sums[kAttnThreads / 32];
+    float m[kN], factor[kN], inv[kN], part[kSoftWarps][kN];
+    uint32_t seen[2][SV_MAX_TREE_ROWS][kWords];  // bit c: column c sees the tree's row
+    uint32_t above[SV_MAX_TREE_ROWS][4];         // rows above a row, itself included
+    int32_t up[SV_MAX_TREE_ROWS];
+    uint32_t bad[SV_MAX_TREE_ROWS / 32];  // places whose values are not all finite
+    uint32_t tmem;
+    int32_t err;
+  };
+  static constexpr uint32_t kSmall = (sizeof(Small) + 127) / 128 * 128;
+  static constexpr int kStages() {
+    const int s = int((kAttnSmem - 1024 - kSmall - 2 * kQBytes - kPBytes) / kSlot);
+    return s < 16 ? s : 16;
+  }
+};
+
+template <int kD, int kN>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
+  using Sh = AttnShared<kD, kN>;
+  constexpr int kC = kN < 32 ? kN : 32;  // columns at a time
+  constexpr int kChunks = kN / kC;
+  constexpr int kStages = Sh::kStages();
+  constexpr uint32_t kCols = kN <= 16 ? 64 : kN <= 32 ? 128 : kN <= 64 ? 256 : 512;
+  static_assert(kStages >= 3, "a ring of three tiles");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const q_at = ring + kStages * Sh::kSlot;
+  uint8_t* const p_at = q_at + 2 * Sh::kQBytes;
+  typename Sh::Small& sm = *reinterpret_cast<typename Sh::Small*>(p_at + Sh::kPBytes);
+
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.item_full[b], 1);
+      mbar_init(&sm.item_empty[b], 3);  // the loads, the products with Q, the softmax
+      mbar_init(&sm.s_full[b], 1);
+    }
+    mbar_init(&sm.p_full, kSoftWarps);
+    mbar_init(&sm.p_free, 1);
+    mbar_init(&sm.drain, 1);
+    fence_barrier_init();
+    sm.err = 0;
+  }
+  if (warp == 5) tc::tmem_alloc(&sm.tmem, kCols);
+  tc::fence_before_sync();
+  dependent_start();
+  __syncthreads();
+  tc::fence_after_sync();
+  find_span(p, sm.span, sm.warp_sums, &sm.err);
+  const uint32_t tmem = sm.tmem;
+  const int32_t n_tiles = int32_t(sm.span.end - sm.span.begin);
+  int32_t* const err = &sm.err;
+  const WsLayout wl = ws_layout(gridDim.x, kN, kD);
+  if (n_tiles == 0) {
+    if (tid == 0) reinterpret_cast<Cut*>(p.ws + wl.cuts)[blockIdx.x].valid = 0;
+  } else if (warp == 6) {
+    // ---- the items ---------------------------------------------------------------------------------
+    int64_t at = sm.span.begin, off = at - sm.span.before;
+    int32_t r = sm.span.r, h = 0, rt = 0;
+    Request rq;
+    round_request(p.rd, r, rq);
+    const int64_t per_head = tiles_of_head(rq, p.tokens);
+    h = int32_t(off / per_head);
+    off -= h * per_head;
+    while (off >= tiles_of(rq, rt, p.tokens)) off -= tiles_of(rq, rt++, p.tokens);
+    Cut cut = {};
+    int64_t built[2] = {-1, -1};
+    bool ok = true;
+    int32_t it = 0;
+    for (; at < sm.span.end && ok; ++it) {
+      const int b = it & 1;
+      const int32_t tok0 = rt * p.tokens, ntok = min(p.tokens, rq.n - tok0);
+      const int32_t columns = ntok * p.group, tiles = tiles_of(rq, rt, p.tokens);
+      Item x;
+      x.first_row = rq.first + tok0;
+      x.r = r, x.head = h, x.columns = columns;
+      x.base0 = rq.ctx + (p.rd.parents ? 0 : tok0);
+      x.end = rq.ctx + tok0 + ntok;
+      x.t0 = int32_t(off);
+      x.t1 = int32_t(min(int64_t(tiles), off + (sm.span.end - at)));
+      x.whole = x.t0 == 0 && x.t1 == tiles;
+      x.begins = x.t0 == 0;
+      x.stop = 0;
+      if (x.begins && !x.whole) {
+        cut.total = sm.span.total;
+        cut.first_row = x.first_row;
+        cut.columns = columns, cut.head = h, cut.valid = 1;
+        cut.last = int32_t(((at + tiles) * gridDim.x - 1) / cut.total);  // the CTA of its last tile
+      }
+      if (it >= 2 && !wait_for_warp(&sm.item_empty[b], ((it >> 1) - 1) & 1, err)) {
+        ok = false;
+        break;
+      }
+      uint8_t* const qb = q_at + b * Sh::kQBytes;
+      for (int32_t c = lane; c < kN; c += 32) {
+        const int32_t i = c / p.group, g = c - i * p.group;
+        const bool in = c < columns;
+        if (in) sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(h * p.group + g) * p.o_head;
+        const __nv_bfloat16* src =
+            in ? p.q + (x.first_row + i) * p.ldq + int64_t(h * p.group + g) * p.q_head : p.q;
+#pragma unroll
+        for (int k = 0; k < kD / 8; ++k)
+          async_copy16(qb + (k >> 3) * kN * 128 + tc::sw128(c, k & 7), src + (in ? k * 8 : 0), in);
+      }
+      const int64_t key = int64_t(r) << 32 | rt;
+      if (p.rd.parents && x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
+        built[b] = key;
+        const int32_t nodes = x.end - rq.ctx;
+        uint32_t a[4][4];
+        for (int32_t i = lane; i < nodes; i += 32) {
+          int32_t up = p.rd.parents[rq.first + i];
+          if (up < -1 || up >= i) {
+            report(err, SV_ERR_BAD_INPUT);
+            up = -1;
+          }
+          sm.up[i] = up;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) sm.above[i][w] = i >> 5 == w ? 1u << (i & 31) : 0u;
+        }
+        __syncwarp();
+        // the way up doubles its length a round: a row takes over what the row at its end has
+        for (int round = 0; round < 7; ++round) {
+          int32_t next[4];
+          bool more = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int32_t i = k * 32 + lane;
+            next[k] = -1;
+            if (i < nodes && sm.up[i] >= 0) {
+              more = true;
+              next[k] = sm.up[sm.up[i]];
+#pragma unroll
+              for (int w = 0; w < 4; ++w) a[k][w] = sm.above[i][w] | sm.above[sm.up[i]][w];
+            }
+          }
+          if (!__any_sync(0xffffffffu, more)) break;
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int32_t i = k * 32 + lane;
+            if (i < nodes && sm.up[i] >= 0) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) sm.above[i][w] = a[k][w];
+              sm.up[i] = next[k];
+            }
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int w = 0; w < Sh::kWords; ++w) {
+          const int32_t c = w * 32 + lane, i = tok0 + c / p.group;
+          const bool in = c < columns;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k * 32 >= nodes) break;
+            const uint32_t mine = in ? sm.above[i][k] : 0u;
+            uint32_t row = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t word = __ballot_sync(0xffffffffu, mine >> j & 1u);
+              if (lane == j) row = word;
+            }
+            sm.seen[b][k * 32 + lane][w] = row;
+          }
+        }
+      }
+      if (lane == 0) sm.item[b] = x;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_full[b]);
+      at += x.t1 - x.t0;
+      off = 0;
+      if (at < sm.span.end && ++rt * p.tokens >= rq.n) {
+        rt = 0;
+        if (++h == p.n_kv) {
+          h = 0;
+          do round_request(p.rd, ++r, rq);
+          while (rq.n == 0);
+        }
+      }
+    }
+    // (one more, to say that there are none)
+    const int b = it & 1;
+    if (ok && (it < 2 || wait_for_warp(&sm.item_empty[b], ((it >> 1) - 1) & 1, err))) {
+      if (lane == 0) {
+        sm.item[b].stop = 1;
+        mbar_arrive(&sm.item_full[b]);
+      }
+    }
+    if (lane == 0) reinterpret_cast<Cut*>(p.ws + wl.cuts)[blockIdx.x] = cut;
+  } else if (warp == 4) {
+    // ---- the loads -----------------------------------------------------------------------------------
+    const uint64_t policy = tc::policy_evict_first();
+    int32_t slot = 0, filled = 0;
+    uint32_t phase = 1;
+    // a tile's boxes, one a lane: its page and first place in it
+    int32_t page = 0, from = 0, boxes = 0, head = 0;
+    int32_t v_page = 0, v_from = 0, v_boxes = 0, v_head = 0;
+    bool ok = true;
+    auto load = [&](const CUtensorMap* map, int32_t pg, int32_t fr, int32_t n, int32_t hd) {
+      if (!wait_for_warp(&sm.empty[slot], phase, err)) return false;
+      uint8_t* const dst = ring + slot * Sh::kSlot;
+      if (elect()) mbar_expect_tx(&sm.full[slot], uint32_t(n) * p.box_rows * kD * 2);
+      __syncwarp();
+      if (lane < n) {
+#pragma unroll
+        for (int k = 0; k < kD / 64; ++k)
+          tma_load_4d(dst + k * 16384 + lane * p.box_rows * 128, map, k * 64, hd, fr, pg,
+                      &sm.full[slot], policy);
+      }
+      __syncwarp();
+      filled = max(filled, slot + 1);
+      if (++slot == kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+      return true;
+    };
+    for (int32_t it = 0; ok; ++it) {
+      const int b = it & 1;
+      if (!wait_for_warp(&sm.item_full[b], (it >> 1) & 1, err)) break;
+      const Item x = sm.item[b];
+      if (x.stop) break;
+      head = x.head;
+      for (int32_t t = x.t0; t < x.t1 && ok; ++t) {
+        boxes = (min(kTile, x.end - t * kTile) + p.box_rows - 1) / p.box_rows;
+        const int32_t place = t * kTile + lane * p.box_rows;
+        page = 0;
+        if (lane < boxes) {
+          page = round_page(p.rd, x.r, place);
+          if (page < 0) {
+            report(err, SV_ERR_BAD_INPUT);
+            page = 0;
+          }
+        }
+        from = place & (p.rd.page_size - 1);
+        ok = load(&map_k, page, from, boxes, head) &&
+             (v_boxes == 0 || load(&map_v, v_page, v_from, v_boxes, v_head));
+        v_page = page, v_from = from, v_boxes = boxes, v_head = head;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[b]);
+    }
+    if (ok && v_boxes) load(&map_v, v_page, v_from, v_boxes, v_head);
+    // every copy in flight lands before the CTA may end
+    for (int32_t k = 0; k < filled; ++k)
+      wait_for_warp(&sm.full[k], k < slot ? phase ^ 1 : phase, err);
+  } else if (warp == 5) {
+    // ---- the products --------------------------------------------------------------------------------
+    constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, kN);
+    constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, kN) | (1u << 15) | (1u << 16);
+    const uint32_t ring_lo = smem_addr(ring) >> 4, q_lo = smem_addr(q_at) >> 4;
+    const uint32_t p_lo = (smem_addr(p_at) >> 4) | kAcross;
+    int32_t slot = 0, t = 0;
+    uint32_t phase = 0;
+    bool ok = true, fresh = false, v_fresh = false;
+    auto next_slot = [&] {
+      if (++slot == kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    // O of the tile before: (+)= V^T P^T
+    auto values = [&] {
+      if (!wait_for_warp(&sm.p_full, (t - 1) & 1, err) || !wait_for_warp(&sm.full[slot], phase, err))
+        return false;
+      tc::fence_after_sync();
+      if (elect()) {
+        const uint32_t v_lo = ring_lo + slot * (Sh::kSlot >> 4) + kAcross;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          tc::mma_bf16(tmem + 2 * kN, desc_of(v_lo + k * 128), desc_of(p_lo + k * 128), kIdO,
+                       !v_fresh || k > 0);
+        tc::mma_commit(&sm.empty[slot]);
+        tc::mma_commit(&sm.p_free);
+      }
+      __syncwarp();
+      next_slot();
+      return true;
+    };
+    for (int32_t it = 0; ok; ++it) {
+      const int b = it & 1;
+      if (!wait_for_warp(&sm.item_full[b], (it >> 1) & 1, err)) break;
+      if (sm.item[b].stop) break;
+      const int32_t n = sm.item[b].t1 - sm.item[b].t0;
+      for (int32_t k = 0; k < n && ok; ++k, ++t) {
+        if (!wait_for_warp(&sm.full[slot], phase, err)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        if (elect()) {
+          const uint32_t k_lo = (ring_lo + slot * (Sh::kSlot >> 4)) | kAlongK;
+          const uint32_t b_lo = (q_lo + b * (Sh::kQBytes >> 4)) | kAlongK;
+#pragma unroll
+          for (int s = 0; s < kD / 16; ++s)
+            tc::mma_bf16(tmem + (t & 1) * kN, desc_of(k_lo + (s >> 2) * 1024 + (s & 3) * 2),
+                         desc_of(b_lo + (s >> 2) * (kN * 8) + (s & 3) * 2), kIdS, s > 0);
+          tc::mma_commit(&sm.empty[slot]);
+          tc::mma_commit(&sm.s_full[t & 1]);
+          if (k + 1 == n) tc::mma_commit(&sm.item_empty[b]);
+        }
+        __syncwarp();
+        next_slot();
+        v_fresh = fresh;
+        fresh = k == 0;
+        if (t > 0) ok = values();
+      }
+    }
+    if (ok && t > 0) {
+      v_fresh = fresh;
+      ok = values();
+    }
+    // nothing reads shared or tensor memory once this has passed
+    if (elect()) tc::mma_commit(&sm.drain);
+    __syncwarp();
+    wait_for_warp(&sm.drain, 0, err);
+  } else if (warp < kSoftWarps) {
+    // ---- softmax and results -------------------------------------------------------------------------
+    const uint32_t lanes = tmem + (uint32_t(32 * warp) << 16);
+    float l[kN];
+    int32_t t = 0;
+    bool ok = true;
+    for (int32_t it = 0; ok; ++it) {
+      const int b = it & 1;
+      if (soft_any(!wait_for(&sm.item_full[b], (it >> 1) & 1, err))) break;
+      const Item& x = sm.item[b];
+      if (x.stop) break;
+      if (tid < kN) sm.m[tid] = kM2Empty;
+      if (tid < SV_MAX_TREE_ROWS / 32) sm.bad[tid] = 0;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) l[c] = 0.f;
+      soft_sync();
+      for (int32_t kt = x.t0; kt < x.t1; ++kt, ++t) {
+        const uint32_t s_at = lanes + (t & 1) * kN;
+        bool free = t == 0;  // P's buffer
+        // a wait that ran out leaves the loop in all four warps together
+        if (soft_any(!wait_for(&sm.s_full[t & 1], (t >> 1) & 1, err))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const bool masked = (kt + 1) * int64_t(kTile) > x.base0;
+        uint32_t seen[Sh::kWords];
+#pragma unroll
+        for (int w = 0; w < Sh::kWords; ++w) seen[w] = ~0u;
+        if (masked) {
+          const int32_t place = kt * kTile + tid, j = place - x.base0;
+          if (place >= x.end) {
+#pragma unroll
+            for (int w = 0; w < Sh::kWords; ++w) seen[w] = 0u;
+          } else if (j >= 0) {
+            if (p.rd.parents) {
+#pragma unroll
+              for (int w = 0; w < Sh::kWords; ++w) seen[w] = sm.seen[b][j][w];
+            } else {  // columns of token j and later ones
+#pragma unroll
+              for (int w = 0; w < Sh::kWords; ++w) {
+                const int32_t from = j * p.group - 32 * w;
+                seen[w] = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+              }
+            }
+          }
+          // Values that some column must not see are finite for the product, a weight of 0 would not
+          // rid it of them: zeros past the end, and zeros for what is not finite, which is added to
+          // the columns that do see it at the end.
+          const int32_t load = t + 1 < n_tiles ? 2 * t + 2 : 2 * t + 1;
+          if (soft_any(!wait_for(&sm.full[load % kStages], (load / kStages) & 1, err))) {
+            ok = false;
+            break;
+          }
+          if (place >= x.base0) {
+            uint8_t* const v = ring + (load % kStages) * Sh::kSlot;
+#pragma unroll 4
+            for (int k = 0; k < kD / 8; ++k) {
+              uint4* const at = reinterpret_cast<uint4*>(v + (k >> 3) * 16384 + tc::sw128(tid, k & 7));
+              if (place >= x.end) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 y = *at;
+              if (not_finite2(y.x) || not_finite2(y.y) || not_finite2(y.z) || not_finite2(y.w)) {
+                uint32_t* const w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                  if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+                }
+                *at = y;
+                atomicOr(&sm.bad[j >> 5], 1u << (j & 31));
+              }
+            }
+          }
+        }
+        // does any score pass its column's m by more than the slack?
+        float s[kC], top = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          tmem_load<kC>(s_at + ch * kC, s);
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            float y = fmaf(s[c], p.scale2, -sm.m[ch * kC + c]);
+            if (masked && !(seen[ch * kC / 32] >> (c & 31) & 1u)) y = -INFINITY;
+            top = fmaxf(top, y);
+          }
+        }
+        if (soft_any(top > kSlack)) {
+#pragma unroll
+          for (int ch = 0; ch < kChunks; ++ch) {
+            float mine = -INFINITY;
+            tmem_load<kC>(s_at + ch * kC, s);
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+              float y = s[c] * p.scale2;
+              if (masked && !(seen[ch * kC / 32] >> (c & 31) & 1u)) y = -INFINITY;
+              const float most = warp_top(y);
+              if (lane == c) mine = most;
+            }
+            if (lane < kC) sm.part[warp][ch * kC + lane] = mine;
+          }
+          soft_sync();
+          if (tid < kN) {
+            const float old = sm.m[tid];
+            const float most = fmaxf(fmaxf(sm.part[0][tid], sm.part[1][tid]),
+                                     fmaxf(sm.part[2][tid], sm.part[3][tid]));
+            const float m = fmaxf(old, most);
+            sm.m[tid] = m;
+            sm.factor[tid] = fast_exp2(old - m);
+          }
+          soft_sync();
+#pragma unroll
+          for (int c = 0; c < kN; ++c) l[c] *= sm.factor[c];
+          if (t > 0) {
+            if (soft_any(!wait_for(&sm.p_free, (t - 1) & 1, err))) {
+              ok = false;
+              break;
+            }
+            free = true;
+            tc::fence_after_sync();
+          }
+          if (kt > x.t0) {  // O has been written
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) {
+              tmem_load<kC>(lanes + 2 * kN + ch * kC, s);
+#pragma unroll
+              for (int c = 0; c < kC; ++c) s[c] *= sm.factor[ch * kC + c];
+              tmem_store<kC>(lanes + 2 * kN + ch * kC, s);
+            }
+          }
+        }
+        if (!free && soft_any(!wait_for(&sm.p_free, (t - 1) & 1, err))) {
+          ok = false;
+          break;
+        }
+        // P, rounded to bf16 for the product (half a step of 2^-8 a weight); its sums take what it was
+        // before that
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          tmem_load<kC>(s_at + ch * kC, s);
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            float y = fmaf(s[c], p.scale2, -sm.m[ch * kC + c]);
+            if (masked && !(seen[ch * kC / 32] >> (c & 31) & 1u)) y = -INFINITY;
+            s[c] = fast_exp2(y);
+            l[ch * kC + c] += s[c];
+          }
+#pragma unroll
+          for (int c = 0; c < kC; c += 8) {
+            uint4 w;
+            uint32_t* const wp = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 two = __floats2bfloat162_rn(s[c + 2 * e], s[c + 2 * e + 1]);
+              wp[e] = *reinterpret_cast<const uint32_t*>(&two);
+            }
+            const int col = ch * kC + c;
+            *reinterpret_cast<uint4*>(p_at + (col >> 6) * 16384 + tc::sw128(tid, (col & 63) >> 3)) = w;
+          }
+        }
+        fence_proxy_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full);
+      }
+      if (!ok) break;
+      // the item's denominators, then its sums
+      if (soft_any(!wait_for(&sm.p_free, (t - 1) & 1, err))) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+#pragma unroll
+      for (int ch = 0; ch < kChunks; ++ch) {
+        const float sum = column_sums<kC>(l + ch * kC);
+        if (lane < kC) sm.part[warp][ch * kC + lane] = sum;
+      }
+      soft_sync();
+      float* const part = reinterpret_cast<float*>(p.ws + wl.parts) +
+                          (2 * int64_t(blockIdx.x) + x.begins) * wl.part_floats;
+      if (tid < x.columns) {
+        const float sum = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]);
+        if (x.whole) {
+          sm.inv[tid] = 1.f / sum;
+          if (p.lse) {
+            const int32_t i = tid / p.group;
+            p.lse[(x.first_row + i) * p.ld_lse + x.head * p.group + tid - i * p.group] =
+                (sm.m[tid] + log2f(sum)) * kLn2;
+          }
+        } else {
+          part[kN * kD + tid] = sm.m[tid];
+          part[kN * kD + kN + tid] = sum;
+        }
+      }
+      soft_sync();
+      if (32 * warp < kD) {
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          if (ch * kC >= x.columns) break;
+          float s[kC];
+          tmem_load<kC>(lanes + 2 * kN + ch * kC, s);
+#pragma unroll 1
+          for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w) {
+            for (uint32_t left = sm.bad[w]; left; left &= left - 1) {  // rare: see above
+              const int32_t j = 32 * w + __ffs(left) - 1, place = x.base0 + j;
+              const int32_t page = max(round_page(p.rd, x.r, place), 0);
+              const float v = __bfloat162float(
+                  p.v_cache[page * p.page_stride +
+                            (place & (p.rd.page_size - 1)) * p.token_stride +
+                            x.head * p.head_stride + tid]);
+              const uint32_t word =
+                  p.rd.parents ? sm.seen[b][j][ch * kC / 32]
+                               : (j * p.group <= ch * kC ? ~0u
+                                  : j * p.group >= ch * kC + 32 ? 0u
+                                                                : ~0u << (j * p.group - ch * kC));
+              if (!isfinite(v)) {
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                  if (word >> c & 1u) s[c] += v;
+              }
+            }
+          }
+          if (x.whole) {
+            // two columns at once: an even lane takes elements (d, d + 1) of one, an odd lane (d - 1,
+            // d) of the next
+            const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
+#pragma unroll
+            for (int c = 0; c < kC; c += 2) {
+              const __nv_bfloat162 two = __floats2bfloat162_rn(s[c] * sm.inv[ch * kC + c],
+                                                               s[c + 1] * sm.inv[ch * kC + c + 1]);
+              const uint32_t mine = *reinterpret_cast<const uint32_t*>(&two);
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+              const int col = ch * kC + c + (lane & 1);
+              if (col < x.columns)
+                *reinterpret_cast<uint32_t*>(p.out + sm.col_off[b][col] + (tid & ~1)) =
+                    __byte_perm(mine, other, pick);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+              if (ch * kC + c < x.columns) part[(ch * kC + c) * kD + tid] = s[c];
+          }
+        }
+      }
+      tc::fence_before_sync();
+      soft_sync();
+      if (tid == 0) mbar_arrive(&sm.item_empty[b]);
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kCols);
+  }
+  if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err;
+}
+
+// ---- the parts of cut items joined -------------------------------------------------------------------
+
+// A warp per column of a CTA's cut item.  Block 0 also gathers the CTAs' errors.
+template <int kD, int kN>
+__global__ void __launch_bounds__(128) join_kernel(AttnParams p, int32_t ctas) {
+  constexpr int kE = kD / 32;
+  constexpr int kBlocks = kN / 4;
+  dependent_start();
+  const WsLayout wl = ws_layout(ctas, kN, kD);
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x < 32 && p.status) {
+    int32_t code = 0;
+    for (int32_t c = lane; c < ctas; c += 32)
+      code = max(code, reinterpret_cast<const int32_t*>(p.ws)[c]);
+    code = __reduce_max_sync(0xffffffffu, code);
+    if (lane == 0) *p.status = code;
+  }
+  const int32_t cta = blockIdx.x / kBlocks;
+  const int32_t col = (blockIdx.x % kBlocks) * 4 + (threadIdx.x >> 5);
+  const Cut cut = reinterpret_cast<const Cut*>(p.ws + wl.cuts)[cta];
+  if (!cut.valid || col >= cut.columns) return;
+  const float* const parts = reinterpret_cast<const float*>(p.ws + wl.parts);
+  // the part in CTA k; none where its run is empty
+  auto part_of = [&](int32_t k) -> const float* {
+    if (k > cta && cut.total * k / ctas == cut.total * (k + 1) / ctas) return nullptr;
+    return parts + (2 * int64_t(k) + (k == cta)) * wl.part_floats;
+  };
+  float top = kM2Empty;
+  for (int32_t k = cta + lane; k <= cut.last; k += 32) {
+    const float* const x = part_of(k);
+    if (x) top = fmaxf(top, x[kN * kD + col]);
+  }
+  top = warp_max(top);
+  float y[kE] = {}, sum = 0.f;
+  for (int32_t k0 = cta; k0 <= cut.last; k0 += 32) {
+    float w = 0.f, d = 0.f;
+    if (k0 + lane <= cut.last) {
+      const float* const x = part_of(k0 + lane);
+      if (x) {
+        w = fast_exp2(x[kN * kD + col] - top);
+        d = w * x[kN * kD + kN + col];
+      }
+    }
+    sum += warp_sum(d);
+    for (int32_t k = k0; k <= min(cut.last, k0 + 31); ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, k - k0);
+      const float* const x = part_of(k);
+      if (!x) continue;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) y[e] += f * x[col * kD + lane * kE + e];
+    }
+  }
+  const int32_t i = col / p.group, h = cut.head * p.group + col - i * p.group;
+  const int64_t row = cut.first_row + i;
+  const float inv = 1.f / sum;
+  __nv_bfloat16* const o = p.out + row * p.ldo + h * p.o_head + lane * kE;
+#pragma unroll
+  for (int e = 0; e < kE; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(o + e) = __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[row * p.ld_lse + h] = (top + log2f(sum)) * kLn2;
+}
+
+// ---- host ----------------------------------------------------------------------------------------------
+
+// Columns of a row tile: the narrowest that takes all of a request's rows, at most 128.
+int32_t columns_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+// [D][heads][places][pages] of a cache, boxes of 64 elements of one head of `box_rows` places.
+bool cache_map(CUtensorMap* map, const void* base, int32_t D, int32_t heads, int32_t page_size,
+               int64_t pages, int64_t head_stride, int64_t token_stride, int64_t page_stride,
+               int32_t box_rows) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(page_size),
+                              cuuint64_t(pages)};
+  // (the stride of an axis of one says nothing)
+  const cuuint64_t st[3] = {heads > 1 ? cuuint64_t(head_stride) * 2 : 16,
+                            page_size > 1 ? cuuint64_t(token_stride) * 2 : 16,
+                            pages > 1 ? cuuint64_t(page_stride) * 2 : 16};
+  const cuuint32_t box[4] = {64, 1, cuuint32_t(box_rows), 1}, es[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, st, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kD, int kN>
+sv_status launch(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, int grid,
+                 cudaStream_t s) {
+  auto* kern = attention_kernel<kD, kN>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
+      cudaSuccess)
+    return SV_ERR_CUDA;
+  const sv_status st =
+      launch_dependent(kern, unsigned(grid), kAttnThreads, kAttnSmem, s, k, v, p);
+  if (st != SV_OK) return st;
+  return launch_dependent(join_kernel<kD, kN>, unsigned(grid) * (kN / 4), 128, 0, s, p, grid);
+}
 
 template <int kD>
-__global__ void __launch_bounds__(32 * kAttnWarps) attention_kernel(AttnParams p, int32_t max_rows) {
-  constexpr int kE = kD / 32;
-  __shared__ uint32_t seen[SV_MAX_TREE_ROWS / 32];
-  __shared__ float part[kAttnWarps][kD + 2];
-  dependent_start();
-  const int32_t h = blockIdx.x % p.n_heads, i = blockIdx.x / p.n_heads % max_rows;
-  const int32_t r = blockIdx.x / p.n_heads / max_rows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Request rq;
-  if (!round_request(p.rd, r, rq)) {
-    if (i == 0 && h == 0 && threadIdx.x == 0) report(p.status, SV_ERR_BAD_INPUT);
-    return;
-  }
-  if (i >= rq.n) return;
-  if (p.rd.parents && threadIdx.x == 0) {
-    for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w) seen[w] = 0;
-    for (int32_t j = i; j >= 0;) {
-      seen[j >> 5] |= 1u << (j & 31);
-      int32_t up = p.rd.parents[rq.first + j];
-      if (up < -1 || up >= j) {
-        report(p.status, SV_ERR_BAD_INPUT);
-        up = -1;
-      }
-      j = up;
-    }
-  }
-  __syncthreads();
-  const int64_t row = rq.first + i;
-  float q[kE], o[kE] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < kE; ++e)
-    q[e] = __bfloat162float(p.q[row * p.ldq + h * p.q_head + lane + 32 * e]) * p.scale2;
-  for (int32_t j = warp; j <= rq.ctx + i; j += kAttnWarps) {
-    if (j >= rq.ctx && p.rd.parents) {
-      const int32_t t = j - rq.ctx;
-      if (!(seen[t >> 5] >> (t & 31) & 1u)) continue;
-    }
-    const int32_t page = round_page(p.rd, r, j);
-    if (page < 0) {
-      if (lane == 0) report(p.status, SV_ERR_BAD_INPUT);
-      continue;
-    }
-    const int64_t at = page * p.cache.page_stride + (j % p.rd.page_size) * p.cache.token_stride +
-                       (h / p.group) * p.cache.head_stride;
-    float x = 0.f;
-    for (int e = 0; e < kE; ++e) x += q[e] * __bfloat162float(p.cache.k[at + lane + 32 * e]);
-    x = warp_sum(x);
-    const float mn = fmaxf(m, x);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(x - (mn == -INFINITY ? 0.f : mn));  // NaN stays
-    l = l * f + w;
-    for (int e = 0; e < kE; ++e)
-      o[e] = o[e] * f + w * __bfloat162float(p.cache.v[at + lane + 32 * e]);
-    m = mn;
-  }
-  for (int e = 0; e < kE; ++e) part[warp][lane + 32 * e] = o[e];
-  if (lane == 0) part[warp][kD] = m, part[warp][kD + 1] = l;
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, part[w][kD]);
-  for (int d = threadIdx.x; d < kD; d += 32 * kAttnWarps) {
-    float y = 0.f;
-    sum = 0.f;
-    for (int w = 0; w < kAttnWarps; ++w) {
-      const float f = part[w][kD] == -INFINITY ? 0.f : exp2f(part[w][kD] - top);
-      y += f * part[w][d];
-      sum += f * part[w][kD + 1];
-    }
-    p.out[row * p.ldo + h * p.o_head + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : y / sum);
-  }
-  if (threadIdx.x == 0 && p.lse) p.lse[row * p.ld_lse + h] = (top + log2f(sum)) * kLn2;
+sv_status launch(int32_t n, const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p,
+                 int grid, cudaStream_t s) {
+  return n == 16   ? launch<kD, 16>(k, v, p, grid, s)
+         : n == 32 ? launch<kD, 32>(k, v, p, grid, s)
+         : n == 64 ? launch<kD, 64>(k, v, p, grid, s)
+                   : launch<kD, 128>(k, v, p, grid, s);
 }
+
+constexpr int kMaxCtas = 192;  // the workspace's size must not depend on the current device
 
 }  // namespace
 }  // namespace sv
@@ -109,7 +1012,8 @@ extern "C" size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t max_dra
       n_kv_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 128 ||
       (D != 64 && D != 128))
     return 0;
-  return 256;
+  const int64_t rows = (max_draft_len + int64_t(bonus_row)) * (n_heads / n_kv_heads);
+  return ws_layout(kMaxCtas, columns_for(rows), D).bytes;
 }
 
 extern "C" sv_status spec_tree_attention(
@@ -127,11 +1031,12 @@ extern "C" sv_status spec_tree_attention(
       (lse && ld_lse < n_heads))
     return SV_ERR_INVALID;
   if (parents && max_draft_len + int64_t(bonus_row) > SV_MAX_TREE_ROWS) return SV_ERR_UNSUPPORTED;
-  if ((D != 64 && D != 128) || n_heads / n_kv_heads > 128 || page_size < 8 ||
-      (page_size & (page_size - 1)))
+  const int32_t group = n_heads / n_kv_heads;
+  if ((D != 64 && D != 128) || group > 128 || page_size < 8 || (page_size & (page_size - 1)))
     return SV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (B == 0 || max_draft_len + bonus_row == 0 || n_rows == 0) return reset_status(status, s);
+  if (B == 0 || max_draft_len + int64_t(bonus_row) == 0 || n_rows == 0)
+    return reset_status(status, s);
   if (!q || !out || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len || !page_table ||
       !workspace)
     return SV_ERR_INVALID;
@@ -145,18 +1050,32 @@ extern "C" sv_status spec_tree_attention(
   AttnParams p = {};
   p.rd = {row0,    draft_len, parents,       ctx_len,   page_table, ld_pages, n_rows,
           n_pages, B,         max_draft_len, bonus_row, max_pages,  page_size};
-  p.cache = {static_cast<__nv_bfloat16*>(const_cast<void*>(k_cache)),
-             static_cast<__nv_bfloat16*>(const_cast<void*>(v_cache)), page_stride, token_stride,
-             head_stride};
   p.q = static_cast<const __nv_bfloat16*>(q), p.ldq = ldq, p.q_head = q_head;
-  p.n_heads = n_heads, p.group = n_heads / n_kv_heads, p.D = D;
+  p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
+  p.page_stride = page_stride, p.token_stride = token_stride, p.head_stride = head_stride;
+  p.n_heads = n_heads, p.n_kv = n_kv_heads, p.group = group;
+  const int64_t rows = (max_draft_len + int64_t(bonus_row)) * group;
+  const int32_t n = columns_for(rows);
+  p.tokens = n / group;
+  p.box_rows = std::min(page_size, kTile);
   p.scale2 = scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(out), p.ldo = ldo, p.o_head = o_head;
   p.lse = lse, p.ld_lse = ld_lse, p.status = status;
-  const int64_t blocks = int64_t(n_heads) * (max_draft_len + int64_t(bonus_row)) * B;
-  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  const sv_status st = reset_status(status, s);
-  if (st != SV_OK) return st;
-  return launch_dependent(D == 64 ? attention_kernel<64> : attention_kernel<128>, unsigned(blocks),
-                          32 * kAttnWarps, 0, s, p, max_draft_len + bonus_row);
+  p.ws = static_cast<uint8_t*>(workspace);
+  const int sms = std::min(device_sm_count(), kMaxCtas);
+  if (sms < 1) return SV_ERR_CUDA;
+  if (n_pages < 1) return SV_ERR_INVALID;
+  CUtensorMap mk, mv;
+  if (!cache_map(&mk, k_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
+                 page_stride, p.box_rows) ||
+      !cache_map(&mv, v_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
+                 page_stride, p.box_rows))
+    return SV_ERR_UNSUPPORTED;
+  // no more CTAs than there can be tiles
+  const int64_t row_tiles = (max_draft_len + int64_t(bonus_row) + p.tokens - 1) / p.tokens;
+  const int64_t key_tiles = (int64_t(max_pages) * page_size + kTile - 1) / kTile;
+  const double most = double(B) * n_kv_heads * double(row_tiles) * double(key_tiles);
+  if (most > 9e15) return SV_ERR_UNSUPPORTED;
+  const int grid = int(std::max(1.0, std::min(double(sms), most)));
+  return D == 64 ? launch<64>(n, mk, mv, p, grid, s) : launch<128>(n, mk, mv, p, grid, s);
 }
