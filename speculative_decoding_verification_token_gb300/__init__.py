@@ -12,7 +12,6 @@ import ctypes as C
 import functools
 import importlib
 import importlib.machinery
-import math
 import os
 import re
 import threading
@@ -142,7 +141,9 @@ def _bind_fastcall(L):
         warnings.warn(f"_fastcall is not used, it does not load ({e}): build again", RuntimeWarning)
         return
     module.bind(*(C.cast(getattr(L, name), C.c_void_p).value for name in (
-        "spec_history_append", "spec_process_logits", "spec_quantize_fp4", "spec_project_fp4")))
+        "spec_history_append", "spec_process_logits", "spec_quantize_fp4", "spec_project_fp4",
+        "spec_cache_append", "spec_tree_attention", "spec_tree_attention_workspace_bytes",
+        "spec_tree_accept", "spec_cache_keep")))
     _fast = module
 
 
@@ -247,13 +248,17 @@ def _dev(t, dtype=None, rows=False, strided=False):
 _ws_cache = {}
 
 
+def _ws_key(index):
+    return index, threading.get_ident(), torch._C._cuda_getCurrentRawStream(index)
+
+
 def workspace(nbytes, device=None):
     """A cached device buffer of at least `nbytes` bytes (256-byte aligned, from torch), one for each
     host thread and stream: calls on two streams must not share their scratch.  A larger request
     replaces it, so a captured graph that outlives that wants a workspace of its own."""
     device = torch.device(device or torch.cuda.current_device())
     index = torch.cuda.current_device() if device.index is None else device.index
-    key = (index, threading.get_ident(), torch._C._cuda_getCurrentRawStream(index))
+    key = _ws_key(index)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -888,6 +893,14 @@ def spec_cache_append(q, k, v, k_cache, v_cache, page_table, ctx_len, row0, draf
     a request], ctx_len int32 [B]; row0, draft_len, bonus_row as in spec_process_logits; parents
     int32 [rows] if the rows form trees (see include/specverify.h).  Returns q_out.  Data errors go
     to `status`; without one they go unreported."""
+    if (q is None or q_out is not None) and (_fast or _load_fast()):
+        code = _fast.cache_append(q, k, v, k_cache, v_cache, page_table, ctx_len, row0, draft_len,
+                                  max_draft_len, cos_sin, adjacent, parents, bonus_row, q_out, status,
+                                  stream)
+        if code == 0:
+            return q_out
+        if code > 0:
+            raise SpecVerifyError(code, "spec_cache_append")
     dev = _device_of(k, "k")
     dt = _dtype_code(k)
     kp, ldk, hk = _heads(k, "k", k.dtype, dev)
@@ -926,7 +939,6 @@ def spec_tree_attention_workspace_bytes(B, max_draft_len, bonus_row, n_heads, n_
                                                          n_kv_heads, D))
 
 
-@_on_its_stream
 def spec_tree_attention(q, k_cache, v_cache, page_table, ctx_len, row0, draft_len, max_draft_len,
                         parents=None, bonus_row=True, scale=None, out=None, lse=None, status=None,
                         workspace=None, stream=None):
@@ -935,6 +947,29 @@ def spec_tree_attention(q, k_cache, v_cache, page_table, ctx_len, row0, draft_le
     `parents` (None: the rows before it) and itself (see include/specverify.h).  scale: 1 / sqrt(D)
     if not given.  lse fp32 [rows, heads] takes the logarithms of the denominators.  Returns out
     (bf16, as q).  Data errors go to `status`; without one they go unreported."""
+    if out is not None and (stream is None or workspace is not None) and (_fast or _load_fast()):
+        ws = workspace
+        if ws is None and not torch._C._cuda_isCurrentStreamCapturing():
+            ws = _ws_cache.get(_ws_key(torch._C._cuda_getDevice()))
+        if ws is not None:
+            try:
+                code = _fast.tree_attention(
+                    q, k_cache, v_cache, page_table, ctx_len, row0, draft_len, max_draft_len, parents,
+                    bonus_row, q.shape[-1] ** -0.5 if scale is None else scale, out, lse, status, ws,
+                    stream)
+            except (AttributeError, IndexError, ZeroDivisionError):  # q is no tensor with a width
+                code = -1
+            if code == 0:
+                return out
+            if code > 0:
+                raise SpecVerifyError(code, "spec_tree_attention")
+    return _tree_attention(q, k_cache, v_cache, page_table, ctx_len, row0, draft_len, max_draft_len,
+                           parents, bonus_row, scale, out, lse, status, workspace, stream)
+
+
+@_on_its_stream
+def _tree_attention(q, k_cache, v_cache, page_table, ctx_len, row0, draft_len, max_draft_len, parents,
+                    bonus_row, scale, out, lse, status, workspace, stream):
     dev = _device_of(q, "q")
     bf16, i32, i64 = torch.bfloat16, torch.int32, torch.int64
     qp, ldq, hq = _heads(q, "q", bf16, dev)
@@ -951,11 +986,14 @@ def spec_tree_attention(q, k_cache, v_cache, page_table, ctx_len, row0, draft_le
     B = draft_len.numel()
     pt, ldp = _mat(page_table, "page_table", i32, dev, B, 0)
     if workspace is None:
-        workspace = globals()["workspace"](spec_tree_attention_workspace_bytes(
-            B, int(max_draft_len), bonus_row, n_heads, n_kv, D), q.device)
+        need = spec_tree_attention_workspace_bytes(B, int(max_draft_len), bonus_row, n_heads, n_kv, D)
+        # a captured graph keeps one of its own: two graphs may run at once
+        workspace = (torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+                     if torch.cuda.is_current_stream_capturing()
+                     else globals()["workspace"](need, q.device))
     wp = _vec(workspace, "workspace", torch.uint8, None, dev)
     code = lib().spec_tree_attention(
-        qp, ldq, hq, rows, n_heads, n_kv, D, 1.0 / math.sqrt(D) if scale is None else float(scale),
+        qp, ldq, hq, rows, n_heads, n_kv, D, D ** -0.5 if scale is None else float(scale),
         _vec(row0, "row0", i64, B, dev), _vec(draft_len, "draft_len", i32, B, dev),
         int(max_draft_len), int(bonus_row), _vec(parents, "parents", i32, rows, dev), B,
         _vec(ctx_len, "ctx_len", i32, B, dev), pt, ldp, page_table.shape[1], kc, vc, pages, page, ps,
@@ -973,6 +1011,16 @@ def spec_tree_accept(sampled, draft_tokens, parents, row0, draft_row0, draft_len
     parents int32 [rows], None: chains.  Returns a dict: accepted_len [B], out_tokens
     [B, max_draft_len + 1] and correction [B] as spec_verify_token's, path [B, max_draft_len] (the
     accepted rows, then -1), status."""
+    if not (accepted_len is None or out_tokens is None or path is None or correction is None
+            or status is None) and (_fast or _load_fast()):
+        code = _fast.tree_accept(sampled, draft_tokens, parents, row0, draft_row0, draft_len,
+                                 max_draft_len, accepted_len, out_tokens, path, correction, status,
+                                 stream)
+        if code == 0:
+            return {"accepted_len": accepted_len, "out_tokens": out_tokens, "path": path,
+                    "correction": correction, "status": status}
+        if code > 0:
+            raise SpecVerifyError(code, "spec_tree_accept")
     dev = _device_of(sampled, "sampled")
     i32, i64 = torch.int32, torch.int64
     B = draft_len.numel()
@@ -1007,6 +1055,13 @@ def spec_cache_keep(k_cache, v_cache, page_table, ctx_len, accepted_len, path, n
     i < accepted_len (see include/specverify.h).  path int32 [B, n], or None for chains.  Returns
     new_len int32 [B] = ctx_len + 1 + accepted_len, the next round's ctx_len.  Data errors go to
     `status`; without one they go unreported."""
+    if new_len is not None and (_fast or _load_fast()):
+        code = _fast.cache_keep(k_cache, v_cache, page_table, ctx_len, accepted_len, path, new_len,
+                                status, stream)
+        if code == 0:
+            return new_len
+        if code > 0:
+            raise SpecVerifyError(code, "spec_cache_keep")
     dev = _device_of(accepted_len, "accepted_len")
     i32 = torch.int32
     B = accepted_len.numel()

@@ -20,26 +20,34 @@ struct AppendParams {
   const float* cos_sin;
   int64_t ld_cos_sin, n_positions;
   int32_t n_heads, n_kv_heads, D, rot;
+  int32_t rows;    // of a CTA
   int32_t chunks;  // CTAs of a request
   int32_t* status;
+  bool one;
 };
 
 constexpr int kAppendThreads = 256;
 constexpr int kRowThreads = 128;  // of a row
-constexpr int kAppendRows = kAppendThreads / kRowThreads;
-constexpr int kAppendUnroll = 4;
+constexpr int kAppendGroups = kAppendThreads / kRowThreads;
+constexpr int kAppendUnroll = 3;
 
-// 8 consecutive elements as binary32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* x, float* f) {
-  const uint4 v = *reinterpret_cast<const uint4*>(x);
-  Elem<bf16_tag>::unpack(v, f);
-}
-__device__ __forceinline__ void load8(const float* x, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(x)[0];
-  const float4 b = reinterpret_cast<const float4*>(x)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
+// 8 consecutive elements: as they lie, and as binary32.
+template <typename T>
+struct Eight {
+  uint4 raw[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* x) {
+#pragma unroll
+    for (int j = 0; j < int(sizeof(T) / 2); ++j) raw[j] = reinterpret_cast<const uint4*>(x)[j];
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (sizeof(T) == 2) {
+      Elem<bf16_tag>::unpack(raw[0], f);
+    } else {
+      Elem<float>::unpack(raw[0], f);
+      Elem<float>::unpack(raw[1], f + 4);
+    }
+  }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* o, const float* f) {
   uint4 v;
   uint32_t* w = reinterpret_cast<uint32_t*>(&v);
@@ -51,112 +59,118 @@ __device__ __forceinline__ void store8(__nv_bfloat16* o, const float* f) {
   *reinterpret_cast<uint4*>(o) = v;
 }
 
-// 128 threads a row: a thread keeps one sixteenth-element part of the heads (two runs of 8, `half`
-// apart: the pairs of a rotation, or neighbours) with that part's cosines and sines, and goes
-// through the heads of q, k and v with it.
+// 128 threads a row: a thread keeps one sixteen-element part of the heads (two runs of 8: the pairs
+// of a rotation, or neighbours) with that part's cosines and sines, and goes through the heads of q, k
+// and v with it.  Returns whether it found bad data.
 template <typename T, bool kAdjacent>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
-  __shared__ int32_t parents[SV_MAX_TREE_ROWS];
-  dependent_start();
+__device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* parents) {
   const int32_t r = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int32_t sub = threadIdx.x / kRowThreads, t = threadIdx.x % kRowThreads;
   Request rq;
-  if (!round_request(p.rd, r, rq)) {
-    if (chunk == 0 && threadIdx.x == 0) report(p.status, SV_ERR_BAD_INPUT);
-    return;
-  }
-  if (chunk * kAppendRows >= rq.n) return;
-  const int32_t i = chunk * kAppendRows + sub;
-  int32_t depth = i;
+  if (!round_request(p.rd, r, rq)) return chunk == 0;
+  const int32_t begin = chunk * p.rows, end = min(begin + p.rows, rq.n);
+  if (begin >= end) return false;
+  bool bad = false;
   if (p.rd.parents) {
-    for (int32_t j = threadIdx.x; j < rq.n; j += kAppendThreads) {
+    for (int32_t j = threadIdx.x; j < end; j += kAppendThreads) {
       int32_t up = p.rd.parents[rq.first + j];
       if (up < -1 || up >= j) {
-        if (chunk == 0) report(p.status, SV_ERR_BAD_INPUT);
+        bad = true;
         up = -1;
       }
       parents[j] = up;
     }
     __syncthreads();
-    if (i < rq.n) {
-      depth = 0;
-      for (int32_t j = parents[i]; j >= 0; j = parents[j]) ++depth;
-    }
   }
-  if (i >= rq.n) return;
   const int32_t parts = p.D >> 4, rot_parts = p.rot >> 4;
   const int32_t part = t % parts, step = kRowThreads / parts;
-  if (t >= parts * step) return;
+  if (t >= parts * step) return bad;
   const bool turn = part < rot_parts;
   const bool halves = turn && !kAdjacent;
   const int32_t e0 = halves ? part * 8 : part * 16, e1 = halves ? e0 + (p.rot >> 1) : e0 + 8;
-  float c[8], s[8];
-  if (turn) {
-    const int64_t pos = int64_t(rq.ctx) + depth;
-    if (pos >= p.n_positions) {
-      if (t == 0) report(p.status, SV_ERR_BAD_INPUT);
-      return;
-    }
-    const float* row = p.cos_sin + pos * p.ld_cos_sin + part * 8;
-    load8(row, c);
-    load8(row + (p.rot >> 1), s);
-  }
-  const int32_t place = rq.ctx + i, page = round_page(p.rd, r, place);
-  if (page < 0 && t == 0) report(p.status, SV_ERR_BAD_INPUT);
-  const int64_t at = page * p.cache.page_stride + (place % p.rd.page_size) * p.cache.token_stride;
-  const int64_t row = rq.first + i;
   const int32_t all = p.n_heads + 2 * p.n_kv_heads;
-  for (int32_t h0 = t / parts; h0 < all; h0 += step * kAppendUnroll) {
-    float a[kAppendUnroll][8], b[kAppendUnroll][8];
-#pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
-      const int32_t h = h0 + u * step;
-      if (h < all) {
-        const T* src = h < p.n_heads
-                           ? static_cast<const T*>(p.q) + row * p.ldq + h * p.q_head
-                       : h < p.n_heads + p.n_kv_heads
-                           ? static_cast<const T*>(p.k) + row * p.ldk + (h - p.n_heads) * p.k_head
-                           : static_cast<const T*>(p.v) + row * p.ldv +
-                                 (h - p.n_heads - p.n_kv_heads) * p.v_head;
-        const bool v_head = h >= p.n_heads + p.n_kv_heads;
-        load8(src + (v_head ? part * 16 : e0), a[u]);
-        load8(src + (v_head ? part * 16 + 8 : e1), b[u]);
-      }
+  for (int32_t i = begin + sub; i < end; i += kAppendGroups) {
+    int32_t depth = i;
+    if (p.rd.parents) {
+      depth = 0;
+      for (int32_t j = parents[i]; j >= 0; j = parents[j]) ++depth;
     }
+    Eight<float> c8, s8;
+    if (turn) {
+      const int64_t pos = int64_t(rq.ctx) + depth;
+      if (pos >= p.n_positions) {
+        bad = true;
+        continue;
+      }
+      const float* row = p.cos_sin + pos * p.ld_cos_sin + part * 8;
+      c8.load(row);
+      s8.load(row + (p.rot >> 1));
+    }
+    const int32_t place = rq.ctx + i, page = round_page(p.rd, r, place);
+    bad |= page < 0;
+    const int64_t at = page * p.cache.page_stride + (place % p.rd.page_size) * p.cache.token_stride;
+    const int64_t row = rq.first + i;
+    for (int32_t h0 = t / parts; h0 < all; h0 += step * kAppendUnroll) {
+      Eight<T> x[kAppendUnroll], y[kAppendUnroll];
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
-      const int32_t h = h0 + u * step;
-      if (h >= all) continue;
-      const int32_t kv = h - p.n_heads;
-      const bool v_head = kv >= p.n_kv_heads;
-      __nv_bfloat16* dst = kv < 0   ? p.q_out + row * p.ldqo + h * p.qo_head
-                           : v_head ? p.cache.v + at + (kv - p.n_kv_heads) * p.cache.head_stride
-                                    : p.cache.k + at + kv * p.cache.head_stride;
-      if (kv >= 0 && page < 0) continue;
-      if (turn && !v_head) {
-        if constexpr (kAdjacent) {  // pairs within each run of 8: angles 0-3 and 4-7
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = a[u][2 * j], y = a[u][2 * j + 1];
-            a[u][2 * j] = x * c[j] - y * s[j];
-            a[u][2 * j + 1] = x * s[j] + y * c[j];
-            const float z = b[u][2 * j], w = b[u][2 * j + 1];
-            b[u][2 * j] = z * c[4 + j] - w * s[4 + j];
-            b[u][2 * j + 1] = z * s[4 + j] + w * c[4 + j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float x = a[u][j], y = b[u][j];
-            a[u][j] = x * c[j] - y * s[j];
-            b[u][j] = x * s[j] + y * c[j];
-          }
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        const int32_t h = h0 + u * step, kv = h - p.n_heads;
+        if (h < all) {
+          const bool v_head = kv >= p.n_kv_heads;
+          const T* src = kv < 0 ? static_cast<const T*>(p.q) + row * p.ldq + h * p.q_head
+                         : v_head ? static_cast<const T*>(p.v) + row * p.ldv + (kv - p.n_kv_heads) * p.v_head
+                                  : static_cast<const T*>(p.k) + row * p.ldk + kv * p.k_head;
+          x[u].load(src + (v_head ? part * 16 : e0));
+          y[u].load(src + (v_head ? part * 16 + 8 : e1));
         }
       }
-      store8(dst + (v_head ? part * 16 : e0), a[u]);
-      store8(dst + (v_head ? part * 16 + 8 : e1), b[u]);
+#pragma unroll
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        const int32_t h = h0 + u * step, kv = h - p.n_heads;
+        if (h >= all || (kv >= 0 && page < 0)) continue;
+        const bool v_head = kv >= p.n_kv_heads;
+        __nv_bfloat16* dst = kv < 0   ? p.q_out + row * p.ldqo + h * p.qo_head
+                             : v_head ? p.cache.v + at + (kv - p.n_kv_heads) * p.cache.head_stride
+                                      : p.cache.k + at + kv * p.cache.head_stride;
+        float a[8], b[8];
+        x[u].get(a);
+        y[u].get(b);
+        if (turn && !v_head) {
+          float c[8], s[8];
+          c8.get(c);
+          s8.get(s);
+          if constexpr (kAdjacent) {  // pairs within each run of 8: angles 0-3 and 4-7
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float f = a[2 * j], g = a[2 * j + 1];
+              a[2 * j] = f * c[j] - g * s[j];
+              a[2 * j + 1] = f * s[j] + g * c[j];
+              const float z = b[2 * j], w = b[2 * j + 1];
+              b[2 * j] = z * c[4 + j] - w * s[4 + j];
+              b[2 * j + 1] = z * s[4 + j] + w * c[4 + j];
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float f = a[j], g = b[j];
+              a[j] = f * c[j] - g * s[j];
+              b[j] = f * s[j] + g * c[j];
+            }
+          }
+        }
+        store8(dst + (v_head ? part * 16 : e0), a);
+        store8(dst + (v_head ? part * 16 + 8 : e1), b);
+      }
     }
   }
+  return bad;
+}
+
+template <typename T, bool kAdjacent>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
+  __shared__ int32_t parents[SV_MAX_TREE_ROWS];
+  dependent_start();
+  round_status(p.status, append_body<T, kAdjacent>(p, parents), p.one);
 }
 
 // ---- accept ----------------------------------------------------------------------------------------
@@ -169,29 +183,26 @@ struct AcceptParams {
   int32_t *accepted_len, *out_tokens, *correction, *path;
   int64_t out_ld, ld_path;
   int32_t* status;
+  bool one;
 };
 
-constexpr int kAcceptWarps = 4;
 constexpr int kTreeWords = SV_MAX_TREE_ROWS / 32;
 
 // A warp per request: the rows' parents, tokens and samples in registers, row i in lane i % 32.  A
 // step compares every row with the one the walk stands on; children follow their parents, so the
 // first match is the lowest child.
-__global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(AcceptParams p) {
-  dependent_start();
-  const int32_t r = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= p.B) return;
+// Returns whether the data are bad.
+__device__ __forceinline__ bool accept_body(const AcceptParams& p) {
+  const int32_t r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= p.B) return false;
   const int32_t drafts = p.draft_len[r];
   const int64_t first = p.row0[r], dfirst = p.draft_row0[r];
   bool bad = drafts < 0 || drafts > p.max_draft_len || first < 0 || first >= p.n_rows ||
              drafts >= p.n_rows - first ||
              (drafts > 0 && (dfirst < 0 || dfirst > p.n_drafts || drafts > p.n_drafts - dfirst));
   if (bad) {
-    if (lane == 0) {
-      report(p.status, SV_ERR_BAD_INPUT);
-      p.accepted_len[r] = 0;
-    }
-    return;
+    if (lane == 0) p.accepted_len[r] = 0;
+    return true;
   }
   int32_t parent[kTreeWords], token[kTreeWords], sample[kTreeWords];
 #pragma unroll
@@ -242,7 +253,12 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) accept_kernel(AcceptParams 
   for (int32_t i = n + 1 + lane; i <= p.max_draft_len; i += 32) out[i] = -1;
   if (path)
     for (int32_t i = n + lane; i < p.max_draft_len; i += 32) path[i] = -1;
-  if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.status, SV_ERR_BAD_INPUT);
+  return bad;
+}
+
+__global__ void __launch_bounds__(1024) accept_kernel(AcceptParams p) {
+  dependent_start();
+  round_status(p.status, accept_body(p), p.one);
 }
 
 // ---- keep ------------------------------------------------------------------------------------------
@@ -258,6 +274,7 @@ struct KeepParams {
   int32_t head_columns;  // of a head
   int32_t* new_len;
   int32_t* status;
+  bool one;
 };
 
 constexpr int kKeepThreads = 256;
@@ -266,16 +283,13 @@ constexpr int kKeepBatch = 8;
 // A CTA per request and layer.  A path ascends from 1 or more, so row path[i] lies at or behind the
 // place i + 1 it goes to, and a thread that takes its own 16-byte column through the moves in order
 // never reads what it has overwritten; it reads a batch of rows ahead of writing them.
-__global__ void __launch_bounds__(kKeepThreads) keep_kernel(KeepParams p) {
-  __shared__ int64_t src[SV_MAX_TREE_ROWS], dst[SV_MAX_TREE_ROWS];
-  __shared__ int32_t moves;
-  dependent_start();
+// Returns whether the data are bad.
+__device__ __forceinline__ bool keep_body(const KeepParams& p, int64_t* src, int64_t* dst) {
   const int32_t r = blockIdx.x % p.rd.B, layer = blockIdx.x / p.rd.B, tid = threadIdx.x;
   const int32_t ctx = p.rd.ctx_len[r], n = p.accepted_len[r];
   const int64_t room = min(int64_t(p.rd.max_pages) * p.rd.page_size, int64_t(INT32_MAX));
   bool bad = n < 0 || n > p.n_path || ctx < 0 || int64_t(ctx) + 1 + n > room;
   int32_t from = 0, page_from = 0, page_to = 0;
-  if (tid == 0) moves = 0;
   if (!bad && p.path && tid < n) {
     const int32_t* const path = p.path + r * p.ld_path;
     from = path[tid];
@@ -286,12 +300,9 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(KeepParams p) {
       bad = page_from < 0 || page_to < 0;
     }
   }
-  if (__syncthreads_or(bad)) {
-    if (layer == 0 && tid == 0) report(p.status, SV_ERR_BAD_INPUT);
-    return;
-  }
+  if (__syncthreads_or(bad)) return layer == 0 && tid == 0;
   if (layer == 0 && tid == 0 && p.new_len) p.new_len[r] = ctx + 1 + n;
-  if (!p.path) return;
+  if (!p.path) return false;
   // a path starts with the rows that lie in place; from its first gap on every row moves
   const bool move = tid < n && from != tid + 1;
   const int32_t count = __syncthreads_count(move);
@@ -316,6 +327,13 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(KeepParams p) {
         if (m0 + u < count) *reinterpret_cast<uint4*>(base + dst[m0 + u]) = x[u];
     }
   }
+  return false;
+}
+
+__global__ void __launch_bounds__(kKeepThreads) keep_kernel(KeepParams p) {
+  __shared__ int64_t src[SV_MAX_TREE_ROWS], dst[SV_MAX_TREE_ROWS];
+  dependent_start();
+  round_status(p.status, keep_body(p, src, dst), p.one);
 }
 
 }  // namespace
@@ -367,17 +385,15 @@ extern "C" sv_status spec_cache_append(
   p.q_out = static_cast<__nv_bfloat16*>(q_out), p.ldqo = ldqo, p.qo_head = qo_head;
   p.cos_sin = cos_sin, p.ld_cos_sin = ld_cos_sin, p.n_positions = n_positions;
   p.n_heads = n_heads, p.n_kv_heads = n_kv_heads, p.D = D, p.rot = rot;
-  p.chunks = int32_t((max_draft_len + int64_t(bonus_row) + kAppendRows - 1) / kAppendRows);
+  const int64_t most = max_draft_len + int64_t(bonus_row);
+  p.rows = kAppendGroups;
+  p.chunks = int32_t((most + p.rows - 1) / p.rows);
   p.status = status;
-  const int64_t blocks = int64_t(p.chunks) * B;
-  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  const sv_status st = reset_status(status, s);
-  if (st != SV_OK) return st;
   auto* kernel = dtype == SV_BF16
                      ? (adjacent ? append_kernel<__nv_bfloat16, true>
                                  : append_kernel<__nv_bfloat16, false>)
                      : (adjacent ? append_kernel<float, true> : append_kernel<float, false>);
-  return launch_dependent(kernel, unsigned(blocks), kAppendThreads, 0, s, p);
+  return launch_round(kernel, int64_t(p.chunks) * B, kAppendThreads, s, p);
 }
 
 extern "C" sv_status spec_tree_accept(const int32_t* sampled, const int32_t* draft_tokens,
@@ -400,11 +416,10 @@ extern "C" sv_status spec_tree_accept(const int32_t* sampled, const int32_t* dra
   AcceptParams p = {sampled,  draft_tokens, parents,       draft_len,    row0,
                     draft_row0, n_rows,     n_drafts,      B,            max_draft_len,
                     accepted_len, out_tokens, correction_token, path,    out_ld,
-                    ld_path,  status};
-  const sv_status st = reset_status(status, s);
-  if (st != SV_OK) return st;
-  return launch_dependent(accept_kernel, unsigned((B + kAcceptWarps - 1) / kAcceptWarps),
-                          32 * kAcceptWarps, 0, s, p);
+                    ld_path,  status,       false};
+  // one cluster as far as it goes, then CTAs of four
+  const int warps = B <= 32 * kOneCluster ? (B + kOneCluster - 1) / kOneCluster : 4;
+  return launch_round(accept_kernel, (B + int64_t(warps) - 1) / warps, 32u * unsigned(warps), s, p);
 }
 
 extern "C" sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t* path,
@@ -438,10 +453,6 @@ extern "C" sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t*
   p.n_layers = path ? n_layers : 1, p.layer_stride = layer_stride;
   p.columns = n_kv_heads * (D / 8), p.head_columns = D / 8;
   p.new_len = new_len, p.status = status;
-  const int64_t blocks = int64_t(std::max(p.n_layers, 1)) * B;
-  if (blocks > INT32_MAX) return SV_ERR_UNSUPPORTED;
   if (p.n_layers == 0) p.path = nullptr;
-  const sv_status st = reset_status(status, s);
-  if (st != SV_OK) return st;
-  return launch_dependent(keep_kernel, unsigned(blocks), kKeepThreads, 0, s, p);
+  return launch_round(keep_kernel, int64_t(std::max(p.n_layers, 1)) * B, kKeepThreads, s, p);
 }

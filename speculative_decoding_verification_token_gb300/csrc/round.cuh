@@ -51,6 +51,65 @@ __device__ __forceinline__ int32_t round_page(const RoundParams& p, int32_t r, i
   return g >= 0 && g < p.n_pages ? g : -1;
 }
 
+// ---- the status of short calls ---------------------------------------------------------------------
+// A call of a few CTAs runs as one cluster, which gathers what its CTAs found and writes the word
+// itself: that saves the launch that resets it.  Larger calls report to a word reset before them.
+constexpr int kOneCluster = 8;  // the largest cluster every device takes
+
+// All threads of all CTAs, at their end.  `one`: the grid is one cluster.
+__device__ __forceinline__ void round_status(int32_t* status, bool bad, bool one) {
+  if (!one) {
+    if (bad) report(status, SV_ERR_BAD_INPUT);
+    return;
+  }
+  __shared__ uint32_t found;
+  const int any = __syncthreads_or(bad);
+  if (gridDim.x == 1) {
+    if (threadIdx.x == 0 && status) *status = any ? SV_ERR_BAD_INPUT : SV_OK;
+    return;
+  }
+  if (threadIdx.x == 0) found = uint32_t(any);
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    uint32_t x = 0;
+    if (threadIdx.x < gridDim.x) {
+      uint32_t at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(&found)), "r"(threadIdx.x));
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    }
+    x = __any_sync(0xffffffffu, x != 0);
+    if (threadIdx.x == 0 && status) *status = x ? SV_ERR_BAD_INPUT : SV_OK;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Launches `kernel` (whose params have a member `one`) over `grid` CTAs, as one cluster if they fit,
+// else behind the reset of the status word.
+template <typename P>
+inline sv_status launch_round(void (*kernel)(P), int64_t grid, unsigned threads, cudaStream_t s, P p) {
+  if (grid > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  p.one = grid <= kOneCluster;
+  if (!p.one) {
+    const sv_status st = reset_status(p.status, s);
+    return st != SV_OK ? st : launch_dependent(kernel, unsigned(grid), threads, 0, s, p);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(grid);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = grid > 1 ? 2 : 1;
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
 // Host side: what the calls over the cache check alike.
 inline bool round_sizes_ok(int32_t max_draft_len, int32_t bonus_row, int32_t B, int64_t n_rows,
                            int64_t ld_pages, int32_t max_pages, int64_t n_pages,
