@@ -8,13 +8,14 @@
 //   O^T += V^T P^T   (D x kN, lane = element of the head).
 // K and V go in as they lie in the cache (K with its elements, V with its places along the contraction);
 // a row costs a 16th of the narrowest instruction, where it would be padded to 128 the other way round.
-//   warps 0-3  softmax: a place a thread.  m is a bound of the columns' maxima that is raised only when
-//              a score passes it by more than 8 (P then reaches 2^8, in 16 bits as exact as 1), so that
-//              nearly every tile costs no reduction over the places; the sums of P stay with the places
-//              and are added over them at the end;
-//   warp 4     TMA loads of K and V, page by page, into a ring;
-//   warp 5     tcgen05.mma: S of a tile ahead of the product with V of the one before;
-//   warp 6     the next work item: its sizes, its rows' queries, and for trees who sees whom.
+//   warps 0-7  softmax: a place a thread, half of the columns for warps 0-3, the others for 4-7.  m is
+//              a bound of a column's maximum that is raised only when a score passes it by more than 8
+//              (P then reaches 2^8, in 16 bits as exact as 1), so that nearly every tile costs no
+//              reduction over the places; the sums of P stay with the places and are added over them at
+//              the end;
+//   warp 8     TMA loads: an item's queries, then K and V, page by page, into a ring;
+//   warp 9     tcgen05.mma: S of a tile ahead of the product with V of the one before;
+//   warp 10    the work items: their sizes, and for trees who sees whom.
 // The work -- (request, key head, row tile, key tile) -- is one list, cut into equal runs for a
 // persistent CTA on every SM, wherever the cuts fall; what a cut leaves in parts goes to the workspace
 // and is joined by a second kernel.
@@ -29,20 +30,20 @@ namespace sv {
 namespace {
 
 constexpr int kTile = 128;        // places of a tile
-constexpr int kAttnThreads = 256;
-constexpr int kSoftWarps = 4;
+constexpr int kAttnThreads = 384;
+constexpr int kSoftWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10;
 constexpr uint32_t kAttnSmem = 232448 - 1024;  // dynamic shared memory of a CTA, less what is static
 constexpr float kSlack = 8.f;     // log2 of what P may reach before m is raised
 
 struct AttnParams {
   RoundParams rd;
-  const __nv_bfloat16 *q, *v_cache;
+  const __nv_bfloat16* v_cache;
   int64_t page_stride, token_stride, head_stride;
-  int64_t ldq, q_head;
-  int32_t n_heads, n_kv, group;
+  int32_t n_kv, group;
   int32_t tokens;    // tokens of a row tile
   int32_t box_rows;  // places of a TMA box
-  int32_t stages;
+  int32_t reread;    // several row tiles read the same keys
   float scale2;  // scale * log2(e)
   __nv_bfloat16* out;
   int64_t ldo, o_head;
@@ -92,55 +93,62 @@ struct Span {
   int32_t r;                  // the request that `begin` lies in
 };
 
-// All threads: this CTA's run of the list.
-__device__ void find_span(const AttnParams& p, Span& span, int64_t* warp_sums, int32_t* err) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kAttnThreads / 32;
-  int64_t running = 0, mine = 0, before = 0;
-  // pass 0 adds everything up, pass 1 finds the place; one chunk of requests needs only the first's sums
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1) {
-      if (tid == 0) {
-        span.total = running;
-        span.begin = running * blockIdx.x / gridDim.x;
-        span.end = running * (blockIdx.x + 1) / gridDim.x;
-      }
-      __syncthreads();
-      if (span.begin == span.end) return;
-      running = 0;
+// One warp: this CTA's run of the list.  Requests in chunks of 32, a lane each; two rounds over them,
+// the second from the first's sums where there is one chunk only.
+__device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
+  const int lane = threadIdx.x & 31;
+  Span span = {};
+  int64_t mine = 0, upto = 0;
+  auto chunk = [&](int32_t r0) {
+    const int32_t r = r0 + lane;
+    mine = 0;
+    if (r < p.rd.B) {
+      Request q;
+      if (!round_request(p.rd, r, q) && blockIdx.x == 0) report(err, SV_ERR_BAD_INPUT);
+      mine = tiles_of_head(q, p.tokens) * p.n_kv;
     }
-    for (int32_t r0 = 0; r0 < p.rd.B; r0 += kAttnThreads) {
-      const int32_t r = r0 + tid;
-      if (pass == 0 || p.rd.B > kAttnThreads) {
-        mine = 0;
-        if (r < p.rd.B) {
-          Request q;
-          if (!round_request(p.rd, r, q) && blockIdx.x == 0) report(err, SV_ERR_BAD_INPUT);
-          mine = tiles_of_head(q, p.tokens) * p.n_kv;
-        }
-        int64_t upto = mine;
+  };
+  auto scan = [&] {
+    upto = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += x;
-        }
-        __syncthreads();
-        if (lane == 31) warp_sums[warp] = upto;
-        __syncthreads();
-        before = upto - mine;
-        for (int w = 0; w < warp; ++w) before += warp_sums[w];
-      }
-      if (pass == 1 && mine > 0) {
-        const int64_t a = running + before;
-        if (a <= span.begin && span.begin < a + mine) {
-          span.before = a;
-          span.r = r;
-        }
-      }
-      for (int w = 0; w < kWarps; ++w) running += warp_sums[w];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
     }
+  };
+  int64_t total = 0;
+#pragma unroll 4
+  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
+    chunk(r0);
+    total += mine;
   }
-  __syncthreads();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  span.total = total;
+  if (total < (int64_t(1) << 22)) {  // (the products stay in 32 bits: at most 192 CTAs)
+    span.begin = uint32_t(total) * blockIdx.x / gridDim.x;
+    span.end = uint32_t(total) * (blockIdx.x + 1) / gridDim.x;
+  } else {
+    span.begin = total * blockIdx.x / gridDim.x;
+    span.end = total * (blockIdx.x + 1) / gridDim.x;
+  }
+  if (span.begin == span.end) return span;
+  int64_t before = 0;
+  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
+    if (p.rd.B > 32) chunk(r0);
+    scan();
+    const int64_t a = before + upto - mine;
+    const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= span.begin &&
+                                                        span.begin < a + mine);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      span.before = __shfl_sync(0xffffffffu, a, l);
+      span.r = r0 + l;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return span;
 }
 
 // ---- small pieces ----------------------------------------------------------------------------------
@@ -185,43 +193,40 @@ __device__ __forceinline__ bool elect() {
   return is != 0;
 }
 
-// Barrier of the softmax warps that also tells whether `x` held in any thread.
-__device__ __forceinline__ bool soft_any(bool x) {
+// Barrier of a half's four softmax warps (1 or 2) that also tells whether `x` held in any thread.
+__device__ __forceinline__ bool soft_any(int half, bool x) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.or.pred p, 1, 128, q;\n\t"
+      "barrier.cta.red.or.pred p, %2, 128, q;\n\t"
       "selp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(any)
-      : "r"(uint32_t(x))
+      : "r"(uint32_t(x)), "r"(1 + half)
       : "memory");
   return any != 0;
 }
-__device__ __forceinline__ void soft_sync() { named_sync(1, 32 * kSoftWarps); }
+__device__ __forceinline__ void soft_sync(int half) { named_sync(1 + half, 128); }
 
-// Largest value of a warp (NaN left out).
-__device__ __forceinline__ float warp_top(float x) {
-  float y;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1,
-                                            int32_t c2, int32_t c3, uint64_t* bar, uint64_t policy) {
+                                            int32_t c2, int32_t c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* map, int32_t c0,
+                                                 int32_t c1, int32_t c2, int32_t c3, uint64_t* bar,
+                                                 uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar)),
       "l"(policy)
       : "memory");
-}
-
-// 16 bytes to shared memory, zeros if not `take` (the address must be valid all the same).
-__device__ __forceinline__ void async_copy16(void* dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
-               "r"(take ? 16 : 0)
-               : "memory");
 }
 
 // Shared-memory descriptors of 128-byte swizzled operands by halves (low word: address >> 4 and leading
@@ -240,31 +245,42 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
 // C columns of this thread's TMEM lane.
 template <int C>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
-  if constexpr (C == 16) tc::tmem_load16(taddr, v);
-  else tc::tmem_load32(taddr, v);
+  if constexpr (C == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7])
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (C == 16) {
+    tc::tmem_load16(taddr, v);
+  } else {
+    tc::tmem_load32(taddr, v);
+  }
 }
 
 template <int C>
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const float* v) {
 #pragma unroll
-  for (int j = 0; j < C; j += 16)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr + j),
-        "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]), "f"(v[j + 5]),
-        "f"(v[j + 6]), "f"(v[j + 7]), "f"(v[j + 8]), "f"(v[j + 9]), "f"(v[j + 10]), "f"(v[j + 11]),
-        "f"(v[j + 12]), "f"(v[j + 13]), "f"(v[j + 14]), "f"(v[j + 15])
-        : "memory");
+  for (int j = 0; j < C; j += 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     taddr + j),
+                 "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
+                 "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
+                 : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Sums over the lanes of C columns a lane: column lane % C's sum in every lane.
-template <int C>
-__device__ __forceinline__ float column_sums(float* v) {
+// C columns a lane joined over the lanes by `op`: column lane % C's result in every lane.  Half of what
+// a lane holds goes to the lane that keeps it, in every step.
+template <int C, typename Op>
+__device__ __forceinline__ float over_lanes(float* v, Op op) {
   const int lane = threadIdx.x & 31;
-  if constexpr (C == 16) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], 16);
+  for (int o = 16; o >= C; o >>= 1) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] = op(v[j], __shfl_xor_sync(0xffffffffu, v[j], o));
   }
 #pragma unroll
   for (int o = C / 2; o > 0; o >>= 1) {
@@ -272,10 +288,39 @@ __device__ __forceinline__ float column_sums(float* v) {
 #pragma unroll
     for (int j = 0; j < o; ++j) {
       const float give = upper ? v[j] : v[j + o], keep = upper ? v[j + o] : v[j];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
     }
   }
   return v[0];
+}
+
+// C consecutive values of shared memory, the same in every lane.
+template <int C>
+__device__ __forceinline__ void broadcast(const float* at, float* v) {
+#pragma unroll
+  for (int j = 0; j < C; j += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(at + j);
+    v[j] = x.x, v[j + 1] = x.y, v[j + 2] = x.z, v[j + 3] = x.w;
+  }
+}
+
+// s scale + minus, in pairs.
+template <int C>
+__device__ __forceinline__ void scaled(float* s, float scale, const float* minus) {
+  const float2 f = splat2(scale);
+#pragma unroll
+  for (int j = 0; j < C; j += 2) {
+    const float2 y = fma2(make_float2(s[j], s[j + 1]), f, make_float2(minus[j], minus[j + 1]));
+    s[j] = y.x, s[j + 1] = y.y;
+  }
+}
+
+// -inf in the columns whose bit is clear.
+template <int C>
+__device__ __forceinline__ void hide(float* y, uint32_t seen) {
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    if (!(seen >> j & 1u)) y[j] = -INFINITY;
 }
 
 __device__ __forceinline__ bool not_finite2(uint32_t w) {  // either half of a bf16 pair
@@ -289,7 +334,7 @@ struct Item {
   int32_t base0;   // places below it are seen by every column
   int32_t end;     // places from it on by none
   int32_t t0, t1;  // its key tiles in this CTA
-  int32_t whole, begins;
+  int32_t whole, begins, last;
   int32_t stop;    // no item: the list is at its end
 };
 
@@ -300,16 +345,19 @@ struct AttnShared {
   static constexpr uint32_t kPBytes = (kN + 63) / 64 * 16384;
   static constexpr int kWords = (kN + 31) / 32;
   struct Small {
-    uint64_t full[16], empty[16], item_full[2], item_empty[2], s_full[2], p_full, p_free, drain;
+    uint64_t full[16], empty[16], item_full[2], item_empty[2], q_full[2], table_full[2], s_full[2];
+    uint64_t p_full, p_free, drain;
     int64_t col_off[2][kN];  // of a column's output
     Item item[2];
-    Span span;
-    int64_t warp_sums[kAttnThreads / 32];
-    float m[kN], factor[kN], inv[kN], part[kSoftWarps][kN];
+    alignas(16) float minus[kN];  // -m; read four at a time, as the next two
+    alignas(16) float factor[kN];
+    alignas(16) float inv[kN];
+    float part[4][kN];
     uint32_t seen[2][SV_MAX_TREE_ROWS][kWords];  // bit c: column c sees the tree's row
     uint32_t above[SV_MAX_TREE_ROWS][4];         // rows above a row, itself included
     int32_t up[SV_MAX_TREE_ROWS];
-    uint32_t bad[SV_MAX_TREE_ROWS / 32];  // places whose values are not all finite
+    uint32_t bad[2][2][SV_MAX_TREE_ROWS / 32];  // an item's rows whose values (of a half of D) are not
+                                                // all finite
     uint32_t tmem;
     int32_t err;
   };
@@ -320,13 +368,81 @@ struct AttnShared {
   }
 };
 
+// Who sees whom in a tree, by one warp: seen[j] = columns that see row j, for the row tile's columns.
+template <int kWords>
+__device__ __forceinline__ void build_table(const AttnParams& p, int64_t first, int32_t tok0,
+                                            int32_t nodes, int32_t columns, int32_t* up,
+                                            uint32_t (*above)[4], uint32_t (*seen)[kWords],
+                                            int32_t* err) {
+  const int lane = threadIdx.x & 31;
+  for (int32_t i = lane; i < nodes; i += 32) {
+    int32_t u = p.rd.parents[first + i];
+    if (u < -1 || u >= i) {
+      report(err, SV_ERR_BAD_INPUT);
+      u = -1;
+    }
+    up[i] = u;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) above[i][w] = i >> 5 == w ? 1u << (i & 31) : 0u;
+  }
+  __syncwarp();
+  // the way up doubles its length a round: a row takes over what the row at its end has
+  for (int round = 0; round < 7; ++round) {
+    uint32_t a[4][4];
+    int32_t next[4];
+    bool more = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t i = k * 32 + lane;
+      next[k] = -1;
+      if (i < nodes && up[i] >= 0) {
+        more = true;
+        next[k] = up[up[i]];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) a[k][w] = above[i][w] | above[up[i]][w];
+      }
+    }
+    if (!__any_sync(0xffffffffu, more)) break;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t i = k * 32 + lane;
+      if (i < nodes && up[i] >= 0) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) above[i][w] = a[k][w];
+        up[i] = next[k];
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const int32_t c = w * 32 + lane, i = tok0 + c / p.group;
+    const bool in = c < columns;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k * 32 >= nodes) break;
+      const uint32_t mine = in ? above[i][k] : 0u;
+      uint32_t row = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t word = __ballot_sync(0xffffffffu, mine >> j & 1u);
+        if (lane == j) row = word;
+      }
+      seen[k * 32 + lane][w] = row;
+    }
+  }
+}
+
 template <int kD, int kN>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    attention_kernel(const __grid_constant__ CUtensorMap map_k,
+    attention_kernel(const __grid_constant__ CUtensorMap map_q,
+                     const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using Sh = AttnShared<kD, kN>;
-  constexpr int kC = kN < 32 ? kN : 32;  // columns at a time
-  constexpr int kChunks = kN / kC;
+  constexpr int kW = kN / 2;                // columns of a half
+  constexpr int kC = kW < 32 ? kW : 32;     // columns at a time
+  constexpr int kChunks = kW / kC;
   constexpr int kStages = Sh::kStages();
   constexpr uint32_t kCols = kN <= 16 ? 64 : kN <= 32 ? 128 : kN <= 64 ? 256 : 512;
   static_assert(kStages >= 3, "a ring of three tiles");
@@ -346,7 +462,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.item_full[b], 1);
-      mbar_init(&sm.item_empty[b], 3);  // the loads, the products with Q, the softmax
+      mbar_init(&sm.item_empty[b], 4);  // the loads, the products with Q, the softmax's halves
+      mbar_init(&sm.q_full[b], 1);
+      mbar_init(&sm.table_full[b], 1);
       mbar_init(&sm.s_full[b], 1);
     }
     mbar_init(&sm.p_full, kSoftWarps);
@@ -355,142 +473,85 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     fence_barrier_init();
     sm.err = 0;
   }
-  if (warp == 5) tc::tmem_alloc(&sm.tmem, kCols);
+  if (warp == kMmaWarp) tc::tmem_alloc(&sm.tmem, kCols);
   tc::fence_before_sync();
   dependent_start();
   __syncthreads();
   tc::fence_after_sync();
-  find_span(p, sm.span, sm.warp_sums, &sm.err);
   const uint32_t tmem = sm.tmem;
-  const int32_t n_tiles = int32_t(sm.span.end - sm.span.begin);
   int32_t* const err = &sm.err;
   const WsLayout wl = ws_layout(gridDim.x, kN, kD);
-  if (n_tiles == 0) {
-    if (tid == 0) reinterpret_cast<Cut*>(p.ws + wl.cuts)[blockIdx.x].valid = 0;
-  } else if (warp == 6) {
+  if (warp == kItemWarp) {
     // ---- the items ---------------------------------------------------------------------------------
-    int64_t at = sm.span.begin, off = at - sm.span.before;
-    int32_t r = sm.span.r, h = 0, rt = 0;
-    Request rq;
-    round_request(p.rd, r, rq);
-    const int64_t per_head = tiles_of_head(rq, p.tokens);
-    h = int32_t(off / per_head);
-    off -= h * per_head;
-    while (off >= tiles_of(rq, rt, p.tokens)) off -= tiles_of(rq, rt++, p.tokens);
+    const Span span = find_span(p, err);
     Cut cut = {};
-    int64_t built[2] = {-1, -1};
     bool ok = true;
     int32_t it = 0;
-    for (; at < sm.span.end && ok; ++it) {
-      const int b = it & 1;
-      const int32_t tok0 = rt * p.tokens, ntok = min(p.tokens, rq.n - tok0);
-      const int32_t columns = ntok * p.group, tiles = tiles_of(rq, rt, p.tokens);
-      Item x;
-      x.first_row = rq.first + tok0;
-      x.r = r, x.head = h, x.columns = columns;
-      x.base0 = rq.ctx + (p.rd.parents ? 0 : tok0);
-      x.end = rq.ctx + tok0 + ntok;
-      x.t0 = int32_t(off);
-      x.t1 = int32_t(min(int64_t(tiles), off + (sm.span.end - at)));
-      x.whole = x.t0 == 0 && x.t1 == tiles;
-      x.begins = x.t0 == 0;
-      x.stop = 0;
-      if (x.begins && !x.whole) {
-        cut.total = sm.span.total;
-        cut.first_row = x.first_row;
-        cut.columns = columns, cut.head = h, cut.valid = 1;
-        cut.last = int32_t(((at + tiles) * gridDim.x - 1) / cut.total);  // the CTA of its last tile
-      }
-      if (it >= 2 && !wait_for_warp(&sm.item_empty[b], ((it >> 1) - 1) & 1, err)) {
-        ok = false;
-        break;
-      }
-      uint8_t* const qb = q_at + b * Sh::kQBytes;
-      for (int32_t c = lane; c < kN; c += 32) {
-        const int32_t i = c / p.group, g = c - i * p.group;
-        const bool in = c < columns;
-        if (in) sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(h * p.group + g) * p.o_head;
-        const __nv_bfloat16* src =
-            in ? p.q + (x.first_row + i) * p.ldq + int64_t(h * p.group + g) * p.q_head : p.q;
-#pragma unroll
-        for (int k = 0; k < kD / 8; ++k)
-          async_copy16(qb + (k >> 3) * kN * 128 + tc::sw128(c, k & 7), src + (in ? k * 8 : 0), in);
-      }
-      const int64_t key = int64_t(r) << 32 | rt;
-      if (p.rd.parents && x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
-        built[b] = key;
-        const int32_t nodes = x.end - rq.ctx;
-        uint32_t a[4][4];
-        for (int32_t i = lane; i < nodes; i += 32) {
-          int32_t up = p.rd.parents[rq.first + i];
-          if (up < -1 || up >= i) {
-            report(err, SV_ERR_BAD_INPUT);
-            up = -1;
-          }
-          sm.up[i] = up;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) sm.above[i][w] = i >> 5 == w ? 1u << (i & 31) : 0u;
+    if (span.begin < span.end) {
+      int64_t at = span.begin, off = at - span.before;
+      int32_t r = span.r, h = 0, rt = 0;
+      Request rq;
+      round_request(p.rd, r, rq);
+      const int64_t per_head = tiles_of_head(rq, p.tokens);
+      for (; off >= per_head; off -= per_head) ++h;
+      while (off >= tiles_of(rq, rt, p.tokens)) off -= tiles_of(rq, rt++, p.tokens);
+      int64_t built[2] = {-1, -1};
+      for (; at < span.end && ok; ++it) {
+        const int b = it & 1;
+        const int32_t tok0 = rt * p.tokens, ntok = min(p.tokens, rq.n - tok0);
+        const int32_t columns = ntok * p.group, tiles = tiles_of(rq, rt, p.tokens);
+        Item x;
+        x.first_row = rq.first + tok0;
+        x.r = r, x.head = h, x.columns = columns;
+        x.base0 = rq.ctx + (p.rd.parents ? 0 : tok0);
+        x.end = rq.ctx + tok0 + ntok;
+        x.t0 = int32_t(off);
+        x.t1 = int32_t(min(int64_t(tiles), off + (span.end - at)));
+        x.whole = x.t0 == 0 && x.t1 == tiles;
+        x.begins = x.t0 == 0;
+        x.last = at + (x.t1 - x.t0) == span.end;
+        x.stop = 0;
+        if (x.begins && !x.whole) {
+          cut.total = span.total;
+          cut.first_row = x.first_row;
+          cut.columns = columns, cut.head = h, cut.valid = 1;
+          cut.last = int32_t(((at + tiles) * gridDim.x - 1) / cut.total);  // its last tile's CTA
+        }
+        if (it >= 2 && !wait_for_warp(&sm.item_empty[b], ((it >> 1) - 1) & 1, err)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          sm.item[b] = x;
+        }
+        for (int32_t c = lane; c < columns; c += 32) {
+          const int32_t i = c / p.group, g = c - i * p.group;
+          sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(h * p.group + g) * p.o_head;
         }
         __syncwarp();
-        // the way up doubles its length a round: a row takes over what the row at its end has
-        for (int round = 0; round < 7; ++round) {
-          int32_t next[4];
-          bool more = false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int32_t i = k * 32 + lane;
-            next[k] = -1;
-            if (i < nodes && sm.up[i] >= 0) {
-              more = true;
-              next[k] = sm.up[sm.up[i]];
-#pragma unroll
-              for (int w = 0; w < 4; ++w) a[k][w] = sm.above[i][w] | sm.above[sm.up[i]][w];
-            }
-          }
-          if (!__any_sync(0xffffffffu, more)) break;
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int32_t i = k * 32 + lane;
-            if (i < nodes && sm.up[i] >= 0) {
-#pragma unroll
-              for (int w = 0; w < 4; ++w) sm.above[i][w] = a[k][w];
-              sm.up[i] = next[k];
-            }
+        if (lane == 0) mbar_arrive(&sm.item_full[b]);
+        if (p.rd.parents) {
+          const int64_t key = int64_t(r) << 32 | rt;
+          if (x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
+            built[b] = key;
+            build_table<Sh::kWords>(p, rq.first, tok0, x.end - rq.ctx, columns, sm.up, sm.above,
+                                    sm.seen[b], err);
           }
           __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.table_full[b]);
         }
-#pragma unroll
-        for (int w = 0; w < Sh::kWords; ++w) {
-          const int32_t c = w * 32 + lane, i = tok0 + c / p.group;
-          const bool in = c < columns;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k * 32 >= nodes) break;
-            const uint32_t mine = in ? sm.above[i][k] : 0u;
-            uint32_t row = 0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const uint32_t word = __ballot_sync(0xffffffffu, mine >> j & 1u);
-              if (lane == j) row = word;
-            }
-            sm.seen[b][k * 32 + lane][w] = row;
+        at += x.t1 - x.t0;
+        off = 0;
+        if (at < span.end && ++rt * p.tokens >= rq.n) {
+          rt = 0;
+          if (++h == p.n_kv) {
+            h = 0;
+            do {
+              if (++r == p.rd.B) break;
+              round_request(p.rd, r, rq);
+            } while (rq.n == 0);
+            ok = r < p.rd.B;
           }
-        }
-      }
-      if (lane == 0) sm.item[b] = x;
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_full[b]);
-      at += x.t1 - x.t0;
-      off = 0;
-      if (at < sm.span.end && ++rt * p.tokens >= rq.n) {
-        rt = 0;
-        if (++h == p.n_kv) {
-          h = 0;
-          do round_request(p.rd, ++r, rq);
-          while (rq.n == 0);
         }
       }
     }
@@ -503,13 +564,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     }
     if (lane == 0) reinterpret_cast<Cut*>(p.ws + wl.cuts)[blockIdx.x] = cut;
-  } else if (warp == 4) {
+  } else if (warp == kLoadWarp) {
     // ---- the loads -----------------------------------------------------------------------------------
-    const uint64_t policy = tc::policy_evict_first();
-    int32_t slot = 0, filled = 0;
+    // (keys that other row tiles read too stay in L2 like anything else)
+    const uint64_t once = tc::policy_evict_first();
+    int32_t slot = 0, filled = 0, items = 0;
     uint32_t phase = 1;
     // a tile's boxes, one a lane: its page and first place in it
-    int32_t page = 0, from = 0, boxes = 0, head = 0;
     int32_t v_page = 0, v_from = 0, v_boxes = 0, v_head = 0;
     bool ok = true;
     auto load = [&](const CUtensorMap* map, int32_t pg, int32_t fr, int32_t n, int32_t hd) {
@@ -519,9 +580,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       if (lane < n) {
 #pragma unroll
-        for (int k = 0; k < kD / 64; ++k)
-          tma_load_4d(dst + k * 16384 + lane * p.box_rows * 128, map, k * 64, hd, fr, pg,
-                      &sm.full[slot], policy);
+        for (int k = 0; k < kD / 64; ++k) {
+          uint8_t* const to = dst + k * 16384 + lane * p.box_rows * 128;
+          if (p.reread) tma_load_4d(to, map, k * 64, hd, fr, pg, &sm.full[slot]);
+          else tma_load_4d_hint(to, map, k * 64, hd, fr, pg, &sm.full[slot], once);
+        }
       }
       __syncwarp();
       filled = max(filled, slot + 1);
@@ -536,11 +599,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!wait_for_warp(&sm.item_full[b], (it >> 1) & 1, err)) break;
       const Item x = sm.item[b];
       if (x.stop) break;
-      head = x.head;
+      if (elect()) {
+        // (rows behind the request's last, and columns behind those, hold anything: nobody reads them)
+        mbar_expect_tx(&sm.q_full[b], uint32_t(p.tokens * p.group) * kD * 2);
+#pragma unroll
+        for (int k = 0; k < kD / 64; ++k)
+          tc::tma_load_3d(q_at + b * Sh::kQBytes + k * kN * 128, &map_q, k * 64, x.head * p.group,
+                          int32_t(x.first_row), &sm.q_full[b]);
+      }
+      __syncwarp();
+      items = it + 1;
       for (int32_t t = x.t0; t < x.t1 && ok; ++t) {
-        boxes = (min(kTile, x.end - t * kTile) + p.box_rows - 1) / p.box_rows;
+        const int32_t boxes = (min(kTile, x.end - t * kTile) + p.box_rows - 1) / p.box_rows;
         const int32_t place = t * kTile + lane * p.box_rows;
-        page = 0;
+        int32_t page = 0;
         if (lane < boxes) {
           page = round_page(p.rd, x.r, place);
           if (page < 0) {
@@ -548,10 +620,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             page = 0;
           }
         }
-        from = place & (p.rd.page_size - 1);
-        ok = load(&map_k, page, from, boxes, head) &&
+        const int32_t from = place & (p.rd.page_size - 1);
+        ok = load(&map_k, page, from, boxes, x.head) &&
              (v_boxes == 0 || load(&map_v, v_page, v_from, v_boxes, v_head));
-        v_page = page, v_from = from, v_boxes = boxes, v_head = head;
+        v_page = page, v_from = from, v_boxes = boxes, v_head = x.head;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[b]);
@@ -560,7 +632,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // every copy in flight lands before the CTA may end
     for (int32_t k = 0; k < filled; ++k)
       wait_for_warp(&sm.full[k], k < slot ? phase ^ 1 : phase, err);
-  } else if (warp == 5) {
+    for (int32_t k = max(0, items - 2); k < items; ++k)
+      wait_for_warp(&sm.q_full[k & 1], (k >> 1) & 1, err);
+  } else if (warp == kMmaWarp) {
     // ---- the products --------------------------------------------------------------------------------
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, kN);
     constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, kN) | (1u << 15) | (1u << 16);
@@ -586,8 +660,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int k = 0; k < kTile / 16; ++k)
           tc::mma_bf16(tmem + 2 * kN, desc_of(v_lo + k * 128), desc_of(p_lo + k * 128), kIdO,
                        !v_fresh || k > 0);
-        tc::mma_commit(&sm.empty[slot]);
         tc::mma_commit(&sm.p_free);
+        tc::mma_commit(&sm.empty[slot]);
       }
       __syncwarp();
       next_slot();
@@ -598,6 +672,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!wait_for_warp(&sm.item_full[b], (it >> 1) & 1, err)) break;
       if (sm.item[b].stop) break;
       const int32_t n = sm.item[b].t1 - sm.item[b].t0;
+      if (!wait_for_warp(&sm.q_full[b], (it >> 1) & 1, err)) break;
       for (int32_t k = 0; k < n && ok; ++k, ++t) {
         if (!wait_for_warp(&sm.full[slot], phase, err)) {
           ok = false;
@@ -611,8 +686,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int s = 0; s < kD / 16; ++s)
             tc::mma_bf16(tmem + (t & 1) * kN, desc_of(k_lo + (s >> 2) * 1024 + (s & 3) * 2),
                          desc_of(b_lo + (s >> 2) * (kN * 8) + (s & 3) * 2), kIdS, s > 0);
-          tc::mma_commit(&sm.empty[slot]);
           tc::mma_commit(&sm.s_full[t & 1]);
+          tc::mma_commit(&sm.empty[slot]);
           if (k + 1 == n) tc::mma_commit(&sm.item_empty[b]);
         }
         __syncwarp();
@@ -632,63 +707,64 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     wait_for_warp(&sm.drain, 0, err);
   } else if (warp < kSoftWarps) {
     // ---- softmax and results -------------------------------------------------------------------------
-    const uint32_t lanes = tmem + (uint32_t(32 * warp) << 16);
-    float l[kN];
+    const int half = warp >> 2, quad = warp & 3;
+    const int row = tid & 127;       // place of a key tile; element of the head
+    const int col0 = half * kW;      // this half's first column
+    const uint32_t lanes = tmem + (uint32_t(32 * quad) << 16) + col0;
+    float* const minus = sm.minus + col0;
+    float* const factor = sm.factor + col0;
+    float* const inv = sm.inv + col0;
+    float l[kW];
     int32_t t = 0;
     bool ok = true;
     for (int32_t it = 0; ok; ++it) {
       const int b = it & 1;
-      if (soft_any(!wait_for(&sm.item_full[b], (it >> 1) & 1, err))) break;
-      const Item& x = sm.item[b];
+      if (soft_any(half, !wait_for(&sm.item_full[b], (it >> 1) & 1, err))) break;
+      const Item x = sm.item[b];
       if (x.stop) break;
-      if (tid < kN) sm.m[tid] = kM2Empty;
-      if (tid < SV_MAX_TREE_ROWS / 32) sm.bad[tid] = 0;
+      if (row < kW) minus[row] = -kM2Empty;
+      if (row < SV_MAX_TREE_ROWS / 32) sm.bad[b][half][row] = 0;
 #pragma unroll
-      for (int c = 0; c < kN; ++c) l[c] = 0.f;
-      soft_sync();
+      for (int c = 0; c < kW; ++c) l[c] = 0.f;
+      bool table = !p.rd.parents;
+      soft_sync(half);
       for (int32_t kt = x.t0; kt < x.t1; ++kt, ++t) {
         const uint32_t s_at = lanes + (t & 1) * kN;
         bool free = t == 0;  // P's buffer
-        // a wait that ran out leaves the loop in all four warps together
-        if (soft_any(!wait_for(&sm.s_full[t & 1], (t >> 1) & 1, err))) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
+        // (a wait that ran out leaves the loop in all four warps together)
+        bool late = !wait_for(&sm.s_full[t & 1], (t >> 1) & 1, err);
         const bool masked = (kt + 1) * int64_t(kTile) > x.base0;
-        uint32_t seen[Sh::kWords];
-#pragma unroll
-        for (int w = 0; w < Sh::kWords; ++w) seen[w] = ~0u;
+        uint32_t seen[kChunks];  // bit c: column c of a chunk sees this thread's place
         if (masked) {
-          const int32_t place = kt * kTile + tid, j = place - x.base0;
-          if (place >= x.end) {
+          if (!table) late |= !wait_for(&sm.table_full[b], (it >> 1) & 1, err);
+          table = true;
+          const int32_t place = kt * kTile + row, j = place - x.base0;
 #pragma unroll
-            for (int w = 0; w < Sh::kWords; ++w) seen[w] = 0u;
-          } else if (j >= 0) {
-            if (p.rd.parents) {
-#pragma unroll
-              for (int w = 0; w < Sh::kWords; ++w) seen[w] = sm.seen[b][j][w];
-            } else {  // columns of token j and later ones
-#pragma unroll
-              for (int w = 0; w < Sh::kWords; ++w) {
-                const int32_t from = j * p.group - 32 * w;
-                seen[w] = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+          for (int ch = 0; ch < kChunks; ++ch) {
+            const int c0 = col0 + ch * kC;
+            seen[ch] = ~0u;
+            if (place >= x.end) {
+              seen[ch] = 0u;
+            } else if (j >= 0) {
+              if (p.rd.parents) {
+                seen[ch] = sm.seen[b][j][c0 >> 5] >> (c0 & 31);
+              } else {  // columns of token j and later ones
+                const int32_t from = j * p.group - c0;
+                seen[ch] = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
               }
             }
           }
           // Values that some column must not see are finite for the product, a weight of 0 would not
           // rid it of them: zeros past the end, and zeros for what is not finite, which is added to
-          // the columns that do see it at the end.
-          const int32_t load = t + 1 < n_tiles ? 2 * t + 2 : 2 * t + 1;
-          if (soft_any(!wait_for(&sm.full[load % kStages], (load / kStages) & 1, err))) {
-            ok = false;
-            break;
-          }
-          if (place >= x.base0) {
+          // the columns that do see it at the end.  Each half looks through half of the elements.
+          const int32_t load = kt + 1 == x.t1 && x.last ? 2 * t + 1 : 2 * t + 2;
+          late |= !wait_for(&sm.full[load % kStages], (load / kStages) & 1, err);
+          if (place >= x.base0 && !late) {
             uint8_t* const v = ring + (load % kStages) * Sh::kSlot;
-#pragma unroll 4
-            for (int k = 0; k < kD / 8; ++k) {
-              uint4* const at = reinterpret_cast<uint4*>(v + (k >> 3) * 16384 + tc::sw128(tid, k & 7));
+#pragma unroll
+            for (int i = 0; i < kD / 16; ++i) {
+              const int k = half * (kD / 16) + i;
+              uint4* const at = reinterpret_cast<uint4*>(v + (k >> 3) * 16384 + tc::sw128(row, k & 7));
               if (place >= x.end) {
                 *at = make_uint4(0, 0, 0, 0);
                 continue;
@@ -702,68 +778,70 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                   if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
                 }
                 *at = y;
-                atomicOr(&sm.bad[j >> 5], 1u << (j & 31));
+                atomicOr(&sm.bad[b][half][j >> 5], 1u << (j & 31));
               }
             }
           }
         }
-        // does any score pass its column's m by more than the slack?
-        float s[kC], top = -INFINITY;
+        tc::fence_after_sync();
+        // does any score pass its column's m by more than the slack?  (A half of up to 32 columns keeps
+        // its scores, a wider one reads them again.)
+        float s[kC], m[kC], top = -INFINITY;
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
+          broadcast<kC>(minus + ch * kC, m);
           tmem_load<kC>(s_at + ch * kC, s);
+          scaled<kC>(s, p.scale2, m);
+          if (masked) hide<kC>(s, seen[ch]);
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            float y = fmaf(s[c], p.scale2, -sm.m[ch * kC + c]);
-            if (masked && !(seen[ch * kC / 32] >> (c & 31) & 1u)) y = -INFINITY;
-            top = fmaxf(top, y);
-          }
+          for (int c = 0; c < kC; c += 2) top = max3(top, s[c], s[c + 1]);
         }
-        if (soft_any(top > kSlack)) {
+        const bool raise = soft_any(half, late || top > kSlack);
+        if (raise) {
+          if (soft_any(half, late)) {
+            ok = false;
+            break;
+          }
 #pragma unroll
           for (int ch = 0; ch < kChunks; ++ch) {
-            float mine = -INFINITY;
             tmem_load<kC>(s_at + ch * kC, s);
 #pragma unroll
-            for (int c = 0; c < kC; ++c) {
-              float y = s[c] * p.scale2;
-              if (masked && !(seen[ch * kC / 32] >> (c & 31) & 1u)) y = -INFINITY;
-              const float most = warp_top(y);
-              if (lane == c) mine = most;
-            }
-            if (lane < kC) sm.part[warp][ch * kC + lane] = mine;
+            for (int c = 0; c < kC; ++c) s[c] *= p.scale2;
+            if (masked) hide<kC>(s, seen[ch]);
+            const float most = over_lanes<kC>(s, [](float a, float b) { return fmaxf(a, b); });
+            if (lane < kC) sm.part[quad][col0 + ch * kC + lane] = most;
           }
-          soft_sync();
-          if (tid < kN) {
-            const float old = sm.m[tid];
-            const float most = fmaxf(fmaxf(sm.part[0][tid], sm.part[1][tid]),
-                                     fmaxf(sm.part[2][tid], sm.part[3][tid]));
-            const float m = fmaxf(old, most);
-            sm.m[tid] = m;
-            sm.factor[tid] = fast_exp2(old - m);
+          soft_sync(half);
+          if (row < kW) {
+            const int c = col0 + row;
+            const float old = -minus[row];
+            const float most = fmaxf(fmaxf(sm.part[0][c], sm.part[1][c]),
+                                     fmaxf(sm.part[2][c], sm.part[3][c]));
+            const float now = fmaxf(old, most);
+            minus[row] = -now;
+            factor[row] = fast_exp2(old - now);
           }
-          soft_sync();
-#pragma unroll
-          for (int c = 0; c < kN; ++c) l[c] *= sm.factor[c];
-          if (t > 0) {
-            if (soft_any(!wait_for(&sm.p_free, (t - 1) & 1, err))) {
+          soft_sync(half);
+          if (kt > x.t0) {  // there are sums
+            if (soft_any(half, !wait_for(&sm.p_free, (t - 1) & 1, err))) {
               ok = false;
               break;
             }
             free = true;
             tc::fence_after_sync();
-          }
-          if (kt > x.t0) {  // O has been written
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
+              broadcast<kC>(factor + ch * kC, m);
+#pragma unroll
+              for (int c = 0; c < kC; ++c) l[ch * kC + c] *= m[c];
               tmem_load<kC>(lanes + 2 * kN + ch * kC, s);
 #pragma unroll
-              for (int c = 0; c < kC; ++c) s[c] *= sm.factor[ch * kC + c];
+              for (int c = 0; c < kC; ++c) s[c] *= m[c];
               tmem_store<kC>(lanes + 2 * kN + ch * kC, s);
             }
           }
         }
-        if (!free && soft_any(!wait_for(&sm.p_free, (t - 1) & 1, err))) {
+        if (!free && soft_any(half, !wait_for(&sm.p_free, (t - 1) & 1, err))) {
           ok = false;
           break;
         }
@@ -771,13 +849,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // before that
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
-          tmem_load<kC>(s_at + ch * kC, s);
+          if (kChunks > 1 || raise) {
+            broadcast<kC>(minus + ch * kC, m);
+            tmem_load<kC>(s_at + ch * kC, s);
+            scaled<kC>(s, p.scale2, m);
+            if (masked) hide<kC>(s, seen[ch]);
+          }
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            float y = fmaf(s[c], p.scale2, -sm.m[ch * kC + c]);
-            if (masked && !(seen[ch * kC / 32] >> (c & 31) & 1u)) y = -INFINITY;
-            s[c] = fast_exp2(y);
-            l[ch * kC + c] += s[c];
+          for (int c = 0; c < kC; ++c) s[c] = fast_exp2(s[c]);
+#pragma unroll
+          for (int c = 0; c < kC; c += 2) {
+            const float2 sum = add2(make_float2(l[ch * kC + c], l[ch * kC + c + 1]),
+                                    make_float2(s[c], s[c + 1]));
+            l[ch * kC + c] = sum.x, l[ch * kC + c + 1] = sum.y;
           }
 #pragma unroll
           for (int c = 0; c < kC; c += 8) {
@@ -788,8 +872,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const __nv_bfloat162 two = __floats2bfloat162_rn(s[c + 2 * e], s[c + 2 * e + 1]);
               wp[e] = *reinterpret_cast<const uint32_t*>(&two);
             }
-            const int col = ch * kC + c;
-            *reinterpret_cast<uint4*>(p_at + (col >> 6) * 16384 + tc::sw128(tid, (col & 63) >> 3)) = w;
+            const int col = col0 + ch * kC + c;
+            *reinterpret_cast<uint4*>(p_at + (col >> 6) * 16384 + tc::sw128(row, (col & 63) >> 3)) = w;
           }
         }
         fence_proxy_async();
@@ -798,59 +882,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive(&sm.p_full);
       }
       if (!ok) break;
-      // the item's denominators, then its sums
-      if (soft_any(!wait_for(&sm.p_free, (t - 1) & 1, err))) {
+      // the item's denominators (while the last product is on its way), then its sums
+#pragma unroll
+      for (int ch = 0; ch < kChunks; ++ch) {
+        const float sum = over_lanes<kC>(l + ch * kC, [](float a, float b) { return a + b; });
+        if (lane < kC) sm.part[quad][col0 + ch * kC + lane] = sum;
+      }
+      if (soft_any(half, !wait_for(&sm.p_free, (t - 1) & 1, err))) {
         ok = false;
         break;
       }
       tc::fence_after_sync();
-#pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch) {
-        const float sum = column_sums<kC>(l + ch * kC);
-        if (lane < kC) sm.part[warp][ch * kC + lane] = sum;
-      }
-      soft_sync();
       float* const part = reinterpret_cast<float*>(p.ws + wl.parts) +
                           (2 * int64_t(blockIdx.x) + x.begins) * wl.part_floats;
-      if (tid < x.columns) {
-        const float sum = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]);
+      if (row < kW && col0 + row < x.columns) {
+        const int c = col0 + row;
+        const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]);
         if (x.whole) {
-          sm.inv[tid] = 1.f / sum;
+          inv[row] = 1.f / sum;
           if (p.lse) {
-            const int32_t i = tid / p.group;
-            p.lse[(x.first_row + i) * p.ld_lse + x.head * p.group + tid - i * p.group] =
-                (sm.m[tid] + log2f(sum)) * kLn2;
+            const int32_t i = c / p.group;
+            p.lse[(x.first_row + i) * p.ld_lse + x.head * p.group + c - i * p.group] =
+                (log2f(sum) - minus[row]) * kLn2;
           }
         } else {
-          part[kN * kD + tid] = sm.m[tid];
-          part[kN * kD + kN + tid] = sum;
+          part[kN * kD + c] = -minus[row];
+          part[kN * kD + kN + c] = sum;
         }
       }
-      soft_sync();
-      if (32 * warp < kD) {
+      soft_sync(half);
+      if (32 * quad < kD) {
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
-          if (ch * kC >= x.columns) break;
-          float s[kC];
+          const int c0 = col0 + ch * kC;
+          if (c0 >= x.columns) break;
+          float s[kC], f[kC];
           tmem_load<kC>(lanes + 2 * kN + ch * kC, s);
 #pragma unroll 1
           for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w) {
-            for (uint32_t left = sm.bad[w]; left; left &= left - 1) {  // rare: see above
+            for (uint32_t left = sm.bad[b][0][w] | sm.bad[b][1][w]; left; left &= left - 1) {  // rare
               const int32_t j = 32 * w + __ffs(left) - 1, place = x.base0 + j;
               const int32_t page = max(round_page(p.rd, x.r, place), 0);
               const float v = __bfloat162float(
                   p.v_cache[page * p.page_stride +
                             (place & (p.rd.page_size - 1)) * p.token_stride +
-                            x.head * p.head_stride + tid]);
-              const uint32_t word =
-                  p.rd.parents ? sm.seen[b][j][ch * kC / 32]
-                               : (j * p.group <= ch * kC ? ~0u
-                                  : j * p.group >= ch * kC + 32 ? 0u
-                                                                : ~0u << (j * p.group - ch * kC));
+                            x.head * p.head_stride + row]);
               if (!isfinite(v)) {
 #pragma unroll
                 for (int c = 0; c < kC; ++c)
-                  if (word >> c & 1u) s[c] += v;
+                  if (p.rd.parents ? sm.seen[b][j][(c0 + c) >> 5] >> ((c0 + c) & 31) & 1u
+                                   : c0 + c >= j * p.group)
+                    s[c] += v;
               }
             }
           }
@@ -858,33 +940,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // two columns at once: an even lane takes elements (d, d + 1) of one, an odd lane (d - 1,
             // d) of the next
             const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
+            broadcast<kC>(inv + ch * kC, f);
+            __nv_bfloat16* to[kC / 2];
+#pragma unroll
+            for (int c = 0; c < kC; c += 2)
+              to[c / 2] = p.out + sm.col_off[b][c0 + c + (lane & 1)] + (row & ~1);
 #pragma unroll
             for (int c = 0; c < kC; c += 2) {
-              const __nv_bfloat162 two = __floats2bfloat162_rn(s[c] * sm.inv[ch * kC + c],
-                                                               s[c + 1] * sm.inv[ch * kC + c + 1]);
+              const __nv_bfloat162 two = __floats2bfloat162_rn(s[c] * f[c], s[c + 1] * f[c + 1]);
               const uint32_t mine = *reinterpret_cast<const uint32_t*>(&two);
               const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-              const int col = ch * kC + c + (lane & 1);
-              if (col < x.columns)
-                *reinterpret_cast<uint32_t*>(p.out + sm.col_off[b][col] + (tid & ~1)) =
-                    __byte_perm(mine, other, pick);
+              if (c0 + c + (lane & 1) < x.columns)
+                *reinterpret_cast<uint32_t*>(to[c / 2]) = __byte_perm(mine, other, pick);
             }
           } else {
+            float* const to = part + c0 * kD + row;
 #pragma unroll
             for (int c = 0; c < kC; ++c)
-              if (ch * kC + c < x.columns) part[(ch * kC + c) * kD + tid] = s[c];
+              if (c0 + c < x.columns) to[c * kD] = s[c];
           }
         }
       }
       tc::fence_before_sync();
-      soft_sync();
-      if (tid == 0) mbar_arrive(&sm.item_empty[b]);
+      soft_sync(half);
+      if (row == 0) mbar_arrive(&sm.item_empty[b]);
     }
   }
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kCols);
   }
@@ -913,34 +998,43 @@ __global__ void __launch_bounds__(128) join_kernel(AttnParams p, int32_t ctas) {
   const Cut cut = reinterpret_cast<const Cut*>(p.ws + wl.cuts)[cta];
   if (!cut.valid || col >= cut.columns) return;
   const float* const parts = reinterpret_cast<const float*>(p.ws + wl.parts);
-  // the part in CTA k; none where its run is empty
-  auto part_of = [&](int32_t k) -> const float* {
-    if (k > cta && cut.total * k / ctas == cut.total * (k + 1) / ctas) return nullptr;
-    return parts + (2 * int64_t(k) + (k == cta)) * wl.part_floats;
+  // CTA k's part
+  auto part_of = [&](int32_t k) { return parts + (2 * int64_t(k) + (k == cta)) * wl.part_floats; };
+  // lane's CTA has none where its run is empty
+  auto has = [&](int32_t k) {
+    return k <= cut.last &&
+           (k == cta || cut.total >= ctas || cut.total * k / ctas != cut.total * (k + 1) / ctas);
   };
   float top = kM2Empty;
-  for (int32_t k = cta + lane; k <= cut.last; k += 32) {
-    const float* const x = part_of(k);
-    if (x) top = fmaxf(top, x[kN * kD + col]);
-  }
+  for (int32_t k = cta + lane; k <= cut.last; k += 32)
+    if (has(k)) top = fmaxf(top, part_of(k)[kN * kD + col]);
   top = warp_max(top);
   float y[kE] = {}, sum = 0.f;
   for (int32_t k0 = cta; k0 <= cut.last; k0 += 32) {
+    const int32_t k = k0 + lane;
+    const bool mine = has(k);
     float w = 0.f, d = 0.f;
-    if (k0 + lane <= cut.last) {
-      const float* const x = part_of(k0 + lane);
-      if (x) {
-        w = fast_exp2(x[kN * kD + col] - top);
-        d = w * x[kN * kD + kN + col];
-      }
+    if (mine) {
+      const float* const x = part_of(k);
+      w = fast_exp2(x[kN * kD + col] - top);
+      d = w * x[kN * kD + kN + col];
     }
     sum += warp_sum(d);
-    for (int32_t k = k0; k <= min(cut.last, k0 + 31); ++k) {
-      const float f = __shfl_sync(0xffffffffu, w, k - k0);
-      const float* const x = part_of(k);
-      if (!x) continue;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) y[e] += f * x[col * kD + lane * kE + e];
+    const uint32_t there = __ballot_sync(0xffffffffu, mine);
+    const int32_t n = min(32, cut.last - k0 + 1);
+#pragma unroll 8
+    for (int32_t i = 0; i < n; ++i) {
+      const float f = __shfl_sync(0xffffffffu, w, i);
+      if (there >> i & 1u) {
+        const float* const x = part_of(k0 + i) + col * kD + lane * kE;
+        if constexpr (kE == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(x);
+          y[0] += f * v.x, y[1] += f * v.y, y[2] += f * v.z, y[3] += f * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(x);
+          y[0] += f * v.x, y[1] += f * v.y;
+        }
+      }
     }
   }
   const int32_t i = col / p.group, h = cut.head * p.group + col - i * p.group;
@@ -976,26 +1070,42 @@ bool cache_map(CUtensorMap* map, const void* base, int32_t D, int32_t heads, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [D][heads][rows] of the queries, boxes of 64 elements of `tokens` rows of a key head's query heads.
+bool query_map(CUtensorMap* map, const void* q, int32_t D, int32_t heads, int64_t rows, int64_t q_head,
+               int64_t ldq, int32_t group, int32_t tokens) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows)};
+  const cuuint64_t st[2] = {heads > 1 ? cuuint64_t(q_head) * 2 : 16,
+                            rows > 1 ? cuuint64_t(ldq) * 2 : 16};
+  const cuuint32_t box[3] = {64, cuuint32_t(group), cuuint32_t(tokens)}, es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, st, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct AttnMaps {
+  CUtensorMap q, k, v;
+};
+
 template <int kD, int kN>
-sv_status launch(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, int grid,
-                 cudaStream_t s) {
+sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
   auto* kern = attention_kernel<kD, kN>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
       cudaSuccess)
     return SV_ERR_CUDA;
   const sv_status st =
-      launch_dependent(kern, unsigned(grid), kAttnThreads, kAttnSmem, s, k, v, p);
+      launch_dependent(kern, unsigned(grid), kAttnThreads, kAttnSmem, s, m.q, m.k, m.v, p);
   if (st != SV_OK) return st;
   return launch_dependent(join_kernel<kD, kN>, unsigned(grid) * (kN / 4), 128, 0, s, p, grid);
 }
 
 template <int kD>
-sv_status launch(int32_t n, const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p,
-                 int grid, cudaStream_t s) {
-  return n == 16   ? launch<kD, 16>(k, v, p, grid, s)
-         : n == 32 ? launch<kD, 32>(k, v, p, grid, s)
-         : n == 64 ? launch<kD, 64>(k, v, p, grid, s)
-                   : launch<kD, 128>(k, v, p, grid, s);
+sv_status launch(int32_t n, const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
+  return n == 16   ? launch<kD, 16>(m, p, grid, s)
+         : n == 32 ? launch<kD, 32>(m, p, grid, s)
+         : n == 64 ? launch<kD, 64>(m, p, grid, s)
+                   : launch<kD, 128>(m, p, grid, s);
 }
 
 constexpr int kMaxCtas = 192;  // the workspace's size must not depend on the current device
@@ -1038,7 +1148,7 @@ extern "C" sv_status spec_tree_attention(
   if (B == 0 || max_draft_len + int64_t(bonus_row) == 0 || n_rows == 0)
     return reset_status(status, s);
   if (!q || !out || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len || !page_table ||
-      !workspace)
+      !workspace || n_pages < 1)
     return SV_ERR_INVALID;
   if (!aligned_bf16(q, ldq, q_head, 0) || !aligned_bf16(out, ldo, o_head, 0) ||
       !aligned_bf16(k_cache, page_stride, token_stride, head_stride) || !aligned16(v_cache) ||
@@ -1050,10 +1160,9 @@ extern "C" sv_status spec_tree_attention(
   AttnParams p = {};
   p.rd = {row0,    draft_len, parents,       ctx_len,   page_table, ld_pages, n_rows,
           n_pages, B,         max_draft_len, bonus_row, max_pages,  page_size};
-  p.q = static_cast<const __nv_bfloat16*>(q), p.ldq = ldq, p.q_head = q_head;
   p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
   p.page_stride = page_stride, p.token_stride = token_stride, p.head_stride = head_stride;
-  p.n_heads = n_heads, p.n_kv = n_kv_heads, p.group = group;
+  p.n_kv = n_kv_heads, p.group = group;
   const int64_t rows = (max_draft_len + int64_t(bonus_row)) * group;
   const int32_t n = columns_for(rows);
   p.tokens = n / group;
@@ -1064,11 +1173,12 @@ extern "C" sv_status spec_tree_attention(
   p.ws = static_cast<uint8_t*>(workspace);
   const int sms = std::min(device_sm_count(), kMaxCtas);
   if (sms < 1) return SV_ERR_CUDA;
-  if (n_pages < 1) return SV_ERR_INVALID;
-  CUtensorMap mk, mv;
-  if (!cache_map(&mk, k_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
+  if (n_rows > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  AttnMaps m;
+  if (!query_map(&m.q, q, D, n_heads, n_rows, q_head, ldq, group, p.tokens) ||
+      !cache_map(&m.k, k_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
                  page_stride, p.box_rows) ||
-      !cache_map(&mv, v_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
+      !cache_map(&m.v, v_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
                  page_stride, p.box_rows))
     return SV_ERR_UNSUPPORTED;
   // no more CTAs than there can be tiles
@@ -1077,5 +1187,6 @@ extern "C" sv_status spec_tree_attention(
   const double most = double(B) * n_kv_heads * double(row_tiles) * double(key_tiles);
   if (most > 9e15) return SV_ERR_UNSUPPORTED;
   const int grid = int(std::max(1.0, std::min(double(sms), most)));
-  return D == 64 ? launch<64>(n, mk, mv, p, grid, s) : launch<128>(n, mk, mv, p, grid, s);
+  p.reread = row_tiles > 1;
+  return D == 64 ? launch<64>(n, m, p, grid, s) : launch<128>(n, m, p, grid, s);
 }
