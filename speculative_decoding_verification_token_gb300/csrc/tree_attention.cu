@@ -34,6 +34,7 @@ constexpr int kAttnThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10;
 constexpr uint32_t kAttnSmem = 232448 - 1024;  // dynamic shared memory of a CTA, less what is static
+constexpr int kMaxCtas = 192;     // the workspace's size does not depend on the current device
 constexpr float kSlack = 8.f;     // log2 of what P may reach before m is raised
 
 struct AttnParams {
@@ -57,10 +58,11 @@ struct AttnParams {
 struct Cut {
   int64_t total;      // tiles of the whole call
   int64_t first_row;  // the row tile's first row
-  int32_t columns, head, last, valid;
+  int32_t head, last;
 };
 
-// Workspace: per CTA its error, its cut, and two parts (0: of an item begun before it, 1: of one it
+// Workspace: per CTA its error (times 256) and the columns of its cut item (0: it begins none that it
+// does not end), its cut, and two parts (0: of an item begun before it, 1: of one it
 // begins) of kN x (D + 2) binary32: [kN][D] sums, [kN] maxima, [kN] denominators.
 struct WsLayout {
   size_t cuts, parts, part_floats, bytes;
@@ -91,39 +93,34 @@ struct Span {
   int64_t total, begin, end;  // tiles of the call, of this CTA
   int64_t before;             // tiles before request `r`
   int32_t r;                  // the request that `begin` lies in
+  Request q;                  // and its sizes
 };
 
-// One warp: this CTA's run of the list.  Requests in chunks of 32, a lane each; two rounds over them,
-// the second from the first's sums where there is one chunk only.
+// One warp: this CTA's run of the list, from the requests in chunks of 32, a lane each.
 __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
   const int lane = threadIdx.x & 31;
+  const int32_t steps = min(p.rd.B, 32);
   Span span = {};
-  int64_t mine = 0, upto = 0;
-  auto chunk = [&](int32_t r0) {
+  Request q = {};
+  int64_t mine = 0, upto = 0, total = 0;
+  auto chunk = [&](int32_t r0, bool tell) {
     const int32_t r = r0 + lane;
     mine = 0;
+    q.n = 0;
     if (r < p.rd.B) {
-      Request q;
-      if (!round_request(p.rd, r, q) && blockIdx.x == 0) report(err, SV_ERR_BAD_INPUT);
+      if (!round_request(p.rd, r, q) && tell) report(err, SV_ERR_BAD_INPUT);
       mine = tiles_of_head(q, p.tokens) * p.n_kv;
     }
-  };
-  auto scan = [&] {
     upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < steps; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
   };
-  int64_t total = 0;
-#pragma unroll 4
   for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
-    chunk(r0);
-    total += mine;
+    chunk(r0, blockIdx.x == 0);
+    total += __shfl_sync(0xffffffffu, upto, steps - 1);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   span.total = total;
   if (total < (int64_t(1) << 22)) {  // (the products stay in 32 bits: at most 192 CTAs)
     span.begin = uint32_t(total) * blockIdx.x / gridDim.x;
@@ -135,8 +132,7 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
   if (span.begin == span.end) return span;
   int64_t before = 0;
   for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
-    if (p.rd.B > 32) chunk(r0);
-    scan();
+    if (p.rd.B > 32) chunk(r0, false);
     const int64_t a = before + upto - mine;
     const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= span.begin &&
                                                         span.begin < a + mine);
@@ -144,9 +140,12 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
       const int l = __ffs(hit) - 1;
       span.before = __shfl_sync(0xffffffffu, a, l);
       span.r = r0 + l;
+      span.q.first = __shfl_sync(0xffffffffu, q.first, l);
+      span.q.n = __shfl_sync(0xffffffffu, q.n, l);
+      span.q.ctx = __shfl_sync(0xffffffffu, q.ctx, l);
       break;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    before += __shfl_sync(0xffffffffu, upto, steps - 1);
   }
   return span;
 }
@@ -359,7 +358,7 @@ struct AttnShared {
     uint32_t bad[2][2][SV_MAX_TREE_ROWS / 32];  // an item's rows whose values (of a half of D) are not
                                                 // all finite
     uint32_t tmem;
-    int32_t err;
+    int32_t err, cut_columns;
   };
   static constexpr uint32_t kSmall = (sizeof(Small) + 127) / 128 * 128;
   static constexpr int kStages() {
@@ -485,15 +484,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ---- the items ---------------------------------------------------------------------------------
     const Span span = find_span(p, err);
     Cut cut = {};
+    int32_t cut_columns = 0;
     bool ok = true;
     int32_t it = 0;
     if (span.begin < span.end) {
       int64_t at = span.begin, off = at - span.before;
       int32_t r = span.r, h = 0, rt = 0;
-      Request rq;
-      round_request(p.rd, r, rq);
+      Request rq = span.q;
       const int64_t per_head = tiles_of_head(rq, p.tokens);
-      for (; off >= per_head; off -= per_head) ++h;
+      h = int32_t(off <= INT32_MAX ? uint32_t(off) / uint32_t(min(per_head, int64_t(INT32_MAX)))
+                                   : off / per_head);
+      off -= h * per_head;
       while (off >= tiles_of(rq, rt, p.tokens)) off -= tiles_of(rq, rt++, p.tokens);
       int64_t built[2] = {-1, -1};
       for (; at < span.end && ok; ++it) {
@@ -511,19 +512,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         x.begins = x.t0 == 0;
         x.last = at + (x.t1 - x.t0) == span.end;
         x.stop = 0;
-        if (x.begins && !x.whole) {
-          cut.total = span.total;
-          cut.first_row = x.first_row;
-          cut.columns = columns, cut.head = h, cut.valid = 1;
-          cut.last = int32_t(((at + tiles) * gridDim.x - 1) / cut.total);  // its last tile's CTA
-        }
         if (it >= 2 && !wait_for_warp(&sm.item_empty[b], ((it >> 1) - 1) & 1, err)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
-          sm.item[b] = x;
-        }
+        if (lane == 0) sm.item[b] = x;
         for (int32_t c = lane; c < columns; c += 32) {
           const int32_t i = c / p.group, g = c - i * p.group;
           sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(h * p.group + g) * p.o_head;
@@ -539,6 +532,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.table_full[b]);
+        }
+        if (x.begins && !x.whole) {
+          cut.total = span.total;
+          cut.first_row = x.first_row;
+          cut.head = h;
+          cut_columns = columns;
+          cut.last = int32_t(((at + tiles) * gridDim.x - 1) / cut.total);  // its last tile's CTA
         }
         at += x.t1 - x.t0;
         off = 0;
@@ -563,7 +563,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_arrive(&sm.item_full[b]);
       }
     }
-    if (lane == 0) reinterpret_cast<Cut*>(p.ws + wl.cuts)[blockIdx.x] = cut;
+    if (lane == 0) {
+      if (cut_columns) reinterpret_cast<Cut*>(p.ws + wl.cuts)[blockIdx.x] = cut;
+      sm.cut_columns = cut_columns;
+    }
   } else if (warp == kLoadWarp) {
     // ---- the loads -----------------------------------------------------------------------------------
     // (keys that other row tiles read too stay in L2 like anything else)
@@ -973,30 +976,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kCols);
   }
-  if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err;
+  if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err * 256 + sm.cut_columns;
 }
 
 // ---- the parts of cut items joined -------------------------------------------------------------------
 
-// A warp per column of a CTA's cut item.  Block 0 also gathers the CTAs' errors.
+constexpr int kJoinThreads = 256;
+
+// A column of the item that CTA `cta` begins, by one warp.
 template <int kD, int kN>
-__global__ void __launch_bounds__(128) join_kernel(AttnParams p, int32_t ctas) {
+__device__ __forceinline__ void join_column(const AttnParams& p, const WsLayout& wl, const Cut& cut,
+                                            int32_t ctas, int32_t cta, int32_t col) {
   constexpr int kE = kD / 32;
-  constexpr int kBlocks = kN / 4;
-  dependent_start();
-  const WsLayout wl = ws_layout(ctas, kN, kD);
   const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x < 32 && p.status) {
-    int32_t code = 0;
-    for (int32_t c = lane; c < ctas; c += 32)
-      code = max(code, reinterpret_cast<const int32_t*>(p.ws)[c]);
-    code = __reduce_max_sync(0xffffffffu, code);
-    if (lane == 0) *p.status = code;
-  }
-  const int32_t cta = blockIdx.x / kBlocks;
-  const int32_t col = (blockIdx.x % kBlocks) * 4 + (threadIdx.x >> 5);
-  const Cut cut = reinterpret_cast<const Cut*>(p.ws + wl.cuts)[cta];
-  if (!cut.valid || col >= cut.columns) return;
   const float* const parts = reinterpret_cast<const float*>(p.ws + wl.parts);
   // CTA k's part
   auto part_of = [&](int32_t k) { return parts + (2 * int64_t(k) + (k == cta)) * wl.part_floats; };
@@ -1005,35 +997,41 @@ __global__ void __launch_bounds__(128) join_kernel(AttnParams p, int32_t ctas) {
     return k <= cut.last &&
            (k == cta || cut.total >= ctas || cut.total * k / ctas != cut.total * (k + 1) / ctas);
   };
-  float top = kM2Empty;
-  for (int32_t k = cta + lane; k <= cut.last; k += 32)
-    if (has(k)) top = fmaxf(top, part_of(k)[kN * kD + col]);
-  top = warp_max(top);
-  float y[kE] = {}, sum = 0.f;
+  float top = kM2Empty, y[kE] = {}, sum = 0.f;
   for (int32_t k0 = cta; k0 <= cut.last; k0 += 32) {
+    // this lane's part: its maximum and denominator
     const int32_t k = k0 + lane;
     const bool mine = has(k);
-    float w = 0.f, d = 0.f;
-    if (mine) {
-      const float* const x = part_of(k);
-      w = fast_exp2(x[kN * kD + col] - top);
-      d = w * x[kN * kD + kN + col];
-    }
-    sum += warp_sum(d);
+    const float* const x = part_of(mine ? k : cta) + kN * kD + col;
+    const float m = mine ? x[0] : kM2Empty, d = mine ? x[kN] : 0.f;
+    const float most = fmaxf(top, warp_max(m));
+    const float old = fast_exp2(top - most), w = mine ? fast_exp2(m - most) : 0.f;
+    sum = sum * old + warp_sum(d * w);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) y[e] *= old;
+    top = most;
     const uint32_t there = __ballot_sync(0xffffffffu, mine);
     const int32_t n = min(32, cut.last - k0 + 1);
-#pragma unroll 8
-    for (int32_t i = 0; i < n; ++i) {
-      const float f = __shfl_sync(0xffffffffu, w, i);
-      if (there >> i & 1u) {
-        const float* const x = part_of(k0 + i) + col * kD + lane * kE;
+    for (int32_t i0 = 0; i0 < n; i0 += 8) {
+      float v[8][kE];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool is = i0 + i < n && (there >> (i0 + i) & 1u);
+        const float* const o = part_of(is ? k0 + i0 + i : cta) + col * kD + lane * kE;
         if constexpr (kE == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(x);
-          y[0] += f * v.x, y[1] += f * v.y, y[2] += f * v.z, y[3] += f * v.w;
+          const float4 z = *reinterpret_cast<const float4*>(o);
+          v[i][0] = z.x, v[i][1] = z.y, v[i][2] = z.z, v[i][3] = z.w;
         } else {
-          const float2 v = *reinterpret_cast<const float2*>(x);
-          y[0] += f * v.x, y[1] += f * v.y;
+          const float2 z = *reinterpret_cast<const float2*>(o);
+          v[i][0] = z.x, v[i][1] = z.y;
         }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+        const bool is = i0 + i < n && (there >> (i0 + i) & 1u);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) y[e] += is ? f * v[i][e] : 0.f;
       }
     }
   }
@@ -1045,6 +1043,51 @@ __global__ void __launch_bounds__(128) join_kernel(AttnParams p, int32_t ctas) {
   for (int e = 0; e < kE; e += 2)
     *reinterpret_cast<__nv_bfloat162*>(o + e) = __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
   if (lane == 0 && p.lse) p.lse[row * p.ld_lse + h] = (top + log2f(sum)) * kLn2;
+}
+
+// A warp for every column that there can be; the first ones, spread over the SMs, take those of
+// the cut items.  Block 0 also gathers the CTAs' errors.
+template <int kD, int kN>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p, int32_t ctas) {
+  constexpr int kE = kD / 32;
+  constexpr int kRounds = (kMaxCtas + 31) / 32;
+  dependent_start();
+  const WsLayout wl = ws_layout(ctas, kN, kD);
+  const int lane = threadIdx.x & 31;
+  int32_t columns[kRounds], all = 0, code = 0;  // of CTA 32 k + lane
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k)
+    columns[k] = k * 32 + lane < ctas ? reinterpret_cast<const int32_t*>(p.ws)[k * 32 + lane] : 0;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    code = max(code, columns[k] >> 8);
+    columns[k] &= 255;
+    all += columns[k];
+  }
+  if (blockIdx.x == 0 && threadIdx.x < 32 && p.status) {
+    code = __reduce_max_sync(0xffffffffu, code);
+    if (lane == 0) *p.status = code;
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  int32_t cta = -1, col = blockIdx.x + gridDim.x * (threadIdx.x >> 5);
+  if (col >= all) return;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    int32_t upto = columns[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, col < upto);
+    const int l = past ? __ffs(past) - 1 : 31;
+    const int32_t before = __shfl_sync(0xffffffffu, upto - (past ? columns[k] : 0), l);
+    if (cta < 0) {
+      col -= before;
+      if (past) cta = k * 32 + l;
+    }
+  }
+  join_column<kD, kN>(p, wl, reinterpret_cast<const Cut*>(p.ws + wl.cuts)[cta], ctas, cta, col);
 }
 
 // ---- host ----------------------------------------------------------------------------------------------
@@ -1097,7 +1140,7 @@ sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t 
   const sv_status st =
       launch_dependent(kern, unsigned(grid), kAttnThreads, kAttnSmem, s, m.q, m.k, m.v, p);
   if (st != SV_OK) return st;
-  return launch_dependent(join_kernel<kD, kN>, unsigned(grid) * (kN / 4), 128, 0, s, p, grid);
+  return launch_dependent(join_kernel<kD, kN>, unsigned(grid) * (kN * 32 / kJoinThreads), kJoinThreads, 0, s, p, grid);
 }
 
 template <int kD>
@@ -1107,8 +1150,6 @@ sv_status launch(int32_t n, const AttnMaps& m, const AttnParams& p, int grid, cu
          : n == 64 ? launch<kD, 64>(m, p, grid, s)
                    : launch<kD, 128>(m, p, grid, s);
 }
-
-constexpr int kMaxCtas = 192;  // the workspace's size must not depend on the current device
 
 }  // namespace
 }  // namespace sv
