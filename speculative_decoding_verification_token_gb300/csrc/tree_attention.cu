@@ -19,8 +19,8 @@
 // The work -- (request, key head, row tile, key tile) -- is one list, cut into equal runs for a
 // persistent CTA on every SM, wherever the cuts fall; what a cut leaves in parts goes to the workspace
 // and is joined by a second kernel.
-#include "round.cuh"
-#include "tc.cuh"
+#include "tree_attention.cuh"
+
 #include "tmap.h"
 
 #include <algorithm>
@@ -29,313 +29,7 @@
 namespace sv {
 namespace {
 
-constexpr int kTile = 128;        // places of a tile
-constexpr int kAttnThreads = 384;
-constexpr int kSoftWarps = 8;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10;
-constexpr uint32_t kAttnSmem = 232448 - 1024;  // dynamic shared memory of a CTA, less what is static
-constexpr int kMaxCtas = 192;     // the workspace's size does not depend on the current device
-constexpr float kSlack = 8.f;     // log2 of what P may reach before m is raised
-
-struct AttnParams {
-  RoundParams rd;
-  const __nv_bfloat16* v_cache;
-  int64_t page_stride, token_stride, head_stride;
-  int32_t n_kv, group;
-  int32_t tokens;    // tokens of a row tile
-  int32_t box_rows;  // places of a TMA box
-  int32_t reread;    // several row tiles read the same keys
-  float scale2;  // scale * log2(e)
-  __nv_bfloat16* out;
-  int64_t ldo, o_head;
-  float* lse;
-  int64_t ld_lse;
-  int32_t* status;
-  uint8_t* ws;
-};
-
-// A cut item: what the joining kernel needs of it, left by the CTA that its first part lies in.
-struct Cut {
-  int64_t total;      // tiles of the whole call
-  int64_t first_row;  // the row tile's first row
-  int32_t head, last;
-};
-
-// Workspace: per CTA its error (times 256) and the columns of its cut item (0: it begins none that it
-// does not end), its cut, and two parts (0: of an item begun before it, 1: of one it
-// begins) of kN x (D + 2) binary32: [kN][D] sums, [kN] maxima, [kN] denominators.
-struct WsLayout {
-  size_t cuts, parts, part_floats, bytes;
-};
-__host__ __device__ inline WsLayout ws_layout(int ctas, int n, int d) {
-  WsLayout w;
-  w.cuts = (size_t(ctas) * 4 + 255) / 256 * 256;
-  w.parts = w.cuts + (size_t(ctas) * sizeof(Cut) + 255) / 256 * 256;
-  w.part_floats = size_t(n) * (d + 2);
-  w.bytes = w.parts + size_t(ctas) * 2 * w.part_floats * 4;
-  return w;
-}
-
-// ---- the list of work ------------------------------------------------------------------------------
-
-__device__ __forceinline__ int32_t tiles_of(const Request& q, int32_t rt, int32_t tokens) {
-  return int32_t((int64_t(q.ctx) + min(q.n, (rt + 1) * tokens) + kTile - 1) / kTile);
-}
-
-// Tiles of one key head of a request (its row tiles together).
-__device__ __forceinline__ int64_t tiles_of_head(const Request& q, int32_t tokens) {
-  int64_t t = 0;
-  for (int32_t rt = 0; rt * tokens < q.n; ++rt) t += tiles_of(q, rt, tokens);
-  return t;
-}
-
-struct Span {
-  int64_t total, begin, end;  // tiles of the call, of this CTA
-  int64_t before;             // tiles before request `r`
-  int32_t r;                  // the request that `begin` lies in
-  Request q;                  // and its sizes
-};
-
-// One warp: this CTA's run of the list, from the requests in chunks of 32, a lane each.
-__device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
-  const int lane = threadIdx.x & 31;
-  const int32_t steps = min(p.rd.B, 32);
-  Span span = {};
-  Request q = {};
-  int64_t mine = 0, upto = 0, total = 0;
-  auto chunk = [&](int32_t r0, bool tell) {
-    const int32_t r = r0 + lane;
-    mine = 0;
-    q.n = 0;
-    if (r < p.rd.B) {
-      if (!round_request(p.rd, r, q) && tell) report(err, SV_ERR_BAD_INPUT);
-      mine = tiles_of_head(q, p.tokens) * p.n_kv;
-    }
-    upto = mine;
-    for (int o = 1; o < steps; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-  };
-  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
-    chunk(r0, blockIdx.x == 0);
-    total += __shfl_sync(0xffffffffu, upto, steps - 1);
-  }
-  span.total = total;
-  if (total < (int64_t(1) << 22)) {  // (the products stay in 32 bits: at most 192 CTAs)
-    span.begin = uint32_t(total) * blockIdx.x / gridDim.x;
-    span.end = uint32_t(total) * (blockIdx.x + 1) / gridDim.x;
-  } else {
-    span.begin = total * blockIdx.x / gridDim.x;
-    span.end = total * (blockIdx.x + 1) / gridDim.x;
-  }
-  if (span.begin == span.end) return span;
-  int64_t before = 0;
-  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
-    if (p.rd.B > 32) chunk(r0, false);
-    const int64_t a = before + upto - mine;
-    const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= span.begin &&
-                                                        span.begin < a + mine);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      span.before = __shfl_sync(0xffffffffu, a, l);
-      span.r = r0 + l;
-      span.q.first = __shfl_sync(0xffffffffu, q.first, l);
-      span.q.n = __shfl_sync(0xffffffffu, q.n, l);
-      span.q.ctx = __shfl_sync(0xffffffffu, q.ctx, l);
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, upto, steps - 1);
-  }
-  return span;
-}
-
-// ---- small pieces ----------------------------------------------------------------------------------
-
-__device__ __forceinline__ bool try_wait_for(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
-      "selp.b32 %0, 1, 0, P;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return done != 0;
-}
-
-// Wait for phase `parity`, asleep; gives up after kWaitLimitNs and reports it.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t* err) {
-  if (try_wait_for(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (!try_wait_for(bar, parity)) {
-    if (global_ns() - t0 > kWaitLimitNs) {
-      report(err, SV_ERR_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
-// The same by a whole warp: one answer.
-__device__ __forceinline__ bool wait_for_warp(uint64_t* bar, uint32_t parity, int32_t* err) {
-  return __all_sync(0xffffffffu, wait_for(bar, parity, err));
-}
-
-__device__ __forceinline__ bool elect() {
-  uint32_t is;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(is));
-  return is != 0;
-}
-
-// Barrier of a half's four softmax warps (1 or 2) that also tells whether `x` held in any thread.
-__device__ __forceinline__ bool soft_any(int half, bool x) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.or.pred p, %2, 128, q;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(any)
-      : "r"(uint32_t(x)), "r"(1 + half)
-      : "memory");
-  return any != 0;
-}
-__device__ __forceinline__ void soft_sync(int half) { named_sync(1 + half, 128); }
-
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1,
-                                            int32_t c2, int32_t c3, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* map, int32_t c0,
-                                                 int32_t c1, int32_t c2, int32_t c3, uint64_t* bar,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar)),
-      "l"(policy)
-      : "memory");
-}
-
-// Shared-memory descriptors of 128-byte swizzled operands by halves (low word: address >> 4 and leading
-// offset, high word: stride offset 1024, version 1, swizzle).  Operands whose rows run along the
-// contraction (K, Q) leave the leading offset unused; in those whose rows run along M or N (V, P: a row
-// of 64 elements a place) it is the distance between groups of 64, and eight places are 1024 bytes.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-constexpr uint32_t kAlongK = 1u << 16;
-constexpr uint32_t kAcross = (16384u >> 4) << 16;  // groups of 64: 128 places of 128 bytes
-__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
-  return d;
-}
-
-// C columns of this thread's TMEM lane.
-template <int C>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
-  if constexpr (C == 8) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-          "=f"(v[7])
-        : "r"(taddr)
-        : "memory");
-  } else if constexpr (C == 16) {
-    tc::tmem_load16(taddr, v);
-  } else {
-    tc::tmem_load32(taddr, v);
-  }
-}
-
-template <int C>
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const float* v) {
-#pragma unroll
-  for (int j = 0; j < C; j += 8)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-                     taddr + j),
-                 "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
-                 "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
-                 : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// C columns a lane joined over the lanes by `op`: column lane % C's result in every lane.  Half of what
-// a lane holds goes to the lane that keeps it, in every step.
-template <int C, typename Op>
-__device__ __forceinline__ float over_lanes(float* v, Op op) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o >= C; o >>= 1) {
-#pragma unroll
-    for (int j = 0; j < C; ++j) v[j] = op(v[j], __shfl_xor_sync(0xffffffffu, v[j], o));
-  }
-#pragma unroll
-  for (int o = C / 2; o > 0; o >>= 1) {
-    const bool upper = lane & o;
-#pragma unroll
-    for (int j = 0; j < o; ++j) {
-      const float give = upper ? v[j] : v[j + o], keep = upper ? v[j + o] : v[j];
-      v[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
-    }
-  }
-  return v[0];
-}
-
-// C consecutive values of shared memory, the same in every lane.
-template <int C>
-__device__ __forceinline__ void broadcast(const float* at, float* v) {
-#pragma unroll
-  for (int j = 0; j < C; j += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(at + j);
-    v[j] = x.x, v[j + 1] = x.y, v[j + 2] = x.z, v[j + 3] = x.w;
-  }
-}
-
-// s scale + minus, in pairs.
-template <int C>
-__device__ __forceinline__ void scaled(float* s, float scale, const float* minus) {
-  const float2 f = splat2(scale);
-#pragma unroll
-  for (int j = 0; j < C; j += 2) {
-    const float2 y = fma2(make_float2(s[j], s[j + 1]), f, make_float2(minus[j], minus[j + 1]));
-    s[j] = y.x, s[j + 1] = y.y;
-  }
-}
-
-// -inf in the columns whose bit is clear.
-template <int C>
-__device__ __forceinline__ void hide(float* y, uint32_t seen) {
-#pragma unroll
-  for (int j = 0; j < C; ++j)
-    if (!(seen >> j & 1u)) y[j] = -INFINITY;
-}
-
-__device__ __forceinline__ bool not_finite2(uint32_t w) {  // either half of a bf16 pair
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-
-// A work item as the warps of a CTA share it.
-struct Item {
-  int64_t first_row;  // row of the tile's first token
-  int32_t r, head, columns;
-  int32_t base0;   // places below it are seen by every column
-  int32_t end;     // places from it on by none
-  int32_t t0, t1;  // its key tiles in this CTA
-  int32_t whole, begins, last;
-  int32_t stop;    // no item: the list is at its end
-};
+using namespace attn;
 
 template <int kD, int kN>
 struct AttnShared {
@@ -369,51 +63,10 @@ struct AttnShared {
 
 // Who sees whom in a tree, by one warp: seen[j] = columns that see row j, for the row tile's columns.
 template <int kWords>
-__device__ __forceinline__ void build_table(const AttnParams& p, int64_t first, int32_t tok0,
-                                            int32_t nodes, int32_t columns, int32_t* up,
-                                            uint32_t (*above)[4], uint32_t (*seen)[kWords],
-                                            int32_t* err) {
+__device__ __forceinline__ void build_seen(const AttnParams& p, const Item& x, uint32_t (*above)[4],
+                                           uint32_t (*seen)[kWords]) {
   const int lane = threadIdx.x & 31;
-  for (int32_t i = lane; i < nodes; i += 32) {
-    int32_t u = p.rd.parents[first + i];
-    if (u < -1 || u >= i) {
-      report(err, SV_ERR_BAD_INPUT);
-      u = -1;
-    }
-    up[i] = u;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) above[i][w] = i >> 5 == w ? 1u << (i & 31) : 0u;
-  }
-  __syncwarp();
-  // the way up doubles its length a round: a row takes over what the row at its end has
-  for (int round = 0; round < 7; ++round) {
-    uint32_t a[4][4];
-    int32_t next[4];
-    bool more = false;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int32_t i = k * 32 + lane;
-      next[k] = -1;
-      if (i < nodes && up[i] >= 0) {
-        more = true;
-        next[k] = up[up[i]];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) a[k][w] = above[i][w] | above[up[i]][w];
-      }
-    }
-    if (!__any_sync(0xffffffffu, more)) break;
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int32_t i = k * 32 + lane;
-      if (i < nodes && up[i] >= 0) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) above[i][w] = a[k][w];
-        up[i] = next[k];
-      }
-    }
-    __syncwarp();
-  }
+  const int32_t nodes = x.end - x.ctx, tok0 = x.tok0, columns = x.columns;
 #pragma unroll
   for (int w = 0; w < kWords; ++w) {
     const int32_t c = w * 32 + lane, i = tok0 + c / p.group;
@@ -482,94 +135,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const WsLayout wl = ws_layout(gridDim.x, kN, kD);
   if (warp == kItemWarp) {
     // ---- the items ---------------------------------------------------------------------------------
-    const Span span = find_span(p, err);
-    Cut cut = {};
-    int32_t cut_columns = 0;
-    bool ok = true;
-    int32_t it = 0;
-    if (span.begin < span.end) {
-      int64_t at = span.begin, off = at - span.before;
-      int32_t r = span.r, h = 0, rt = 0;
-      Request rq = span.q;
-      const int64_t per_head = tiles_of_head(rq, p.tokens);
-      h = int32_t(off <= INT32_MAX ? uint32_t(off) / uint32_t(min(per_head, int64_t(INT32_MAX)))
-                                   : off / per_head);
-      off -= h * per_head;
-      while (off >= tiles_of(rq, rt, p.tokens)) off -= tiles_of(rq, rt++, p.tokens);
-      int64_t built[2] = {-1, -1};
-      for (; at < span.end && ok; ++it) {
-        const int b = it & 1;
-        const int32_t tok0 = rt * p.tokens, ntok = min(p.tokens, rq.n - tok0);
-        const int32_t columns = ntok * p.group, tiles = tiles_of(rq, rt, p.tokens);
-        Item x;
-        x.first_row = rq.first + tok0;
-        x.r = r, x.head = h, x.columns = columns;
-        x.base0 = rq.ctx + (p.rd.parents ? 0 : tok0);
-        x.end = rq.ctx + tok0 + ntok;
-        x.t0 = int32_t(off);
-        x.t1 = int32_t(min(int64_t(tiles), off + (span.end - at)));
-        x.whole = x.t0 == 0 && x.t1 == tiles;
-        x.begins = x.t0 == 0;
-        x.last = at + (x.t1 - x.t0) == span.end;
-        x.stop = 0;
-        if (it >= 2 && !wait_for_warp(&sm.item_empty[b], ((it >> 1) - 1) & 1, err)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) sm.item[b] = x;
-        for (int32_t c = lane; c < columns; c += 32) {
-          const int32_t i = c / p.group, g = c - i * p.group;
-          sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(h * p.group + g) * p.o_head;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.item_full[b]);
-        if (p.rd.parents) {
-          const int64_t key = int64_t(r) << 32 | rt;
+    int64_t built[2] = {-1, -1};
+    const int32_t columns = walk_items(
+        p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item, sm.item_full, sm.item_empty, err,
+        [&](int b, const Item& x) {
+          for (int32_t c = lane; c < x.columns; c += 32) {
+            const int32_t i = c / p.group, g = c - i * p.group;
+            sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(x.head * p.group + g) * p.o_head;
+          }
+        },
+        [&](int b, const Item& x, int64_t first) {
+          if (!p.rd.parents) return;
+          const int64_t key = int64_t(x.r) << 32 | x.tok0;
           if (x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
             built[b] = key;
-            build_table<Sh::kWords>(p, rq.first, tok0, x.end - rq.ctx, columns, sm.up, sm.above,
-                                    sm.seen[b], err);
+            build_above(p, first, x.end - x.ctx, sm.up, sm.above, err);
+            build_seen<Sh::kWords>(p, x, sm.above, sm.seen[b]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.table_full[b]);
-        }
-        if (x.begins && !x.whole) {
-          cut.total = span.total;
-          cut.first_row = x.first_row;
-          cut.head = h;
-          cut_columns = columns;
-          cut.last = int32_t(((at + tiles) * gridDim.x - 1) / cut.total);  // its last tile's CTA
-        }
-        at += x.t1 - x.t0;
-        off = 0;
-        if (at < span.end && ++rt * p.tokens >= rq.n) {
-          rt = 0;
-          if (++h == p.n_kv) {
-            h = 0;
-            do {
-              if (++r == p.rd.B) break;
-              round_request(p.rd, r, rq);
-            } while (rq.n == 0);
-            ok = r < p.rd.B;
-          }
-        }
-      }
-    }
-    // (one more, to say that there are none)
-    const int b = it & 1;
-    if (ok && (it < 2 || wait_for_warp(&sm.item_empty[b], ((it >> 1) - 1) & 1, err))) {
-      if (lane == 0) {
-        sm.item[b].stop = 1;
-        mbar_arrive(&sm.item_full[b]);
-      }
-    }
-    if (lane == 0) {
-      if (cut_columns) reinterpret_cast<Cut*>(p.ws + wl.cuts)[blockIdx.x] = cut;
-      sm.cut_columns = cut_columns;
-    }
+        });
+    if (lane == 0) sm.cut_columns = columns;
   } else if (warp == kLoadWarp) {
     // ---- the loads -----------------------------------------------------------------------------------
-    // (keys that other row tiles read too stay in L2 like anything else)
     const uint64_t once = tc::policy_evict_first();
     int32_t slot = 0, filled = 0, items = 0;
     uint32_t phase = 1;
@@ -578,18 +166,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     auto load = [&](const CUtensorMap* map, int32_t pg, int32_t fr, int32_t n, int32_t hd) {
       if (!wait_for_warp(&sm.empty[slot], phase, err)) return false;
-      uint8_t* const dst = ring + slot * Sh::kSlot;
-      if (elect()) mbar_expect_tx(&sm.full[slot], uint32_t(n) * p.box_rows * kD * 2);
-      __syncwarp();
-      if (lane < n) {
-#pragma unroll
-        for (int k = 0; k < kD / 64; ++k) {
-          uint8_t* const to = dst + k * 16384 + lane * p.box_rows * 128;
-          if (p.reread) tma_load_4d(to, map, k * 64, hd, fr, pg, &sm.full[slot]);
-          else tma_load_4d_hint(to, map, k * 64, hd, fr, pg, &sm.full[slot], once);
-        }
-      }
-      __syncwarp();
+      load_tile<kD>(p, ring + slot * Sh::kSlot, map, pg, fr, n, hd, &sm.full[slot], once);
       filled = max(filled, slot + 1);
       if (++slot == kStages) {
         slot = 0;
@@ -604,7 +181,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (x.stop) break;
       if (elect()) {
         // (rows behind the request's last, and columns behind those, hold anything: nobody reads them)
-        mbar_expect_tx(&sm.q_full[b], uint32_t(p.tokens * p.group) * kD * 2);
+        mbar_expect_tx(&sm.q_full[b], uint32_t(p.tile_tokens * p.group) * kD * 2);
 #pragma unroll
         for (int k = 0; k < kD / 64; ++k)
           tc::tma_load_3d(q_at + b * Sh::kQBytes + k * kN * 128, &map_q, k * 64, x.head * p.group,
@@ -613,17 +190,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       items = it + 1;
       for (int32_t t = x.t0; t < x.t1 && ok; ++t) {
-        const int32_t boxes = (min(kTile, x.end - t * kTile) + p.box_rows - 1) / p.box_rows;
-        const int32_t place = t * kTile + lane * p.box_rows;
-        int32_t page = 0;
-        if (lane < boxes) {
-          page = round_page(p.rd, x.r, place);
-          if (page < 0) {
-            report(err, SV_ERR_BAD_INPUT);
-            page = 0;
-          }
-        }
-        const int32_t from = place & (p.rd.page_size - 1);
+        int32_t page, from;
+        const int32_t boxes = tile_boxes(p, x, t, page, from, err);
         ok = load(&map_k, page, from, boxes, x.head) &&
              (v_boxes == 0 || load(&map_v, v_page, v_from, v_boxes, v_head));
         v_page = page, v_from = from, v_boxes = boxes, v_head = x.head;
@@ -757,34 +325,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
             }
           }
-          // Values that some column must not see are finite for the product, a weight of 0 would not
-          // rid it of them: zeros past the end, and zeros for what is not finite, which is added to
-          // the columns that do see it at the end.  Each half looks through half of the elements.
+          // each half looks through half of the elements
           const int32_t load = kt + 1 == x.t1 && x.last ? 2 * t + 1 : 2 * t + 2;
           late |= !wait_for(&sm.full[load % kStages], (load / kStages) & 1, err);
-          if (place >= x.base0 && !late) {
-            uint8_t* const v = ring + (load % kStages) * Sh::kSlot;
-#pragma unroll
-            for (int i = 0; i < kD / 16; ++i) {
-              const int k = half * (kD / 16) + i;
-              uint4* const at = reinterpret_cast<uint4*>(v + (k >> 3) * 16384 + tc::sw128(row, k & 7));
-              if (place >= x.end) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 y = *at;
-              if (not_finite2(y.x) || not_finite2(y.y) || not_finite2(y.z) || not_finite2(y.w)) {
-                uint32_t* const w = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
-                  if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
-                }
-                *at = y;
-                atomicOr(&sm.bad[b][half][j >> 5], 1u << (j & 31));
-              }
-            }
-          }
+          if (place >= x.base0 && !late &&
+              make_finite<kD / 16>(ring + (load % kStages) * Sh::kSlot, row, half * (kD / 16),
+                                   place >= x.end))
+            atomicOr(&sm.bad[b][half][j >> 5], 1u << (j & 31));
         }
         tc::fence_after_sync();
         // does any score pass its column's m by more than the slack?  (A half of up to 32 columns keeps
@@ -924,12 +471,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
           for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w) {
             for (uint32_t left = sm.bad[b][0][w] | sm.bad[b][1][w]; left; left &= left - 1) {  // rare
-              const int32_t j = 32 * w + __ffs(left) - 1, place = x.base0 + j;
-              const int32_t page = max(round_page(p.rd, x.r, place), 0);
-              const float v = __bfloat162float(
-                  p.v_cache[page * p.page_stride +
-                            (place & (p.rd.page_size - 1)) * p.token_stride +
-                            x.head * p.head_stride + row]);
+              const int32_t j = 32 * w + __ffs(left) - 1;
+              const float v = value_at(p, x, j, row);
               if (!isfinite(v)) {
 #pragma unroll
                 for (int c = 0; c < kC; ++c)
@@ -976,7 +519,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kCols);
   }
-  if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err * 256 + sm.cut_columns;
+  if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err * 512 + sm.cut_columns;
 }
 
 // ---- the parts of cut items joined -------------------------------------------------------------------
@@ -1060,8 +603,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p, int32_
     columns[k] = k * 32 + lane < ctas ? reinterpret_cast<const int32_t*>(p.ws)[k * 32 + lane] : 0;
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
-    code = max(code, columns[k] >> 8);
-    columns[k] &= 255;
+    code = max(code, columns[k] >> 9);
+    columns[k] &= 511;
     all += columns[k];
   }
   if (blockIdx.x == 0 && threadIdx.x < 32 && p.status) {
@@ -1092,8 +635,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p, int32_
 
 // ---- host ----------------------------------------------------------------------------------------------
 
-// Columns of a row tile: the narrowest that takes all of a request's rows, at most 128.
-int32_t columns_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Columns of a row tile: the narrowest that takes all of a request's rows.
+int32_t columns_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kWide; }
 
 // [D][heads][places][pages] of a cache, boxes of 64 elements of one head of `box_rows` places.
 bool cache_map(CUtensorMap* map, const void* base, int32_t D, int32_t heads, int32_t page_size,
@@ -1127,9 +670,11 @@ bool query_map(CUtensorMap* map, const void* q, int32_t D, int32_t heads, int64_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct AttnMaps {
-  CUtensorMap q, k, v;
-};
+template <int kD, int kN>
+sv_status launch_join(const AttnParams& p, int grid, cudaStream_t s) {
+  return launch_dependent(join_kernel<kD, kN>, unsigned(grid) * (kN * 32 / kJoinThreads),
+                          kJoinThreads, 0, s, p, grid);
+}
 
 template <int kD, int kN>
 sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
@@ -1140,21 +685,23 @@ sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t 
   const sv_status st =
       launch_dependent(kern, unsigned(grid), kAttnThreads, kAttnSmem, s, m.q, m.k, m.v, p);
   if (st != SV_OK) return st;
-  return launch_dependent(join_kernel<kD, kN>, unsigned(grid) * (kN * 32 / kJoinThreads), kJoinThreads, 0, s, p, grid);
+  return launch_join<kD, kN>(p, grid, s);
 }
 
 template <int kD>
 sv_status launch(int32_t n, const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
-  return n == 16   ? launch<kD, 16>(m, p, grid, s)
-         : n == 32 ? launch<kD, 32>(m, p, grid, s)
-         : n == 64 ? launch<kD, 64>(m, p, grid, s)
-                   : launch<kD, 128>(m, p, grid, s);
+  if (n == 16) return launch<kD, 16>(m, p, grid, s);
+  if (n == 32) return launch<kD, 32>(m, p, grid, s);
+  if (n == 64) return launch<kD, 64>(m, p, grid, s);
+  const sv_status st = launch_wide(kD, m, p, grid, s);
+  return st != SV_OK ? st : launch_join<kD, kWide>(p, grid, s);
 }
 
 }  // namespace
 }  // namespace sv
 
 using namespace sv;
+using namespace sv::attn;
 
 extern "C" size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t max_draft_len,
                                                       int32_t bonus_row, int32_t n_heads,
@@ -1206,7 +753,8 @@ extern "C" sv_status spec_tree_attention(
   p.n_kv = n_kv_heads, p.group = group;
   const int64_t rows = (max_draft_len + int64_t(bonus_row)) * group;
   const int32_t n = columns_for(rows);
-  p.tokens = n / group;
+  p.tile_tokens = std::min(n, kTile) / group;
+  p.tokens = p.tile_tokens * (n / std::min(n, kTile));
   p.box_rows = std::min(page_size, kTile);
   p.scale2 = scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(out), p.ldo = ldo, p.o_head = o_head;
@@ -1216,7 +764,7 @@ extern "C" sv_status spec_tree_attention(
   if (sms < 1) return SV_ERR_CUDA;
   if (n_rows > INT32_MAX) return SV_ERR_UNSUPPORTED;
   AttnMaps m;
-  if (!query_map(&m.q, q, D, n_heads, n_rows, q_head, ldq, group, p.tokens) ||
+  if (!query_map(&m.q, q, D, n_heads, n_rows, q_head, ldq, group, p.tile_tokens) ||
       !cache_map(&m.k, k_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
                  page_stride, p.box_rows) ||
       !cache_map(&m.v, v_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,

@@ -134,10 +134,11 @@ def test_scales(sv, scale):
 
 @pytest.mark.parametrize("tree", [None, "random"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-@pytest.mark.parametrize("ctx", [0, 60, 125])
-def test_unseen_rows_do_not_reach(sv, tree, bad, ctx):
-    """What a drafted row left in the cache reaches only the rows that see it."""
-    D, kv, heads, N = 128, 2, 8, 9
+@pytest.mark.parametrize("ctx,heads", [(0, 8), (60, 8), (125, 8), (0, 16), (250, 16), (125, 64), (3, 64)])
+def test_unseen_rows_do_not_reach(sv, tree, bad, ctx, heads):
+    """What a drafted row left in the cache reaches only the rows that see it (up to 64 rows a key head,
+    up to 128, more)."""
+    D, kv, N = 128, 2, 9
     host, dev, n, _ = pr.make_round([ctx], [N], N, 16, heads, kv, D, seed=7, tree=tree)
     clean = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in host.items()}
     for j in (4, 7):
@@ -159,13 +160,15 @@ def test_unseen_rows_do_not_reach(sv, tree, bad, ctx):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [2, 12, 40])
+@pytest.mark.parametrize("tree", [None, "random"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_values_that_are_not_finite_reach_who_sees_them(sv, bad, D):
+def test_values_that_are_not_finite_reach_who_sees_them(sv, bad, tree, heads, D):
     """An infinite or NaN value of the context or of an ancestor makes that element of the result
     what the sum is; the other elements stay."""
     N, ctx = 6, 140
     for j in (3, ctx + 2):
-        host, dev, n, _ = pr.make_round([ctx], [N], N, 16, 2, 1, D, seed=8, tree="random", q_scale=0.1)
+        host, dev, n, _ = pr.make_round([ctx], [N], N, 16, heads, 1, D, seed=8, tree=tree, q_scale=0.1)
         clean = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in host.items()}
         host["v_cache"][pr.place(host["page_table"], 0, j, 16)][0, 5] = bad
         dev["v_cache"] = host["v_cache"].cuda()
@@ -184,8 +187,9 @@ def test_values_that_are_not_finite_reach_who_sees_them(sv, bad, D):
             assert off.all(), (j, i)
 
 
-def test_bad_queries_stay_alone(sv):
-    host, dev, n, _ = pr.make_round([200], [5], 5, 16, 8, 2, 128, seed=9)
+@pytest.mark.parametrize("kv", [1, 2, 8])
+def test_bad_queries_stay_alone(sv, kv):
+    host, dev, n, _ = pr.make_round([200], [5 if kv > 1 else 20], 20, 16, 8, kv, 128, seed=9)
     first = int(host["row0"][0])
     q = host["q"].clone()
     q[first + 2, 3] = float("nan")
