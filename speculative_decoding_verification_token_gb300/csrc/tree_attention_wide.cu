@@ -23,7 +23,7 @@ struct WideShared {
   static constexpr uint32_t kQTile = kTile * kD * 2;
   struct Small {
     uint64_t full[16], empty[16], item_full[2], item_empty[2], table_full[2];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q_full, q_empty, s_full[2], p_half[2], p_full[2], o_full[2], drain;
     Item item[2];
     uint32_t above[2][SV_MAX_TREE_ROWS][4];
     int32_t up[SV_MAX_TREE_ROWS];
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&sm.item_empty[b], 4);  // the loads, the products, the streams
       mbar_init(&sm.table_full[b], 1);
       mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.p_half[b], 4);
       mbar_init(&sm.p_full[b], 4);
       mbar_init(&sm.o_full[b], 1);
     }
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (items > 0) wait_for_warp(&sm.q_full, (items - 1) & 1, err);
   } else if (warp == kMmaWarp) {
     // ---- the products --------------------------------------------------------------------------------
-    constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, 128);
+    // (bit 13: Q negated, so that the scale is positive)
+    const uint32_t kIdS = tc::idesc_bf16_f32(128, 128) | (p.scale2 < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, kD) | (1u << 16);
     const uint32_t ring_lo = smem_addr(ring) >> 4, q_lo = smem_addr(q_at) >> 4;
     int32_t slot = 0;
@@ -252,12 +254,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                      desc_of(k_lo + (k >> 2) * 1024 + (k & 3) * 2), kIdS, k > 0);
       tc::mma_commit(&sm.s_full[s]);
     };
-    auto values = [&](int s, int32_t at, bool first) {  // O of stream s (+)= P V
+    // O of stream s (+)= P V, for the first or second half of the places
+    auto values = [&](int s, int32_t at, int half, bool first) {
       const uint32_t v_lo = ring_lo + at * (Sh::kSlot >> 4) + kAcross;
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
+      for (int i = 0; i < kTile / 32; ++i) {
+        const int k = half * (kTile / 32) + i;
         mma_from_tmem(tmem + 256 + s * 128, tmem + s * 128 + k * 8, desc_of(v_lo + k * 128), kIdO,
                       !first || k > 0);
+      }
     };
     for (int32_t it = 0; ok; ++it) {
       const int b = it & 1;
@@ -288,12 +293,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool more = i + 1 < n;  // (of a pair)
         if (twin) {
           const int s = i & 1;
-          ok = ok && wait_for_warp(&sm.p_full[s], p_phase[s], err);
+          ok = ok && wait_for_warp(&sm.p_half[s], p_phase[s], err);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (elect()) values(s, v_slot, 0, i < 2);
+          __syncwarp();
+          ok = wait_for_warp(&sm.p_full[s], p_phase[s], err);
           if (!ok) break;
           p_phase[s] ^= 1;
           tc::fence_after_sync();
           if (elect()) {
-            values(s, v_slot, i < 2);
+            values(s, v_slot, 1, i < 2);
             tc::mma_commit(&sm.empty[v_slot]);
             if (i + 2 >= n) tc::mma_commit(&sm.o_full[s]);
           }
@@ -313,12 +323,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         } else {
           // a tile whose values are looked through waits for both streams' look
           const bool masked = (x.t0 + i + 1) * int64_t(kTile) > x.base0;
-          ok = ok && wait_for_warp(&sm.p_full[0], p_phase[0], err) &&
-               (!masked || wait_for_warp(&sm.p_full[1], p_phase[1], err));
+          ok = ok && wait_for_warp(&sm.p_half[0], p_phase[0], err) &&
+               (!masked || wait_for_warp(&sm.p_half[1], p_phase[1], err));
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (elect()) values(0, v_slot, 0, i == 0);
+          __syncwarp();
+          ok = wait_for_warp(&sm.p_full[0], p_phase[0], err);
           if (!ok) break;
           tc::fence_after_sync();
           if (elect()) {
-            values(0, v_slot, i == 0);
+            values(0, v_slot, 1, i == 0);
             if (!more) tc::mma_commit(&sm.o_full[0]);
           }
           __syncwarp();
@@ -331,13 +346,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (elect()) scores(0, 0, k_slot);
             __syncwarp();
           }
+          ok = wait_for_warp(&sm.p_half[1], p_phase[1], err);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (elect()) values(1, v_slot, 0, i == 0);
+          __syncwarp();
           ok = wait_for_warp(&sm.p_full[1], p_phase[1], err);
           if (!ok) break;
           p_phase[0] ^= 1;
           p_phase[1] ^= 1;
           tc::fence_after_sync();
           if (elect()) {
-            values(1, v_slot, i == 0);
+            values(1, v_slot, 1, i == 0);
             tc::mma_commit(&sm.empty[v_slot]);
             if (!more) {
               tc::mma_commit(&sm.o_full[1]);
@@ -362,7 +382,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int row = tid & 127;  // of the stream's tile; place of a key tile where values are looked through
     const uint32_t lanes = tmem + (uint32_t(32 * quad) << 16);
     const uint32_t s_at = lanes + s * 128, o_at = lanes + 256 + s * 128;
-    const float2 scale = splat2(p.scale2);
+    const float scale1 = fabsf(p.scale2);
+    const float2 scale = splat2(scale1);
     uint32_t s_phase = 0, o_phase = 0;
     int32_t loads = 0;  // tiles that went through the ring before this item
     bool failed = false;  // a wait ran out: no further ones, on to where all meet
@@ -432,16 +453,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           landed(a[ch & 1]);
           if (ch < 3) load32(s_at + 32 * ch + 32, a[~ch & 1]);
           float* const f = a[ch & 1];
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 y = mul2(make_float2(f[c], f[c + 1]), scale);
-            f[c] = y.x, f[c + 1] = y.y;
-          }
           if (masked) hide<32>(f, seen[ch]);
+          float t[4] = {f[0], f[1], f[2], f[3]};
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) top = max3(top, f[c], f[c + 1]);
+          for (int c = 4; c < 28; c += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = max3(t[e], f[c + 2 * e], f[c + 2 * e + 1]);
+          }
+          top = max3(top, max3(t[0], t[1], max3(f[28], f[29], t[2])), max3(t[3], f[30], f[31]));
         }
         load32(s_at, a[0]);  // once more, for the weights
+        top *= scale1;       // (0 times an infinity is a NaN, which raises nothing: its weights are NaN)
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float now = fmaxf(m, top), factor = fast_exp2(m - now);
           m = now;
@@ -486,6 +508,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             w[c / 2] = bf16_pair(e.x, e.y);
           }
           store16(s_at + 16 * ch, w);
+          if (ch == 1) {
+            wait_stores();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_half[s]);
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         wait_stores();
