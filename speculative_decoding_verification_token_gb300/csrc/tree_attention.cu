@@ -525,112 +525,142 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---- the parts of cut items joined -------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
+// Columns of a warp: one where there are few columns, and many parts of each.
+constexpr int join_columns_of(int n) { return n <= 64 ? 1 : 4; }
 
-// A column of the item that CTA `cta` begins, by one warp.
+// Columns from col0 on of the item that CTA `cta` begins, by one warp.
 template <int kD, int kN>
-__device__ __forceinline__ void join_column(const AttnParams& p, const WsLayout& wl, const Cut& cut,
-                                            int32_t ctas, int32_t cta, int32_t col) {
+__device__ __forceinline__ void join_columns(const AttnParams& p, const WsLayout& wl, const Cut& cut,
+                                             int32_t columns, int32_t ctas, int32_t cta, int32_t col0) {
   constexpr int kE = kD / 32;
+  constexpr int kC = join_columns_of(kN), kParts = 32 / kC;
   const int lane = threadIdx.x & 31;
   const float* const parts = reinterpret_cast<const float*>(p.ws + wl.parts);
   // CTA k's part
   auto part_of = [&](int32_t k) { return parts + (2 * int64_t(k) + (k == cta)) * wl.part_floats; };
-  // lane's CTA has none where its run is empty
+  // CTA k has none where its run is empty
   auto has = [&](int32_t k) {
     return k <= cut.last &&
            (k == cta || cut.total >= ctas || cut.total * k / ctas != cut.total * (k + 1) / ctas);
   };
-  float top = kM2Empty, y[kE] = {}, sum = 0.f;
-  for (int32_t k0 = cta; k0 <= cut.last; k0 += 32) {
-    // this lane's part: its maximum and denominator
-    const int32_t k = k0 + lane;
+  // kParts parts at a time: lane l looks at part l / kC of them and column l % kC
+  const int32_t my_col = min(col0 + lane % kC, columns - 1);
+  float top = kM2Empty, sum = 0.f;  // of this lane's column
+  float y[kC][kE] = {};
+  for (int32_t k0 = cta; k0 <= cut.last; k0 += kParts) {
+    const int32_t k = k0 + lane / kC;
     const bool mine = has(k);
-    const float* const x = part_of(mine ? k : cta) + kN * kD + col;
+    const float* const x = part_of(mine ? k : cta) + kN * kD + my_col;
     const float m = mine ? x[0] : kM2Empty, d = mine ? x[kN] : 0.f;
-    const float most = fmaxf(top, warp_max(m));
+    float most = m;
+#pragma unroll
+    for (int o = kC; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    most = fmaxf(most, top);
     const float old = fast_exp2(top - most), w = mine ? fast_exp2(m - most) : 0.f;
-    sum = sum * old + warp_sum(d * w);
+    float all = d * w;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) y[e] *= old;
+    for (int o = kC; o < 32; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    sum = sum * old + all;
     top = most;
-    const uint32_t there = __ballot_sync(0xffffffffu, mine);
-    const int32_t n = min(32, cut.last - k0 + 1);
-    for (int32_t i0 = 0; i0 < n; i0 += 8) {
-      float v[8][kE];
+    if (k0 > cta) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool is = i0 + i < n && (there >> (i0 + i) & 1u);
-        const float* const o = part_of(is ? k0 + i0 + i : cta) + col * kD + lane * kE;
+      for (int c = 0; c < kC; ++c) {
+        const float f = __shfl_sync(0xffffffffu, old, c);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) y[c][e] *= f;
+      }
+    }
+    const uint32_t there = __ballot_sync(0xffffffffu, mine);
+    const int32_t n = min(kParts, cut.last - k0 + 1);
+    for (int32_t i0 = 0; i0 < n; i0 += 8 / kC) {
+      float v[8][kE];  // in flight together
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int32_t i = i0 + q / kC;
+        const bool is = i < n && (there >> (kC * i) & 1u);
+        // (columns behind the last are there too, and are not written)
+        const float* const o = part_of(is ? k0 + i : cta) + (col0 + q % kC) * kD + lane * kE;
         if constexpr (kE == 4) {
           const float4 z = *reinterpret_cast<const float4*>(o);
-          v[i][0] = z.x, v[i][1] = z.y, v[i][2] = z.z, v[i][3] = z.w;
+          v[q][0] = z.x, v[q][1] = z.y, v[q][2] = z.z, v[q][3] = z.w;
         } else {
           const float2 z = *reinterpret_cast<const float2*>(o);
-          v[i][0] = z.x, v[i][1] = z.y;
+          v[q][0] = z.x, v[q][1] = z.y;
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
-        const bool is = i0 + i < n && (there >> (i0 + i) & 1u);
+      for (int q = 0; q < 8; ++q) {
+        const int32_t i = i0 + q / kC;
+        const bool is = i < n && (there >> (kC * i) & 1u);
+        const float f = __shfl_sync(0xffffffffu, w, (kC * i + q % kC) & 31);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) y[e] += is ? f * v[i][e] : 0.f;
+        for (int e = 0; e < kE; ++e) y[q % kC][e] += is ? f * v[q][e] : 0.f;
       }
     }
   }
-  const int32_t i = col / p.group, h = cut.head * p.group + col - i * p.group;
-  const int64_t row = cut.first_row + i;
-  const float inv = 1.f / sum;
-  __nv_bfloat16* const o = p.out + row * p.ldo + h * p.o_head + lane * kE;
+  const float my_inv = 1.f / sum, my_lse = (top + log2f(sum)) * kLn2;
 #pragma unroll
-  for (int e = 0; e < kE; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(o + e) = __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[row * p.ld_lse + h] = (top + log2f(sum)) * kLn2;
+  for (int c = 0; c < kC; ++c) {
+    const float inv = __shfl_sync(0xffffffffu, my_inv, c);
+    if (col0 + c >= columns) break;
+    const int32_t i = (col0 + c) / p.group, h = cut.head * p.group + col0 + c - i * p.group;
+    const int64_t row = cut.first_row + i;
+    __nv_bfloat16* const o = p.out + row * p.ldo + h * p.o_head + lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(o + e) = __floats2bfloat162_rn(y[c][e] * inv, y[c][e + 1] * inv);
+    if (lane == c && p.lse) p.lse[row * p.ld_lse + h] = my_lse;
+  }
 }
 
-// A warp for every column that there can be; the first ones, spread over the SMs, take those of
+// A warp for every kC columns that there can be; the first ones, spread over the SMs, take those of
 // the cut items.  Block 0 also gathers the CTAs' errors.
 template <int kD, int kN>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnParams p, int32_t ctas) {
-  constexpr int kE = kD / 32;
-  constexpr int kRounds = (kMaxCtas + 31) / 32;
+  constexpr int kRounds = (kMaxCtas + 31) / 32, kC = join_columns_of(kN);
   dependent_start();
   const WsLayout wl = ws_layout(ctas, kN, kD);
   const int lane = threadIdx.x & 31;
-  int32_t columns[kRounds], all = 0, code = 0;  // of CTA 32 k + lane
+  int32_t word[kRounds], all = 0, code = 0;  // of CTA 32 k + lane
 #pragma unroll
   for (int k = 0; k < kRounds; ++k)
-    columns[k] = k * 32 + lane < ctas ? reinterpret_cast<const int32_t*>(p.ws)[k * 32 + lane] : 0;
+    word[k] = k * 32 + lane < ctas ? reinterpret_cast<const int32_t*>(p.ws)[k * 32 + lane] : 0;
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
-    code = max(code, columns[k] >> 9);
-    columns[k] &= 511;
-    all += columns[k];
+    code = max(code, word[k] >> 9);
+    word[k] &= 511;
+    all += (word[k] + kC - 1) / kC;
   }
   if (blockIdx.x == 0 && threadIdx.x < 32 && p.status) {
     code = __reduce_max_sync(0xffffffffu, code);
     if (lane == 0) *p.status = code;
   }
   all = __reduce_add_sync(0xffffffffu, all);
-  int32_t cta = -1, col = blockIdx.x + gridDim.x * (threadIdx.x >> 5);
-  if (col >= all) return;
+  int32_t cta = -1, group = blockIdx.x + gridDim.x * (threadIdx.x >> 5), columns = 0;
+  if (group >= all) return;
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
-    int32_t upto = columns[k];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, col < upto);
-    const int l = past ? __ffs(past) - 1 : 31;
-    const int32_t before = __shfl_sync(0xffffffffu, upto - (past ? columns[k] : 0), l);
     if (cta < 0) {
-      col -= before;
-      if (past) cta = k * 32 + l;
+      const int32_t mine = (word[k] + kC - 1) / kC;
+      int32_t upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, group < upto);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        group -= __shfl_sync(0xffffffffu, upto - mine, l);
+        columns = __shfl_sync(0xffffffffu, word[k], l);
+        cta = k * 32 + l;
+      } else {
+        group -= __shfl_sync(0xffffffffu, upto, 31);
+      }
     }
   }
-  join_column<kD, kN>(p, wl, reinterpret_cast<const Cut*>(p.ws + wl.cuts)[cta], ctas, cta, col);
+  join_columns<kD, kN>(p, wl, reinterpret_cast<const Cut*>(p.ws + wl.cuts)[cta], columns, ctas, cta,
+                       group * kC);
 }
 
 // ---- host ----------------------------------------------------------------------------------------------
@@ -672,7 +702,8 @@ bool query_map(CUtensorMap* map, const void* q, int32_t D, int32_t heads, int64_
 
 template <int kD, int kN>
 sv_status launch_join(const AttnParams& p, int grid, cudaStream_t s) {
-  return launch_dependent(join_kernel<kD, kN>, unsigned(grid) * (kN * 32 / kJoinThreads),
+  constexpr int kPerBlock = kJoinThreads / 32 * join_columns_of(kN);
+  return launch_dependent(join_kernel<kD, kN>, unsigned(grid * kN + kPerBlock - 1) / kPerBlock,
                           kJoinThreads, 0, s, p, grid);
 }
 
@@ -777,5 +808,6 @@ extern "C" sv_status spec_tree_attention(
   if (most > 9e15) return SV_ERR_UNSUPPORTED;
   const int grid = int(std::max(1.0, std::min(double(sms), most)));
   p.reread = row_tiles > 1;
+  p.item_cost = n == kWide ? 6 : 4;
   return D == 64 ? launch<64>(n, m, p, grid, s) : launch<128>(n, m, p, grid, s);
 }

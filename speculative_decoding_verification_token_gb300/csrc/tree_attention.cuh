@@ -26,6 +26,7 @@ struct AttnParams {
   int32_t tile_tokens;  // tokens of a row tile
   int32_t box_rows;  // places of a TMA box
   int32_t reread;    // several row tiles read the same keys
+  int32_t item_cost; // what an item costs beside its key tiles, in key tiles
   float scale2;  // scale * log2(e)
   __nv_bfloat16* out;
   int64_t ldo, o_head;
@@ -63,16 +64,19 @@ __device__ __forceinline__ int32_t tiles_of(const Request& q, int32_t rt, int32_
   return int32_t((int64_t(q.ctx) + min(q.n, (rt + 1) * tokens) + kTile - 1) / kTile);
 }
 
-// Tiles of one key head of a request (its row tiles together).
-__device__ __forceinline__ int64_t tiles_of_head(const Request& q, int32_t tokens) {
+// Items and key tiles of one key head of a request.
+__device__ __forceinline__ int64_t tiles_of_head(const Request& q, int32_t tokens, int32_t& items) {
   int64_t t = 0;
-  for (int32_t rt = 0; rt * tokens < q.n; ++rt) t += tiles_of(q, rt, tokens);
+  items = 0;
+  for (; items * tokens < q.n; ++items) t += tiles_of(q, items, tokens);
   return t;
 }
 
+// The list is cut into runs of equal cost: an item counts its key tiles and `cost` units ahead of them.
 struct Span {
-  int64_t total, begin, end;  // tiles of the call, of this CTA
-  int64_t before;             // tiles before request `r`
+  int64_t total, begin, end;  // units of the call, of this CTA
+  int64_t before;             // units before request `r`
+  int32_t cost;
   int32_t r;                  // the request that `begin` lies in
   Request q;                  // and its sizes
 };
@@ -83,26 +87,31 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
   const int32_t steps = min(p.rd.B, 32);
   Span span = {};
   Request q = {};
-  int64_t mine = 0, upto = 0, total = 0;
+  int64_t tiles = 0, items = 0;  // of the lane's request
   auto chunk = [&](int32_t r0, bool tell) {
     const int32_t r = r0 + lane;
-    mine = 0;
+    tiles = items = 0;
     q.n = 0;
     if (r < p.rd.B) {
       if (!round_request(p.rd, r, q) && tell) report(err, SV_ERR_BAD_INPUT);
-      mine = tiles_of_head(q, p.tokens) * p.n_kv;
-    }
-    upto = mine;
-    for (int o = 1; o < steps; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+      int32_t n;
+      tiles = tiles_of_head(q, p.tokens, n) * p.n_kv;
+      items = int64_t(n) * p.n_kv;
     }
   };
+  auto sum = [&](int64_t x) {  // over the chunk's lanes
+    for (int o = 1; o < steps; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return __shfl_sync(0xffffffffu, x, 0);
+  };
+  int64_t all_tiles = 0, all_items = 0;
   for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
     chunk(r0, blockIdx.x == 0);
-    total += __shfl_sync(0xffffffffu, upto, steps - 1);
+    all_tiles += sum(tiles);
+    all_items += sum(items);
   }
-  span.total = total;
+  // (with few tiles for each CTA their number alone counts)
+  span.cost = all_tiles > 2 * int64_t(gridDim.x) ? p.item_cost : 0;
+  const int64_t total = span.total = all_tiles + span.cost * all_items;
   if (total < (int64_t(1) << 22)) {  // (the products stay in 32 bits: at most 192 CTAs)
     span.begin = uint32_t(total) * blockIdx.x / gridDim.x;
     span.end = uint32_t(total) * (blockIdx.x + 1) / gridDim.x;
@@ -114,6 +123,12 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
   int64_t before = 0;
   for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
     if (p.rd.B > 32) chunk(r0, false);
+    const int64_t mine = tiles + span.cost * items;
+    int64_t upto = mine;
+    for (int o = 1; o < steps; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
     const int64_t a = before + upto - mine;
     const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= span.begin &&
                                                         span.begin < a + mine);
@@ -334,47 +349,57 @@ __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, It
   bool ok = true;
   int32_t it = 0;
   if (span.begin < span.end) {
-    int64_t at = span.begin, off = at - span.before;
+    int64_t at = span.begin, off = at - span.before;  // units of the call, and of the request's first item
     int32_t r = span.r, h = 0, rt = 0;
     Request rq = span.q;
-    const int64_t per_head = tiles_of_head(rq, p.tokens);
+    int32_t n_items;
+    int64_t per_head = tiles_of_head(rq, p.tokens, n_items);
+    per_head += int64_t(span.cost) * n_items;
     h = int32_t(off <= INT32_MAX ? uint32_t(off) / uint32_t(min(per_head, int64_t(INT32_MAX)))
                                  : off / per_head);
     off -= h * per_head;
-    while (off >= tiles_of(rq, rt, p.tokens)) off -= tiles_of(rq, rt++, p.tokens);
-    for (; at < span.end && ok; ++it) {
-      const int b = it & 1;
-      const int32_t tok0 = rt * p.tokens, ntok = min(p.tokens, rq.n - tok0);
-      const int32_t columns = ntok * p.group, tiles = tiles_of(rq, rt, p.tokens);
-      Item x;
-      x.first_row = rq.first + tok0;
-      x.r = r, x.head = h, x.columns = columns;
-      x.tok0 = tok0, x.ctx = rq.ctx;
-      x.base0 = rq.ctx + (p.rd.parents ? 0 : tok0);
-      x.end = rq.ctx + tok0 + ntok;
-      x.t0 = int32_t(off);
-      x.t1 = int32_t(min(int64_t(tiles), off + (span.end - at)));
-      x.whole = x.t0 == 0 && x.t1 == tiles;
-      x.begins = x.t0 == 0;
-      x.last = at + (x.t1 - x.t0) == span.end;
-      x.stop = 0;
-      if (it >= 2 && !wait_for_warp(&item_empty[b], ((it >> 1) - 1) & 1, err)) {
-        ok = false;
-        break;
+    while (off >= tiles_of(rq, rt, p.tokens) + span.cost)
+      off -= tiles_of(rq, rt++, p.tokens) + span.cost;
+    while (at < span.end && ok) {
+      const int32_t tiles = tiles_of(rq, rt, p.tokens);
+      const int64_t units = min(tiles + span.cost - off, span.end - at);
+      const int64_t t0 = max(off - span.cost, int64_t(0)), t1 = off + units - span.cost;
+      if (t1 > t0) {  // (else the run ends within what stands for the item's own cost)
+        const int b = it & 1;
+        const int32_t tok0 = rt * p.tokens, ntok = min(p.tokens, rq.n - tok0);
+        const int32_t columns = ntok * p.group;
+        Item x;
+        x.first_row = rq.first + tok0;
+        x.r = r, x.head = h, x.columns = columns;
+        x.tok0 = tok0, x.ctx = rq.ctx;
+        x.base0 = rq.ctx + (p.rd.parents ? 0 : tok0);
+        x.end = rq.ctx + tok0 + ntok;
+        x.t0 = int32_t(t0);
+        x.t1 = int32_t(t1);
+        x.whole = x.t0 == 0 && x.t1 == tiles;
+        x.begins = x.t0 == 0;
+        x.last = span.end - (at + units) <= span.cost;
+        x.stop = 0;
+        if (it >= 2 && !wait_for_warp(&item_empty[b], ((it >> 1) - 1) & 1, err)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) item[b] = x;
+        before(b, x);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_full[b]);
+        after(b, x, rq.first);
+        if (x.begins && !x.whole) {
+          cut.total = span.total;
+          cut.first_row = x.first_row;
+          cut.head = h;
+          // the CTA that the item's last unit lies in
+          cut.last = int32_t(((at - off + tiles + span.cost) * gridDim.x - 1) / cut.total);
+          cut_columns = columns;
+        }
+        ++it;
       }
-      if (lane == 0) item[b] = x;
-      before(b, x);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_full[b]);
-      after(b, x, rq.first);
-      if (x.begins && !x.whole) {
-        cut.total = span.total;
-        cut.first_row = x.first_row;
-        cut.head = h;
-        cut.last = int32_t(((at + tiles) * gridDim.x - 1) / cut.total);  // its last tile's CTA
-        cut_columns = columns;
-      }
-      at += x.t1 - x.t0;
+      at += units;
       off = 0;
       if (at < span.end && ++rt * p.tokens >= rq.n) {
         rt = 0;
