@@ -29,7 +29,14 @@ struct AppendParams {
 constexpr int kAppendThreads = 256;
 constexpr int kRowThreads = 128;  // of a row
 constexpr int kAppendGroups = kAppendThreads / kRowThreads;
-constexpr int kAppendUnroll = 3;
+// Heads whose loads a thread has in flight, and CTAs an SM, within the registers there are: 8 prompts of
+// up to 8192 tokens (bf16) 136 us (6.0 TB/s of the 811 MB that have to move; two CTAs 149), 64 trees of
+// 16 rows (fp32) 8.2 us (three CTAs spill: 16.6).
+template <typename T>
+constexpr int kAppendUnroll = sizeof(T) == 2 ? 3 : 2;
+template <typename T>
+constexpr int kAppendCtas = sizeof(T) == 2 ? 3 : 2;
+constexpr int kAppendMostRows = 16;  // of a CTA
 
 // 8 consecutive elements: as they lie, and as binary32.
 template <typename T>
@@ -110,10 +117,10 @@ __device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* pare
     bad |= page < 0;
     const int64_t at = page * p.cache.page_stride + (place % p.rd.page_size) * p.cache.token_stride;
     const int64_t row = rq.first + i;
-    for (int32_t h0 = t / parts; h0 < all; h0 += step * kAppendUnroll) {
-      Eight<T> x[kAppendUnroll], y[kAppendUnroll];
+    for (int32_t h0 = t / parts; h0 < all; h0 += step * kAppendUnroll<T>) {
+      Eight<T> x[kAppendUnroll<T>], y[kAppendUnroll<T>];
 #pragma unroll
-      for (int u = 0; u < kAppendUnroll; ++u) {
+      for (int u = 0; u < kAppendUnroll<T>; ++u) {
         const int32_t h = h0 + u * step, kv = h - p.n_heads;
         if (h < all) {
           const bool v_head = kv >= p.n_kv_heads;
@@ -125,7 +132,7 @@ __device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* pare
         }
       }
 #pragma unroll
-      for (int u = 0; u < kAppendUnroll; ++u) {
+      for (int u = 0; u < kAppendUnroll<T>; ++u) {
         const int32_t h = h0 + u * step, kv = h - p.n_heads;
         if (h >= all || (kv >= 0 && page < 0)) continue;
         const bool v_head = kv >= p.n_kv_heads;
@@ -167,7 +174,7 @@ __device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* pare
 }
 
 template <typename T, bool kAdjacent>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas<T>) append_kernel(AppendParams p) {
   __shared__ int32_t parents[SV_MAX_TREE_ROWS];
   dependent_start();
   round_status(p.status, append_body<T, kAdjacent>(p, parents), p.one);
@@ -269,6 +276,7 @@ struct KeepParams {
   const int32_t *accepted_len, *path;
   int64_t ld_path;
   int32_t n_path, n_layers;
+  int32_t layers;  // of a CTA
   int64_t layer_stride;
   int32_t columns;       // 16-byte columns of a place in one cache
   int32_t head_columns;  // of a head
@@ -279,13 +287,15 @@ struct KeepParams {
 
 constexpr int kKeepThreads = 256;
 constexpr int kKeepBatch = 8;
+constexpr int kKeepCtas = 6;  // aimed at an SM: 64 requests in 32 layers 10.2 us (2: 13.4, 16: 11.7)
 
-// A CTA per request and layer.  A path ascends from 1 or more, so row path[i] lies at or behind the
+// A CTA per request and run of layers.  A path ascends from 1 or more, so row path[i] lies at or behind the
 // place i + 1 it goes to, and a thread that takes its own 16-byte column through the moves in order
 // never reads what it has overwritten; it reads a batch of rows ahead of writing them.
 // Returns whether the data are bad.
 __device__ __forceinline__ bool keep_body(const KeepParams& p, int64_t* src, int64_t* dst) {
-  const int32_t r = blockIdx.x % p.rd.B, layer = blockIdx.x / p.rd.B, tid = threadIdx.x;
+  const int32_t r = blockIdx.x % p.rd.B, tid = threadIdx.x;
+  const int32_t layer0 = blockIdx.x / p.rd.B * p.layers;
   const int32_t ctx = p.rd.ctx_len[r], n = p.accepted_len[r];
   const int64_t room = min(int64_t(p.rd.max_pages) * p.rd.page_size, int64_t(INT32_MAX));
   bool bad = n < 0 || n > p.n_path || ctx < 0 || int64_t(ctx) + 1 + n > room;
@@ -300,8 +310,8 @@ __device__ __forceinline__ bool keep_body(const KeepParams& p, int64_t* src, int
       bad = page_from < 0 || page_to < 0;
     }
   }
-  if (__syncthreads_or(bad)) return layer == 0 && tid == 0;
-  if (layer == 0 && tid == 0 && p.new_len) p.new_len[r] = ctx + 1 + n;
+  if (__syncthreads_or(bad)) return layer0 == 0 && tid == 0;
+  if (layer0 == 0 && tid == 0 && p.new_len) p.new_len[r] = ctx + 1 + n;
   if (!p.path) return false;
   // a path starts with the rows that lie in place; from its first gap on every row moves
   const bool move = tid < n && from != tid + 1;
@@ -312,19 +322,22 @@ __device__ __forceinline__ bool keep_body(const KeepParams& p, int64_t* src, int
     dst[m] = page_to * p.cache.page_stride + ((ctx + 1 + tid) % ps) * p.cache.token_stride;
   }
   __syncthreads();
+  const int32_t layers = min(p.layers, p.n_layers - layer0);
   for (int32_t c = tid; c < 2 * p.columns; c += kKeepThreads) {
     const int32_t col = c < p.columns ? c : c - p.columns;
-    __nv_bfloat16* const base = (c < p.columns ? p.cache.k : p.cache.v) + layer * p.layer_stride +
-                                (col / p.head_columns) * p.cache.head_stride +
-                                (col % p.head_columns) * 8;
-    for (int32_t m0 = 0; m0 < count; m0 += kKeepBatch) {
-      uint4 x[kKeepBatch];
+    __nv_bfloat16* base = (c < p.columns ? p.cache.k : p.cache.v) + layer0 * p.layer_stride +
+                          (col / p.head_columns) * p.cache.head_stride +
+                          (col % p.head_columns) * 8;
+    for (int32_t layer = 0; layer < layers; ++layer, base += p.layer_stride) {
+      for (int32_t m0 = 0; m0 < count; m0 += kKeepBatch) {
+        uint4 x[kKeepBatch];
 #pragma unroll
-      for (int u = 0; u < kKeepBatch; ++u)
-        if (m0 + u < count) x[u] = *reinterpret_cast<const uint4*>(base + src[m0 + u]);
+        for (int u = 0; u < kKeepBatch; ++u)
+          if (m0 + u < count) x[u] = *reinterpret_cast<const uint4*>(base + src[m0 + u]);
 #pragma unroll
-      for (int u = 0; u < kKeepBatch; ++u)
-        if (m0 + u < count) *reinterpret_cast<uint4*>(base + dst[m0 + u]) = x[u];
+        for (int u = 0; u < kKeepBatch; ++u)
+          if (m0 + u < count) *reinterpret_cast<uint4*>(base + dst[m0 + u]) = x[u];
+      }
     }
   }
   return false;
@@ -386,7 +399,13 @@ extern "C" sv_status spec_cache_append(
   p.cos_sin = cos_sin, p.ld_cos_sin = ld_cos_sin, p.n_positions = n_positions;
   p.n_heads = n_heads, p.n_kv_heads = n_kv_heads, p.D = D, p.rot = rot;
   const int64_t most = max_draft_len + int64_t(bonus_row);
+  // a CTA takes several rows where there are enough of them for two rounds of CTAs: what it finds out of
+  // its request first costs as much as a row (prompts as above 165 -> 136 us)
+  if ((most + kAppendMostRows - 1) / kAppendMostRows * B > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms < 1) return SV_ERR_CUDA;
   p.rows = kAppendGroups;
+  while (p.rows < kAppendMostRows && most * B >= int64_t(4) * 3 * sms * p.rows) p.rows *= 2;
   p.chunks = int32_t((most + p.rows - 1) / p.rows);
   p.status = status;
   auto* kernel = dtype == SV_BF16
@@ -454,5 +473,12 @@ extern "C" sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t*
   p.columns = n_kv_heads * (D / 8), p.head_columns = D / 8;
   p.new_len = new_len, p.status = status;
   if (p.n_layers == 0) p.path = nullptr;
-  return launch_round(keep_kernel, int64_t(std::max(p.n_layers, 1)) * B, kKeepThreads, s, p);
+  p.n_layers = std::max(p.n_layers, 1);
+  // several layers a CTA once there are CTAs enough: what it finds out first is the same for all
+  if (int64_t(p.n_layers) * B > int64_t(INT32_MAX)) return SV_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms < 1) return SV_ERR_CUDA;
+  p.layers = int32_t(std::max<int64_t>(1, int64_t(p.n_layers) * B / (kKeepCtas * sms)));
+  return launch_round(keep_kernel, int64_t((p.n_layers + p.layers - 1) / p.layers) * B, kKeepThreads, s,
+                      p);
 }
