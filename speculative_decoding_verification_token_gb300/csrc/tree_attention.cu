@@ -24,6 +24,7 @@
 #include "tmap.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 namespace sv {
@@ -788,6 +789,7 @@ extern "C" sv_status spec_tree_attention(
   p.tokens = p.tile_tokens * (n / std::min(n, kTile));
   p.box_rows = std::min(page_size, kTile);
   p.scale2 = scale * kLog2e;
+  if (p.scale2 == 0.f) p.scale2 = FLT_MIN;  // (so that -inf, a place not seen, stays -inf)
   p.out = static_cast<__nv_bfloat16*>(out), p.ldo = ldo, p.o_head = o_head;
   p.lse = lse, p.ld_lse = ld_lse, p.status = status;
   p.ws = static_cast<uint8_t*>(workspace);

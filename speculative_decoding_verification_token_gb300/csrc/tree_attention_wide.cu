@@ -445,65 +445,51 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         tc::fence_after_sync();
         // the row's largest score
-        float a[2][32], top = -INFINITY;
-        load32(s_at, a[0]);
+        float a[128];
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          wait_loads();
-          landed(a[ch & 1]);
-          if (ch < 3) load32(s_at + 32 * ch + 32, a[~ch & 1]);
-          float* const f = a[ch & 1];
-          if (masked) hide<32>(f, seen[ch]);
-          float t[4] = {f[0], f[1], f[2], f[3]};
+        for (int ch = 0; ch < 4; ++ch) load32(s_at + 32 * ch, a + 32 * ch);
+        wait_loads();
 #pragma unroll
-          for (int c = 4; c < 28; c += 8) {
+        for (int ch = 0; ch < 4; ++ch) landed(a + 32 * ch);
+        if (masked) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = max3(t[e], f[c + 2 * e], f[c + 2 * e + 1]);
-          }
-          top = max3(top, max3(t[0], t[1], max3(f[28], f[29], t[2])), max3(t[3], f[30], f[31]));
+          for (int ch = 0; ch < 4; ++ch) hide<32>(a + 32 * ch, seen[ch]);
         }
-        load32(s_at, a[0]);  // once more, for the weights
-        top *= scale1;       // (0 times an infinity is a NaN, which raises nothing: its weights are NaN)
+        float t[4] = {a[0], a[1], a[2], a[3]};
+#pragma unroll
+        for (int c = 4; c < 124; c += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] = max3(t[e], a[c + 2 * e], a[c + 2 * e + 1]);
+        }
+        float top = max3(max3(t[0], t[1], a[124]), max3(t[2], t[3], a[125]), fmaxf(a[126], a[127]));
+        top *= scale1;  // (0 times an infinity is a NaN, which raises nothing: its weights are NaN)
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float now = fmaxf(m, top), factor = fast_exp2(m - now);
           m = now;
           l *= factor;
           if (!fresh) {
-            wait_loads();
-            landed(a[0]);
 #pragma unroll 1
-            for (int d = 0; d < kD; d += 32) {
-              load32(o_at + d, a[1]);
-              wait_loads();
-              landed(a[1]);
+            for (int d = 0; d < kD; d += 8) {
+              float o[8];
+              tmem_load<8>(o_at + d, o);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) a[1][c] *= factor;
-              store16(o_at + d, reinterpret_cast<const uint32_t*>(a[1]));
-              store16(o_at + d + 16, reinterpret_cast<const uint32_t*>(a[1]) + 16);
+              for (int c = 0; c < 8; ++c) o[c] *= factor;
+              tmem_store<8>(o_at + d, o);
             }
           }
         }
         fresh = false;
         // P, rounded to bf16 for the product (half a step of 2^-8 a weight); its sum takes what it was
-        // before that.  Chunk ch of P lies in columns that chunks 0 .. ch of S have left.
+        // before that.  It goes over S, which is in registers by now.
         const float2 minus = splat2(-m);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
-          wait_loads();
-          landed(a[ch & 1]);
-          if (ch < 3) load32(s_at + 32 * ch + 32, a[~ch & 1]);
-          float* const f = a[ch & 1];
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 y = fma2(make_float2(f[c], f[c + 1]), scale, minus);
-            f[c] = y.x, f[c + 1] = y.y;
-          }
-          if (masked) hide<32>(f, seen[ch]);
+          float* const f = a + 32 * ch;
           uint32_t w[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
-            const float2 e = exp2_2(make_float2(f[c], f[c + 1]));
+            const float2 e = exp2_2(fma2(make_float2(f[c], f[c + 1]), scale, minus));
             sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], e);
             w[c / 2] = bf16_pair(e.x, e.y);
           }

@@ -108,11 +108,12 @@ def test_each_place_alone(sv):
         assert ((out[first + i, 0].float() - v).abs() <= 2.0 ** -7 * v.abs() * 1.01).all(), i
 
 
-def test_rising_scores(sv):
+@pytest.mark.parametrize("heads", [8, 40, 64])
+def test_rising_scores(sv, heads):
     """Keys whose scores climb along the context, far beyond any first guess of the maximum, and
     fall again."""
     D = 128
-    host, dev, n, _ = pr.make_round([2000], [5], 5, 32, 8, 2, D, seed=4)
+    host, dev, n, _ = pr.make_round([2000], [5], 5, 32, heads, 2, D, seed=4)
     for j in range(2006):
         f = min(j, 2 * 1300 - j) / 60
         host["k_cache"][pr.place(host["page_table"], 0, j, 32)] = (
@@ -125,8 +126,9 @@ def test_rising_scores(sv):
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
-def test_scales(sv, scale):
-    host, dev, n, _ = pr.make_round([300, 9], [4, 2], 4, 16, 8, 2, 64, seed=6, tree="random")
+@pytest.mark.parametrize("heads", [8, 32, 80])
+def test_scales(sv, scale, heads):
+    host, dev, n, _ = pr.make_round([300, 9], [4, 2], 4, 16, heads, 2, 64, seed=6, tree="random")
     out, lse, st = run(sv, dev, scale=scale)
     assert st == sv.SV_OK
     check(host, n, out, lse, scale)
