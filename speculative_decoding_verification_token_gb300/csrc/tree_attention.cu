@@ -127,6 +127,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     sm.err = 0;
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&sm.tmem, kCols);
+  if (warp == kLoadWarp && elect()) {
+    prefetch_map(&map_q);
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
+  }
+  __syncwarp();
   tc::fence_before_sync();
   dependent_start();
   __syncthreads();
@@ -139,16 +145,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int64_t built[2] = {-1, -1};
     const int32_t columns = walk_items(
         p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item, sm.item_full, sm.item_empty, err,
-        [&](int b, const Item& x) {
+        [&](int b, const Item& x, int64_t first) {
           for (int32_t c = lane; c < x.columns; c += 32) {
             const int32_t i = c / p.group, g = c - i * p.group;
             sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(x.head * p.group + g) * p.o_head;
           }
-        },
-        [&](int b, const Item& x, int64_t first) {
-          if (!p.rd.parents) return;
           const int64_t key = int64_t(x.r) << 32 | x.tok0;
-          if (x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
+          if (p.rd.parents && x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
             built[b] = key;
             build_above(p, first, x.end - x.ctx, sm.up, sm.above, err);
             build_seen<Sh::kWords>(p, x, sm.above, sm.seen[b]);
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (row < SV_MAX_TREE_ROWS / 32) sm.bad[b][half][row] = 0;
 #pragma unroll
       for (int c = 0; c < kW; ++c) l[c] = 0.f;
-      bool table = !p.rd.parents;
+      bool table = false;
       soft_sync(half);
       for (int32_t kt = x.t0; kt < x.t1; ++kt, ++t) {
         const uint32_t s_at = lanes + (t & 1) * kN;
@@ -434,12 +437,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (!ok) break;
       // the item's denominators (while the last product is on its way), then its sums
+      bool late = !table && !wait_for(&sm.table_full[b], (it >> 1) & 1, err);
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
         const float sum = over_lanes<kC>(l + ch * kC, [](float a, float b) { return a + b; });
         if (lane < kC) sm.part[quad][col0 + ch * kC + lane] = sum;
       }
-      if (soft_any(half, !wait_for(&sm.p_free, (t - 1) & 1, err))) {
+      late |= !wait_for(&sm.p_free, (t - 1) & 1, err);
+      if (soft_any(half, late)) {
         ok = false;
         break;
       }
@@ -462,6 +467,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       soft_sync(half);
+      bool any_bad = false;
+#pragma unroll
+      for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w)
+        any_bad |= (sm.bad[b][0][w] | sm.bad[b][1][w]) != 0;
       if (32 * quad < kD) {
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
@@ -469,18 +478,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (c0 >= x.columns) break;
           float s[kC], f[kC];
           tmem_load<kC>(lanes + 2 * kN + ch * kC, s);
+          if (any_bad) {  // values that were left out of the product for not being finite
 #pragma unroll 1
-          for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w) {
-            for (uint32_t left = sm.bad[b][0][w] | sm.bad[b][1][w]; left; left &= left - 1) {  // rare
-              const int32_t j = 32 * w + __ffs(left) - 1;
+            for (int32_t j = 0; j < SV_MAX_TREE_ROWS; ++j) {
+              if (!((sm.bad[b][0][j >> 5] | sm.bad[b][1][j >> 5]) >> (j & 31) & 1u)) continue;
               const float v = value_at(p, x, j, row);
-              if (!isfinite(v)) {
+              if (isfinite(v)) continue;
+              const uint32_t sees = p.rd.parents ? sm.seen[b][j][c0 >> 5] >> (c0 & 31)
+                                    : j * p.group <= c0 ? ~0u
+                                    : j * p.group >= c0 + 32 ? 0u
+                                                             : ~0u << (j * p.group - c0);
 #pragma unroll
-                for (int c = 0; c < kC; ++c)
-                  if (p.rd.parents ? sm.seen[b][j][(c0 + c) >> 5] >> ((c0 + c) & 31) & 1u
-                                   : c0 + c >= j * p.group)
-                    s[c] += v;
-              }
+              for (int c = 0; c < kC; ++c)
+                if (sees >> c & 1u) s[c] += v;
             }
           }
           if (x.whole) {
@@ -806,10 +816,13 @@ extern "C" sv_status spec_tree_attention(
   // no more CTAs than there can be tiles
   const int64_t row_tiles = (max_draft_len + int64_t(bonus_row) + p.tokens - 1) / p.tokens;
   const int64_t key_tiles = (int64_t(max_pages) * page_size + kTile - 1) / kTile;
-  const double most = double(B) * n_kv_heads * double(row_tiles) * double(key_tiles);
+  const double items = double(B) * n_kv_heads * double(row_tiles), most = items * double(key_tiles);
   if (most > 9e15) return SV_ERR_UNSUPPORTED;
   const int grid = int(std::max(1.0, std::min(double(sms), most)));
   p.reread = row_tiles > 1;
+  // (17 x 9 narrow rows over up to 3000 places: 0 33.9 us, 1 24.0, 2 19.8, 4 19.6; 32 trees of 64 rows
+  // over up to 4096: 0 198 us, 2 182, 4 176, 6 171)
   p.item_cost = n == kWide ? 6 : 4;
+  p.big = most + p.item_cost * items >= double(1 << 22);  // (times 192 CTAs it fits 32 bits)
   return D == 64 ? launch<64>(n, m, p, grid, s) : launch<128>(n, m, p, grid, s);
 }

@@ -27,6 +27,7 @@ struct AttnParams {
   int32_t box_rows;  // places of a TMA box
   int32_t reread;    // several row tiles read the same keys
   int32_t item_cost; // what an item costs beside its key tiles, in key tiles
+  int32_t big;       // the call's cost may pass 2^22
   float scale2;  // scale * log2(e)
   __nv_bfloat16* out;
   int64_t ldo, o_head;
@@ -81,13 +82,23 @@ struct Span {
   Request q;                  // and its sizes
 };
 
-// One warp: this CTA's run of the list, from the requests in chunks of 32, a lane each.
+__device__ __forceinline__ int32_t warp_add(int32_t x, int32_t) {
+  return __reduce_add_sync(0xffffffffu, x);
+}
+__device__ __forceinline__ int64_t warp_add(int64_t x, int32_t steps) {
+  for (int o = 1; o < steps; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
+// One warp: this CTA's run of the list, from the requests in chunks of 32, a lane each.  T holds the
+// call's cost times the number of CTAs.
+template <typename T>
 __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
   const int lane = threadIdx.x & 31;
   const int32_t steps = min(p.rd.B, 32);
   Span span = {};
   Request q = {};
-  int64_t tiles = 0, items = 0;  // of the lane's request
+  T tiles = 0, items = 0;  // of the lane's request
   auto chunk = [&](int32_t r0, bool tell) {
     const int32_t r = r0 + lane;
     tiles = items = 0;
@@ -95,43 +106,33 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
     if (r < p.rd.B) {
       if (!round_request(p.rd, r, q) && tell) report(err, SV_ERR_BAD_INPUT);
       int32_t n;
-      tiles = tiles_of_head(q, p.tokens, n) * p.n_kv;
-      items = int64_t(n) * p.n_kv;
+      tiles = T(tiles_of_head(q, p.tokens, n)) * p.n_kv;
+      items = T(n) * p.n_kv;
     }
   };
-  auto sum = [&](int64_t x) {  // over the chunk's lanes
-    for (int o = 1; o < steps; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return __shfl_sync(0xffffffffu, x, 0);
-  };
-  int64_t all_tiles = 0, all_items = 0;
+  T all_tiles = 0, all_items = 0;
   for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
     chunk(r0, blockIdx.x == 0);
-    all_tiles += sum(tiles);
-    all_items += sum(items);
+    all_tiles += warp_add(tiles, steps);
+    all_items += warp_add(items, steps);
   }
   // (with few tiles for each CTA their number alone counts)
-  span.cost = all_tiles > 2 * int64_t(gridDim.x) ? p.item_cost : 0;
-  const int64_t total = span.total = all_tiles + span.cost * all_items;
-  if (total < (int64_t(1) << 22)) {  // (the products stay in 32 bits: at most 192 CTAs)
-    span.begin = uint32_t(total) * blockIdx.x / gridDim.x;
-    span.end = uint32_t(total) * (blockIdx.x + 1) / gridDim.x;
-  } else {
-    span.begin = total * blockIdx.x / gridDim.x;
-    span.end = total * (blockIdx.x + 1) / gridDim.x;
-  }
-  if (span.begin == span.end) return span;
-  int64_t before = 0;
+  span.cost = all_tiles > 2 * T(gridDim.x) ? p.item_cost : 0;
+  const T total = all_tiles + span.cost * all_items;
+  const T begin = total * T(blockIdx.x) / T(gridDim.x), end = total * T(blockIdx.x + 1) / T(gridDim.x);
+  span.total = total, span.begin = begin, span.end = end;
+  if (begin == end) return span;
+  T before = 0;
   for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
     if (p.rd.B > 32) chunk(r0, false);
-    const int64_t mine = tiles + span.cost * items;
-    int64_t upto = mine;
+    const T mine = tiles + span.cost * items;
+    T upto = mine;
     for (int o = 1; o < steps; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      const T x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
-    const int64_t a = before + upto - mine;
-    const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= span.begin &&
-                                                        span.begin < a + mine);
+    const T a = before + upto - mine;
+    const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= begin && begin < a + mine);
     if (hit) {
       const int l = __ffs(hit) - 1;
       span.before = __shfl_sync(0xffffffffu, a, l);
@@ -205,6 +206,9 @@ __device__ __forceinline__ void soft_sync(int half) { named_sync(1 + half, 128);
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3, uint64_t* bar) {
   asm volatile(
@@ -318,10 +322,6 @@ __device__ __forceinline__ void hide(float* y, uint32_t seen) {
     if (!(seen >> j & 1u)) y[j] = -INFINITY;
 }
 
-__device__ __forceinline__ bool not_finite2(uint32_t w) {  // either half of a bf16 pair
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-
 // A work item as the warps of a CTA share it.
 struct Item {
   int64_t first_row;  // row of the tile's first token
@@ -334,16 +334,16 @@ struct Item {
   int32_t stop;    // no item: the list is at its end
 };
 
-// The warps that move the work on share these barriers: an item's description is there (item_full), and
-// nobody needs it or its queries any more (item_empty).  One warp: `before` adds what belongs to item
-// `b` (of two) ahead of its arrival, `after` what may come later.  Ends the list with an item that says
-// so, and leaves the CTA's cut item in the workspace; returns its columns.
-template <typename Before, typename After>
+// The items of this CTA's run, by one warp: item_full says that an item's description is there (of two),
+// item_empty that nobody needs it or its queries any more.  `after` adds what is not needed at once.
+// Ends the list with an item that says so, and leaves the CTA's cut item in the workspace; returns its
+// columns.
+template <typename After>
 __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, Item* item,
                                               uint64_t* item_full, uint64_t* item_empty,
-                                              int32_t* err, Before before, After after) {
+                                              int32_t* err, After after) {
   const int lane = threadIdx.x & 31;
-  const Span span = find_span(p, err);
+  const Span span = p.big ? find_span<int64_t>(p, err) : find_span<int32_t>(p, err);
   Cut cut = {};
   int32_t cut_columns = 0;
   bool ok = true;
@@ -355,8 +355,7 @@ __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, It
     int32_t n_items;
     int64_t per_head = tiles_of_head(rq, p.tokens, n_items);
     per_head += int64_t(span.cost) * n_items;
-    h = int32_t(off <= INT32_MAX ? uint32_t(off) / uint32_t(min(per_head, int64_t(INT32_MAX)))
-                                 : off / per_head);
+    h = p.big ? int32_t(off / per_head) : int32_t(uint32_t(off) / uint32_t(per_head));
     off -= h * per_head;
     while (off >= tiles_of(rq, rt, p.tokens) + span.cost)
       off -= tiles_of(rq, rt++, p.tokens) + span.cost;
@@ -384,17 +383,19 @@ __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, It
           ok = false;
           break;
         }
-        if (lane == 0) item[b] = x;
-        before(b, x);
+        if (lane == 0) {
+          item[b] = x;
+          mbar_arrive(&item_full[b]);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&item_full[b]);
         after(b, x, rq.first);
         if (x.begins && !x.whole) {
           cut.total = span.total;
           cut.first_row = x.first_row;
           cut.head = h;
           // the CTA that the item's last unit lies in
-          cut.last = int32_t(((at - off + tiles + span.cost) * gridDim.x - 1) / cut.total);
+          const int64_t end = (at - off + tiles + span.cost) * gridDim.x - 1;
+          cut.last = p.big ? int32_t(end / cut.total) : int32_t(uint32_t(end) / uint32_t(cut.total));
           cut_columns = columns;
         }
         ++it;
@@ -513,28 +514,36 @@ __device__ __forceinline__ void load_tile(const AttnParams& p, uint8_t* dst, con
 // is added to the rows that do see it at the end.
 template <int kCount>
 __device__ __forceinline__ bool make_finite(uint8_t* v, int row, int k0, bool past) {
-  bool found = false;
+  auto chunk = [&](int i) {
+    const int k = k0 + i;
+    return reinterpret_cast<uint4*>(v + (k >> 3) * 16384 + tc::sw128(row, k & 7));
+  };
+  if (past) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) *chunk(i) = make_uint4(0, 0, 0, 0);
+    return false;
+  }
+  // an exponent of all ones carries into the sign's place
+  auto ones = [](uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; };
+  uint32_t found = 0;
 #pragma unroll
   for (int i = 0; i < kCount; ++i) {
-    const int k = k0 + i;
-    uint4* const at = reinterpret_cast<uint4*>(v + (k >> 3) * 16384 + tc::sw128(row, k & 7));
-    if (past) {
-      *at = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    uint4 y = *at;
-    if (not_finite2(y.x) || not_finite2(y.y) || not_finite2(y.z) || not_finite2(y.w)) {
-      uint32_t* const w = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
-        if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
-      }
-      *at = y;
-      found = true;
-    }
+    const uint4 y = *chunk(i);
+    found |= ones(y.x) | ones(y.y) | ones(y.z) | ones(y.w);
   }
-  return found;
+  if (!(found & 0x80008000u)) return false;
+#pragma unroll 1
+  for (int i = 0; i < kCount; ++i) {
+    uint4 y = *chunk(i);
+    uint32_t* const w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t o = ones(w[e]);
+      w[e] &= (o & 0x8000u ? 0u : 0xFFFFu) | (o & 0x80000000u ? 0u : 0xFFFF0000u);
+    }
+    *chunk(i) = y;
+  }
+  return true;
 }
 
 // Element d of row j (of those that not everybody sees) in the cache.

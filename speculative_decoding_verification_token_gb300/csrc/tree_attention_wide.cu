@@ -17,6 +17,11 @@ namespace sv {
 namespace attn {
 namespace {
 
+// A warp's results go out through shared memory, 64 bytes of each of its 32 rows at a time, so that four
+// lanes write a row's 64 bytes (16 bytes of 32 rows at once take four times as long).  80 bytes apart the
+// rows' pieces lie in different banks.
+constexpr int kStageRow = 80;
+
 template <int kD>
 struct WideShared {
   static constexpr uint32_t kSlot = kTile * kD * 2;
@@ -25,10 +30,11 @@ struct WideShared {
     uint64_t full[16], empty[16], item_full[2], item_empty[2], table_full[2];
     uint64_t q_full, q_empty, s_full[2], p_half[2], p_full[2], o_full[2], drain;
     Item item[2];
-    uint32_t above[2][SV_MAX_TREE_ROWS][4];
+    alignas(16) uint32_t above[2][SV_MAX_TREE_ROWS][4];
     int32_t up[SV_MAX_TREE_ROWS];
     uint32_t bad[2][2][SV_MAX_TREE_ROWS / 32];  // rows whose values are not all finite, by who found it
     float m[kTile], l[kTile];                   // of stream 1, for joining
+    alignas(16) uint8_t stage[kSoftWarps][32 * kStageRow];  // results on their way out
     uint32_t tmem;
     int32_t err, cut_columns;
   };
@@ -143,6 +149,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     sm.err = 0;
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&sm.tmem, 512);
+  if (warp == kLoadWarp && elect()) {
+    prefetch_map(&map_q);
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
+  }
+  __syncwarp();
   tc::fence_before_sync();
   dependent_start();
   __syncthreads();
@@ -156,7 +168,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int64_t built[2] = {-1, -1};
     const int32_t columns = walk_items(
         p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item, sm.item_full, sm.item_empty, err,
-        [](int, const Item&) {},
         [&](int b, const Item& x, int64_t first) {
           if (!p.rd.parents) return;
           const int64_t key = int64_t(x.r) << 32 | x.tok0;
@@ -417,13 +428,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           table = true;
           const int32_t j0 = kt * kTile - x.base0;  // the tile's first place among those of the rows
           if (p.rd.parents) {
-            const uint32_t* const above = sm.above[b][min(x.tok0 + i_item, SV_MAX_TREE_ROWS - 1)];
-            auto word = [&](int32_t k) { return k < 0 ? ~0u : k < 4 && mine ? above[k] : 0u; };
+            // the row's 128 bits from j0 on: ones before them, zeros behind them
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                sm.above[b][min(x.tok0 + i_item, SV_MAX_TREE_ROWS - 1)]);
+            const uint32_t above[4] = {v.x, v.y, v.z, v.w};
+            const int32_t k0 = j0 >> 5;
+            uint32_t word[5];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int32_t j = j0 + 32 * w, k = j >> 5;
-              seen[w] = __funnelshift_r(word(k), word(k + 1), j & 31);
+            for (int w = 0; w < 5; ++w) {
+              const int32_t k = k0 + w;
+              word[w] = k < 0 ? ~0u : 0u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) word[w] = k == e ? above[e] : word[w];
             }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) seen[w] = __funnelshift_r(word[w], word[w + 1], j0 & 31);
           } else {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {  // places up to the row's own
@@ -540,7 +559,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             p.lse[out_row * p.ld_lse + head] = (log2f(l) + m) * kLn2;
           }
         }
-        const float inv = x.whole ? 1.f / l : 1.f;
+        const float inv = 1.f / l;
+        const int64_t out_at = mine ? out_row * p.ldo + head * p.o_head : -1;
+        // the rows' values that were left out of the product for not being finite: elements d0 .. of what
+        // is on its way out
+        bool any_bad = false;
+#pragma unroll
+        for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w)
+          any_bad |= (sm.bad[b][0][w] | sm.bad[b][1][w]) != 0;
+        auto add_bad = [&](auto* to, int n, int d0) {
+#pragma unroll 1
+          for (int32_t j = 0; j < SV_MAX_TREE_ROWS; ++j) {
+            if (!((sm.bad[b][0][j >> 5] | sm.bad[b][1][j >> 5]) >> (j & 31) & 1u)) continue;
+            if (!mine || !(p.rd.parents ? sm.above[b][x.tok0 + i_item][j >> 5] >> (j & 31) & 1u
+                                        : j <= i_item))
+              continue;
+#pragma unroll 1
+            for (int c = 0; c < n; ++c) {
+              const float v = value_at(p, x, j, d0 + c);
+              if (!isfinite(v)) to[c] = float(to[c]) + v;
+            }
+          }
+        };
+        // the warp's columns: from column0 on, the first rows_here of its lanes'
+        const int32_t column0 = column - lane;
+        const int32_t rows_here = __popc(__ballot_sync(0xffffffffu, mine));
 #pragma unroll 1
         for (int d = 0; d < kD; d += 32) {
           float o[32];
@@ -560,33 +603,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               for (int c = 0; c < 32; ++c) o[c] += o1[c] * other_f;
             }
           }
-#pragma unroll 1
-          for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w) {
-            for (uint32_t left = sm.bad[b][0][w] | sm.bad[b][1][w]; left; left &= left - 1) {  // rare
-              const int32_t j = 32 * w + __ffs(left) - 1;
-              const bool sees = mine && (p.rd.parents
-                                             ? sm.above[b][x.tok0 + i_item][j >> 5] >> (j & 31) & 1u
-                                             : j <= i_item);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const float v = value_at(p, x, j, d + c);
-                if (sees && !isfinite(v)) o[c] += v;
-              }
-            }
-          }
-          if (mine && x.whole) {
-            uint4* const to = reinterpret_cast<uint4*>(p.out + out_row * p.ldo + head * p.o_head + d);
+          // this lane's row into the stage, and 16 bytes of row 8 q + lane / 4 out of it
+          uint8_t* const in = sm.stage[warp] + lane * kStageRow;
+          const uint8_t* const from = sm.stage[warp] + (lane >> 2) * kStageRow + (lane & 3) * 16;
+          if (x.whole) {
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < 32; c += 8)
-              to[c / 8] = make_uint4(bf16_pair(o[c] * inv, o[c + 1] * inv),
-                                     bf16_pair(o[c + 2] * inv, o[c + 3] * inv),
-                                     bf16_pair(o[c + 4] * inv, o[c + 5] * inv),
-                                     bf16_pair(o[c + 6] * inv, o[c + 7] * inv));
-          } else if (mine) {
-            float4* const to = reinterpret_cast<float4*>(part + column * kD + d);
+              *reinterpret_cast<uint4*>(in + 2 * c) =
+                  make_uint4(bf16_pair(o[c] * inv, o[c + 1] * inv),
+                             bf16_pair(o[c + 2] * inv, o[c + 3] * inv),
+                             bf16_pair(o[c + 4] * inv, o[c + 5] * inv),
+                             bf16_pair(o[c + 6] * inv, o[c + 7] * inv));
+            if (any_bad) add_bad(reinterpret_cast<__nv_bfloat16*>(in), 32, d);
+            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              to[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+            for (int q = 0; q < 4; ++q) {
+              const int64_t to = __shfl_sync(0xffffffffu, out_at, 8 * q + (lane >> 2));
+              if (to >= 0)
+                *reinterpret_cast<uint4*>(p.out + to + d + (lane & 3) * 8) =
+                    *reinterpret_cast<const uint4*>(from + q * 8 * kStageRow);
+            }
+          } else {
+#pragma unroll
+            for (int part_of = 0; part_of < 2; ++part_of) {  // 16 elements at a time
+              __syncwarp();
+#pragma unroll
+              for (int c = 0; c < 16; c += 4)
+                *reinterpret_cast<float4*>(in + 4 * c) =
+                    make_float4(o[16 * part_of + c], o[16 * part_of + c + 1], o[16 * part_of + c + 2],
+                                o[16 * part_of + c + 3]);
+              if (any_bad) add_bad(reinterpret_cast<float*>(in), 16, d + 16 * part_of);
+              __syncwarp();
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int32_t col = column0 + 8 * q + (lane >> 2);
+                if (8 * q + (lane >> 2) < rows_here)
+                  *reinterpret_cast<float4*>(part + col * kD + d + 16 * part_of + (lane & 3) * 4) =
+                      *reinterpret_cast<const float4*>(from + q * 8 * kStageRow);
+              }
+            }
           }
         }
       }
