@@ -405,28 +405,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int b = it & 1;
       wait(&sm.item_full[b], (it >> 1) & 1);
       if (both_any(failed)) break;
-      const Item x = sm.item[b];
+      const Item& x = sm.item[b];  // (not in registers: a row's scores want them)
       if (x.stop) break;
       const bool twin = x.columns <= tile_rows;
       const int32_t n = x.t1 - x.t0, ahead = twin ? 2 : 1;
-      const int32_t i_row = row / p.group;                       // token in the row tile
-      const int32_t i_item = (twin ? 0 : s * p.tile_tokens) + i_row;  // and in the item
-      const int32_t column = (twin ? 0 : s * tile_rows) + row;
-      const bool mine = row < tile_rows && column < x.columns;
+      // this thread's token in the item, and its column
+      auto token = [&] { return (twin ? 0 : s * p.tile_tokens) + row / p.group; };
+      auto column_of = [&] { return (twin ? 0 : s * tile_rows) + row; };
+      auto is_mine = [&] { return row < tile_rows && column_of() < x.columns; };
       if (row < SV_MAX_TREE_ROWS / 32) sm.bad[b][s][row] = 0;
       soft_sync(s);
       float m = kM2Empty, l = 0.f;
       bool table = !p.rd.parents, fresh = true;
+      const int32_t mask_from = x.base0 / kTile - x.t0;  // tiles from here on hold places not all see
       for (int32_t i = twin ? s : 0; i < n; i += ahead) {
-        const int32_t kt = x.t0 + i;
-        const bool masked = (kt + 1) * int64_t(kTile) > x.base0;
+        const bool masked = i >= mask_from;
         wait(&sm.s_full[s], s_phase);
         s_phase ^= 1;
         uint32_t seen[4];  // bit c of word w: this row sees place 32 w + c of the tile
         if (masked) {
           if (!table) wait(&sm.table_full[b], (it >> 1) & 1);
           table = true;
-          const int32_t j0 = kt * kTile - x.base0;  // the tile's first place among those of the rows
+          const int32_t i_item = token();
+          const bool mine = is_mine();
+          const int32_t kt = x.t0 + i, j0 = kt * kTile - x.base0;  // the tile's first place among those of the rows
           if (p.rd.parents) {
             // the row's 128 bits from j0 on: ones before them, zeros behind them
             const uint4 v = *reinterpret_cast<const uint4*>(
@@ -536,7 +538,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (twin && s == 1) sm.m[row] = m, sm.l[row] = l;
       if (both_any(failed)) break;
       tc::fence_after_sync();
-      const bool writes = !twin || s == 0;
+      const bool writes = !twin || s == 0, mine = is_mine();
+      const int32_t i_item = token(), column = column_of();
       if (writes) {
         float mine_f = 1.f, other_f = 0.f;
         if (twin) {
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           m = now;
         }
         const bool other = twin && n > 1;
-        const int32_t g = row - i_row * p.group, head = x.head * p.group + g;
+        const int32_t head = x.head * p.group + row % p.group;
         const int64_t out_row = x.first_row + i_item;
         float* const part = reinterpret_cast<float*>(p.ws + wl.parts) +
                             (2 * int64_t(blockIdx.x) + x.begins) * wl.part_floats;
