@@ -18,7 +18,8 @@
 //   warp 10    the work items: their sizes, and for trees who sees whom.
 // The work -- (request, key head, row tile, key tile) -- is one list, cut into equal runs for a
 // persistent CTA on every SM, wherever the cuts fall; what a cut leaves in parts goes to the workspace
-// and is joined by a second kernel.
+// and is joined by a second kernel.  Where there are few items of few tiles, a cluster takes each, and its
+// CTAs, a run of the tiles each, join their parts through one another's shared memory: one launch.
 #include "tree_attention.cuh"
 
 #include "tmap.h"
@@ -54,6 +55,7 @@ struct AttnShared {
                                                 // all finite
     uint32_t tmem;
     int32_t err, cut_columns;
+    uint32_t had;  // this CTA of a cluster has a part
   };
   static constexpr uint32_t kSmall = (sizeof(Small) + 127) / 128 * 128;
   static constexpr int kStages() {
@@ -87,7 +89,133 @@ __device__ __forceinline__ void build_seen(const AttnParams& p, const Item& x, u
   }
 }
 
+constexpr int kCluster = 8;
+
+// The item of this CTA's cluster and the CTA's tiles of it, by one warp (at most 32 requests).
+__device__ __forceinline__ Item cluster_item(const AttnParams& p, int64_t& first) {
+  const int lane = threadIdx.x & 31;
+  const int32_t cluster = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  Request q = {};
+  int32_t tiles = 0;  // row tiles
+  if (lane < p.rd.B) {
+    round_request(p.rd, lane, q);
+    tiles = (q.n + p.tokens - 1) / p.tokens;
+  }
+  const int32_t items = tiles * p.n_kv;
+  int32_t upto = items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  Item x = {};
+  const uint32_t past = __ballot_sync(0xffffffffu, cluster < upto);
+  if (past) {
+    const int r = __ffs(past) - 1;
+    const int32_t left = cluster - __shfl_sync(0xffffffffu, upto - items, r);
+    tiles = __shfl_sync(0xffffffffu, tiles, r);
+    q.first = __shfl_sync(0xffffffffu, q.first, r);
+    q.n = __shfl_sync(0xffffffffu, q.n, r);
+    q.ctx = __shfl_sync(0xffffffffu, q.ctx, r);
+    first = q.first;
+    x.head = left / tiles, x.r = r;
+    const int32_t rt = left - x.head * tiles, tok0 = rt * p.tokens, ntok = min(p.tokens, q.n - tok0);
+    x.first_row = q.first + tok0;
+    x.columns = ntok * p.group;
+    x.tok0 = tok0, x.ctx = q.ctx;
+    x.base0 = q.ctx + (p.rd.parents ? 0 : tok0);
+    x.end = q.ctx + tok0 + ntok;
+    const int64_t all = tiles_of(q, rt, p.tokens);
+    x.t0 = int32_t(all * rank / kCluster), x.t1 = int32_t(all * (rank + 1) / kCluster);
+  }
+  x.begins = x.last = 1;
+  x.stop = x.t0 == x.t1;
+  return x;
+}
+
+// All there is to check of a call of few requests, by one warp: whether it is bad.
+__device__ __forceinline__ bool bad_round(const RoundParams& rd) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  for (int32_t r = 0; r < rd.B; ++r) {
+    Request q;
+    if (!round_request(rd, r, q)) bad = true;
+    if (q.n == 0) continue;
+    const int32_t pages = int32_t((int64_t(q.ctx) + q.n + rd.page_size - 1) / rd.page_size);
+#pragma unroll 8
+    for (int32_t i = lane; i < pages; i += 32) {
+      const int32_t g = rd.page_table[r * rd.ld_pages + i];
+      bad |= g < 0 || g >= rd.n_pages;
+    }
+    if (rd.parents) {
+#pragma unroll 4
+      for (int32_t i = lane; i < q.n; i += 32) {
+        const int32_t up = rd.parents[q.first + i];
+        bad |= up < -1 || up >= i;
+      }
+    }
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(uint32_t at, int rank) {
+  uint32_t to;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
+  return to;
+}
+__device__ __forceinline__ float peer_load(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// The parts of a cluster's item joined by all of its threads: CTA `rank` takes every eighth column.
 template <int kD, int kN>
+__device__ __forceinline__ void cluster_join(const AttnParams& p, const Item& x, const float* part,
+                                             const uint32_t* had, const int64_t* col_off) {
+  const uint32_t at = smem_addr(part), had_at = smem_addr(had);
+  for (int32_t u = threadIdx.x;; u += kAttnThreads) {
+    const int32_t col = blockIdx.x % kCluster + kCluster * (u / (kD / 2)), d = u % (kD / 2) * 2;
+    if (col >= x.columns) return;
+    float m[kCluster], l[kCluster], a[kCluster], b[kCluster];
+    bool has[kCluster];
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      const uint32_t from = peer(at, r);
+      has[r] = __float_as_uint(peer_load(peer(had_at, r))) != 0;
+      m[r] = peer_load(from + 4 * (kN * kD + col));
+      l[r] = peer_load(from + 4 * (kN * kD + kN + col));
+      a[r] = peer_load(from + 4 * (col * kD + d));
+      b[r] = peer_load(from + 4 * (col * kD + d + 1));
+    }
+    float top = kM2Empty, sum = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r)
+      if (has[r]) top = fmaxf(top, m[r]);
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      if (!has[r]) continue;
+      const float w = fast_exp2(m[r] - top);
+      sum += w * l[r];
+      y0 += w * a[r];
+      y1 += w * b[r];
+    }
+    const float inv = 1.f / sum;
+    *reinterpret_cast<__nv_bfloat162*>(p.out + col_off[col] + d) =
+        __floats2bfloat162_rn(y0 * inv, y1 * inv);
+    if (d == 0 && p.lse) {
+      const int32_t i = col / p.group;
+      p.lse[(x.first_row + i) * p.ld_lse + x.head * p.group + col - i * p.group] =
+          (top + log2f(sum)) * kLn2;
+    }
+  }
+}
+
+template <int kD, int kN, bool kShort>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ CUtensorMap map_k,
@@ -125,6 +253,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     mbar_init(&sm.drain, 1);
     fence_barrier_init();
     sm.err = 0;
+    sm.had = 0;
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&sm.tmem, kCols);
   if (warp == kLoadWarp && elect()) {
@@ -143,23 +272,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == kItemWarp) {
     // ---- the items ---------------------------------------------------------------------------------
     int64_t built[2] = {-1, -1};
-    const int32_t columns = walk_items(
-        p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item, sm.item_full, sm.item_empty, err,
-        [&](int b, const Item& x, int64_t first) {
-          for (int32_t c = lane; c < x.columns; c += 32) {
-            const int32_t i = c / p.group, g = c - i * p.group;
-            sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(x.head * p.group + g) * p.o_head;
-          }
-          const int64_t key = int64_t(x.r) << 32 | x.tok0;
-          if (p.rd.parents && x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
-            built[b] = key;
-            build_above(p, first, x.end - x.ctx, sm.up, sm.above, err);
-            build_seen<Sh::kWords>(p, x, sm.above, sm.seen[b]);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.table_full[b]);
-        });
-    if (lane == 0) sm.cut_columns = columns;
+    auto details = [&](int b, const Item& x, int64_t first) {
+      for (int32_t c = lane; c < x.columns; c += 32) {
+        const int32_t i = c / p.group, g = c - i * p.group;
+        sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(x.head * p.group + g) * p.o_head;
+      }
+      const int64_t key = int64_t(x.r) << 32 | x.tok0;
+      if (p.rd.parents && x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
+        built[b] = key;
+        build_above(p, first, x.end - x.ctx, sm.up, sm.above, err);
+        build_seen<Sh::kWords>(p, x, sm.above, sm.seen[b]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.table_full[b]);
+    };
+    if constexpr (kShort) {
+      int64_t first = 0;
+      const Item x = cluster_item(p, first);
+      if (lane == 0) {
+        sm.item[0] = x;
+        mbar_arrive(&sm.item_full[0]);
+        sm.item[1].stop = 1;  // there is no other
+        mbar_arrive(&sm.item_full[1]);
+      }
+      __syncwarp();
+      details(0, x, first);
+    } else {
+      const int32_t columns = walk_items(p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item,
+                                         sm.item_full, sm.item_empty, err, details);
+      if (lane == 0) sm.cut_columns = columns;
+    }
   } else if (warp == kLoadWarp) {
     // ---- the loads -----------------------------------------------------------------------------------
     const uint64_t once = tc::policy_evict_first();
@@ -213,8 +355,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ---- the products --------------------------------------------------------------------------------
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(128, kN);
     constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, kN) | (1u << 15) | (1u << 16);
-    const uint32_t ring_lo = smem_addr(ring) >> 4, q_lo = smem_addr(q_at) >> 4;
-    const uint32_t p_lo = (smem_addr(p_at) >> 4) | kAcross;
+    const uint32_t ring_lo = desc_at(ring), q_lo = desc_at(q_at);
+    const uint32_t p_lo = desc_at(p_at) | kAcross;
     int32_t slot = 0, t = 0;
     uint32_t phase = 0;
     bool ok = true, fresh = false, v_fresh = false;
@@ -449,8 +591,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         break;
       }
       tc::fence_after_sync();
-      float* const part = reinterpret_cast<float*>(p.ws + wl.parts) +
-                          (2 * int64_t(blockIdx.x) + x.begins) * wl.part_floats;
+      // (a cluster's CTA has a single item, and its ring is free)
+      float* const part = kShort ? reinterpret_cast<float*>(ring)
+                                 : reinterpret_cast<float*>(p.ws + wl.parts) +
+                                       (2 * int64_t(blockIdx.x) + x.begins) * wl.part_floats;
+      if (kShort && tid == 0) sm.had = 1;
       if (row < kW && col0 + row < x.columns) {
         const int c = col0 + row;
         const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]);
@@ -523,6 +668,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (row == 0) mbar_arrive(&sm.item_empty[b]);
     }
   }
+  if constexpr (kShort) {
+    // CTA 0 looks at all there is to check, and the status is its own; what ran out of time says so later
+    if (warp == kItemWarp + 1 && blockIdx.x == 0 && p.status) {
+      const bool bad = bad_round(p.rd);
+      if (lane == 0) *p.status = bad ? SV_ERR_BAD_INPUT : SV_OK;
+    }
+  }
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
@@ -530,10 +682,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kCols);
   }
-  if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err * 512 + sm.cut_columns;
+  if constexpr (kShort) {
+    if (tid == 0 && sm.err == SV_ERR_TIMEOUT) report(p.status, SV_ERR_TIMEOUT);
+    __syncwarp();
+    cluster_sync();
+    cluster_join<kD, kN>(p, sm.item[0], reinterpret_cast<const float*>(ring), &sm.had, sm.col_off[0]);
+    __syncwarp();
+    cluster_sync();  // nobody's shared memory goes away while others read it
+  } else {
+    if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err * 512 + sm.cut_columns;
+  }
 }
-
-// ---- the parts of cut items joined -------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
 // Columns of a warp: one where there are few columns, and many parts of each.
@@ -718,9 +877,45 @@ sv_status launch_join(const AttnParams& p, int grid, cudaStream_t s) {
                           kJoinThreads, 0, s, p, grid);
 }
 
+// Few items of few tiles: a cluster for each.  They have to be there at once, an SM a CTA; more tiles are
+// worth more SMs than a cluster has; and one warp looks through all the pages.
+constexpr int kShortItems = 16, kShortTiles = 64, kShortPages = 1024;
+
+template <int kD, int kN>
+sv_status launch_short(const AttnMaps& m, const AttnParams& p, int items, cudaStream_t s) {
+  auto* kern = attention_kernel<kD, kN, true>;
+  static_assert(kN * (kD + 2) * 4 <= AttnShared<kD, kN>::kStages() * AttnShared<kD, kN>::kSlot,
+                "a part fits the ring");
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
+      cudaSuccess)
+    return SV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(items) * kCluster);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = kAttnSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, m.q, m.k, m.v, p));
+}
+
+template <int kD>
+sv_status launch_short(int32_t n, const AttnMaps& m, const AttnParams& p, int items,
+                       cudaStream_t s) {
+  return n == 16   ? launch_short<kD, 16>(m, p, items, s)
+         : n == 32 ? launch_short<kD, 32>(m, p, items, s)
+                   : launch_short<kD, 64>(m, p, items, s);
+}
+
 template <int kD, int kN>
 sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
-  auto* kern = attention_kernel<kD, kN>;
+  auto* kern = attention_kernel<kD, kN, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
       cudaSuccess)
     return SV_ERR_CUDA;
@@ -824,5 +1019,7 @@ extern "C" sv_status spec_tree_attention(
   // over up to 4096: 0 198 us, 2 182, 4 176, 6 171)
   p.item_cost = n == kWide ? 6 : 4;
   p.big = most + p.item_cost * items >= double(1 << 22);  // (times 192 CTAs it fits 32 bits)
+  if (n <= 64 && items <= kShortItems && key_tiles <= kShortTiles && int64_t(B) * max_pages <= kShortPages)
+    return D == 64 ? launch_short<64>(n, m, p, int(items), s) : launch_short<128>(n, m, p, int(items), s);
   return D == 64 ? launch<64>(n, m, p, grid, s) : launch<128>(n, m, p, grid, s);
 }

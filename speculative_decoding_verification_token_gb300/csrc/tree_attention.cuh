@@ -235,6 +235,8 @@ __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kAlongK = 1u << 16;
 constexpr uint32_t kAcross = (16384u >> 4) << 16;  // groups of 64: 128 places of 128 bytes
+// A descriptor's address bits (a CTA of a cluster has its rank in the upper ones of its own addresses).
+__device__ __forceinline__ uint32_t desc_at(const void* p) { return (smem_addr(p) & 0x3FFFFu) >> 4; }
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // (bit 13: Q negated, so that the scale is positive)
     const uint32_t kIdS = tc::idesc_bf16_f32(128, 128) | (p.scale2 < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t kIdO = tc::idesc_bf16_f32(128, kD) | (1u << 16);
-    const uint32_t ring_lo = smem_addr(ring) >> 4, q_lo = smem_addr(q_at) >> 4;
+    const uint32_t ring_lo = desc_at(ring), q_lo = desc_at(q_at);
     int32_t slot = 0;
     uint32_t phase = 0, p_phase[2] = {0, 0};
     bool ok = true;

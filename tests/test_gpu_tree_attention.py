@@ -31,6 +31,13 @@ def run(sv, dev, scale=None, **kw):
     return out.cpu(), lse.cpu(), int(st)
 
 
+def wide_table(dev, columns):
+    """The same pages in a table of more columns (calls of few pages may take another way)."""
+    t = torch.full((dev["page_table"].shape[0], columns), -7, dtype=torch.int32, device="cuda")
+    t[:, :dev["page_table"].shape[1]] = dev["page_table"]
+    return dict(dev, page_table=t)
+
+
 def check(host, n, out, lse, scale):
     want = pr.attention(host, n, scale)
     for row in range(out.shape[0]):
@@ -66,14 +73,25 @@ SHAPES = [  # contexts, drafts, most drafts, page, heads, kv heads, D, tree
 
 
 @pytest.mark.parametrize("case", SHAPES, ids=[str(i) for i in range(len(SHAPES))])
-@pytest.mark.parametrize("q_scale", [1.0, 6.0])
-def test_shapes(sv, case, q_scale):
+@pytest.mark.parametrize("q_scale,columns", [(1.0, 0), (6.0, 0), (1.0, 1100)])
+def test_shapes(sv, case, q_scale, columns):
     ctx, drafts, gmax, page, heads, kv, D, tree = case
     host, dev, n, _ = pr.make_round(ctx, drafts, gmax, page, heads, kv, D, seed=len(ctx) + page,
                                     tree=tree, q_scale=q_scale)
-    out, lse, st = run(sv, dev)
+    out, lse, st = run(sv, wide_table(dev, columns) if columns else dev)
     assert st == sv.SV_OK
     check(host, n, out, lse, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("heads,kv", [(8, 8), (24, 2), (6, 2), (40, 4)])
+@pytest.mark.parametrize("ctx,drafts", [([8100], [5]), ([1023, 4], [1, 3]), ([5000, 0, 900], [2, 1, 0])])
+def test_few_requests_of_longer_contexts(sv, ctx, drafts, heads, kv):
+    """The work of a call of few requests, in runs of tiles of any number."""
+    host, dev, n, _ = pr.make_round(ctx, drafts, 5, 32, heads, kv, 128, seed=sum(ctx), tree="random")
+    for d in (dev, wide_table(dev, 1100)):
+        out, lse, st = run(sv, d)
+        assert st == sv.SV_OK
+        check(host, n, out, lse, 1 / math.sqrt(128))
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -300,11 +318,14 @@ def test_nothing_to_do(sv):
     check(host, n, out, lse, 1 / 8)
 
 
+@pytest.mark.parametrize("heads,columns", [(4, 0), (4, 1100), (64, 0)])
 @pytest.mark.parametrize("what", ["length", "negative length", "context", "table", "page", "negative page",
                                   "row", "parent", "own parent"])
-def test_bad_data_is_reported(sv, what):
+def test_bad_data_is_reported(sv, what, heads, columns):
     """... and leaves the other requests alone."""
-    host, dev, n, rows = pr.make_round([70, 30, 90], [5, 5, 5], 5, 16, 4, 2, 64, seed=16, tree="random")
+    host, dev, n, rows = pr.make_round([70, 30, 90], [5, 5, 5], 5, 16, heads, 2, 64, seed=16, tree="random")
+    if columns:
+        dev = wide_table(dev, columns)
     first = int(host["row0"][1])
     if what == "length":
         dev["draft_len"][1] = 6
