@@ -25,6 +25,7 @@
 #include "tmap.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 
@@ -133,24 +134,32 @@ __device__ __forceinline__ Item cluster_item(const AttnParams& p, int64_t& first
   return x;
 }
 
-// All there is to check of a call of few requests, by one warp: whether it is bad.
+// All there is to check of a call of at most 32 requests, by one warp: whether it is bad.  A lane looks at
+// a request's sizes, then all of them at everybody's pages and parents.
 __device__ __forceinline__ bool bad_round(const RoundParams& rd) {
   const int lane = threadIdx.x & 31;
-  bool bad = false;
-  for (int32_t r = 0; r < rd.B; ++r) {
-    Request q;
-    if (!round_request(rd, r, q)) bad = true;
-    if (q.n == 0) continue;
-    const int32_t pages = int32_t((int64_t(q.ctx) + q.n + rd.page_size - 1) / rd.page_size);
+  Request q = {};
+  bool bad = lane < rd.B && !round_request(rd, lane, q);
+  const int32_t pages =
+      q.n ? int32_t((int64_t(q.ctx) + q.n + rd.page_size - 1) / rd.page_size) : 0;
 #pragma unroll 8
-    for (int32_t i = lane; i < pages; i += 32) {
+  for (int32_t i0 = 0; i0 < rd.B * rd.max_pages; i0 += 32) {
+    const int32_t r = (i0 + lane) / rd.max_pages, i = i0 + lane - r * rd.max_pages;
+    const int32_t n = __shfl_sync(0xffffffffu, pages, r & 31);
+    if (r < rd.B && i < n) {
       const int32_t g = rd.page_table[r * rd.ld_pages + i];
       bad |= g < 0 || g >= rd.n_pages;
     }
-    if (rd.parents) {
+  }
+  if (rd.parents) {
+    const int32_t rows = rd.max_draft_len + rd.bonus_row;
 #pragma unroll 4
-      for (int32_t i = lane; i < q.n; i += 32) {
-        const int32_t up = rd.parents[q.first + i];
+    for (int32_t i0 = 0; i0 < rd.B * rows; i0 += 32) {
+      const int32_t r = (i0 + lane) / rows, i = i0 + lane - r * rows;
+      const int32_t n = __shfl_sync(0xffffffffu, q.n, r & 31);
+      const int64_t first = __shfl_sync(0xffffffffu, q.first, r & 31);
+      if (r < rd.B && i < n) {
+        const int32_t up = rd.parents[first + i];
         bad |= up < -1 || up >= i;
       }
     }
@@ -877,40 +886,71 @@ sv_status launch_join(const AttnParams& p, int grid, cudaStream_t s) {
                           kJoinThreads, 0, s, p, grid);
 }
 
-// Few items of few tiles: a cluster for each.  They have to be there at once, an SM a CTA; more tiles are
-// worth more SMs than a cluster has; and one warp looks through all the pages.
-constexpr int kShortItems = 16, kShortTiles = 64, kShortPages = 1024;
+// Few items of few tiles: a cluster for each.  They have to be there at once (see clusters_at_once); more
+// tiles are worth more SMs than a cluster has; and one warp looks through all the pages.  A request of 6
+// rows under 32 heads (8 key heads): 9.1 us over 1000 places (14.6 from the list), 11.0 over 4000 (15.7),
+// 15.1 over 8000 (17.7).
+constexpr int kShortItems = 32, kShortTiles = 64, kShortPages = 1024;
 
+struct ShortLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ShortLaunch(int items, cudaStream_t s) {
+    cfg.gridDim = dim3(unsigned(items) * kCluster);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = kAttnSmem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// Clusters that the current device runs at once (asked once per device; 0 if it cannot be asked).
 template <int kD, int kN>
-sv_status launch_short(const AttnMaps& m, const AttnParams& p, int items, cudaStream_t s) {
+int clusters_at_once() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // and one
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    auto* kern = attention_kernel<kD, kN, true>;
+    ShortLaunch l(1, nullptr);
+    l.cfg.numAttrs = 1;
+    int most = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&most, kern, &l.cfg) != cudaSuccess)
+      most = 0;
+    n = most + 1;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
+// Sets `taken` where the call is one for clusters, and makes it.
+template <int kD, int kN>
+sv_status launch_short(const AttnMaps& m, const AttnParams& p, int items, cudaStream_t s, bool& taken) {
   auto* kern = attention_kernel<kD, kN, true>;
   static_assert(kN * (kD + 2) * 4 <= AttnShared<kD, kN>::kStages() * AttnShared<kD, kN>::kSlot,
                 "a part fits the ring");
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
-      cudaSuccess)
-    return SV_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(items) * kCluster);
-  cfg.blockDim = dim3(kAttnThreads);
-  cfg.dynamicSmemBytes = kAttnSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return launch_status(cudaLaunchKernelEx(&cfg, kern, m.q, m.k, m.v, p));
+  if (items > clusters_at_once<kD, kN>()) return SV_OK;
+  taken = true;
+  ShortLaunch l(items, s);
+  return launch_status(cudaLaunchKernelEx(&l.cfg, kern, m.q, m.k, m.v, p));
 }
 
 template <int kD>
-sv_status launch_short(int32_t n, const AttnMaps& m, const AttnParams& p, int items,
-                       cudaStream_t s) {
-  return n == 16   ? launch_short<kD, 16>(m, p, items, s)
-         : n == 32 ? launch_short<kD, 32>(m, p, items, s)
-                   : launch_short<kD, 64>(m, p, items, s);
+sv_status launch_short(int32_t n, const AttnMaps& m, const AttnParams& p, int items, cudaStream_t s,
+                       bool& taken) {
+  return n == 16   ? launch_short<kD, 16>(m, p, items, s, taken)
+         : n == 32 ? launch_short<kD, 32>(m, p, items, s, taken)
+                   : launch_short<kD, 64>(m, p, items, s, taken);
 }
 
 template <int kD, int kN>
@@ -1019,7 +1059,12 @@ extern "C" sv_status spec_tree_attention(
   // over up to 4096: 0 198 us, 2 182, 4 176, 6 171)
   p.item_cost = n == kWide ? 6 : 4;
   p.big = most + p.item_cost * items >= double(1 << 22);  // (times 192 CTAs it fits 32 bits)
-  if (n <= 64 && items <= kShortItems && key_tiles <= kShortTiles && int64_t(B) * max_pages <= kShortPages)
-    return D == 64 ? launch_short<64>(n, m, p, int(items), s) : launch_short<128>(n, m, p, int(items), s);
+  if (n <= 64 && B <= 32 && items <= kShortItems && key_tiles <= kShortTiles && max_pages > 0 &&
+      int64_t(B) * max_pages <= kShortPages) {
+    bool taken = false;
+    const sv_status st = D == 64 ? launch_short<64>(n, m, p, int(items), s, taken)
+                                 : launch_short<128>(n, m, p, int(items), s, taken);
+    if (taken) return st;
+  }
   return D == 64 ? launch<64>(n, m, p, grid, s) : launch<128>(n, m, p, grid, s);
 }
