@@ -129,19 +129,20 @@ def test_append_in_place_and_strided(sv):
     assert torch.equal(kc, k2) and torch.equal(vc, v2)
 
 
+@pytest.mark.parametrize("gmax", [5, 100])  # one cluster of CTAs; many CTAs
 @pytest.mark.parametrize("what", ["length", "context", "table", "page", "row", "parent", "position"])
-def test_append_bad_data(sv, what):
-    host, dev, n, rows = pr.make_round([70, 30, 90], [5, 5, 5], 5, 16, 4, 2, 64, seed=22, tree="random")
+def test_append_bad_data(sv, what, gmax):
+    host, dev, n, rows = pr.make_round([70, 90], [5, 5], gmax, 16, 4, 2, 64, seed=22, tree="random")
     qkv = torch.randn((rows, 8, 64), device="cuda")
     cs = torch.randn((100 if what != "position" else 92, 64), device="cuda")
     if what == "length":
-        dev["draft_len"][1] = 6
+        dev["draft_len"][1] = gmax + 1
     elif what == "context":
         dev["ctx_len"][1] = -3
     elif what == "table":
         dev["ctx_len"][1] = 2**31 - 2
     elif what == "page":
-        dev["page_table"][1, 2] = -1
+        dev["page_table"][1, 5] = -1
     elif what == "row":
         dev["row0"][1] = -1
     elif what == "parent":
@@ -151,7 +152,7 @@ def test_append_bad_data(sv, what):
     st = status()
     kc, vc = dev["k_cache"].clone(), dev["v_cache"].clone()
     sv.spec_cache_append(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], kc, vc, dev["page_table"], dev["ctx_len"],
-                         dev["row0"], dev["draft_len"], 5, cos_sin=cs, parents=dev["parents"], status=st)
+                         dev["row0"], dev["draft_len"], gmax, cos_sin=cs, parents=dev["parents"], status=st)
     assert int(st) == sv.SV_ERR_BAD_INPUT
     # the places of the first request are right all the same
     for i in range(6):
@@ -164,7 +165,8 @@ def test_append_bad_data(sv, what):
 @pytest.mark.parametrize("B,gmax,tokens,tree", [(1, 0, 2, None), (1, 15, 2, "random"), (5, 5, 2, None),
                                                 (130, 63, 3, "random"), (40, 127, 2, "random"),
                                                 (33, 127, 1, None), (9, 40, 1, "star"),
-                                                (17, 31, 2, "forest"), (64, 1, 2, "random")])
+                                                (17, 31, 2, "forest"), (64, 1, 2, "random"), (256, 7, 2, "random"),
+                                                (300, 9, 2, "random")])
 @pytest.mark.parametrize("ragged", [False, True])
 def test_accept(sv, B, gmax, tokens, tree, ragged):
     g = torch.Generator().manual_seed(B + gmax)
@@ -194,19 +196,20 @@ def test_accept(sv, B, gmax, tokens, tree, ragged):
         assert got["correction"][r] == emitted[-1]
 
 
+@pytest.mark.parametrize("B", [3, 40, 400])
 @pytest.mark.parametrize("what", ["length", "row", "draft row", "parent", "sample"])
-def test_accept_bad_data(sv, what):
+def test_accept_bad_data(sv, what, B):
     i32 = dict(dtype=torch.int32, device="cuda")
-    sampled, tok = torch.zeros(12, **i32), torch.zeros(9, **i32)
-    parents = torch.tensor([-1, 0, 1, 2] * 3, **i32)
-    row0, drow0 = torch.tensor([0, 4, 8], device="cuda"), torch.tensor([0, 3, 6], device="cuda")
-    n = torch.full((3,), 3, **i32)
+    sampled, tok = torch.zeros(4 * B, **i32), torch.zeros(3 * B, **i32)
+    parents = torch.tensor([-1, 0, 1, 2] * B, **i32)
+    row0, drow0 = torch.arange(B, device="cuda") * 4, torch.arange(B, device="cuda") * 3
+    n = torch.full((B,), 3, **i32)
     if what == "length":
         n[1] = 4
     elif what == "row":
-        row0[1] = 9
+        row0[1] = 4 * B - 3
     elif what == "draft row":
-        drow0[1] = 7
+        drow0[1] = 3 * B - 2
     elif what == "parent":
         parents[5] = 1
     else:
@@ -214,7 +217,7 @@ def test_accept_bad_data(sv, what):
     st = status()
     out = sv.spec_tree_accept(sampled, tok, parents, row0, drow0, n, 3, status=st)
     assert int(st) == sv.SV_ERR_BAD_INPUT
-    assert out["path"][0].tolist() == [1, 2, 3] and out["path"][2].tolist() == [1, 2, 3]
+    assert (out["path"][torch.arange(B, device="cuda") != 1] == torch.tensor([1, 2, 3], **i32)).all()
 
 
 # ---- keep --------------------------------------------------------------------------------------
@@ -263,8 +266,9 @@ def test_keep_one_layer_strided_and_chain(sv):
         assert torch.equal(both[:, c].cpu(), x[0])
 
 
+@pytest.mark.parametrize("layers", [1, 5])
 @pytest.mark.parametrize("what", ["accepted", "order", "zero", "context", "page", "far"])
-def test_keep_bad_data(sv, what):
+def test_keep_bad_data(sv, what, layers):
     host, dev, n, _ = pr.make_round([20, 30, 40], [6] * 3, 6, 16, 1, 2, 64, seed=32, nan_elsewhere=False)
     accepted = torch.tensor([2, 2, 2], dtype=torch.int32, device="cuda")
     path = torch.tensor([[2, 4, 5]] * 3, dtype=torch.int32, device="cuda")
@@ -283,12 +287,12 @@ def test_keep_bad_data(sv, what):
     else:
         path[1, 1] = 2**31 - 1
     st = status()
-    k, v = dev["k_cache"].clone(), dev["v_cache"].clone()
+    k, v = (dev[c][None].repeat(layers, 1, 1, 1, 1) for c in ("k_cache", "v_cache"))
     sv.spec_cache_keep(k, v, dev["page_table"], dev["ctx_len"], accepted, path, status=st)
     assert int(st) == sv.SV_ERR_BAD_INPUT
-    want = host["k_cache"][None].clone()  # the others' entries moved, the bad request's did not
+    want = host["k_cache"][None].repeat(layers, 1, 1, 1, 1)
     pr.keep(want, host["page_table"], [20, 30, 40], [2, 0, 2], path.tolist())
-    assert torch.equal(k.cpu(), want[0])
+    assert torch.equal(k.cpu(), want)  # the others' entries moved, the bad request's did not
 
 
 # ---- a round -----------------------------------------------------------------------------------
