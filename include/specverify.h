@@ -435,6 +435,7 @@ sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_scales,
  * Lengths out of range (draft_len outside [0, max_draft_len], rows outside the n_rows, places past
  * the table), pages outside [0, n_pages), parents outside [-1, i): SV_ERR_BAD_INPUT in status.  No
  * call reads or writes outside the arrays it is given for them.
+ * Different requests' rows must be different rows; contexts may share pages.
  * Rows, heads, tokens and pages are 16-byte aligned (bases and strides).
  * ------------------------------------------------------------------------------------------- */
 

@@ -902,6 +902,8 @@ def spec_cache_append(q, k, v, k_cache, v_cache, page_table, ctx_len, row0, draf
         if code > 0:
             raise SpecVerifyError(code, "spec_cache_append")
     dev = _device_of(k, "k")
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q, k and v must be bfloat16 or float32, got {k.dtype}")
     dt = _dtype_code(k)
     kp, ldk, hk = _heads(k, "k", k.dtype, dev)
     rows, n_kv, D = k.shape

@@ -374,7 +374,8 @@ extern "C" sv_status spec_cache_append(
   if (parents && max_draft_len + int64_t(bonus_row) > SV_MAX_TREE_ROWS) return SV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (B == 0 || max_draft_len + bonus_row == 0 || n_rows == 0) return reset_status(status, s);
-  if (!k || !v || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len || !page_table ||
+  if (!k || !v || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len ||
+      (!page_table && max_pages > 0) ||
       (n_heads > 0 && (!q || !q_out)))
     return SV_ERR_INVALID;
   if (D % 16 || D > 256 || rot % 16) return SV_ERR_UNSUPPORTED;
@@ -456,7 +457,7 @@ extern "C" sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t*
   if (new_len && new_len == ctx_len) return SV_ERR_INVALID;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (B == 0) return reset_status(status, s);
-  if (!accepted_len || !ctx_len || !page_table) return SV_ERR_INVALID;
+  if (!accepted_len || !ctx_len || (!page_table && max_pages > 0)) return SV_ERR_INVALID;
   if (path && n_layers > 0 && (!k_cache || !v_cache)) return SV_ERR_INVALID;
   if (D % 8 || D > (1 << 16) || n_kv_heads > (1 << 12)) return SV_ERR_UNSUPPORTED;
   if (path && (!aligned_bf16(k_cache, page_stride, token_stride, head_stride) ||

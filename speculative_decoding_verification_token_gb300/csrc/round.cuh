@@ -31,11 +31,12 @@ struct Request {
   int32_t ctx;    // places filled before
 };
 
-// Request r's sizes; false if any is out of range: the request is then left alone.
-__device__ __forceinline__ bool round_request(const RoundParams& p, int32_t r, Request& q) {
-  const int32_t drafts = p.draft_len[r];
-  q.ctx = p.ctx_len[r];
-  q.first = p.row0[r];
+// A request's sizes from its draft length, context and first row; false if any is out of range: the request
+// is then left alone.
+__device__ __forceinline__ bool round_request(const RoundParams& p, int32_t drafts, int32_t ctx,
+                                              int64_t first, Request& q) {
+  q.ctx = ctx;
+  q.first = first;
   q.n = drafts + p.bonus_row;
   const bool ok = drafts >= 0 && drafts <= p.max_draft_len && q.ctx >= 0 && q.first >= 0 &&
                   q.first <= p.n_rows && q.n <= p.n_rows - q.first &&
@@ -43,6 +44,10 @@ __device__ __forceinline__ bool round_request(const RoundParams& p, int32_t r, R
                       min(int64_t(p.max_pages) * p.page_size, int64_t(INT32_MAX));
   if (!ok) q.n = 0;
   return ok;
+}
+
+__device__ __forceinline__ bool round_request(const RoundParams& p, int32_t r, Request& q) {
+  return round_request(p, p.draft_len[r], p.ctx_len[r], p.row0[r], q);
 }
 
 // Page of place `at`; -1 where the table names none.

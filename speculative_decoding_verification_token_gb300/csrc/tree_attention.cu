@@ -1012,7 +1012,8 @@ extern "C" sv_status spec_tree_attention(
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (B == 0 || max_draft_len + int64_t(bonus_row) == 0 || n_rows == 0)
     return reset_status(status, s);
-  if (!q || !out || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len || !page_table ||
+  if (!q || !out || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len ||
+      (!page_table && max_pages > 0) ||
       !workspace || n_pages < 1)
     return SV_ERR_INVALID;
   if (!aligned_bf16(q, ldq, q_head, 0) || !aligned_bf16(out, ldo, o_head, 0) ||

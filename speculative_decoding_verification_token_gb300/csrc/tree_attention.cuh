@@ -91,30 +91,45 @@ __device__ __forceinline__ int64_t warp_add(int64_t x, int32_t steps) {
 }
 
 // One warp: this CTA's run of the list, from the requests in chunks of 32, a lane each.  T holds the
-// call's cost times the number of CTAs.
-template <typename T>
+// call's cost times the number of CTAs; the loads of kU chunks are in flight together.
+template <typename T, int kU>
 __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
   const int lane = threadIdx.x & 31;
   const int32_t steps = min(p.rd.B, 32);
   Span span = {};
-  Request q = {};
-  T tiles = 0, items = 0;  // of the lane's request
-  auto chunk = [&](int32_t r0, bool tell) {
-    const int32_t r = r0 + lane;
-    tiles = items = 0;
-    q.n = 0;
-    if (r < p.rd.B) {
-      if (!round_request(p.rd, r, q) && tell) report(err, SV_ERR_BAD_INPUT);
-      int32_t n;
-      tiles = T(tiles_of_head(q, p.tokens, n)) * p.n_kv;
-      items = T(n) * p.n_kv;
+  Request q[kU];
+  T tiles[kU], items[kU];  // of the lane's requests
+  auto chunks = [&](int32_t r0, bool tell) {
+    int32_t drafts[kU], ctx[kU];
+    int64_t first[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int32_t r = r0 + 32 * u + lane;
+      if (r < p.rd.B) drafts[u] = p.rd.draft_len[r], ctx[u] = p.rd.ctx_len[r], first[u] = p.rd.row0[r];
     }
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      tiles[u] = items[u] = 0;
+      q[u] = {};
+      if (r0 + 32 * u + lane < p.rd.B) {
+        bad |= !round_request(p.rd, drafts[u], ctx[u], first[u], q[u]);
+        int32_t n;
+        tiles[u] = T(tiles_of_head(q[u], p.tokens, n)) * p.n_kv;
+        items[u] = T(n) * p.n_kv;
+      }
+    }
+    if (bad && tell) report(err, SV_ERR_BAD_INPUT);
   };
   T all_tiles = 0, all_items = 0;
-  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
-    chunk(r0, blockIdx.x == 0);
-    all_tiles += warp_add(tiles, steps);
-    all_items += warp_add(items, steps);
+  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32 * kU) {
+    chunks(r0, blockIdx.x == 0);
+#pragma unroll
+    for (int u = 1; u < kU; ++u) tiles[0] += tiles[u], items[0] += items[u];
+    all_tiles += warp_add(tiles[0], steps);
+    all_items += warp_add(items[0], steps);
+#pragma unroll
+    for (int u = 1; u < kU; ++u) tiles[0] -= tiles[u], items[0] -= items[u];
   }
   // (with few tiles for each CTA their number alone counts)
   span.cost = all_tiles > 2 * T(gridDim.x) ? p.item_cost : 0;
@@ -123,26 +138,30 @@ __device__ __forceinline__ Span find_span(const AttnParams& p, int32_t* err) {
   span.total = total, span.begin = begin, span.end = end;
   if (begin == end) return span;
   T before = 0;
-  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32) {
-    if (p.rd.B > 32) chunk(r0, false);
-    const T mine = tiles + span.cost * items;
-    T upto = mine;
-    for (int o = 1; o < steps; o <<= 1) {
-      const T x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+  for (int32_t r0 = 0; r0 < p.rd.B; r0 += 32 * kU) {
+    if (p.rd.B > 32 * kU) chunks(r0, false);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (r0 + 32 * u >= p.rd.B) break;
+      const T mine = tiles[u] + span.cost * items[u];
+      T upto = mine;
+      for (int o = 1; o < steps; o <<= 1) {
+        const T x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const T a = before + upto - mine;
+      const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= begin && begin < a + mine);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        span.before = __shfl_sync(0xffffffffu, a, l);
+        span.r = r0 + 32 * u + l;
+        span.q.first = __shfl_sync(0xffffffffu, q[u].first, l);
+        span.q.n = __shfl_sync(0xffffffffu, q[u].n, l);
+        span.q.ctx = __shfl_sync(0xffffffffu, q[u].ctx, l);
+        return span;
+      }
+      before += __shfl_sync(0xffffffffu, upto, steps - 1);
     }
-    const T a = before + upto - mine;
-    const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && a <= begin && begin < a + mine);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      span.before = __shfl_sync(0xffffffffu, a, l);
-      span.r = r0 + l;
-      span.q.first = __shfl_sync(0xffffffffu, q.first, l);
-      span.q.n = __shfl_sync(0xffffffffu, q.n, l);
-      span.q.ctx = __shfl_sync(0xffffffffu, q.ctx, l);
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, upto, steps - 1);
   }
   return span;
 }
@@ -345,7 +364,9 @@ __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, It
                                               uint64_t* item_full, uint64_t* item_empty,
                                               int32_t* err, After after) {
   const int lane = threadIdx.x & 31;
-  const Span span = p.big ? find_span<int64_t>(p, err) : find_span<int32_t>(p, err);
+  const Span span = p.big          ? find_span<int64_t, 4>(p, err)
+                    : p.rd.B > 32 ? find_span<int32_t, 4>(p, err)
+                                  : find_span<int32_t, 1>(p, err);
   Cut cut = {};
   int32_t cut_columns = 0;
   bool ok = true;

@@ -21,6 +21,7 @@ namespace {
 // lanes write a row's 64 bytes (16 bytes of 32 rows at once take four times as long).  80 bytes apart the
 // rows' pieces lie in different banks.
 constexpr int kStageRow = 80;
+constexpr int kBadWords = kWide / 32;  // (an item has up to 256 rows of a chain, with a head a key head)
 
 template <int kD>
 struct WideShared {
@@ -32,7 +33,7 @@ struct WideShared {
     Item item[2];
     alignas(16) uint32_t above[2][SV_MAX_TREE_ROWS][4];
     int32_t up[SV_MAX_TREE_ROWS];
-    uint32_t bad[2][2][SV_MAX_TREE_ROWS / 32];  // rows whose values are not all finite, by who found it
+    uint32_t bad[2][2][kBadWords];  // an item's rows whose values are not all finite, by who found it
     float m[kTile], l[kTile];                   // of stream 1, for joining
     alignas(16) uint8_t stage[kSoftWarps][32 * kStageRow];  // results on their way out
     uint32_t tmem;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       auto token = [&] { return (twin ? 0 : s * p.tile_tokens) + row / p.group; };
       auto column_of = [&] { return (twin ? 0 : s * tile_rows) + row; };
       auto is_mine = [&] { return row < tile_rows && column_of() < x.columns; };
-      if (row < SV_MAX_TREE_ROWS / 32) sm.bad[b][s][row] = 0;
+      if (row < kBadWords) sm.bad[b][s][row] = 0;
       soft_sync(s);
       float m = kM2Empty, l = 0.f;
       bool table = !p.rd.parents, fresh = true;
@@ -568,11 +569,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // is on its way out
         bool any_bad = false;
 #pragma unroll
-        for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w)
+        for (int w = 0; w < kBadWords; ++w)
           any_bad |= (sm.bad[b][0][w] | sm.bad[b][1][w]) != 0;
         auto add_bad = [&](auto* to, int n, int d0) {
 #pragma unroll 1
-          for (int32_t j = 0; j < SV_MAX_TREE_ROWS; ++j) {
+          for (int32_t j = 0; j < 32 * kBadWords; ++j) {
             if (!((sm.bad[b][0][j >> 5] | sm.bad[b][1][j >> 5]) >> (j & 31) & 1u)) continue;
             if (!mine || !(p.rd.parents ? sm.above[b][x.tok0 + i_item][j >> 5] >> (j & 31) & 1u
                                         : j <= i_item))

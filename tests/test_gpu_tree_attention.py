@@ -207,6 +207,55 @@ def test_values_that_are_not_finite_reach_who_sees_them(sv, bad, tree, heads, D)
             assert off.all(), (j, i)
 
 
+@pytest.mark.parametrize("heads,kv,rows", [(2, 2, 230), (4, 1, 150), (3, 3, 100)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_of_long_chains_that_are_not_finite(sv, bad, heads, kv, rows):
+    """... in rows far into a prompt, for the rows before them and those behind."""
+    D, ctx = 128, 40
+    host, dev, n, _ = pr.make_round([ctx, 300], [rows, 2], rows, 16, heads, kv, D, seed=18, bonus=0, q_scale=0.1)
+    clean = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in host.items()}
+    spots = [rows - 5, rows // 2 + 7, 3]
+    for e, j in enumerate(spots):
+        host["v_cache"][pr.place(host["page_table"], 0, ctx + j, 16)][0, 60 + 10 * e] = bad
+    dev["v_cache"] = host["v_cache"].cuda()
+    out, lse, st = run(sv, dev)
+    assert st == sv.SV_OK
+    want = pr.attention(clean, n, 1 / math.sqrt(D))
+    first = int(host["row0"][0])
+    for row, (o, z, tol, tol_z) in want.items():
+        off = (out[row].double() - o).abs() <= tol
+        assert ((lse[row].double() - z).abs() <= tol_z).all()
+        for e, j in enumerate(spots):
+            if first <= row < first + rows and row - first >= j:
+                x = out[row, :heads // kv, 60 + 10 * e].float()
+                assert (x != x).all() if bad != bad else (x == bad).all(), (row - first, j)
+                off[:heads // kv, 60 + 10 * e] = True
+        assert off.all(), row - first
+
+
+@pytest.mark.parametrize("B", [33, 130, 700])
+@pytest.mark.parametrize("heads", [2, 16])
+def test_many_requests(sv, B, heads):
+    """More requests than a warp has lanes, some without rows, some bad."""
+    g = torch.Generator().manual_seed(B)
+    ctx = torch.randint(0, 60, (B,), generator=g).tolist()
+    drafts = torch.randint(0, 9, (B,), generator=g).tolist()
+    drafts[-1] = 3
+    host, dev, n, _ = pr.make_round(ctx, drafts, 8, 16, heads, 1, 64, seed=19, bonus=0, gap=0)
+    out, lse, st = run(sv, dev)
+    assert st == sv.SV_OK
+    check(host, n, out, lse, 1 / 8)
+    bad = [0, B // 2, B - 2]
+    dev["draft_len"][torch.tensor(bad, device="cuda")] = 9
+    for r in bad:
+        n[r] = 0
+    out, lse, st = run(sv, dev)
+    assert st == sv.SV_ERR_BAD_INPUT
+    want = pr.attention(host, n, 1 / 8)
+    for row, (o, z, tol, tol_z) in want.items():
+        assert ((out[row].double() - o).abs() <= tol).all(), row
+
+
 @pytest.mark.parametrize("kv", [1, 2, 8])
 def test_bad_queries_stay_alone(sv, kv):
     host, dev, n, _ = pr.make_round([200], [5 if kv > 1 else 20], 20, 16, 8, kv, 128, seed=9)
