@@ -230,9 +230,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                      const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using Sh = AttnShared<kD, kN>;
-  constexpr int kW = kN / 2;                // columns of a half
-  constexpr int kC = kW < 32 ? kW : 32;     // columns at a time
-  constexpr int kChunks = kW / kC;
+  constexpr int kC = kN / 2;  // columns of a half
   constexpr int kStages = Sh::kStages();
   constexpr uint32_t kCols = kN <= 16 ? 64 : kN <= 32 ? 128 : kN <= 64 ? 256 : 512;
   static_assert(kStages >= 3, "a ring of three tiles");
@@ -435,12 +433,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // ---- softmax and results -------------------------------------------------------------------------
     const int half = warp >> 2, quad = warp & 3;
     const int row = tid & 127;       // place of a key tile; element of the head
-    const int col0 = half * kW;      // this half's first column
+    const int col0 = half * kC;      // this half's first column
     const uint32_t lanes = tmem + (uint32_t(32 * quad) << 16) + col0;
     float* const minus = sm.minus + col0;
     float* const factor = sm.factor + col0;
     float* const inv = sm.inv + col0;
-    float l[kW];
+    float l[kC];
     int32_t t = 0;
     bool ok = true;
     for (int32_t it = 0; ok; ++it) {
@@ -448,10 +446,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (soft_any(half, !wait_for(&sm.item_full[b], (it >> 1) & 1, err))) break;
       const Item x = sm.item[b];
       if (x.stop) break;
-      if (row < kW) minus[row] = -kM2Empty;
+      if (row < kC) minus[row] = -kM2Empty;
       if (row < SV_MAX_TREE_ROWS / 32) sm.bad[b][half][row] = 0;
 #pragma unroll
-      for (int c = 0; c < kW; ++c) l[c] = 0.f;
+      for (int c = 0; c < kC; ++c) l[c] = 0.f;
       bool table = false;
       soft_sync(half);
       for (int32_t kt = x.t0; kt < x.t1; ++kt, ++t) {
@@ -460,25 +458,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // (a wait that ran out leaves the loop in all four warps together)
         bool late = !wait_for(&sm.s_full[t & 1], (t >> 1) & 1, err);
         const bool masked = (kt + 1) * int64_t(kTile) > x.base0;
-        uint32_t seen[kChunks];  // bit c: column c of a chunk sees this thread's place
+        uint32_t seen = ~0u;  // bit c: column c of this half sees this thread's place
         if (masked) {
           if (!table) late |= !wait_for(&sm.table_full[b], (it >> 1) & 1, err);
           table = true;
           const int32_t place = kt * kTile + row, j = place - x.base0;
-#pragma unroll
-          for (int ch = 0; ch < kChunks; ++ch) {
-            const int c0 = col0 + ch * kC;
-            seen[ch] = ~0u;
-            if (place >= x.end) {
-              seen[ch] = 0u;
-            } else if (j >= 0) {
-              if (p.rd.parents) {
-                seen[ch] = sm.seen[b][j][c0 >> 5] >> (c0 & 31);
-              } else {  // columns of token j and later ones
-                const int32_t from = j * p.group - c0;
-                seen[ch] = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
-              }
-            }
+          if (place >= x.end) {
+            seen = 0u;
+          } else if (j >= 0 && p.rd.parents) {
+            seen = sm.seen[b][j][col0 >> 5] >> (col0 & 31);
+          } else if (j >= 0) {  // columns of token j and later ones
+            const int32_t from = j * p.group - col0;
+            seen = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
           }
           // each half looks through half of the elements
           const int32_t load = kt + 1 == x.t1 && x.last ? 2 * t + 1 : 2 * t + 2;
@@ -489,15 +480,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             atomicOr(&sm.bad[b][half][j >> 5], 1u << (j & 31));
         }
         tc::fence_after_sync();
-        // does any score pass its column's m by more than the slack?  (A half of up to 32 columns keeps
-        // its scores, a wider one reads them again.)
-        float s[kC], m[kC], top = -INFINITY;
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          broadcast<kC>(minus + ch * kC, m);
-          tmem_load<kC>(s_at + ch * kC, s);
+        // does any score pass its column's m by more than the slack?
+        float s[kC], m[kC], top = kt == x.t0 ? INFINITY : -INFINITY;  // (the first tile's surely do)
+        if (kt > x.t0) {
+          broadcast<kC>(minus, m);
+          tmem_load<kC>(s_at, s);
           scaled<kC>(s, p.scale2, m);
-          if (masked) hide<kC>(s, seen[ch]);
+          if (masked) hide<kC>(s, seen);
 #pragma unroll
           for (int c = 0; c < kC; c += 2) top = max3(top, s[c], s[c + 1]);
         }
@@ -507,17 +496,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ok = false;
             break;
           }
+          tmem_load<kC>(s_at, s);
 #pragma unroll
-          for (int ch = 0; ch < kChunks; ++ch) {
-            tmem_load<kC>(s_at + ch * kC, s);
-#pragma unroll
-            for (int c = 0; c < kC; ++c) s[c] *= p.scale2;
-            if (masked) hide<kC>(s, seen[ch]);
-            const float most = over_lanes<kC>(s, [](float a, float b) { return fmaxf(a, b); });
-            if (lane < kC) sm.part[quad][col0 + ch * kC + lane] = most;
-          }
+          for (int c = 0; c < kC; ++c) s[c] *= p.scale2;
+          if (masked) hide<kC>(s, seen);
+          const float most = over_lanes<kC>(s, [](float a, float b) { return fmaxf(a, b); });
+          if (lane < kC) sm.part[quad][col0 + lane] = most;
           soft_sync(half);
-          if (row < kW) {
+          if (row < kC) {
             const int c = col0 + row;
             const float old = -minus[row];
             const float most = fmaxf(fmaxf(sm.part[0][c], sm.part[1][c]),
@@ -534,16 +520,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             free = true;
             tc::fence_after_sync();
+            broadcast<kC>(factor, m);
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) {
-              broadcast<kC>(factor + ch * kC, m);
+            for (int c = 0; c < kC; ++c) l[c] *= m[c];
+            tmem_load<kC>(lanes + 2 * kN, s);
 #pragma unroll
-              for (int c = 0; c < kC; ++c) l[ch * kC + c] *= m[c];
-              tmem_load<kC>(lanes + 2 * kN + ch * kC, s);
-#pragma unroll
-              for (int c = 0; c < kC; ++c) s[c] *= m[c];
-              tmem_store<kC>(lanes + 2 * kN + ch * kC, s);
-            }
+            for (int c = 0; c < kC; ++c) s[c] *= m[c];
+            tmem_store<kC>(lanes + 2 * kN, s);
           }
         }
         if (!free && soft_any(half, !wait_for(&sm.p_free, (t - 1) & 1, err))) {
@@ -552,34 +535,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         // P, rounded to bf16 for the product (half a step of 2^-8 a weight); its sums take what it was
         // before that
+        if (raise) {
+          broadcast<kC>(minus, m);
+          tmem_load<kC>(s_at, s);
+          scaled<kC>(s, p.scale2, m);
+          if (masked) hide<kC>(s, seen);
+        }
 #pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          if (kChunks > 1 || raise) {
-            broadcast<kC>(minus + ch * kC, m);
-            tmem_load<kC>(s_at + ch * kC, s);
-            scaled<kC>(s, p.scale2, m);
-            if (masked) hide<kC>(s, seen[ch]);
+        for (int c = 0; c < kC; ++c) s[c] = fast_exp2(s[c]);
+#pragma unroll
+        for (int c = 0; c < kC; c += 2) {
+          const float2 sum = add2(make_float2(l[c], l[c + 1]), make_float2(s[c], s[c + 1]));
+          l[c] = sum.x, l[c + 1] = sum.y;
+        }
+#pragma unroll
+        for (int c = 0; c < kC; c += 8) {
+          uint4 w;
+          uint32_t* const wp = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(s[c + 2 * e], s[c + 2 * e + 1]);
+            wp[e] = *reinterpret_cast<const uint32_t*>(&two);
           }
-#pragma unroll
-          for (int c = 0; c < kC; ++c) s[c] = fast_exp2(s[c]);
-#pragma unroll
-          for (int c = 0; c < kC; c += 2) {
-            const float2 sum = add2(make_float2(l[ch * kC + c], l[ch * kC + c + 1]),
-                                    make_float2(s[c], s[c + 1]));
-            l[ch * kC + c] = sum.x, l[ch * kC + c + 1] = sum.y;
-          }
-#pragma unroll
-          for (int c = 0; c < kC; c += 8) {
-            uint4 w;
-            uint32_t* const wp = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 two = __floats2bfloat162_rn(s[c + 2 * e], s[c + 2 * e + 1]);
-              wp[e] = *reinterpret_cast<const uint32_t*>(&two);
-            }
-            const int col = col0 + ch * kC + c;
-            *reinterpret_cast<uint4*>(p_at + (col >> 6) * 16384 + tc::sw128(row, (col & 63) >> 3)) = w;
-          }
+          const int col = col0 + c;
+          *reinterpret_cast<uint4*>(p_at + (col >> 6) * 16384 + tc::sw128(row, (col & 63) >> 3)) = w;
         }
         fence_proxy_async();
         tc::fence_before_sync();
@@ -589,11 +568,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!ok) break;
       // the item's denominators (while the last product is on its way), then its sums
       bool late = !table && !wait_for(&sm.table_full[b], (it >> 1) & 1, err);
-#pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch) {
-        const float sum = over_lanes<kC>(l + ch * kC, [](float a, float b) { return a + b; });
-        if (lane < kC) sm.part[quad][col0 + ch * kC + lane] = sum;
-      }
+      const float sum = over_lanes<kC>(l, [](float a, float b) { return a + b; });
+      if (lane < kC) sm.part[quad][col0 + lane] = sum;
       late |= !wait_for(&sm.p_free, (t - 1) & 1, err);
       if (soft_any(half, late)) {
         ok = false;
@@ -605,7 +581,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                  : reinterpret_cast<float*>(p.ws + wl.parts) +
                                        (2 * int64_t(blockIdx.x) + x.begins) * wl.part_floats;
       if (kShort && tid == 0) sm.had = 1;
-      if (row < kW && col0 + row < x.columns) {
+      if (row < kC && col0 + row < x.columns) {
         const int c = col0 + row;
         const float sum = (sm.part[0][c] + sm.part[1][c]) + (sm.part[2][c] + sm.part[3][c]);
         if (x.whole) {
@@ -625,51 +601,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
       for (int w = 0; w < SV_MAX_TREE_ROWS / 32; ++w)
         any_bad |= (sm.bad[b][0][w] | sm.bad[b][1][w]) != 0;
-      if (32 * quad < kD) {
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          const int c0 = col0 + ch * kC;
-          if (c0 >= x.columns) break;
-          float s[kC], f[kC];
-          tmem_load<kC>(lanes + 2 * kN + ch * kC, s);
-          if (any_bad) {  // values that were left out of the product for not being finite
+      if (32 * quad < kD && col0 < x.columns) {
+        float s[kC], f[kC];
+        tmem_load<kC>(lanes + 2 * kN, s);
+        if (any_bad) {  // values that were left out of the product for not being finite
 #pragma unroll 1
-            for (int32_t j = 0; j < SV_MAX_TREE_ROWS; ++j) {
-              if (!((sm.bad[b][0][j >> 5] | sm.bad[b][1][j >> 5]) >> (j & 31) & 1u)) continue;
-              const float v = value_at(p, x, j, row);
-              if (isfinite(v)) continue;
-              const uint32_t sees = p.rd.parents ? sm.seen[b][j][c0 >> 5] >> (c0 & 31)
-                                    : j * p.group <= c0 ? ~0u
-                                    : j * p.group >= c0 + 32 ? 0u
-                                                             : ~0u << (j * p.group - c0);
-#pragma unroll
-              for (int c = 0; c < kC; ++c)
-                if (sees >> c & 1u) s[c] += v;
-            }
-          }
-          if (x.whole) {
-            // two columns at once: an even lane takes elements (d, d + 1) of one, an odd lane (d - 1,
-            // d) of the next
-            const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
-            broadcast<kC>(inv + ch * kC, f);
-            __nv_bfloat16* to[kC / 2];
-#pragma unroll
-            for (int c = 0; c < kC; c += 2)
-              to[c / 2] = p.out + sm.col_off[b][c0 + c + (lane & 1)] + (row & ~1);
-#pragma unroll
-            for (int c = 0; c < kC; c += 2) {
-              const __nv_bfloat162 two = __floats2bfloat162_rn(s[c] * f[c], s[c + 1] * f[c + 1]);
-              const uint32_t mine = *reinterpret_cast<const uint32_t*>(&two);
-              const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-              if (c0 + c + (lane & 1) < x.columns)
-                *reinterpret_cast<uint32_t*>(to[c / 2]) = __byte_perm(mine, other, pick);
-            }
-          } else {
-            float* const to = part + c0 * kD + row;
+          for (int32_t j = 0; j < SV_MAX_TREE_ROWS; ++j) {
+            if (!((sm.bad[b][0][j >> 5] | sm.bad[b][1][j >> 5]) >> (j & 31) & 1u)) continue;
+            const float v = value_at(p, x, j, row);
+            if (isfinite(v)) continue;
+            const uint32_t sees = p.rd.parents ? sm.seen[b][j][col0 >> 5] >> (col0 & 31)
+                                  : j * p.group <= col0 ? ~0u
+                                  : j * p.group >= col0 + 32 ? 0u
+                                                           : ~0u << (j * p.group - col0);
 #pragma unroll
             for (int c = 0; c < kC; ++c)
-              if (c0 + c < x.columns) to[c * kD] = s[c];
+              if (sees >> c & 1u) s[c] += v;
           }
+        }
+        if (x.whole) {
+          // two columns at once: an even lane takes elements (d, d + 1) of one, an odd lane (d - 1,
+          // d) of the next
+          const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
+          broadcast<kC>(inv, f);
+          __nv_bfloat16* to[kC / 2];
+#pragma unroll
+          for (int c = 0; c < kC; c += 2)
+            to[c / 2] = p.out + sm.col_off[b][col0 + c + (lane & 1)] + (row & ~1);
+#pragma unroll
+          for (int c = 0; c < kC; c += 2) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(s[c] * f[c], s[c + 1] * f[c + 1]);
+            const uint32_t mine = *reinterpret_cast<const uint32_t*>(&two);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+            if (col0 + c + (lane & 1) < x.columns)
+              *reinterpret_cast<uint32_t*>(to[c / 2]) = __byte_perm(mine, other, pick);
+          }
+        } else {
+          float* const to = part + col0 * kD + row;
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            if (col0 + c < x.columns) to[c * kD] = s[c];
         }
       }
       tc::fence_before_sync();
@@ -1013,8 +984,7 @@ extern "C" sv_status spec_tree_attention(
   if (B == 0 || max_draft_len + int64_t(bonus_row) == 0 || n_rows == 0)
     return reset_status(status, s);
   if (!q || !out || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len ||
-      (!page_table && max_pages > 0) ||
-      !workspace || n_pages < 1)
+      (!page_table && max_pages > 0) || !workspace || n_pages < 1)
     return SV_ERR_INVALID;
   if (!aligned_bf16(q, ldq, q_head, 0) || !aligned_bf16(out, ldo, o_head, 0) ||
       !aligned_bf16(k_cache, page_stride, token_stride, head_stride) || !aligned16(v_cache) ||
