@@ -13,7 +13,7 @@
 //              (P then reaches 2^8, in 16 bits as exact as 1), so that nearly every tile costs no
 //              reduction over the places; the sums of P stay with the places and are added over them at
 //              the end;
-//   warp 8     TMA loads: an item's queries, then K and V, page by page, into a ring;
+//   warps 8, 11  TMA loads: an item's queries, then K and V, page by page, into a ring;
 //   warp 9     tcgen05.mma: S of a tile ahead of the product with V of the one before;
 //   warp 10    the work items: their sizes, and for trees who sees whom.
 // The work -- (request, key head, row tile, key tile) -- is one list, cut into equal runs for a
@@ -245,12 +245,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.full[s], 2);  // either loading warp's part
       mbar_init(&sm.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.item_full[b], 1);
-      mbar_init(&sm.item_empty[b], 4);  // the loads, the products with Q, the softmax's halves
+      mbar_init(&sm.item_empty[b], 5);  // the loads, the products with Q, the softmax's halves
       mbar_init(&sm.q_full[b], 1);
       mbar_init(&sm.table_full[b], 1);
       mbar_init(&sm.s_full[b], 1);
@@ -309,9 +309,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                          sm.item_full, sm.item_empty, err, details);
       if (lane == 0) sm.cut_columns = columns;
     }
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kLoadWarp || warp == kLoadWarp2) {
     // ---- the loads -----------------------------------------------------------------------------------
     const uint64_t once = tc::policy_evict_first();
+    const int part = warp == kLoadWarp2;
     int32_t slot = 0, filled = 0, items = 0;
     uint32_t phase = 1;
     // a tile's boxes, one a lane: its page and first place in it
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     auto load = [&](const CUtensorMap* map, int32_t pg, int32_t fr, int32_t n, int32_t hd) {
       if (!wait_for_warp(&sm.empty[slot], phase, err)) return false;
-      load_tile<kD>(p, ring + slot * Sh::kSlot, map, pg, fr, n, hd, &sm.full[slot], once);
+      load_tile<kD, 2>(p, ring + slot * Sh::kSlot, map, part, pg, fr, n, hd, &sm.full[slot], once);
       filled = max(filled, slot + 1);
       if (++slot == kStages) {
         slot = 0;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (!wait_for_warp(&sm.item_full[b], (it >> 1) & 1, err)) break;
       const Item x = sm.item[b];
       if (x.stop) break;
-      if (elect()) {
+      if (part == 0 && elect()) {
         // (rows behind the request's last, and columns behind those, hold anything: nobody reads them)
         mbar_expect_tx(&sm.q_full[b], uint32_t(p.tile_tokens * p.group) * kD * 2);
 #pragma unroll
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       items = it + 1;
       for (int32_t t = x.t0; t < x.t1 && ok; ++t) {
         int32_t page, from;
-        const int32_t boxes = tile_boxes(p, x, t, page, from, err);
+        const int32_t boxes = tile_boxes<kD, 2>(p, x, t, part, page, from, err);
         ok = load(&map_k, page, from, boxes, x.head) &&
              (v_boxes == 0 || load(&map_v, v_page, v_from, v_boxes, v_head));
         v_page = page, v_from = from, v_boxes = boxes, v_head = x.head;
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
   if constexpr (kShort) {
     // CTA 0 looks at all there is to check, and the status is its own; what ran out of time says so later
-    if (warp == kItemWarp + 1 && blockIdx.x == 0 && p.status) {
+    if (warp == kItemWarp && blockIdx.x == 0 && p.status) {
       const bool bad = bad_round(p.rd);
       if (lane == 0) *p.status = bad ? SV_ERR_BAD_INPUT : SV_OK;
     }

@@ -11,7 +11,7 @@ namespace attn {
 constexpr int kTile = 128;        // places of a tile
 constexpr int kAttnThreads = 384;
 constexpr int kSoftWarps = 8;     // warps 0-7: two halves of four, a TMEM lane a thread
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10, kLoadWarp2 = 11;
 constexpr uint32_t kAttnSmem = 232448 - 1024;  // dynamic shared memory of a CTA, less what is static
 constexpr int kWide = 256;        // rows of an item of the wide kernel: two tiles of 128
 constexpr int kMaxCtas = 192;     // the workspace's size does not depend on the current device
@@ -493,14 +493,24 @@ __device__ __forceinline__ void build_above(const AttnParams& p, int64_t first, 
   }
 }
 
-// The TMA boxes of key tile t, one a lane: page and first place in it.  Returns how many.
-__device__ __forceinline__ int32_t tile_boxes(const AttnParams& p, const Item& x, int32_t t,
-                                              int32_t& page, int32_t& from, int32_t* err) {
+// The boxes of a tile, one a lane, are loaded by kLoaders warps: of two, each takes 64 of the 128 elements, or
+// every other box of 64.  One warp's issue is what bounds small pages -- 256 requests of one token over up
+// to 4096 places in pages of 16: 449 us by one warp, 360 by two.
+template <int kD, int kLoaders>
+__device__ __forceinline__ int box_of_lane(int part) {
   const int lane = threadIdx.x & 31;
+  return kLoaders == 1 || kD == 128 ? lane : 2 * lane + part;
+}
+
+// The TMA boxes of key tile t, one a lane: page and first place in it.  Returns how many.
+template <int kD, int kLoaders>
+__device__ __forceinline__ int32_t tile_boxes(const AttnParams& p, const Item& x, int32_t t,
+                                              int part, int32_t& page, int32_t& from, int32_t* err) {
+  const int box = box_of_lane<kD, kLoaders>(part);
   const int32_t boxes = (min(kTile, x.end - t * kTile) + p.box_rows - 1) / p.box_rows;
-  const int32_t place = t * kTile + lane * p.box_rows;
+  const int32_t place = t * kTile + box * p.box_rows;
   page = 0;
-  if (lane < boxes) {
+  if (box < boxes) {
     page = round_page(p.rd, x.r, place);
     if (page < 0) {
       report(err, SV_ERR_BAD_INPUT);
@@ -511,18 +521,20 @@ __device__ __forceinline__ int32_t tile_boxes(const AttnParams& p, const Item& x
   return boxes;
 }
 
-// A tile of K or V into a ring slot of [D / 64][128 places][64 elements], swizzled; one warp.
-template <int kD>
+// A warp's part of a tile of K or V into a ring slot of [D / 64][128 places][64 elements], swizzled.
+template <int kD, int kLoaders>
 __device__ __forceinline__ void load_tile(const AttnParams& p, uint8_t* dst, const CUtensorMap* map,
-                                          int32_t page, int32_t from, int32_t boxes, int32_t head,
-                                          uint64_t* full, uint64_t once) {
-  const int lane = threadIdx.x & 31;
-  if (elect()) mbar_expect_tx(full, uint32_t(boxes) * p.box_rows * kD * 2);
+                                          int part, int32_t page, int32_t from, int32_t boxes,
+                                          int32_t head, uint64_t* full, uint64_t once) {
+  constexpr int kEach = kLoaders == 2 ? 1 : kD / 64;  // loads of a box
+  const int box = box_of_lane<kD, kLoaders>(part), k0 = kD == 128 ? part : 0;
+  const int32_t mine = kLoaders == 1 || kD == 128 ? boxes : (boxes + 1 - part) / 2;
+  if (elect()) mbar_expect_tx(full, uint32_t(mine) * p.box_rows * kEach * 128);
   __syncwarp();
-  if (lane < boxes) {
+  if (box < boxes) {
 #pragma unroll
-    for (int k = 0; k < kD / 64; ++k) {
-      uint8_t* const to = dst + k * 16384 + lane * p.box_rows * 128;
+    for (int k = k0; k < k0 + kEach; ++k) {
+      uint8_t* const to = dst + k * 16384 + box * p.box_rows * 128;
       // (keys that other row tiles read too stay in L2 like anything else)
       if (p.reread) tma_load_4d(to, map, k * 64, head, from, page, full);
       else tma_load_4d_hint(to, map, k * 64, head, from, page, full, once);

@@ -9,7 +9,7 @@
 //   Two streams share the tensor cores, each with its S, its O and four softmax warps: while one takes
 //   exponentials, the other's products run.  They are two tiles of 128 rows over the same keys, or, where
 //   an item has one tile only, its odd and even key tiles, joined at the end.
-//   warps 0-3, 4-7  softmax and results of stream 0, 1; 8 loads; 9 products; 10 items.
+//   warps 0-3, 4-7  softmax and results of stream 0, 1; 8, 11 loads; 9 products; 10 items.
 // m is raised, and O scaled, only when a row's score passes it by more than 8 (as in tree_attention.cu).
 #include "tree_attention.cuh"
 
@@ -113,7 +113,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&two);
 }
 
-template <int kD>
+template <int kD, int kLoaders>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     wide_kernel(const __grid_constant__ CUtensorMap map_q,
                 const __grid_constant__ CUtensorMap map_k,
@@ -131,12 +131,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.full[s], kLoaders);  // their parts
       mbar_init(&sm.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.item_full[b], 1);
-      mbar_init(&sm.item_empty[b], 4);  // the loads, the products, the streams
+      mbar_init(&sm.item_empty[b], 3 + kLoaders);  // the loads, the products, the streams
       mbar_init(&sm.table_full[b], 1);
       mbar_init(&sm.s_full[b], 1);
       mbar_init(&sm.p_half[b], 4);
@@ -180,17 +180,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (lane == 0) mbar_arrive(&sm.table_full[b]);
         });
     if (lane == 0) sm.cut_columns = columns;
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kLoadWarp || (kLoaders == 2 && warp == kLoadWarp2)) {
     // ---- the loads -----------------------------------------------------------------------------------
     // in the order of use: K of the first tile (two streams of tiles: the first two), then V of a tile
     // and K of the next one that its stream needs
     const uint64_t once = tc::policy_evict_first();
+    const int part = kLoaders == 2 && warp == kLoadWarp2;
     int32_t slot = 0, filled = 0, items = 0;
     uint32_t phase = 1;
     bool ok = true;
     auto load = [&](const CUtensorMap* map, int32_t page, int32_t from, int32_t boxes, int32_t head) {
       if (!wait_for_warp(&sm.empty[slot], phase, err)) return false;
-      load_tile<kD>(p, ring + slot * Sh::kSlot, map, page, from, boxes, head, &sm.full[slot], once);
+      load_tile<kD, kLoaders>(p, ring + slot * Sh::kSlot, map, part, page, from, boxes, head,
+                              &sm.full[slot], once);
       filled = max(filled, slot + 1);
       if (++slot == kStages) {
         slot = 0;
@@ -212,13 +214,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (i >= ahead) page[0] = page[1], from[0] = from[1], boxes[0] = boxes[1];
         if (i < n && ok) {
           int32_t pg, fr;
-          const int32_t bx = tile_boxes(p, x, x.t0 + i, pg, fr, err);
+          const int32_t bx = tile_boxes<kD, kLoaders>(p, x, x.t0 + i, part, pg, fr, err);
           ok = load(&map_k, pg, fr, bx, x.head);
           const bool second = i >= 1 && ahead == 2;
           if (second) page[1] = pg, from[1] = fr, boxes[1] = bx;
           else page[0] = pg, from[0] = fr, boxes[0] = bx;
         }
-        if (i == ahead - 1 && ok) {
+        if (i == ahead - 1 && ok && part == 0) {
           ok = it == 0 || wait_for_warp(&sm.q_empty, (it - 1) & 1, err);
           if (ok && elect()) {
             // (rows behind the request's last hold anything: nobody reads what becomes of them)
@@ -666,9 +668,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid == 0) reinterpret_cast<int32_t*>(p.ws)[blockIdx.x] = sm.err * 512 + sm.cut_columns;
 }
 
-template <int kD>
+template <int kD, int kLoaders>
 sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
-  auto* kern = wide_kernel<kD>;
+  auto* kern = wide_kernel<kD, kLoaders>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
       cudaSuccess)
     return SV_ERR_CUDA;
@@ -677,8 +679,12 @@ sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t 
 
 }  // namespace
 
+// Two loading warps for pages of at most 16 places, where one's issue is the bound; where it is not, the other
+// costs the products 2% (8 x 64 rows, 16000 to 32768 places, one warp and two: 355 and 306 us in pages of
+// 16, 298 and 319 of 32; 8 prompts of 2048 rows: 345 and 308, 301 and 309).
 sv_status launch_wide(int32_t D, const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
-  return D == 64 ? launch<64>(m, p, grid, s) : launch<128>(m, p, grid, s);
+  if (p.box_rows <= 16) return D == 64 ? launch<64, 2>(m, p, grid, s) : launch<128, 2>(m, p, grid, s);
+  return D == 64 ? launch<64, 1>(m, p, grid, s) : launch<128, 1>(m, p, grid, s);
 }
 
 }  // namespace attn
