@@ -34,6 +34,11 @@ namespace {
 
 using namespace attn;
 
+constexpr int kCluster = 8;
+// Items whose descriptions are there at once: of short ones several lie in the ring, and the loads wait for the
+// results of none (256 rows over 100 to 400 places each: 80 us with two, 66 with four).
+constexpr int kItemsLog = 2, kItems = 1 << kItemsLog;
+
 template <int kD, int kN>
 struct AttnShared {
   static constexpr uint32_t kSlot = kTile * kD * 2;
@@ -41,19 +46,20 @@ struct AttnShared {
   static constexpr uint32_t kPBytes = (kN + 63) / 64 * 16384;
   static constexpr int kWords = (kN + 31) / 32;
   struct Small {
-    uint64_t full[16], empty[16], item_full[2], item_empty[2], q_full[2], table_full[2], s_full[2];
+    uint64_t full[16], empty[16], item_full[kItems], item_empty[kItems], table_full[kItems];
+    uint64_t q_full[2], q_empty[2], s_full[2];
     uint64_t p_full, p_free, drain;
-    int64_t col_off[2][kN];  // of a column's output
-    Item item[2];
+    int64_t col_off[kItems][kN];  // of a column's output
+    Item item[kItems];
     alignas(16) float minus[kN];  // -m; read four at a time, as the next two
     alignas(16) float factor[kN];
     alignas(16) float inv[kN];
     float part[4][kN];
-    uint32_t seen[2][SV_MAX_TREE_ROWS][kWords];  // bit c: column c sees the tree's row
+    uint32_t seen[kItems][SV_MAX_TREE_ROWS][kWords];  // bit c: column c sees the tree's row
     uint32_t above[SV_MAX_TREE_ROWS][4];         // rows above a row, itself included
     int32_t up[SV_MAX_TREE_ROWS];
-    uint32_t bad[2][2][SV_MAX_TREE_ROWS / 32];  // an item's rows whose values (of a half of D) are not
-                                                // all finite
+    uint32_t bad[kItems][2][SV_MAX_TREE_ROWS / 32];  // an item's rows whose values (of a half of D) are
+                                                     // not all finite
     uint32_t tmem;
     int32_t err, cut_columns;
     uint32_t had;  // this CTA of a cluster has a part
@@ -90,7 +96,6 @@ __device__ __forceinline__ void build_seen(const AttnParams& p, const Item& x, u
   }
 }
 
-constexpr int kCluster = 8;
 
 // The item of this CTA's cluster and the CTA's tiles of it, by one warp (at most 32 requests).
 __device__ __forceinline__ Item cluster_item(const AttnParams& p, int64_t& first) {
@@ -248,11 +253,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(&sm.full[s], 2);  // either loading warp's part
       mbar_init(&sm.empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kItems; ++b) {
       mbar_init(&sm.item_full[b], 1);
       mbar_init(&sm.item_empty[b], 5);  // the loads, the products with Q, the softmax's halves
-      mbar_init(&sm.q_full[b], 1);
       mbar_init(&sm.table_full[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.q_full[b], 1);
+      mbar_init(&sm.q_empty[b], 1);
       mbar_init(&sm.s_full[b], 1);
     }
     mbar_init(&sm.p_full, kSoftWarps);
@@ -278,7 +286,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const WsLayout wl = ws_layout(gridDim.x, kN, kD);
   if (warp == kItemWarp) {
     // ---- the items ---------------------------------------------------------------------------------
-    int64_t built[2] = {-1, -1};
+    int64_t built[kItems];
+#pragma unroll
+    for (int b = 0; b < kItems; ++b) built[b] = -1;
     auto details = [&](int b, const Item& x, int64_t first) {
       for (int32_t c = lane; c < x.columns; c += 32) {
         const int32_t i = c / p.group, g = c - i * p.group;
@@ -305,8 +315,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       details(0, x, first);
     } else {
-      const int32_t columns = walk_items(p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item,
-                                         sm.item_full, sm.item_empty, err, details);
+      const int32_t columns = walk_items<kItemsLog>(p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item,
+                                                 sm.item_full, sm.item_empty, err, details);
       if (lane == 0) sm.cut_columns = columns;
     }
   } else if (warp == kLoadWarp || warp == kLoadWarp2) {
@@ -329,20 +339,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       return true;
     };
     for (int32_t it = 0; ok; ++it) {
-      const int b = it & 1;
-      if (!wait_for_warp(&sm.item_full[b], (it >> 1) & 1, err)) break;
+      const int b = it & (kItems - 1), qb = it & 1;
+      if (!wait_for_warp(&sm.item_full[b], (it >> kItemsLog) & 1, err)) break;
       const Item x = sm.item[b];
       if (x.stop) break;
+      if (part == 0 && it >= 2 && !wait_for_warp(&sm.q_empty[qb], ((it >> 1) - 1) & 1, err)) break;
       if (part == 0 && elect()) {
         // (rows behind the request's last, and columns behind those, hold anything: nobody reads them)
-        mbar_expect_tx(&sm.q_full[b], uint32_t(p.tile_tokens * p.group) * kD * 2);
+        mbar_expect_tx(&sm.q_full[qb], uint32_t(p.tile_tokens * p.group) * kD * 2);
 #pragma unroll
         for (int k = 0; k < kD / 64; ++k)
-          tc::tma_load_3d(q_at + b * Sh::kQBytes + k * kN * 128, &map_q, k * 64, x.head * p.group,
-                          int32_t(x.first_row), &sm.q_full[b]);
+          tc::tma_load_3d(q_at + qb * Sh::kQBytes + k * kN * 128, &map_q, k * 64, x.head * p.group,
+                          int32_t(x.first_row), &sm.q_full[qb]);
       }
       __syncwarp();
-      items = it + 1;
+      if (part == 0) items = it + 1;
       for (int32_t t = x.t0; t < x.t1 && ok; ++t) {
         int32_t page, from;
         const int32_t boxes = tile_boxes<kD, 2>(p, x, t, part, page, from, err);
@@ -393,11 +404,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       return true;
     };
     for (int32_t it = 0; ok; ++it) {
-      const int b = it & 1;
-      if (!wait_for_warp(&sm.item_full[b], (it >> 1) & 1, err)) break;
+      const int b = it & (kItems - 1), qb = it & 1;
+      if (!wait_for_warp(&sm.item_full[b], (it >> kItemsLog) & 1, err)) break;
       if (sm.item[b].stop) break;
       const int32_t n = sm.item[b].t1 - sm.item[b].t0;
-      if (!wait_for_warp(&sm.q_full[b], (it >> 1) & 1, err)) break;
+      if (!wait_for_warp(&sm.q_full[qb], (it >> 1) & 1, err)) break;
       for (int32_t k = 0; k < n && ok; ++k, ++t) {
         if (!wait_for_warp(&sm.full[slot], phase, err)) {
           ok = false;
@@ -406,14 +417,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tc::fence_after_sync();
         if (elect()) {
           const uint32_t k_lo = (ring_lo + slot * (Sh::kSlot >> 4)) | kAlongK;
-          const uint32_t b_lo = (q_lo + b * (Sh::kQBytes >> 4)) | kAlongK;
+          const uint32_t b_lo = (q_lo + qb * (Sh::kQBytes >> 4)) | kAlongK;
 #pragma unroll
           for (int s = 0; s < kD / 16; ++s)
             tc::mma_bf16(tmem + (t & 1) * kN, desc_of(k_lo + (s >> 2) * 1024 + (s & 3) * 2),
                          desc_of(b_lo + (s >> 2) * (kN * 8) + (s & 3) * 2), kIdS, s > 0);
           tc::mma_commit(&sm.s_full[t & 1]);
           tc::mma_commit(&sm.empty[slot]);
-          if (k + 1 == n) tc::mma_commit(&sm.item_empty[b]);
+          if (k + 1 == n) {
+            tc::mma_commit(&sm.q_empty[qb]);
+            tc::mma_commit(&sm.item_empty[b]);
+          }
         }
         __syncwarp();
         next_slot();
@@ -443,8 +457,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     int32_t t = 0;
     bool ok = true;
     for (int32_t it = 0; ok; ++it) {
-      const int b = it & 1;
-      if (soft_any(half, !wait_for(&sm.item_full[b], (it >> 1) & 1, err))) break;
+      const int b = it & (kItems - 1);
+      if (soft_any(half, !wait_for(&sm.item_full[b], (it >> kItemsLog) & 1, err))) break;
       const Item x = sm.item[b];
       if (x.stop) break;
       if (row < kC) minus[row] = -kM2Empty;
@@ -461,7 +475,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool masked = (kt + 1) * int64_t(kTile) > x.base0;
         uint32_t seen = ~0u;  // bit c: column c of this half sees this thread's place
         if (masked) {
-          if (!table) late |= !wait_for(&sm.table_full[b], (it >> 1) & 1, err);
+          if (!table) late |= !wait_for(&sm.table_full[b], (it >> kItemsLog) & 1, err);
           table = true;
           const int32_t place = kt * kTile + row, j = place - x.base0;
           if (place >= x.end) {
@@ -568,7 +582,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (!ok) break;
       // the item's denominators (while the last product is on its way), then its sums
-      bool late = !table && !wait_for(&sm.table_full[b], (it >> 1) & 1, err);
+      bool late = !table && !wait_for(&sm.table_full[b], (it >> kItemsLog) & 1, err);
       const float sum = over_lanes<kC>(l, [](float a, float b) { return a + b; });
       if (lane < kC) sm.part[quad][col0 + lane] = sum;
       late |= !wait_for(&sm.p_free, (t - 1) & 1, err);

@@ -355,14 +355,16 @@ struct Item {
   int32_t stop;    // no item: the list is at its end
 };
 
-// The items of this CTA's run, by one warp: item_full says that an item's description is there (of two),
+// The items of this CTA's run, by one warp: item_full says that an item's description is there (of
+// 2^kLog),
 // item_empty that nobody needs it or its queries any more.  `after` adds what is not needed at once.
 // Ends the list with an item that says so, and leaves the CTA's cut item in the workspace; returns its
 // columns.
-template <typename After>
+template <int kLog, typename After>
 __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, Item* item,
                                               uint64_t* item_full, uint64_t* item_empty,
                                               int32_t* err, After after) {
+  constexpr int kItems = 1 << kLog;
   const int lane = threadIdx.x & 31;
   const Span span = p.big          ? find_span<int64_t, 4>(p, err)
                     : p.rd.B > 32 ? find_span<int32_t, 4>(p, err)
@@ -387,7 +389,7 @@ __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, It
       const int64_t units = min(tiles + span.cost - off, span.end - at);
       const int64_t t0 = max(off - span.cost, int64_t(0)), t1 = off + units - span.cost;
       if (t1 > t0) {  // (else the run ends within what stands for the item's own cost)
-        const int b = it & 1;
+        const int b = it & (kItems - 1);
         const int32_t tok0 = rt * p.tokens, ntok = min(p.tokens, rq.n - tok0);
         const int32_t columns = ntok * p.group;
         Item x;
@@ -402,7 +404,7 @@ __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, It
         x.begins = x.t0 == 0;
         x.last = span.end - (at + units) <= span.cost;
         x.stop = 0;
-        if (it >= 2 && !wait_for_warp(&item_empty[b], ((it >> 1) - 1) & 1, err)) {
+        if (it >= kItems && !wait_for_warp(&item_empty[b], ((it >> kLog) - 1) & 1, err)) {
           ok = false;
           break;
         }
@@ -438,8 +440,8 @@ __device__ __forceinline__ int32_t walk_items(const AttnParams& p, Cut* cuts, It
       }
     }
   }
-  const int b = it & 1;
-  if (ok && (it < 2 || wait_for_warp(&item_empty[b], ((it >> 1) - 1) & 1, err)) && lane == 0) {
+  const int b = it & (kItems - 1);
+  if (ok && (it < kItems || wait_for_warp(&item_empty[b], ((it >> kLog) - 1) & 1, err)) && lane == 0) {
     item[b].stop = 1;
     mbar_arrive(&item_full[b]);
   }

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == kItemWarp) {
     // ---- the items ---------------------------------------------------------------------------------
     int64_t built[2] = {-1, -1};
-    const int32_t columns = walk_items(
+    const int32_t columns = walk_items<1>(
         p, reinterpret_cast<Cut*>(p.ws + wl.cuts), sm.item, sm.item_full, sm.item_empty, err,
         [&](int b, const Item& x, int64_t first) {
           if (!p.rd.parents) return;
