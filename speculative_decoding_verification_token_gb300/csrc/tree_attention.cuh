@@ -355,9 +355,8 @@ struct Item {
   int32_t stop;    // no item: the list is at its end
 };
 
-// The items of this CTA's run, by one warp: item_full says that an item's description is there (of
-// 2^kLog),
-// item_empty that nobody needs it or its queries any more.  `after` adds what is not needed at once.
+// The items of this CTA's run, by one warp: item_full says that an item's description is there (of 2^kLog
+// at a time), item_empty that nobody needs it any more.  `after` adds what is not needed at once.
 // Ends the list with an item that says so, and leaves the CTA's cut item in the workspace; returns its
 // columns.
 template <int kLog, typename After>
