@@ -473,7 +473,7 @@ size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t max_draft_len, int
  * is rounded to bf16 for its product with v_j, and added up in fp32 for the denominator.  Places
  * that a row does not see do not reach its result, whatever they hold, NaN included.  Rows that
  * belong to no request are not written.  n_heads a multiple of n_kv_heads, at most 128 times it;
- * D 64 or 128; page_size a power of two, at least 8; scale finite. */
+ * D 64 or 128; page_size a power of two, at least 8; scale log2(e) finite. */
 sv_status spec_tree_attention(const void* q, int64_t ldq, int64_t q_head, int64_t n_rows,
                               int32_t n_heads, int32_t n_kv_heads, int32_t D, float scale,
                               const int64_t* row0, const int32_t* draft_len,
@@ -509,10 +509,11 @@ sv_status spec_tree_accept(const int32_t* sampled, const int32_t* draft_tokens,
  * place ctx_len[r] + path[r][i] goes to place ctx_len[r] + 1 + i, in each of n_layers caches
  * layer_stride elements apart; place ctx_len[r] (row 0) stays.  path (int32 [B][ld_path], n_path
  * columns, fewer than SV_MAX_TREE_ROWS): strictly ascending from 1 or more; NULL: a chain, whose
- * entries lie in place.  new_len (nullable, not ctx_len itself) = ctx_len + 1 + accepted_len, the
- * next round's ctx_len.  Other places keep what they hold, the rejected rows' among them.
- * accepted_len outside [0, n_path] or a path that does not ascend: SV_ERR_BAD_INPUT, that request
- * is left out.  Requests must not share the pages of their own rows.  D a multiple of 8. */
+ * entries lie in place.  new_len (nullable, neither ctx_len nor accepted_len) = ctx_len + 1 +
+ * accepted_len, the next round's ctx_len.  Other places keep what they hold, the rejected rows'
+ * among them.  accepted_len outside [0, n_path] or a path that does not ascend: SV_ERR_BAD_INPUT,
+ * that request is left out.  Requests must not share the pages of their own rows.  D a multiple of
+ * 8. */
 sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t* path, int64_t ld_path,
                           int32_t n_path, int32_t B, const int32_t* ctx_len,
                           const int32_t* page_table, int64_t ld_pages, int32_t max_pages,

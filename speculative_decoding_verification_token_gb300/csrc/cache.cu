@@ -454,7 +454,7 @@ extern "C" sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t*
   if (n_path < 0 || (path && ld_path < n_path) || n_layers < 0 || n_kv_heads < 1 || D < 1)
     return SV_ERR_INVALID;
   if (n_path >= SV_MAX_TREE_ROWS && path) return SV_ERR_UNSUPPORTED;
-  if (new_len && new_len == ctx_len) return SV_ERR_INVALID;
+  if (new_len && (new_len == ctx_len || new_len == accepted_len)) return SV_ERR_INVALID;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (B == 0) return reset_status(status, s);
   if (!accepted_len || !ctx_len || (!page_table && max_pages > 0)) return SV_ERR_INVALID;

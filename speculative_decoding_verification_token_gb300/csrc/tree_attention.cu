@@ -988,7 +988,7 @@ extern "C" sv_status spec_tree_attention(
     size_t workspace_bytes, void* stream) {
   if (!round_sizes_ok(max_draft_len, bonus_row, B, n_rows, ld_pages, max_pages, n_pages, page_size))
     return SV_ERR_INVALID;
-  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || D < 1 || !std::isfinite(scale) ||
+  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || D < 1 || !std::isfinite(scale * kLog2e) ||
       (lse && ld_lse < n_heads))
     return SV_ERR_INVALID;
   if (parents && max_draft_len + int64_t(bonus_row) > SV_MAX_TREE_ROWS) return SV_ERR_UNSUPPORTED;

@@ -16,6 +16,7 @@ def sv():
 
 FAKE = C.c_void_p(4096)  # never dereferenced: validation fails first
 ODD = C.c_void_p(4100)
+OTHER = C.c_void_p(8192)
 
 
 def test_append_refusals(sv):
@@ -49,7 +50,8 @@ def test_attention_refusals(sv):
     bad, no = sv.SV_ERR_INVALID, sv.SV_ERR_UNSUPPORTED
     for kw in (dict(g=-1), dict(bonus=-1), dict(B=-1), dict(rows=-2), dict(ldp=3), dict(pages=-1), dict(page=0),
                dict(heads=0), dict(kv=0), dict(heads=5), dict(D=0), dict(scale=float("nan")),
-               dict(scale=float("inf")), dict(lse=FAKE, ldl=3), dict(q=None), dict(kc=None), dict(out=None),
+               dict(scale=float("inf")), dict(scale=3e38), dict(lse=FAKE, ldl=3), dict(q=None), dict(kc=None),
+               dict(out=None),
                dict(row0=None), dict(ws=None), dict(wb=0)):
         assert call(**kw) == bad, kw
     for kw in (dict(D=32), dict(D=256), dict(heads=258), dict(page=4), dict(page=24), dict(parents=FAKE, g=128),
@@ -83,6 +85,8 @@ def test_keep_refusals(sv):
     for kw in (dict(acc=None), dict(ldpath=4), dict(n=-1), dict(B=-1), dict(ldp=3), dict(kc=None), dict(layers=-1),
                dict(pages=-1), dict(page=0), dict(kv=0), dict(D=0), dict(ctx=None), dict(new=FAKE)):
         assert call(**kw) == bad, kw
+    # the lengths that a request's other layers still read
+    assert call(acc=OTHER, new=OTHER) == bad
     for kw in (dict(n=128, ldpath=128), dict(D=12), dict(kc=ODD), dict(ls=4), dict(ps=2047), dict(ts=4),
                dict(B=2**20, layers=2**12)):
         assert call(**kw) == no, kw
