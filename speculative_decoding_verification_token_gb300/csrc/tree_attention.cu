@@ -34,7 +34,6 @@ namespace {
 
 using namespace attn;
 
-constexpr int kCluster = 8;
 // Items whose descriptions are there at once: of short ones several lie in the ring, and the loads wait for the
 // results of none (256 rows over 100 to 400 places each: 80 us with two, 66 with four).
 constexpr int kItemsLog = 2, kItems = 1 << kItemsLog;
@@ -97,10 +96,11 @@ __device__ __forceinline__ void build_seen(const AttnParams& p, const Item& x, u
 }
 
 
-// The item of this CTA's cluster and the CTA's tiles of it, by one warp (at most 32 requests).
+// The item of this CTA's cluster of kCtas and the CTA's tiles of it, by one warp (at most 32 requests).
+template <int kCtas>
 __device__ __forceinline__ Item cluster_item(const AttnParams& p, int64_t& first) {
   const int lane = threadIdx.x & 31;
-  const int32_t cluster = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  const int32_t cluster = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
   Request q = {};
   int32_t tiles = 0;  // row tiles
   if (lane < p.rd.B) {
@@ -132,7 +132,7 @@ __device__ __forceinline__ Item cluster_item(const AttnParams& p, int64_t& first
     x.base0 = q.ctx + (p.rd.parents ? 0 : tok0);
     x.end = q.ctx + tok0 + ntok;
     const int64_t all = tiles_of(q, rt, p.tokens);
-    x.t0 = int32_t(all * rank / kCluster), x.t1 = int32_t(all * (rank + 1) / kCluster);
+    x.t0 = int32_t(all * rank / kCtas), x.t1 = int32_t(all * (rank + 1) / kCtas);
   }
   x.begins = x.last = 1;
   x.stop = x.t0 == x.t1;
@@ -187,18 +187,19 @@ __device__ __forceinline__ float peer_load(uint32_t at) {
   return v;
 }
 
-// The parts of a cluster's item joined by all of its threads: CTA `rank` takes every eighth column.
-template <int kD, int kN>
+// The parts of a cluster's item joined by all of its threads: CTA `rank` takes
+// every kCtas-th column.
+template <int kD, int kN, int kCtas>
 __device__ __forceinline__ void cluster_join(const AttnParams& p, const Item& x, const float* part,
                                              const uint32_t* had, const int64_t* col_off) {
   const uint32_t at = smem_addr(part), had_at = smem_addr(had);
   for (int32_t u = threadIdx.x;; u += kAttnThreads) {
-    const int32_t col = blockIdx.x % kCluster + kCluster * (u / (kD / 2)), d = u % (kD / 2) * 2;
+    const int32_t col = blockIdx.x % kCtas + kCtas * (u / (kD / 2)), d = u % (kD / 2) * 2;
     if (col >= x.columns) return;
-    float m[kCluster], l[kCluster], a[kCluster], b[kCluster];
-    bool has[kCluster];
+    float m[kCtas], l[kCtas], a[kCtas], b[kCtas];
+    bool has[kCtas];
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) {
+    for (int r = 0; r < kCtas; ++r) {
       const uint32_t from = peer(at, r);
       has[r] = __float_as_uint(peer_load(peer(had_at, r))) != 0;
       m[r] = peer_load(from + 4 * (kN * kD + col));
@@ -208,10 +209,10 @@ __device__ __forceinline__ void cluster_join(const AttnParams& p, const Item& x,
     }
     float top = kM2Empty, sum = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r)
+    for (int r = 0; r < kCtas; ++r)
       if (has[r]) top = fmaxf(top, m[r]);
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) {
+    for (int r = 0; r < kCtas; ++r) {
       if (!has[r]) continue;
       const float w = fast_exp2(m[r] - top);
       sum += w * l[r];
@@ -229,12 +230,13 @@ __device__ __forceinline__ void cluster_join(const AttnParams& p, const Item& x,
   }
 }
 
-template <int kD, int kN, bool kShort>
+template <int kD, int kN, int kCtas>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_q,
                      const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using Sh = AttnShared<kD, kN>;
+  constexpr bool kShort = kCtas > 0;
   constexpr int kC = kN / 2;  // columns of a half
   constexpr int kStages = Sh::kStages();
   constexpr uint32_t kCols = kN <= 16 ? 64 : kN <= 32 ? 128 : kN <= 64 ? 256 : 512;
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     };
     if constexpr (kShort) {
       int64_t first = 0;
-      const Item x = cluster_item(p, first);
+      const Item x = cluster_item<kCtas>(p, first);
       if (lane == 0) {
         sm.item[0] = x;
         mbar_arrive(&sm.item_full[0]);
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (tid == 0 && sm.err == SV_ERR_TIMEOUT) report(p.status, SV_ERR_TIMEOUT);
     __syncwarp();
     cluster_sync();
-    cluster_join<kD, kN>(p, sm.item[0], reinterpret_cast<const float*>(ring), &sm.had, sm.col_off[0]);
+    cluster_join<kD, kN, kCtas>(p, sm.item[0], reinterpret_cast<const float*>(ring), &sm.had, sm.col_off[0]);
     __syncwarp();
     cluster_sync();  // nobody's shared memory goes away while others read it
   } else {
@@ -872,22 +874,23 @@ sv_status launch_join(const AttnParams& p, int grid, cudaStream_t s) {
                           kJoinThreads, 0, s, p, grid);
 }
 
-// Few items of few tiles: a cluster for each.  They have to be there at once (see clusters_at_once); more
-// tiles are worth more SMs than a cluster has; and one warp looks through all the pages.  A request of 6
-// rows under 32 heads (8 key heads): 9.1 us over 1000 places (14.6 from the list), 11.0 over 4000 (15.7),
-// 15.1 over 8000 (17.7).
-constexpr int kShortItems = 32, kShortTiles = 64, kShortPages = 1024;
+// Few items of few tiles: a cluster of 8 CTAs for each, or of 4.  They have to be there at once (see
+// clusters_at_once); more tiles are worth more SMs than a cluster has; and one warp looks through all the
+// pages.  Rows of 6 under 32 heads (8 key heads): one request 8.6 us over 1000 places (14.6 from the list),
+// two 12.2 over 2000 each (14.7), four 12.6 (17.7).  Eight in clusters of 2: 18.4 over 2000 places each (22.6),
+// but 17.9 over 1 to 2000 (16.3), the list's runs being equal.
+constexpr int kShortItems = 48, kShortRun = 8, kShortPages = 1024;
 
 struct ShortLaunch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  ShortLaunch(int items, cudaStream_t s) {
-    cfg.gridDim = dim3(unsigned(items) * kCluster);
+  ShortLaunch(int items, int ctas, cudaStream_t s) {
+    cfg.gridDim = dim3(unsigned(items * ctas));
     cfg.blockDim = dim3(kAttnThreads);
     cfg.dynamicSmemBytes = kAttnSmem;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.x = unsigned(ctas);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -896,8 +899,8 @@ struct ShortLaunch {
   }
 };
 
-// Clusters that the current device runs at once (asked once per device; 0 if it cannot be asked).
-template <int kD, int kN>
+// Clusters of kCtas that the current device runs at once (asked once per device; 0 if it cannot be asked).
+template <int kD, int kN, int kCtas>
 int clusters_at_once() {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices];  // and one
@@ -905,8 +908,8 @@ int clusters_at_once() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
   int n = known[dev].load(std::memory_order_relaxed);
   if (n == 0) {
-    auto* kern = attention_kernel<kD, kN, true>;
-    ShortLaunch l(1, nullptr);
+    auto* kern = attention_kernel<kD, kN, kCtas>;
+    ShortLaunch l(1, kCtas, nullptr);
     l.cfg.numAttrs = 1;
     int most = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
@@ -919,29 +922,37 @@ int clusters_at_once() {
   return n - 1;
 }
 
-// Sets `taken` where the call is one for clusters, and makes it.
-template <int kD, int kN>
-sv_status launch_short(const AttnMaps& m, const AttnParams& p, int items, cudaStream_t s, bool& taken) {
-  auto* kern = attention_kernel<kD, kN, true>;
+// Sets `taken` where the call is one for clusters of kCtas, and makes it.
+template <int kD, int kN, int kCtas>
+sv_status launch_short(const AttnMaps& m, const AttnParams& p, int64_t items, int64_t tiles,
+                       cudaStream_t s, bool& taken) {
+  auto* kern = attention_kernel<kD, kN, kCtas>;
   static_assert(kN * (kD + 2) * 4 <= AttnShared<kD, kN>::kStages() * AttnShared<kD, kN>::kSlot,
                 "a part fits the ring");
-  if (items > clusters_at_once<kD, kN>()) return SV_OK;
+  if (tiles > kShortRun * kCtas || items > clusters_at_once<kD, kN, kCtas>()) return SV_OK;
   taken = true;
-  ShortLaunch l(items, s);
+  ShortLaunch l(int(items), kCtas, s);
   return launch_status(cudaLaunchKernelEx(&l.cfg, kern, m.q, m.k, m.v, p));
 }
 
+template <int kD, int kN>
+sv_status launch_short(const AttnMaps& m, const AttnParams& p, int64_t items, int64_t tiles,
+                       cudaStream_t s, bool& taken) {
+  const sv_status st = launch_short<kD, kN, 8>(m, p, items, tiles, s, taken);
+  return taken ? st : launch_short<kD, kN, 4>(m, p, items, tiles, s, taken);
+}
+
 template <int kD>
-sv_status launch_short(int32_t n, const AttnMaps& m, const AttnParams& p, int items, cudaStream_t s,
-                       bool& taken) {
-  return n == 16   ? launch_short<kD, 16>(m, p, items, s, taken)
-         : n == 32 ? launch_short<kD, 32>(m, p, items, s, taken)
-                   : launch_short<kD, 64>(m, p, items, s, taken);
+sv_status launch_short(int32_t n, const AttnMaps& m, const AttnParams& p, int64_t items, int64_t tiles,
+                       cudaStream_t s, bool& taken) {
+  return n == 16   ? launch_short<kD, 16>(m, p, items, tiles, s, taken)
+         : n == 32 ? launch_short<kD, 32>(m, p, items, tiles, s, taken)
+                   : launch_short<kD, 64>(m, p, items, tiles, s, taken);
 }
 
 template <int kD, int kN>
 sv_status launch(const AttnMaps& m, const AttnParams& p, int grid, cudaStream_t s) {
-  auto* kern = attention_kernel<kD, kN, false>;
+  auto* kern = attention_kernel<kD, kN, 0>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) !=
       cudaSuccess)
     return SV_ERR_CUDA;
@@ -1045,11 +1056,11 @@ extern "C" sv_status spec_tree_attention(
   // over up to 4096: 0 198 us, 2 182, 4 176, 6 171)
   p.item_cost = n == kWide ? 6 : 4;
   p.big = most + p.item_cost * items >= double(1 << 22);  // (times 192 CTAs it fits 32 bits)
-  if (n <= 64 && B <= 32 && items <= kShortItems && key_tiles <= kShortTiles && max_pages > 0 &&
+  if (n <= 64 && B <= 32 && items <= kShortItems && max_pages > 0 &&
       int64_t(B) * max_pages <= kShortPages) {
     bool taken = false;
-    const sv_status st = D == 64 ? launch_short<64>(n, m, p, int(items), s, taken)
-                                 : launch_short<128>(n, m, p, int(items), s, taken);
+    const sv_status st = D == 64 ? launch_short<64>(n, m, p, int64_t(items), key_tiles, s, taken)
+                                 : launch_short<128>(n, m, p, int64_t(items), key_tiles, s, taken);
     if (taken) return st;
   }
   return D == 64 ? launch<64>(n, m, p, grid, s) : launch<128>(n, m, p, grid, s);

@@ -95,6 +95,24 @@ def test_few_requests_of_longer_contexts(sv, ctx, drafts, heads, kv):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads,kv", [(8, 8), (32, 8), (64, 8)])
+@pytest.mark.parametrize("ctx,drafts", [([900, 2000, 1], [5, 0, 3]), ([3900, 0, 128, 77], [7, 7, 1, 4])])
+@pytest.mark.parametrize("tree", [None, "random"])
+def test_some_requests(sv, ctx, drafts, heads, kv, D, tree):
+    """Too many for the largest runs of SMs each, too few for the whole device: among them contexts of fewer tiles
+    than a run has SMs, and none; the same rows from a table that takes the other way."""
+    page = 16 if ctx[0] < 1000 else 64
+    host, dev, n, _ = pr.make_round(ctx, drafts, 7, page, heads, kv, D, seed=len(ctx) + heads, tree=tree)
+    for d in (dev, wide_table(dev, 1100)):
+        out, lse, st = run(sv, d)
+        assert st == sv.SV_OK
+        check(host, n, out, lse, 1 / math.sqrt(D))
+    dev["page_table"][1, 0] = dev["k_cache"].shape[0]
+    out, lse, st = run(sv, dev)
+    assert st == sv.SV_ERR_BAD_INPUT
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("heads,kv", [(8, 2), (12, 12), (32, 2)])
 def test_long_ragged_batch(sv, D, heads, kv):
     """Requests of very different lengths: their work is cut anywhere."""
