@@ -496,7 +496,7 @@ __device__ __forceinline__ void build_above(const AttnParams& p, int64_t first, 
 
 // The boxes of a tile, one a lane, are loaded by kLoaders warps: of two, each takes 64 of the 128 elements, or
 // every other box of 64.  One warp's issue is what bounds small pages -- 256 requests of one token over up
-// to 4096 places in pages of 16: 449 us by one warp, 360 by two.
+// to 4096 places in pages of 16: 449 us by one warp, 361 by two.
 template <int kD, int kLoaders>
 __device__ __forceinline__ int box_of_lane(int part) {
   const int lane = threadIdx.x & 31;
