@@ -75,8 +75,9 @@ __device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* pare
   const int32_t sub = threadIdx.x / kRowThreads, t = threadIdx.x % kRowThreads;
   Request rq;
   if (!round_request(p.rd, r, rq)) return chunk == 0;
-  const int32_t begin = chunk * p.rows, end = min(begin + p.rows, rq.n);
-  if (begin >= end) return false;
+  const int32_t begin = chunk * p.rows;
+  if (begin >= rq.n) return false;
+  const int32_t end = begin + min(p.rows, rq.n - begin);
   bool bad = false;
   if (p.rd.parents) {
     for (int32_t j = threadIdx.x; j < end; j += kAppendThreads) {
@@ -373,7 +374,7 @@ extern "C" sv_status spec_cache_append(
     return SV_ERR_INVALID;
   if (parents && max_draft_len + int64_t(bonus_row) > SV_MAX_TREE_ROWS) return SV_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (B == 0 || max_draft_len + bonus_row == 0 || n_rows == 0) return reset_status(status, s);
+  if (B == 0 || max_draft_len + int64_t(bonus_row) == 0 || n_rows == 0) return reset_status(status, s);
   if (!k || !v || !k_cache || !v_cache || !row0 || !draft_len || !ctx_len ||
       (!page_table && max_pages > 0) ||
       (n_heads > 0 && (!q || !q_out)))

@@ -37,12 +37,11 @@ __device__ __forceinline__ bool round_request(const RoundParams& p, int32_t draf
                                               int64_t first, Request& q) {
   q.ctx = ctx;
   q.first = first;
-  q.n = drafts + p.bonus_row;
+  const int64_t n = int64_t(drafts) + p.bonus_row;  // (2^31 - 1 drafts have a row more)
   const bool ok = drafts >= 0 && drafts <= p.max_draft_len && q.ctx >= 0 && q.first >= 0 &&
-                  q.first <= p.n_rows && q.n <= p.n_rows - q.first &&
-                  int64_t(q.ctx) + q.n <=
-                      min(int64_t(p.max_pages) * p.page_size, int64_t(INT32_MAX));
-  if (!ok) q.n = 0;
+                  q.first <= p.n_rows && n <= p.n_rows - q.first &&
+                  q.ctx + n <= min(int64_t(p.max_pages) * p.page_size, int64_t(INT32_MAX));
+  q.n = ok ? int32_t(n) : 0;
   return ok;
 }
 

@@ -1006,6 +1006,7 @@ extern "C" sv_status spec_tree_attention(
   const int32_t group = n_heads / n_kv_heads;
   if ((D != 64 && D != 128) || group > 128 || page_size < 8 || (page_size & (page_size - 1)))
     return SV_ERR_UNSUPPORTED;
+  if (n_rows > INT32_MAX - kWide) return SV_ERR_UNSUPPORTED;  // (the end of a row tile fits 32 bits)
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (B == 0 || max_draft_len + int64_t(bonus_row) == 0 || n_rows == 0)
     return reset_status(status, s);
@@ -1037,7 +1038,6 @@ extern "C" sv_status spec_tree_attention(
   p.ws = static_cast<uint8_t*>(workspace);
   const int sms = std::min(device_sm_count(), kMaxCtas);
   if (sms < 1) return SV_ERR_CUDA;
-  if (n_rows > INT32_MAX) return SV_ERR_UNSUPPORTED;
   AttnMaps m;
   if (!query_map(&m.q, q, D, n_heads, n_rows, q_head, ldq, group, p.tile_tokens) ||
       !cache_map(&m.k, k_cache, D, n_kv_heads, page_size, n_pages, head_stride, token_stride,
