@@ -496,8 +496,11 @@ sv_status spec_tree_attention(const void* q, int64_t ldq, int64_t q_head, int64_
  * Outputs: accepted_len[B], out_tokens[B][out_ld] (out_ld >= max_draft_len + 1) and correction_token
  * (nullable) as for spec_verify_token; path (nullable) int32 [B][ld_path] (ld_path >=
  * max_draft_len): the accepted rows, then -1.  Columns of out_tokens from max_draft_len + 1 on, and
- * of path from max_draft_len on, are not written.  A negative sampled token on the way is
- * SV_ERR_BAD_INPUT.  max_draft_len below SV_MAX_TREE_ROWS. */
+ * of path from max_draft_len on, are not written.  A request whose length or rows are out of range,
+ * or that meets a negative sampled token on the way, emits nothing: SV_ERR_BAD_INPUT in status,
+ * accepted_len -1, its out_tokens, path and correction_token all -1 (padding to
+ * spec_history_append, and a length that spec_cache_keep leaves out).  A row whose parent is out of
+ * range is SV_ERR_BAD_INPUT too and nobody's child.  max_draft_len below SV_MAX_TREE_ROWS. */
 sv_status spec_tree_accept(const int32_t* sampled, const int32_t* draft_tokens,
                            const int32_t* parents, const int64_t* row0, const int64_t* draft_row0,
                            const int32_t* draft_len, int32_t max_draft_len, int32_t B,

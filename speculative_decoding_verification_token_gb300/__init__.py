@@ -1012,7 +1012,7 @@ def spec_tree_accept(sampled, draft_tokens, parents, row0, draft_row0, draft_len
     [rows]; see include/specverify.h): the walk from row 0 to the children that were sampled.
     parents int32 [rows], None: chains.  Returns a dict: accepted_len [B], out_tokens
     [B, max_draft_len + 1] and correction [B] as spec_verify_token's, path [B, max_draft_len] (the
-    accepted rows, then -1), status."""
+    accepted rows, then -1), status.  A request whose data are bad emits nothing: -1 in all of them."""
     if not (accepted_len is None or out_tokens is None or path is None or correction is None
             or status is None) and (_fast or _load_fast()):
         code = _fast.tree_accept(sampled, draft_tokens, parents, row0, draft_row0, draft_len,

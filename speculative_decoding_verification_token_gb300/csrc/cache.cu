@@ -208,10 +208,22 @@ __device__ __forceinline__ bool accept_body(const AcceptParams& p) {
   bool bad = drafts < 0 || drafts > p.max_draft_len || first < 0 || first >= p.n_rows ||
              drafts >= p.n_rows - first ||
              (drafts > 0 && (dfirst < 0 || dfirst > p.n_drafts || drafts > p.n_drafts - dfirst));
-  if (bad) {
-    if (lane == 0) p.accepted_len[r] = 0;
+  int32_t* const out = p.out_tokens + r * p.out_ld;
+  int32_t* const path = p.path ? p.path + r * p.ld_path : nullptr;
+  // Nothing is emitted: a length of -1, with which spec_cache_keep leaves the request as it was, and no token
+  // of an earlier round for the history.
+  auto nothing = [&] {
+    __syncwarp();  // (over what a walk has written)
+    if (lane == 0) {
+      p.accepted_len[r] = -1;
+      if (p.correction) p.correction[r] = -1;
+    }
+    for (int32_t i = lane; i <= p.max_draft_len; i += 32) out[i] = -1;
+    if (path)
+      for (int32_t i = lane; i < p.max_draft_len; i += 32) path[i] = -1;
     return true;
-  }
+  };
+  if (bad) return nothing();
   int32_t parent[kTreeWords], token[kTreeWords], sample[kTreeWords];
 #pragma unroll
   for (int k = 0; k < kTreeWords; ++k) {
@@ -226,16 +238,11 @@ __device__ __forceinline__ bool accept_body(const AcceptParams& p) {
     }
   }
   int32_t at = 0, n = 0, t = 0;
-  int32_t* const out = p.out_tokens + r * p.out_ld;
-  int32_t* const path = p.path ? p.path + r * p.ld_path : nullptr;
   for (;;) {
     const int32_t word = at >> 5;
     const int32_t mine = word == 0 ? sample[0] : word == 1 ? sample[1] : word == 2 ? sample[2] : sample[3];
     t = __shfl_sync(0xffffffffu, mine, at & 31);
-    if (t < 0) {
-      bad = true;
-      break;
-    }
+    if (t < 0) return nothing();
     int32_t next = -1;
 #pragma unroll
     for (int k = kTreeWords - 1; k >= 0; --k) {
