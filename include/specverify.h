@@ -514,9 +514,10 @@ sv_status spec_tree_accept(const int32_t* sampled, const int32_t* draft_tokens,
  * columns, fewer than SV_MAX_TREE_ROWS): strictly ascending from 1 or more; NULL: a chain, whose
  * entries lie in place.  new_len (nullable, neither ctx_len nor accepted_len) = ctx_len + 1 +
  * accepted_len, the next round's ctx_len.  Other places keep what they hold, the rejected rows'
- * among them.  accepted_len outside [0, n_path] or a path that does not ascend: SV_ERR_BAD_INPUT,
- * that request is left out.  Requests must not share the pages of their own rows.  D a multiple of
- * 8. */
+ * among them.  accepted_len outside [0, n_path] (-1: spec_tree_accept's of a bad request), a path
+ * that does not ascend, or places or pages out of range: SV_ERR_BAD_INPUT, nothing of that request
+ * moves, and its new_len is its ctx_len.  Requests must not share the pages of their own rows.  D a
+ * multiple of 8. */
 sv_status spec_cache_keep(const int32_t* accepted_len, const int32_t* path, int64_t ld_path,
                           int32_t n_path, int32_t B, const int32_t* ctx_len,
                           const int32_t* page_table, int64_t ld_pages, int32_t max_pages,

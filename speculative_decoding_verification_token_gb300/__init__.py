@@ -1055,8 +1055,8 @@ def spec_cache_keep(k_cache, v_cache, page_table, ctx_len, accepted_len, path, n
     """The accepted rows' entries moved behind the context in the caches bf16 [pages, page size, kv
     heads, D] or [layers, pages, ...], in place: place ctx_len + path[:, i] to ctx_len + 1 + i for
     i < accepted_len (see include/specverify.h).  path int32 [B, n], or None for chains.  Returns
-    new_len int32 [B] = ctx_len + 1 + accepted_len, the next round's ctx_len.  Data errors go to
-    `status`; without one they go unreported."""
+    new_len int32 [B] = ctx_len + 1 + accepted_len, the next round's ctx_len (a request of bad data
+    keeps its own).  Data errors go to `status`; without one they go unreported."""
     if new_len is not None and (_fast or _load_fast()):
         code = _fast.cache_keep(k_cache, v_cache, page_table, ctx_len, accepted_len, path, new_len,
                                 status, stream)

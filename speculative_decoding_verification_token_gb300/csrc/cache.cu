@@ -318,8 +318,9 @@ __device__ __forceinline__ bool keep_body(const KeepParams& p, int64_t* src, int
       bad = page_from < 0 || page_to < 0;
     }
   }
-  if (__syncthreads_or(bad)) return layer0 == 0 && tid == 0;
-  if (layer0 == 0 && tid == 0 && p.new_len) p.new_len[r] = ctx + 1 + n;
+  bad = __syncthreads_or(bad);
+  if (layer0 == 0 && tid == 0 && p.new_len) p.new_len[r] = bad ? ctx : ctx + 1 + n;
+  if (bad) return layer0 == 0 && tid == 0;
   if (!p.path) return false;
   // a path starts with the rows that lie in place; from its first gap on every row moves
   const bool move = tid < n && from != tid + 1;
