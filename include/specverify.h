@@ -444,7 +444,7 @@ sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_scales,
  * rotation): fp32 [n_positions][ld_cos_sin], the cosines of a position's rot / 2 angles, then their
  * sines; the first `rot` elements of every head of q and k turn by them, a' = a cos - b sin, b' =
  * a sin + b cos (binary32) with pairs (a, b) at (e, e + rot / 2), or at (2 e, 2 e + 1) if adjacent =
- * 1.  A position outside [0, n_positions) is SV_ERR_BAD_INPUT.
+ * 1.  A row whose position is outside [0, n_positions) is SV_ERR_BAD_INPUT and left out whole.
  * q and q_out may be NULL (n_heads = 0), and q_out may be q itself (bf16, equal strides).  Places
  * other than the rows' are not written.  Different rows must have different places.
  * D and rot multiples of 16, rot <= D <= 256. */

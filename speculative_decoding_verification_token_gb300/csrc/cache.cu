@@ -104,12 +104,12 @@ __device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* pare
       for (int32_t j = parents[i]; j >= 0; j = parents[j]) ++depth;
     }
     Eight<float> c8, s8;
+    const int64_t pos = int64_t(rq.ctx) + depth;
+    if (p.cos_sin && pos >= p.n_positions) {  // (for the threads of parts that do not turn too)
+      bad = true;
+      continue;
+    }
     if (turn) {
-      const int64_t pos = int64_t(rq.ctx) + depth;
-      if (pos >= p.n_positions) {
-        bad = true;
-        continue;
-      }
       const float* row = p.cos_sin + pos * p.ld_cos_sin + part * 8;
       c8.load(row);
       s8.load(row + (p.rot >> 1));
