@@ -432,9 +432,9 @@ sv_status spec_project_fp4(const uint8_t* x_packed, const uint8_t* x_scales,
  * of the request, or from the context (-1); NULL: a chain, row i from row i - 1.  A row's position
  * is ctx_len[r] + its depth (0 below the context), and it sees the context, its ancestors and
  * itself.  With parents n is at most SV_MAX_TREE_ROWS; chains may be longer (prompts).
- * Lengths out of range (draft_len outside [0, max_draft_len], rows outside the n_rows, places past
- * the table), pages outside [0, n_pages), parents outside [-1, i): SV_ERR_BAD_INPUT in status.  No
- * call reads or writes outside the arrays it is given for them.
+ * Lengths out of range (draft_len outside [0, max_draft_len] or above 2^31 - 513, rows outside the
+ * n_rows, places past the table), pages outside [0, n_pages), parents outside [-1, i):
+ * SV_ERR_BAD_INPUT in status.  No call reads or writes outside the arrays it is given for them.
  * Different requests' rows must be different rows; contexts may share pages.
  * Rows, heads, tokens and pages are 16-byte aligned (bases and strides).
  * ------------------------------------------------------------------------------------------- */

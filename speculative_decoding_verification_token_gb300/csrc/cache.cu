@@ -18,7 +18,7 @@ struct AppendParams {
   __nv_bfloat16* q_out;
   int64_t ldqo, qo_head;
   const float* cos_sin;
-  int64_t ld_cos_sin, n_positions;
+  int64_t ld_cos_sin, n_positions;  // (without a rotation any position will do)
   int32_t n_heads, n_kv_heads, D, rot;
   int32_t rows;    // of a CTA
   int32_t chunks;  // CTAs of a request
@@ -75,9 +75,8 @@ __device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* pare
   const int32_t sub = threadIdx.x / kRowThreads, t = threadIdx.x % kRowThreads;
   Request rq;
   if (!round_request(p.rd, r, rq)) return chunk == 0;
-  const int32_t begin = chunk * p.rows;
-  if (begin >= rq.n) return false;
-  const int32_t end = begin + min(p.rows, rq.n - begin);
+  const int32_t begin = chunk * p.rows, end = min(begin + p.rows, rq.n);
+  if (begin >= end) return false;
   bool bad = false;
   if (p.rd.parents) {
     for (int32_t j = threadIdx.x; j < end; j += kAppendThreads) {
@@ -105,7 +104,7 @@ __device__ __forceinline__ bool append_body(const AppendParams& p, int32_t* pare
     }
     Eight<float> c8, s8;
     const int64_t pos = int64_t(rq.ctx) + depth;
-    if (p.cos_sin && pos >= p.n_positions) {  // (for the threads of parts that do not turn too)
+    if (pos >= p.n_positions) {  // (for the threads of parts that do not turn too)
       bad = true;
       continue;
     }
@@ -399,6 +398,7 @@ extern "C" sv_status spec_cache_append(
   if (n_heads > 0 && q_out == q && (dtype != SV_BF16 || ldqo != ldq || qo_head != q_head))
     return SV_ERR_INVALID;
   AppendParams p = {};
+  max_draft_len = round_most_drafts(max_draft_len);
   p.rd = {row0,    draft_len, parents,       ctx_len,   page_table, ld_pages, n_rows,
           n_pages, B,         max_draft_len, bonus_row, max_pages,  page_size};
   p.cache = {static_cast<__nv_bfloat16*>(k_cache), static_cast<__nv_bfloat16*>(v_cache),
@@ -406,7 +406,8 @@ extern "C" sv_status spec_cache_append(
   p.q = q, p.k = k, p.v = v;
   p.ldq = ldq, p.q_head = q_head, p.ldk = ldk, p.k_head = k_head, p.ldv = ldv, p.v_head = v_head;
   p.q_out = static_cast<__nv_bfloat16*>(q_out), p.ldqo = ldqo, p.qo_head = qo_head;
-  p.cos_sin = cos_sin, p.ld_cos_sin = ld_cos_sin, p.n_positions = n_positions;
+  p.cos_sin = cos_sin, p.ld_cos_sin = ld_cos_sin;
+  p.n_positions = cos_sin ? n_positions : INT64_MAX;
   p.n_heads = n_heads, p.n_kv_heads = n_kv_heads, p.D = D, p.rot = rot;
   const int64_t most = max_draft_len + int64_t(bonus_row);
   // a CTA takes several rows where there are enough of them for two rounds of CTAs: what it finds out of

@@ -4,6 +4,8 @@
 
 #include "dependent.cuh"
 
+#include <algorithm>
+
 namespace sv {
 
 struct RoundParams {
@@ -37,11 +39,12 @@ __device__ __forceinline__ bool round_request(const RoundParams& p, int32_t draf
                                               int64_t first, Request& q) {
   q.ctx = ctx;
   q.first = first;
-  const int64_t n = int64_t(drafts) + p.bonus_row;  // (2^31 - 1 drafts have a row more)
+  q.n = drafts + p.bonus_row;  // (a length that max_draft_len allows fits: round_most_drafts)
   const bool ok = drafts >= 0 && drafts <= p.max_draft_len && q.ctx >= 0 && q.first >= 0 &&
-                  q.first <= p.n_rows && n <= p.n_rows - q.first &&
-                  q.ctx + n <= min(int64_t(p.max_pages) * p.page_size, int64_t(INT32_MAX));
-  q.n = ok ? int32_t(n) : 0;
+                  q.first <= p.n_rows && q.n <= p.n_rows - q.first &&
+                  int64_t(q.ctx) + q.n <=
+                      min(int64_t(p.max_pages) * p.page_size, int64_t(INT32_MAX));
+  if (!ok) q.n = 0;
   return ok;
 }
 
@@ -120,6 +123,12 @@ inline bool round_sizes_ok(int32_t max_draft_len, int32_t bonus_row, int32_t B, 
                            int32_t page_size) {
   return max_draft_len >= 0 && (bonus_row == 0 || bonus_row == 1) && B >= 0 && n_rows >= 0 &&
          max_pages >= 0 && ld_pages >= max_pages && n_pages >= 0 && page_size >= 1;
+}
+
+// RoundParams::max_draft_len.  The rows of longer requests, and the ends of their tiles and chunks, would pass
+// 32 bits: they are out of range.
+inline int32_t round_most_drafts(int32_t max_draft_len) {
+  return std::min(max_draft_len, INT32_MAX - 512);
 }
 
 inline bool aligned_bf16(const void* p, int64_t a, int64_t b, int64_t c) {

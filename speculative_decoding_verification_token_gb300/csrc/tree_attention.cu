@@ -1021,6 +1021,7 @@ extern "C" sv_status spec_tree_attention(
                                                             n_kv_heads, D))
     return SV_ERR_INVALID;
   AttnParams p = {};
+  max_draft_len = round_most_drafts(max_draft_len);
   p.rd = {row0,    draft_len, parents,       ctx_len,   page_table, ld_pages, n_rows,
           n_pages, B,         max_draft_len, bonus_row, max_pages,  page_size};
   p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
