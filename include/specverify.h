@@ -471,8 +471,10 @@ size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t max_draft_len, int
  * lse (nullable, fp32 [n_rows][ld_lse]) = log sum_j e^(x_j).
  * q and out: bf16 as for spec_cache_append.  Products are taken in bf16 with fp32 sums; e^(x_j - m)
  * is rounded to bf16 for its product with v_j, and added up in fp32 for the denominator.  Places
- * that a row does not see do not reach its result, whatever they hold, NaN included.  Rows that
- * belong to no request are not written.  n_heads a multiple of n_kv_heads, at most 128 times it;
+ * that a row does not see do not reach its result, whatever they hold, NaN included.  Scores x_j up
+ * to 2^27 in magnitude: m, a score's binary32 value times log2(e), is rounded, for larger ones by
+ * more than a weight's exponent allows, and the row's result may be NaN.  Rows that belong to no
+ * request are not written.  n_heads a multiple of n_kv_heads, at most 128 times it;
  * D 64 or 128; page_size a power of two, at least 8; scale log2(e) finite. */
 sv_status spec_tree_attention(const void* q, int64_t ldq, int64_t q_head, int64_t n_rows,
                               int32_t n_heads, int32_t n_kv_heads, int32_t D, float scale,

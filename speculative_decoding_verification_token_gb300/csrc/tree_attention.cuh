@@ -15,7 +15,9 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kItemWarp = 10, kLoadWarp2 = 11;
 constexpr uint32_t kAttnSmem = 232448 - 1024;  // dynamic shared memory of a CTA, less what is static
 constexpr int kWide = 256;        // rows of an item of the wide kernel: two tiles of 128
 constexpr int kMaxCtas = 192;     // the workspace's size does not depend on the current device
-constexpr float kSlack = 8.f;     // log2 of what P may reach before m is raised
+// log2 of what P may reach before m is raised.  (m is a rounded product and P's exponent an unrounded one less
+// m: with scores of 2^27, of 2^28 in base 2, P may be 2^8 off besides, the same for all of a row's.)
+constexpr float kSlack = 8.f;
 
 struct AttnParams {
   RoundParams rd;

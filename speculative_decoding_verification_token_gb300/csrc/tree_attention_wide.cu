@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int e = 0; e < 4; ++e) t[e] = max3(t[e], a[c + 2 * e], a[c + 2 * e + 1]);
         }
         float top = max3(max3(t[0], t[1], a[124]), max3(t[2], t[3], a[125]), fmaxf(a[126], a[127]));
-        top *= scale1;  // (0 times an infinity is a NaN, which raises nothing: its weights are NaN)
+        top *= scale1;  // (an infinite score makes m infinite, and the row's weights NaN, as a NaN does itself)
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float now = fmaxf(m, top), factor = fast_exp2(m - now);
           m = now;
