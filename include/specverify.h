@@ -489,8 +489,12 @@ sv_status spec_tree_attention(const void* q, int64_t ldq, int64_t q_head, int64_
                               void* stream);
 
 /* Verification of a tree of drafts by tokens sampled from the target.  sampled (DEVICE int32,
- * indexed like the rows) holds one token drawn from each row's distribution (spec_sample_draft on
- * the target rows with a seed of its own, or their argmax); row i > 0 of request r is the drafted
+ * indexed like the rows) holds one token drawn from each row's distribution: spec_sample_draft on
+ * the target rows with a seed of its own, or their argmax.  That call takes up to SV_MAX_DRAFT_LEN
+ * rows a request, so 63 drafts and a root; for larger trees every row is a request of one row
+ * (draft_row0 = 0, 1, .. n_rows - 1, each draft_len 1), with request ids of their own.  Biases and
+ * masks of spec_process_logits hold for a tree's rows; its penalties take the drafts before a row
+ * for a chain, and do not.  Row i > 0 of request r is the drafted
  * token draft_tokens[draft_row0[r] + i - 1].  From row 0 the walk goes to the child whose token was
  * sampled at the row it stands on (the lowest such child), until there is none; the token sampled
  * there ends the round.  Every token emitted is thus a sample of the target's distribution behind
