@@ -70,15 +70,15 @@ struct AttnShared {
   }
 };
 
-// Who sees whom in a tree, by one warp: seen[j] = columns that see row j, for the row tile's columns.
+// Who sees whom in a tree, by one warp: seen[j] = columns that see row j.
 template <int kWords>
 __device__ __forceinline__ void build_seen(const AttnParams& p, const Item& x, uint32_t (*above)[4],
                                            uint32_t (*seen)[kWords]) {
   const int lane = threadIdx.x & 31;
-  const int32_t nodes = x.end - x.ctx, tok0 = x.tok0, columns = x.columns;
+  const int32_t nodes = x.end - x.ctx, columns = x.columns;
 #pragma unroll
   for (int w = 0; w < kWords; ++w) {
-    const int32_t c = w * 32 + lane, i = tok0 + c / p.group;
+    const int32_t c = w * 32 + lane, i = c / p.group;
     const bool in = c < columns;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -95,43 +95,20 @@ __device__ __forceinline__ void build_seen(const AttnParams& p, const Item& x, u
   }
 }
 
-
-// The item of this CTA's cluster of kCtas and the CTA's tiles of it, by one warp (at most 32 requests).
+// The item of this CTA's cluster of kCtas, a key head of a request, and the CTA's tiles of it.
 template <int kCtas>
 __device__ __forceinline__ Item cluster_item(const AttnParams& p, int64_t& first) {
-  const int lane = threadIdx.x & 31;
-  const int32_t cluster = blockIdx.x / kCtas, rank = blockIdx.x % kCtas;
-  Request q = {};
-  int32_t tiles = 0;  // row tiles
-  if (lane < p.rd.B) {
-    round_request(p.rd, lane, q);
-    tiles = (q.n + p.tokens - 1) / p.tokens;
-  }
-  const int32_t items = tiles * p.n_kv;
-  int32_t upto = items;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
+  const int32_t cluster = blockIdx.x / kCtas, rank = blockIdx.x % kCtas, r = cluster / p.n_kv;
+  Request q;
   Item x = {};
-  const uint32_t past = __ballot_sync(0xffffffffu, cluster < upto);
-  if (past) {
-    const int r = __ffs(past) - 1;
-    const int32_t left = cluster - __shfl_sync(0xffffffffu, upto - items, r);
-    tiles = __shfl_sync(0xffffffffu, tiles, r);
-    q.first = __shfl_sync(0xffffffffu, q.first, r);
-    q.n = __shfl_sync(0xffffffffu, q.n, r);
-    q.ctx = __shfl_sync(0xffffffffu, q.ctx, r);
+  if (round_request(p.rd, r, q) && q.n > 0) {
     first = q.first;
-    x.head = left / tiles, x.r = r;
-    const int32_t rt = left - x.head * tiles, tok0 = rt * p.tokens, ntok = min(p.tokens, q.n - tok0);
-    x.first_row = q.first + tok0;
-    x.columns = ntok * p.group;
-    x.tok0 = tok0, x.ctx = q.ctx;
-    x.base0 = q.ctx + (p.rd.parents ? 0 : tok0);
-    x.end = q.ctx + tok0 + ntok;
-    const int64_t all = tiles_of(q, rt, p.tokens);
+    x.head = cluster - r * p.n_kv, x.r = r;
+    x.first_row = q.first;
+    x.columns = q.n * p.group;
+    x.ctx = x.base0 = q.ctx;
+    x.end = q.ctx + q.n;
+    const int64_t all = tiles_of(q, 0, p.tokens);
     x.t0 = int32_t(all * rank / kCtas), x.t1 = int32_t(all * (rank + 1) / kCtas);
   }
   x.begins = x.last = 1;
@@ -239,7 +216,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr bool kShort = kCtas > 0;
   constexpr int kC = kN / 2;  // columns of a half
   constexpr int kStages = Sh::kStages();
-  constexpr uint32_t kCols = kN <= 16 ? 64 : kN <= 32 ? 128 : kN <= 64 ? 256 : 512;
+  constexpr uint32_t kCols = kN <= 16 ? 64 : kN <= 32 ? 128 : 256;
   static_assert(kStages >= 3, "a ring of three tiles");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const ring = reinterpret_cast<uint8_t*>(
@@ -288,7 +265,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const WsLayout wl = ws_layout(gridDim.x, kN, kD);
   if (warp == kItemWarp) {
     // ---- the items ---------------------------------------------------------------------------------
-    int64_t built[kItems];
+    int32_t built[kItems];  // the request whose tree a slot has
 #pragma unroll
     for (int b = 0; b < kItems; ++b) built[b] = -1;
     auto details = [&](int b, const Item& x, int64_t first) {
@@ -296,9 +273,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int32_t i = c / p.group, g = c - i * p.group;
         sm.col_off[b][c] = (x.first_row + i) * p.ldo + int64_t(x.head * p.group + g) * p.o_head;
       }
-      const int64_t key = int64_t(x.r) << 32 | x.tok0;
-      if (p.rd.parents && x.t1 * int64_t(kTile) > x.base0 && built[b] != key) {
-        built[b] = key;
+      if (p.rd.parents && x.t1 * int64_t(kTile) > x.base0 && built[b] != x.r) {
+        built[b] = x.r;
         build_above(p, first, x.end - x.ctx, sm.up, sm.above, err);
         build_seen<Sh::kWords>(p, x, sm.above, sm.seen[b]);
       }
@@ -332,7 +308,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     auto load = [&](const CUtensorMap* map, int32_t pg, int32_t fr, int32_t n, int32_t hd) {
       if (!wait_for_warp(&sm.empty[slot], phase, err)) return false;
-      load_tile<kD, 2>(p, ring + slot * Sh::kSlot, map, part, pg, fr, n, hd, &sm.full[slot], once);
+      load_tile<kD, 2, false>(p, ring + slot * Sh::kSlot, map, part, pg, fr, n, hd, &sm.full[slot], once);
       filled = max(filled, slot + 1);
       if (++slot == kStages) {
         slot = 0;

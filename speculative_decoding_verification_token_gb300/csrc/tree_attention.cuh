@@ -525,7 +525,7 @@ __device__ __forceinline__ int32_t tile_boxes(const AttnParams& p, const Item& x
 }
 
 // A warp's part of a tile of K or V into a ring slot of [D / 64][128 places][64 elements], swizzled.
-template <int kD, int kLoaders>
+template <int kD, int kLoaders, bool kRowTiles>
 __device__ __forceinline__ void load_tile(const AttnParams& p, uint8_t* dst, const CUtensorMap* map,
                                           int part, int32_t page, int32_t from, int32_t boxes,
                                           int32_t head, uint64_t* full, uint64_t once) {
@@ -538,8 +538,8 @@ __device__ __forceinline__ void load_tile(const AttnParams& p, uint8_t* dst, con
 #pragma unroll
     for (int k = k0; k < k0 + kEach; ++k) {
       uint8_t* const to = dst + k * 16384 + box * p.box_rows * 128;
-      // (keys that other row tiles read too stay in L2 like anything else)
-      if (p.reread) tma_load_4d(to, map, k * 64, head, from, page, full);
+      // (keys that other row tiles of the request read too stay in L2 like anything else)
+      if (kRowTiles && p.reread) tma_load_4d(to, map, k * 64, head, from, page, full);
       else tma_load_4d_hint(to, map, k * 64, head, from, page, full, once);
     }
   }

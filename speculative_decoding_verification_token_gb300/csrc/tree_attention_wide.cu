@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     auto load = [&](const CUtensorMap* map, int32_t page, int32_t from, int32_t boxes, int32_t head) {
       if (!wait_for_warp(&sm.empty[slot], phase, err)) return false;
-      load_tile<kD, kLoaders>(p, ring + slot * Sh::kSlot, map, part, page, from, boxes, head,
+      load_tile<kD, kLoaders, true>(p, ring + slot * Sh::kSlot, map, part, page, from, boxes, head,
                               &sm.full[slot], once);
       filled = max(filled, slot + 1);
       if (++slot == kStages) {
