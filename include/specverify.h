@@ -474,8 +474,10 @@ size_t spec_tree_attention_workspace_bytes(int32_t B, int32_t max_draft_len, int
  * that a row does not see do not reach its result, whatever they hold, NaN included.  Scores x_j up
  * to 2^27 in magnitude: m, a score's binary32 value times log2(e), is rounded, for larger ones by
  * more than a weight's exponent allows, and the row's result may be NaN.  Rows that belong to no
- * request are not written.  n_heads a multiple of n_kv_heads, at most 128 times it;
- * D 64 or 128; page_size a power of two, at least 8; scale log2(e) finite. */
+ * request are not written.  The call is laid out by max_pages, not by the contexts: a few requests
+ * under no more columns than the longest of them needs take one launch.  n_heads a multiple of
+ * n_kv_heads, at most 128 times it; D 64 or 128; page_size a power of two, at least 8; scale log2(e)
+ * finite. */
 sv_status spec_tree_attention(const void* q, int64_t ldq, int64_t q_head, int64_t n_rows,
                               int32_t n_heads, int32_t n_kv_heads, int32_t D, float scale,
                               const int64_t* row0, const int32_t* draft_len,

@@ -30,8 +30,8 @@ constexpr int kAppendThreads = 256;
 constexpr int kRowThreads = 128;  // of a row
 constexpr int kAppendGroups = kAppendThreads / kRowThreads;
 // Heads whose loads a thread has in flight, and CTAs an SM, within the registers there are: 8 prompts of
-// up to 8192 tokens (bf16) 136 us (6.0 TB/s of the 811 MB that have to move; two CTAs 149), 64 trees of
-// 16 rows (fp32) 8.2 us (three CTAs spill: 16.6).
+// up to 8192 tokens (bf16) 136 us (5.8 TB/s of the 784 MB that have to move; two CTAs 149), in fp32 203 us (5.8
+// TB/s); 64 trees of 16 rows (fp32) 8.1 us where everything lies in L2 (three CTAs spill: 16.6), 10 to 12 from memory.
 template <typename T>
 constexpr int kAppendUnroll = sizeof(T) == 2 ? 3 : 2;
 template <typename T>
@@ -294,7 +294,8 @@ struct KeepParams {
 
 constexpr int kKeepThreads = 256;
 constexpr int kKeepBatch = 8;
-constexpr int kKeepCtas = 6;  // aimed at an SM: 64 requests in 32 layers 10.2 us (2: 13.4, 16: 11.7)
+// CTAs aimed at an SM: 64 requests in 32 layers 10.2 us where the rows lie in L2 (2: 13.4, 16: 11.7), 15 from memory.
+constexpr int kKeepCtas = 6;
 
 // A CTA per request and run of layers.  A path ascends from 1 or more, so row path[i] lies at or behind the
 // place i + 1 it goes to, and a thread that takes its own 16-byte column through the moves in order

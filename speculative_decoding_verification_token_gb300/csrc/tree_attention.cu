@@ -852,7 +852,7 @@ sv_status launch_join(const AttnParams& p, int grid, cudaStream_t s) {
 
 // Few items of few tiles: a cluster of 8 CTAs for each, or of 4.  They have to be there at once (see
 // clusters_at_once); more tiles are worth more SMs than a cluster has; and one warp looks through all the
-// pages.  Rows of 6 under 32 heads (8 key heads): one request 8.6 us over 1000 places (14.6 from the list),
+// pages.  Rows of 6 under 32 heads (8 key heads): one request 8.4 us over 1000 places (14.6 from the list),
 // two 12.2 over 2000 each (14.7), four 12.6 (17.7).  Eight in clusters of 2: 18.4 over 2000 places each (22.6),
 // but 17.9 over 1 to 2000 (16.3), the list's runs being equal.
 constexpr int kShortItems = 48, kShortRun = 8, kShortPages = 1024;
