@@ -31,7 +31,7 @@ constexpr int kRowThreads = 128;  // of a row
 constexpr int kAppendGroups = kAppendThreads / kRowThreads;
 // Heads whose loads a thread has in flight, and CTAs an SM, within the registers there are: 8 prompts of
 // up to 8192 tokens (bf16) 136 us (5.8 TB/s of the 784 MB that have to move; two CTAs 149), in fp32 203 us (5.8
-// TB/s); 64 trees of 16 rows (fp32) 8.1 us where everything lies in L2 (three CTAs spill: 16.6), 10 to 12 from memory.
+// TB/s); 64 trees of 16 rows (fp32) 8.1 us where everything lies in L2 (three CTAs spill: 16.6), 9 to 12 from memory.
 template <typename T>
 constexpr int kAppendUnroll = sizeof(T) == 2 ? 3 : 2;
 template <typename T>
