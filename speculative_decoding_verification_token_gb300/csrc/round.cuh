@@ -39,7 +39,8 @@ __device__ __forceinline__ bool round_request(const RoundParams& p, int32_t draf
                                               int64_t first, Request& q) {
   q.ctx = ctx;
   q.first = first;
-  q.n = drafts + p.bonus_row;  // (a length that max_draft_len allows fits: round_most_drafts)
+  // (a length that max_draft_len allows fits: round_most_drafts; another may wrap, and is refused below)
+  q.n = int32_t(uint32_t(drafts) + uint32_t(p.bonus_row));
   const bool ok = drafts >= 0 && drafts <= p.max_draft_len && q.ctx >= 0 && q.first >= 0 &&
                   q.first <= p.n_rows && q.n <= p.n_rows - q.first &&
                   int64_t(q.ctx) + q.n <=
